@@ -29,7 +29,9 @@ EXPORTED = ("attn_abi_version", "attn_status_string", "attn_fwd_workspace_size",
             "attn_bwd_workspace_size", "attn_resolve_layout", "attn_fwd", "attn_bwd",
             "attn_read_status", "attn_set_trace_events", "attn_event_create",
             "attn_event_destroy", "attn_event_elapsed_ms", "attn_fwd_noalloc",
-            "attn_build_flags")
+            "attn_build_flags", "attn_paged_workspace_size", "attn_paged_append",
+            "attn_paged_fwd")
+ATTN_PAGED_PARAMS_VERSION = 1
 FWD_NOALLOC_SCRATCH_BYTES = 4 << 20
 TRACE_SLOTS = ("meta", "fwd", "bwd_pre", "dkdv", "dq", "dbias")
 
@@ -73,6 +75,26 @@ class attn_resolved_t(ctypes.Structure):
                 ("dv", c_vp)]
 
 
+class attn_paged_params_t(ctypes.Structure):
+    _fields_ = [
+        ("struct_version", c_i32), ("dtype", c_i32), ("cache_dtype", c_i32), ("mask", c_i32),
+        ("num_seqs", c_i32), ("num_tokens", c_i32), ("max_q_len", c_i32),
+        ("Hq", c_i32), ("Hkv", c_i32), ("d_qk", c_i32), ("d_v", c_i32),
+        ("page_size", c_i32), ("num_pages", c_i32), ("max_pages", c_i32),
+        ("page_table", c_vp), ("table_stride", c_i64), ("seq_lens", c_vp),
+        ("cu_seqlens_q", c_vp),
+        ("k_cache", c_vp), ("v_cache", c_vp), ("k_cache_stride", c_i64 * 3),
+        ("v_cache_stride", c_i64 * 3),
+        ("k_scale", c_vp), ("v_scale", c_vp), ("status", c_vp),
+        ("q", c_vp), ("k_new", c_vp), ("v_new", c_vp), ("q_rot", c_vp),
+        ("q_stride", c_i64), ("k_new_stride", c_i64), ("v_new_stride", c_i64),
+        ("q_rot_stride", c_i64),
+        ("rot_dim", c_i32), ("rot_interleaved", c_i32), ("rope_len", c_i32),
+        ("rope_cos", c_vp), ("rope_sin", c_vp), ("rope_pos", c_vp),
+        ("scale", c_f32), ("window_left", c_i32), ("sink", c_vp),
+    ]
+
+
 _lib = None
 
 
@@ -112,6 +134,13 @@ def load_library(path: str = LIB_PATH):
     lib.attn_event_destroy.argtypes = [c_vp]
     lib.attn_event_elapsed_ms.restype = c_i32
     lib.attn_event_elapsed_ms.argtypes = [c_vp, c_vp, ctypes.POINTER(ctypes.c_float)]
+    PP = ctypes.POINTER(attn_paged_params_t)
+    lib.attn_paged_workspace_size.restype = c_sz
+    lib.attn_paged_workspace_size.argtypes = [PP]
+    lib.attn_paged_append.restype = c_i32
+    lib.attn_paged_append.argtypes = [PP, c_vp]
+    lib.attn_paged_fwd.restype = c_i32
+    lib.attn_paged_fwd.argtypes = [PP, c_vp, c_vp, c_vp, c_sz, c_vp]
     if lib.attn_abi_version() != ATTN_PARAMS_VERSION:
         raise RuntimeError("attention library ABI version mismatch")
     _lib = lib
@@ -249,6 +278,148 @@ def attn_bwd(p, o, d_o, lse, dq, dk, dv, dbias, ws, stream=None):
                                 _stream(stream))
     if s != 0:
         raise AttnError(s, "attn_bwd")
+
+
+def _rows(name, t, heads, dim):
+    """Token stride in elements of a [tokens, heads, dim] tensor whose rows may
+    lie apart (a slice of a fused projection) but are whole inside."""
+    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, dim):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [tokens, {heads}, {dim}]")
+    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{name}: heads and dims must be contiguous inside a token's row")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def make_paged_params(*, dtype, cache_dtype, k_cache, v_cache, page_table, seq_lens, q=None,
+                      k_new=None, v_new=None, q_rot=None, k_scale=None, v_scale=None,
+                      cu_seqlens_q=None, max_q_len=1, rope_cos=None, rope_sin=None,
+                      rope_pos=None, rope_interleaved=False, scale=None, mask="CAUSAL",
+                      window_left=None, sink=None, status=None):
+    """Fill an ``attn_paged_params_t`` from tensors (see attn.h).
+
+    k_cache / v_cache: [num_pages, Hkv, page_size, dim] views in any order of
+    memory with contiguous dims (a cache kept as [num_pages, page_size, Hkv,
+    dim] is passed as ``cache.transpose(1, 2)``); page_table: int32 [num_seqs,
+    max_pages]; seq_lens: int32 [num_seqs], new tokens included; q, q_rot
+    [tokens, Hq, d_qk], k_new, v_new [tokens, Hkv, dim]; rope_cos, rope_sin:
+    fp32 [rope_len, rot_dim / 2] (None: no rotation); scale: softmax scale
+    (None: d_qk ** -0.5).  The block holds the tensors' addresses, so they must
+    outlive its calls; their contents may change between calls.  All tensors
+    are on the device that is current when the block is made, which is also
+    the one its calls must be made on."""
+    import torch
+
+    if q is None and q_rot is None and k_new is None:
+        raise ValueError("neither queries nor new keys are given")
+    Hkv, page, d_qk = (int(x) for x in k_cache.shape[1:])
+    d_v = int(v_cache.shape[3])
+    if k_cache.dim() != 4 or v_cache.dim() != 4 or v_cache.shape[:3] != k_cache.shape[:3]:
+        raise ValueError("k_cache and v_cache: [num_pages, Hkv, page_size, dim] with the same "
+                         "pages, heads and page size")
+    elem = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp8_e4m3": torch.float8_e4m3fn}
+    want = {}
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        ok = (elem[cache_dtype], torch.uint8) if cache_dtype == "fp8_e4m3" else (elem[cache_dtype],)
+        if t.dtype not in ok:
+            raise ValueError(f"{name}: {t.dtype}, expected {cache_dtype}")
+        if t.stride(3) != 1:
+            raise ValueError(f"{name}: dims must be contiguous")
+    for name, t, dt in (("q", q, elem[dtype]), ("k_new", k_new, elem[dtype]),
+                        ("v_new", v_new, elem[dtype]), ("q_rot", q_rot, elem[dtype]),
+                        ("k_scale", k_scale, torch.float32), ("v_scale", v_scale, torch.float32),
+                        ("rope_cos", rope_cos, torch.float32),
+                        ("rope_sin", rope_sin, torch.float32), ("sink", sink, torch.float32),
+                        ("rope_pos", rope_pos, torch.int32), ("status", status, torch.int32),
+                        ("page_table", page_table, torch.int32),
+                        ("seq_lens", seq_lens, torch.int32),
+                        ("cu_seqlens_q", cu_seqlens_q, torch.int32)):
+        if t is not None and t.dtype != dt:
+            raise ValueError(f"{name}: {t.dtype}, expected {dt}")
+        want[name] = t
+    given = dict(want, k_cache=k_cache, v_cache=v_cache)
+    devices = {t.device for t in given.values() if t is not None}
+    if len(devices) != 1:
+        raise ValueError(f"tensors on several devices: {sorted(map(str, devices))}")
+    device = devices.pop()
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    for name in ("k_scale", "v_scale", "rope_cos", "rope_sin", "rope_pos", "sink", "seq_lens",
+                 "cu_seqlens_q"):
+        if given[name] is not None and not given[name].is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+    num_seqs = int(seq_lens.shape[0])
+    if page_table.dim() != 2 or page_table.shape[0] != num_seqs or (
+            page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table: [num_seqs, max_pages] with contiguous rows")
+    if cu_seqlens_q is not None and tuple(cu_seqlens_q.shape) != (num_seqs + 1,):
+        raise ValueError("cu_seqlens_q: [num_seqs + 1]")
+    for name in ("k_scale", "v_scale"):
+        if given[name] is not None and tuple(given[name].shape) != (k_cache.shape[0], Hkv):
+            raise ValueError(f"{name}: [num_pages, Hkv]")
+
+    p = attn_paged_params_t()
+    p.struct_version = ATTN_PAGED_PARAMS_VERSION
+    p.dtype, p.cache_dtype, p.mask = DTYPES[dtype], DTYPES[cache_dtype], MASKS[mask]
+    rows = next(t for t in (q, q_rot, k_new) if t is not None)
+    heads = next((t for t in (q, q_rot) if t is not None), None)
+    p.num_seqs, p.num_tokens, p.max_q_len = num_seqs, int(rows.shape[0]), int(max_q_len)
+    p.Hq, p.Hkv = (Hkv if heads is None else int(heads.shape[1])), Hkv
+    p.d_qk, p.d_v = d_qk, d_v
+    p.page_size, p.num_pages = page, int(k_cache.shape[0])
+    p.max_pages = int(page_table.shape[1])
+    p.page_table, p.seq_lens, p.cu_seqlens_q = (_ptr(page_table), _ptr(seq_lens),
+                                                _ptr(cu_seqlens_q))
+    p.table_stride = page_table.stride(0) if num_seqs > 1 else p.max_pages
+    p.k_cache, p.v_cache = _ptr(k_cache), _ptr(v_cache)
+    for field, t in ((p.k_cache_stride, k_cache), (p.v_cache_stride, v_cache)):
+        for i in range(3):  # the stride of an axis of one is never used
+            field[i] = t.stride(i) if t.shape[i] > 1 else 16
+    p.k_scale, p.v_scale, p.status = _ptr(k_scale), _ptr(v_scale), _ptr(status)
+    for name, t, h, d in (("q", q, p.Hq, d_qk), ("q_rot", q_rot, p.Hq, d_qk),
+                          ("k_new", k_new, Hkv, d_qk), ("v_new", v_new, Hkv, d_v)):
+        if t is not None:
+            if t.shape[0] != p.num_tokens:
+                raise ValueError(f"{name}: {t.shape[0]} rows, expected {p.num_tokens}")
+            setattr(p, name + "_stride", _rows(name, t, h, d))
+            setattr(p, name, _ptr(t))
+    if (rope_cos is None) != (rope_sin is None):
+        raise ValueError("rope_cos and rope_sin go together")
+    if rope_cos is not None:
+        if rope_cos.dim() != 2 or rope_cos.shape != rope_sin.shape:
+            raise ValueError("rope_cos, rope_sin: [rope_len, rot_dim / 2]")
+        p.rot_dim, p.rope_len = 2 * int(rope_cos.shape[1]), int(rope_cos.shape[0])
+        p.rope_cos, p.rope_sin = _ptr(rope_cos), _ptr(rope_sin)
+    if rope_pos is not None and tuple(rope_pos.shape) != (p.num_tokens,):
+        raise ValueError("rope_pos: [tokens]")
+    p.rope_pos = _ptr(rope_pos)
+    p.rot_interleaved = 1 if rope_interleaved else 0
+    p.scale = float(d_qk ** -0.5 if scale is None else scale)
+    p.window_left = -1 if window_left is None else int(window_left)
+    if sink is not None and tuple(sink.shape) != (p.Hq,):
+        raise ValueError("sink: [Hq]")
+    p.sink = _ptr(sink)
+    return p
+
+
+def attn_paged_workspace_size(p):
+    return int(load_library().attn_paged_workspace_size(ctypes.byref(p)))
+
+
+def attn_paged_append(p, stream=None):
+    """Enqueue the append on `stream` (default: torch's current stream)."""
+    s = load_library().attn_paged_append(ctypes.byref(p), _stream(stream))
+    if s != 0:
+        raise AttnError(s, "attn_paged_append")
+
+
+def attn_paged_fwd(p, o, lse, ws, stream=None):
+    """Enqueue the attention over the cache on `stream` (default: torch's
+    current stream).  o: [tokens, Hq, d_v]; lse: fp32 [Hq, tokens] or None."""
+    s = load_library().attn_paged_fwd(ctypes.byref(p), _ptr(o), _ptr(lse), _ptr(ws),
+                                      ws.numel() * ws.element_size(), _stream(stream))
+    if s != 0:
+        raise AttnError(s, "attn_paged_fwd")
 
 
 def attn_read_status(ws, stream=None):

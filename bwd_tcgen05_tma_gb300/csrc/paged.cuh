@@ -1,0 +1,149 @@
+// Shared by the paged-cache kernels: the device view of one call, and the
+// arithmetic of pages, positions and E4M3 scales.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/attn.h"
+#include "sm103_ptx.cuh"
+
+namespace attn {
+namespace paged {
+
+// Element kinds of a cache.
+enum CacheKind { kCacheBf16 = 0, kCacheF16 = 1, kCacheE4m3 = 2 };
+
+struct Args {
+  int num_seqs, num_tokens, Hq, Hkv, group;
+  int page_shift, num_pages, max_pages;
+  int f16;     // 16-bit tensors are fp16 (else bf16)
+  int causal;  // attention: keys behind the row's position are masked
+  int window;  // attention: keys more than this before it are masked (< 0: none)
+  float scale;
+  const int32_t* table;
+  const int32_t* seq_lens;
+  const int32_t* cu;
+  int64_t table_stride;
+  char* kc;  // cache bases; strides in bytes
+  char* vc;
+  int64_t k_page, k_head, k_tok, v_page, v_head, v_tok;
+  float* k_scale;
+  float* v_scale;
+  int32_t* status;
+  // new tokens (strides in elements)
+  const uint16_t* q;
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  uint16_t* q_rot;
+  int64_t q_stride, k_new_stride, v_new_stride, q_rot_stride;
+  int rot, interleaved, rope_len, d_qk, d_v;
+  const float* cos;
+  const float* sin;
+  const int32_t* rope_pos;
+  // attention outputs and split partials
+  const float* sink;
+  uint16_t* o;
+  float* lse;
+  float* part;       // [2 * ctas][rows][d_v] unnormalised O
+  float2* part_ml;   // [2 * ctas][rows] (max in log2 units, sum)
+  int4* split_desc;  // [ctas]
+  int part_rows;
+};
+
+// One sequence: its new rows and its length.
+struct Seq {
+  int row0, n, len;
+};
+
+__device__ __forceinline__ void flag_bounds(const Args& a) {
+  if (a.status) *a.status = ATTN_ERR_DEVICE_BOUNDS;
+}
+
+// Rows and length of sequence s.  Offsets outside [0, num_tokens] or
+// decreasing, and negative lengths, are reported and read as empty.
+__device__ __forceinline__ Seq load_seq(const Args& a, int s) {
+  Seq q;
+  q.len = a.seq_lens[s];
+  q.row0 = s;
+  q.n = 1;
+  if (a.cu) {
+    q.row0 = a.cu[s];
+    const int end = a.cu[s + 1];
+    q.n = end - q.row0;
+    if (q.row0 < 0 || end > a.num_tokens || q.n < 0) {
+      flag_bounds(a);
+      q.row0 = 0;
+      q.n = 0;
+    }
+  }
+  if (q.len < 0) {
+    flag_bounds(a);
+    q.len = 0;
+    q.n = 0;
+  }
+  return q;
+}
+
+// Page of position j of sequence s, or -1 (reported) when the table cannot
+// give one.
+__device__ __forceinline__ int page_of(const Args& a, int s, int j) {
+  const int c = j >> a.page_shift;
+  if (j < 0 || c >= a.max_pages) {
+    flag_bounds(a);
+    return -1;
+  }
+  const int p = a.table[s * a.table_stride + c];
+  if (p < 0 || p >= a.num_pages) {
+    flag_bounds(a);
+    return -1;
+  }
+  return p;
+}
+
+__device__ __forceinline__ float elem(uint16_t x, int f16) {
+  return f16 ? __half2float(__ushort_as_half(x)) : __uint_as_float(uint32_t(x) << 16);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, int f16) {
+  return f16 ? sm103::pack_f16x2(lo, hi) : sm103::pack_bf16x2(lo, hi);
+}
+__device__ __forceinline__ uint16_t round16(float x, int f16) {
+  return static_cast<uint16_t>(pack2(x, 0.f, f16));
+}
+
+// Two E4M3 codes (low byte first) to a pair of fp16 values, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t c) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(c));
+  return d;
+}
+__device__ __forceinline__ float e4m3_value(uint8_t c) {
+  return __half2float(__ushort_as_half(static_cast<uint16_t>(e4m3x2_f16x2(c))));
+}
+// Two values to E4M3 codes, nearest even; the callers' values are at most 448
+// in magnitude but for infinities, which become NaN here like NaN itself.
+__device__ __forceinline__ uint16_t f32x2_e4m3x2(float lo, float hi) {
+  const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fc00000);
+  lo = fabsf(lo) == inf ? nan : lo;
+  hi = fabsf(hi) == inf ? nan : hi;
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+constexpr int kMinExp = -64;
+// Smallest power of two s >= 2^-64 with amax <= 448 s (amax finite): with
+// amax = 1.f * 2^x, 448 = 1.75 * 2^8, so e = x - 8, or one more if 1.f > 1.75.
+__device__ __forceinline__ float page_scale(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = e < kMinExp ? kMinExp : e;
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+cudaError_t launch_append(const Args& a, int kind, cudaStream_t st);
+cudaError_t launch_attend(const Args& a, int kind, cudaStream_t st);
+
+}  // namespace paged
+}  // namespace attn

@@ -1,0 +1,188 @@
+// Host side of the paged-cache calls: argument validation, workspace layout
+// and launches.
+#include <cmath>
+#include <cstring>
+
+#include "paged.cuh"
+
+namespace attn {
+namespace paged {
+namespace {
+
+inline bool aligned(const void* p, uintptr_t n) {
+  return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+
+int64_t cache_bytes(const attn_paged_params_t* p) {
+  return p->cache_dtype == ATTN_DTYPE_FP8_E4M3 ? 1 : 2;
+}
+
+int kind_of(const attn_paged_params_t* p) {
+  if (p->cache_dtype == ATTN_DTYPE_FP8_E4M3) return kCacheE4m3;
+  return p->cache_dtype == ATTN_DTYPE_FP16 ? kCacheF16 : kCacheBf16;
+}
+
+bool row_stride_ok(const void* ptr, int64_t stride, int64_t width) {
+  return !ptr || (aligned(ptr, 16) && stride >= width && stride % 8 == 0);
+}
+
+// What both calls require.
+attn_status_t validate(const attn_paged_params_t* p) {
+  if (!p || p->struct_version != ATTN_PAGED_PARAMS_VERSION) return ATTN_ERR_INVALID_ARG;
+  if (p->dtype != ATTN_DTYPE_BF16 && p->dtype != ATTN_DTYPE_FP16) return ATTN_ERR_INVALID_ARG;
+  if (p->cache_dtype != p->dtype && p->cache_dtype != ATTN_DTYPE_FP8_E4M3)
+    return ATTN_ERR_INVALID_ARG;
+  if (p->mask != ATTN_MASK_NONE && p->mask != ATTN_MASK_CAUSAL) return ATTN_ERR_INVALID_ARG;
+  if (p->num_seqs < 0 || p->num_tokens < 0 || p->max_q_len < 1 || p->Hq <= 0 || p->Hkv <= 0 ||
+      p->num_pages < 0 || p->max_pages < 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (p->Hq % p->Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  if (p->Hq > 256) return ATTN_ERR_UNSUPPORTED;
+  if (p->d_qk != 64 && p->d_qk != 128 && p->d_qk != 192) return ATTN_ERR_UNSUPPORTED;
+  if (p->d_v != 64 && p->d_v != 128) return ATTN_ERR_UNSUPPORTED;
+  if (p->page_size < 16 || p->page_size > 256 || (p->page_size & (p->page_size - 1)))
+    return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(p->max_pages) * p->page_size >= (1ll << 31)) return ATTN_ERR_UNSUPPORTED;
+  if (!p->cu_seqlens_q && p->num_tokens != p->num_seqs) return ATTN_ERR_SHAPE_MISMATCH;
+  const bool none = p->num_seqs == 0 || p->num_tokens == 0;
+  if (!none && (!p->seq_lens || (!p->page_table && p->max_pages > 0) ||
+                ((!p->k_cache || !p->v_cache) && p->num_pages > 0)))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(p->seq_lens, 4) || !aligned(p->page_table, 4) || !aligned(p->cu_seqlens_q, 4) ||
+      !aligned(p->status, 4) || !aligned(p->k_scale, 4) || !aligned(p->v_scale, 4) ||
+      !aligned(p->k_cache, 16) || !aligned(p->v_cache, 16))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->num_seqs > 1 && p->table_stride < p->max_pages) return ATTN_ERR_INVALID_ARG;
+  const int64_t per16 = 16 / cache_bytes(p);
+  for (int i = 0; i < 3; ++i)
+    if (p->k_cache_stride[i] <= 0 || p->k_cache_stride[i] % per16 || p->v_cache_stride[i] <= 0 ||
+        p->v_cache_stride[i] % per16)
+      return ATTN_ERR_INVALID_ARG;
+  const bool scales = p->k_scale && p->v_scale, any = p->k_scale || p->v_scale;
+  if (p->cache_dtype == ATTN_DTYPE_FP8_E4M3 ? (!none && !scales) : any) return ATTN_ERR_INVALID_ARG;
+  const int64_t wq = static_cast<int64_t>(p->Hq) * p->d_qk;
+  if (!row_stride_ok(p->q, p->q_stride, wq) || !row_stride_ok(p->q_rot, p->q_rot_stride, wq))
+    return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+attn_status_t validate_append(const attn_paged_params_t* p) {
+  const attn_status_t s = validate(p);
+  if (s != ATTN_OK) return s;
+  if (!p->k_new != !p->v_new) return ATTN_ERR_INVALID_ARG;
+  if (!p->k_new && p->num_tokens > 0) return ATTN_ERR_INVALID_ARG;
+  if (p->q && !p->q_rot) return ATTN_ERR_INVALID_ARG;
+  if (!row_stride_ok(p->k_new, p->k_new_stride, static_cast<int64_t>(p->Hkv) * p->d_qk) ||
+      !row_stride_ok(p->v_new, p->v_new_stride, static_cast<int64_t>(p->Hkv) * p->d_v))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->rot_dim < 0 || p->rot_dim > p->d_qk) return ATTN_ERR_INVALID_ARG;
+  if (p->rot_dim % 16) return ATTN_ERR_UNSUPPORTED;
+  if (p->rot_dim > 0 && (!p->rope_cos || !p->rope_sin || !aligned(p->rope_cos, 16) ||
+                         !aligned(p->rope_sin, 16) || p->rope_len <= 0))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(p->rope_pos, 4)) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+attn_status_t validate_fwd(const attn_paged_params_t* p) {
+  const attn_status_t s = validate(p);
+  if (s != ATTN_OK) return s;
+  if (!p->q && !p->q_rot && p->num_tokens > 0) return ATTN_ERR_INVALID_ARG;
+  if (!(p->scale > 0.f) || !std::isfinite(p->scale)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(p->sink, 4)) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+void fill(Args& a, const attn_paged_params_t* p) {
+  std::memset(&a, 0, sizeof(a));
+  const int64_t cb = cache_bytes(p);
+  a.num_seqs = p->num_seqs;
+  a.num_tokens = p->num_tokens;
+  a.Hq = p->Hq;
+  a.Hkv = p->Hkv;
+  a.group = p->Hq / p->Hkv;
+  while ((1 << a.page_shift) < p->page_size) ++a.page_shift;
+  a.num_pages = p->num_pages;
+  a.max_pages = p->max_pages;
+  a.f16 = p->dtype == ATTN_DTYPE_FP16;
+  a.causal = p->mask == ATTN_MASK_CAUSAL;
+  a.window = p->window_left < 0 ? -1 : p->window_left;
+  a.scale = p->scale;
+  a.table = p->page_table;
+  a.table_stride = p->table_stride;
+  a.seq_lens = p->seq_lens;
+  a.cu = p->cu_seqlens_q;
+  a.kc = static_cast<char*>(p->k_cache);
+  a.vc = static_cast<char*>(p->v_cache);
+  a.k_page = p->k_cache_stride[0] * cb;
+  a.k_head = p->k_cache_stride[1] * cb;
+  a.k_tok = p->k_cache_stride[2] * cb;
+  a.v_page = p->v_cache_stride[0] * cb;
+  a.v_head = p->v_cache_stride[1] * cb;
+  a.v_tok = p->v_cache_stride[2] * cb;
+  a.k_scale = p->k_scale;
+  a.v_scale = p->v_scale;
+  a.status = p->status;
+  a.d_qk = p->d_qk;
+  a.d_v = p->d_v;
+}
+
+}  // namespace
+}  // namespace paged
+}  // namespace attn
+
+using namespace attn::paged;
+
+extern "C" {
+
+size_t attn_paged_workspace_size(const attn_paged_params_t* p) {
+  if (validate_fwd(p) != ATTN_OK) return 0;
+  return 256;
+}
+
+attn_status_t attn_paged_append(const attn_paged_params_t* p, void* stream) {
+  const attn_status_t s = validate_append(p);
+  if (s != ATTN_OK) return s;
+  if (p->num_seqs == 0 || p->num_tokens == 0) return ATTN_OK;
+  Args a;
+  fill(a, p);
+  a.q = static_cast<const uint16_t*>(p->q);
+  a.q_stride = p->q_stride;
+  a.k_new = static_cast<const uint16_t*>(p->k_new);
+  a.v_new = static_cast<const uint16_t*>(p->v_new);
+  a.q_rot = static_cast<uint16_t*>(p->q_rot);
+  a.k_new_stride = p->k_new_stride;
+  a.v_new_stride = p->v_new_stride;
+  a.q_rot_stride = p->q_rot_stride;
+  a.rot = p->rot_dim;
+  a.interleaved = p->rot_interleaved != 0;
+  a.rope_len = p->rope_len;
+  a.cos = p->rope_cos;
+  a.sin = p->rope_sin;
+  a.rope_pos = p->rope_pos;
+  return launch_append(a, kind_of(p), static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
+}
+
+attn_status_t attn_paged_fwd(const attn_paged_params_t* p, void* o, float* lse, void* ws,
+                             size_t ws_bytes, void* stream) {
+  const attn_status_t s = validate_fwd(p);
+  if (s != ATTN_OK) return s;
+  if (p->num_seqs == 0 || p->num_tokens == 0) return ATTN_OK;
+  if (!o || !aligned(o, 16) || !aligned(lse, 4) || !ws || !aligned(ws, 256))
+    return ATTN_ERR_INVALID_ARG;
+  if (ws_bytes < attn_paged_workspace_size(p)) return ATTN_ERR_WORKSPACE_TOO_SMALL;
+  Args a;
+  fill(a, p);
+  a.q = static_cast<const uint16_t*>(p->q_rot ? p->q_rot : p->q);
+  a.q_stride = p->q_rot ? p->q_rot_stride : p->q_stride;
+  a.sink = p->sink;
+  a.o = static_cast<uint16_t*>(o);
+  a.lse = lse;
+  return launch_attend(a, kind_of(p), static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,354 @@
+// Appending new tokens to the paged cache.
+//
+// One block per (run of new tokens inside one page, KV head): it rotates the
+// head's new keys and the queries of its group, and writes keys and values
+// into the page.  With an E4M3 cache the block owns the page's two scales of
+// that head, so the scale, the codes already there and the new ones are
+// settled in one place without atomics: the result does not depend on the
+// order of blocks.
+//
+// Work goes in units of 16 elements, two 16-byte loads: the eight pairs of a
+// rotation (halves rot/2 apart, or neighbours), or sixteen values that pass.
+// The values stay in registers from the load over the block's maximum to the
+// store (up to kHold units a thread; pages of more read them twice).
+#include "paged.cuh"
+
+namespace attn {
+namespace paged {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kHold = 4;
+
+struct Unit {
+  float x[16];  // first eight, second eight
+};
+
+// Element offsets of a unit's two halves inside a head of width d.
+__device__ __forceinline__ int2 unit_at(int u, int rot, int interleaved) {
+  if (!interleaved && u < rot / 16) return make_int2(8 * u, rot / 2 + 8 * u);
+  return make_int2(16 * u, 16 * u + 8);
+}
+
+__device__ __forceinline__ void unpack8(uint4 v, float* x, int f16) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (f16) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    } else {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+
+// Unit u of a head at `src`, rotated where u < rot / 16 by row `cs` of the
+// tables.  a' = a c - b s and b' = b c + a s, each product and the sum rounded
+// in fp32.
+__device__ __forceinline__ void load_unit(const Args& a, const uint16_t* src, int u, int rot,
+                                          int64_t cs, Unit& r) {
+  const int2 at = unit_at(u, rot, a.interleaved);
+  const uint4 lo = *reinterpret_cast<const uint4*>(src + at.x);
+  const uint4 hi = *reinterpret_cast<const uint4*>(src + at.y);
+  unpack8(lo, r.x, a.f16);
+  unpack8(hi, r.x + 8, a.f16);
+  if (u < rot / 16) {
+    float c[8], s[8];
+    const float4* cp = reinterpret_cast<const float4*>(a.cos + cs * (rot / 2) + 8 * u);
+    const float4* sp = reinterpret_cast<const float4*>(a.sin + cs * (rot / 2) + 8 * u);
+    *reinterpret_cast<float4*>(c) = __ldg(cp);
+    *reinterpret_cast<float4*>(c + 4) = __ldg(cp + 1);
+    *reinterpret_cast<float4*>(s) = __ldg(sp);
+    *reinterpret_cast<float4*>(s + 4) = __ldg(sp + 1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int p = a.interleaved ? 2 * i : i, q = a.interleaved ? 2 * i + 1 : i + 8;
+      const float x = r.x[p], y = r.x[q];
+      r.x[p] = __fsub_rn(__fmul_rn(x, c[i]), __fmul_rn(y, s[i]));
+      r.x[q] = __fadd_rn(__fmul_rn(y, c[i]), __fmul_rn(x, s[i]));
+    }
+  }
+}
+
+__device__ __forceinline__ void store16(uint16_t* dst, int2 at, const Unit& r, int f16) {
+  uint4 lo, hi;
+  lo.x = pack2(r.x[0], r.x[1], f16);
+  lo.y = pack2(r.x[2], r.x[3], f16);
+  lo.z = pack2(r.x[4], r.x[5], f16);
+  lo.w = pack2(r.x[6], r.x[7], f16);
+  hi.x = pack2(r.x[8], r.x[9], f16);
+  hi.y = pack2(r.x[10], r.x[11], f16);
+  hi.z = pack2(r.x[12], r.x[13], f16);
+  hi.w = pack2(r.x[14], r.x[15], f16);
+  *reinterpret_cast<uint4*>(dst + at.x) = lo;
+  *reinterpret_cast<uint4*>(dst + at.y) = hi;
+}
+
+__device__ __forceinline__ void store8(uint8_t* dst, int2 at, const Unit& r, float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = f32x2_e4m3x2(r.x[4 * i] * inv, r.x[4 * i + 1] * inv);
+    const uint32_t hi = f32x2_e4m3x2(r.x[4 * i + 2] * inv, r.x[4 * i + 3] * inv);
+    w[i] = lo | (hi << 16);
+  }
+  *reinterpret_cast<uint2*>(dst + at.x) = make_uint2(w[0], w[1]);
+  *reinterpret_cast<uint2*>(dst + at.y) = make_uint2(w[2], w[3]);
+}
+
+// Largest finite magnitude (infinities and NaN become NaN codes).
+__device__ __forceinline__ float unit_amax(const Unit& r) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float x = fabsf(r.x[i]);
+    m = x < __int_as_float(0x7f800000) ? fmaxf(m, x) : m;
+  }
+  return m;
+}
+
+// The run of new tokens a block works on.
+struct Run {
+  int seq, page, slot0, n, row0, pos0;
+};
+
+// Block `c`'s run: the runs of all sequences in order, each sequence's new
+// positions cut at page borders.  With one token per sequence run c is
+// sequence c; otherwise every block sums the sequences' run counts.
+__device__ __forceinline__ bool find_run(const Args& a, int c, Run* out) {
+  __shared__ int s_sum[kThreads / 32];
+  __shared__ int s_seq, s_left;
+  if (threadIdx.x == 0) s_seq = -1;
+  int base = 0;
+  if (a.cu) {
+    for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
+      const int s = s0 + threadIdx.x;
+      int cnt = 0;
+      if (s < a.num_seqs) {
+        const Seq q = load_seq(a, s);
+        if (q.n > 0) {
+          const int first = max(0, q.len - q.n);
+          if (q.len > 0) cnt = ((q.len - 1) >> a.page_shift) - (first >> a.page_shift) + 1;
+        }
+      }
+      int x = cnt;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        if ((threadIdx.x & 31) >= d) x += y;
+      }
+      if ((threadIdx.x & 31) == 31) s_sum[threadIdx.x / 32] = x;
+      __syncthreads();
+      int before = base;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        const int t = s_sum[w];
+        if (w < static_cast<int>(threadIdx.x) / 32) before += t;
+        base += t;
+      }
+      if (c >= before + x - cnt && c < before + x) {
+        s_seq = s;
+        s_left = c - (before + x - cnt);
+      }
+      __syncthreads();
+      if (s_seq >= 0 || c < base) break;
+    }
+  } else {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      s_seq = c;
+      s_left = 0;
+    }
+    __syncthreads();
+  }
+  if (s_seq < 0) return false;
+  const Seq q = load_seq(a, s_seq);
+  const int first = q.len - q.n;  // may be negative: those tokens have no slot
+  const int lo = max(0, first);
+  if (q.n <= 0 || q.len <= 0) return false;  // length 0: the rows are padding
+  if (first < 0 && threadIdx.x == 0) flag_bounds(a);
+  const int col = (lo >> a.page_shift) + s_left;
+  const int p0 = max(lo, col << a.page_shift);
+  const int p1 = min(q.len, (col + 1) << a.page_shift);
+  out->seq = s_seq;
+  out->page = page_of(a, s_seq, p0);
+  out->slot0 = p0 & ((1 << a.page_shift) - 1);
+  out->n = p1 - p0;
+  out->row0 = q.row0 + (p0 - first);
+  out->pos0 = p0;
+  return out->page >= 0;
+}
+
+// kind: CacheKind
+template <int kKind>
+__global__ void __launch_bounds__(kThreads) append_kernel(Args a) {
+  Run run;
+  if (!find_run(a, blockIdx.x, &run)) return;
+  const int h = blockIdx.y, tid = threadIdx.x;
+  const int uk = a.d_qk / 16, uv = a.d_v / 16;
+  const int nk = run.n * uk, nkv = nk + run.n * uv;
+  const int rot = a.rot;
+  char* kdst = a.kc + run.page * a.k_page + h * a.k_head + run.slot0 * a.k_tok;
+  char* vdst = a.vc + run.page * a.v_page + h * a.v_head + run.slot0 * a.v_tok;
+
+  // Row of the rotation tables for token i of the run, or -1 (reported).
+  auto table_row = [&](int i) -> int {
+    const int p = a.rope_pos ? a.rope_pos[run.row0 + i] : run.pos0 + i;
+    if (p < 0 || p >= a.rope_len) {
+      flag_bounds(a);
+      return -1;
+    }
+    return p;
+  };
+  // Unit e of the run's keys, then values: false if it is not to be written.
+  auto load_kv = [&](int e, Unit& r) -> bool {
+    const bool key = e < nk;
+    const int i = key ? e / uk : (e - nk) / uv, u = key ? e % uk : (e - nk) % uv;
+    int row = 0;
+    if (rot > 0 && (row = table_row(i)) < 0) return false;
+    const int64_t t = run.row0 + i;
+    if (key)
+      load_unit(a, a.k_new + t * a.k_new_stride + h * a.d_qk, u, rot, row, r);
+    else
+      load_unit(a, a.v_new + t * a.v_new_stride + h * a.d_v, u, 0, 0, r);
+    return true;
+  };
+  auto store_kv = [&](int e, const Unit& r, float inv_k, float inv_v) {
+    const bool key = e < nk;
+    const int i = key ? e / uk : (e - nk) / uv, u = key ? e % uk : (e - nk) % uv;
+    char* dst = key ? kdst + i * a.k_tok : vdst + i * a.v_tok;
+    const int2 at = unit_at(u, key ? rot : 0, a.interleaved);
+    if (kKind == kCacheE4m3)
+      store8(reinterpret_cast<uint8_t*>(dst), at, r, key ? inv_k : inv_v);
+    else
+      store16(reinterpret_cast<uint16_t*>(dst), at, r, kKind == kCacheF16);
+  };
+  auto turn_queries = [&]() {
+    if (!a.q) return;
+    const int per = a.group * uk;
+    for (int e = tid; e < run.n * per; e += kThreads) {
+      const int i = e / per, hu = e % per;
+      int row = 0;
+      if (rot > 0 && (row = table_row(i)) < 0) continue;
+      const int64_t t = run.row0 + i;
+      const int head = (h * a.group + hu / uk) * a.d_qk;
+      Unit r;
+      load_unit(a, a.q + t * a.q_stride + head, hu % uk, rot, row, r);
+      store16(a.q_rot + t * a.q_rot_stride + head, unit_at(hu % uk, rot, a.interleaved), r, a.f16);
+    }
+  };
+
+  if (kKind != kCacheE4m3) {
+    for (int e = tid; e < nkv; e += kThreads) {
+      Unit r;
+      if (load_kv(e, r)) store_kv(e, r, 1.f, 1.f);
+    }
+    turn_queries();
+    return;
+  }
+
+  // E4M3: the maxima first
+  Unit hold[kHold];
+  float mk = 0.f, mv = 0.f;
+  unsigned ok = 0;
+  bool any = false;  // some token is written
+#pragma unroll
+  for (int j = 0; j < kHold; ++j) {
+    const int e = tid + j * kThreads;
+    if (e < nkv && load_kv(e, hold[j])) {
+      ok |= 1u << j;
+      any = true;
+      const float m = unit_amax(hold[j]);
+      if (e < nk) mk = fmaxf(mk, m);
+      else mv = fmaxf(mv, m);
+    }
+  }
+  for (int e = tid + kHold * kThreads; e < nkv; e += kThreads) {
+    Unit r;
+    if (load_kv(e, r)) {
+      any = true;
+      const float m = unit_amax(r);
+      if (e < nk) mk = fmaxf(mk, m);
+      else mv = fmaxf(mv, m);
+    }
+  }
+  turn_queries();
+  __shared__ float s_mk[kThreads / 32], s_mv[kThreads / 32];
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, d));
+    mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, d));
+  }
+  if ((tid & 31) == 0) {
+    s_mk[tid / 32] = mk;
+    s_mv[tid / 32] = mv;
+  }
+  float* pk = a.k_scale + static_cast<int64_t>(run.page) * a.Hkv + h;
+  float* pv = a.v_scale + static_cast<int64_t>(run.page) * a.Hkv + h;
+  const float old_k = run.slot0 ? *pk : 0.f, old_v = run.slot0 ? *pv : 0.f;
+  if (!__syncthreads_or(any)) return;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    mk = fmaxf(mk, s_mk[w]);
+    mv = fmaxf(mv, s_mv[w]);
+  }
+  const float new_k = fmaxf(page_scale(mk), old_k), new_v = fmaxf(page_scale(mv), old_v);
+  // codes of earlier tokens again under a grown scale
+  auto again = [&](char* base, int64_t tok, int d, float ratio) {
+    const int per = d / 16;
+    for (int e = tid; e < run.slot0 * per; e += kThreads) {
+      uint4* at = reinterpret_cast<uint4*>(base + (e / per - run.slot0) * tok + (e % per) * 16);
+      uint4 v = *at;
+      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t r = 0;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const uint32_t f2 = e4m3x2_f16x2(static_cast<uint16_t>(w[i] >> (16 * b)));
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&f2));
+          r |= static_cast<uint32_t>(f32x2_e4m3x2(f.x * ratio, f.y * ratio)) << (16 * b);
+        }
+        w[i] = r;
+      }
+      *at = v;
+    }
+  };
+  if (new_k > old_k && run.slot0) again(kdst, a.k_tok, a.d_qk, old_k / new_k);
+  if (new_v > old_v && run.slot0) again(vdst, a.v_tok, a.d_v, old_v / new_v);
+  // scales are powers of two of at least 2^-64, but a caller's own may be
+  // anything: the quotient is exact for the former
+  const float inv_k = 1.f / new_k, inv_v = 1.f / new_v;
+#pragma unroll
+  for (int j = 0; j < kHold; ++j)
+    if (ok >> j & 1) store_kv(tid + j * kThreads, hold[j], inv_k, inv_v);
+  for (int e = tid + kHold * kThreads; e < nkv; e += kThreads) {
+    Unit r;
+    if (load_kv(e, r)) store_kv(e, r, inv_k, inv_v);
+  }
+  if (tid == 0) {
+    *pk = new_k;
+    *pv = new_v;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_append(const Args& a, int kind, cudaStream_t st) {
+  // runs of one sequence: one per page its new tokens touch
+  int64_t runs = a.num_seqs;
+  if (a.cu) {
+    runs = (static_cast<int64_t>(a.num_tokens) >> a.page_shift) + 2ll * a.num_seqs;
+    if (runs > a.num_tokens) runs = a.num_tokens;
+  }
+  const dim3 grid(static_cast<unsigned>(runs), a.Hkv);
+  if (kind == kCacheE4m3) append_kernel<kCacheE4m3><<<grid, kThreads, 0, st>>>(a);
+  else if (kind == kCacheF16) append_kernel<kCacheF16><<<grid, kThreads, 0, st>>>(a);
+  else append_kernel<kCacheBf16><<<grid, kThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace paged
+}  // namespace attn

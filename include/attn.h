@@ -366,6 +366,136 @@ attn_status_t attn_event_elapsed_ms(const void* start, const void* end, float* m
 #define ATTN_FWD_NOALLOC_SCRATCH_BYTES (4u << 20)
 attn_status_t attn_fwd_noalloc(const attn_params_t* p, void* o, float* lse, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Paged KV cache: appending new tokens and attending to them (serving).
+ *
+ * The pages have no counterpart; these are the calls a decoder makes around
+ * the attention above once its keys and values outlive a step.  A cache is a
+ * pool of pages of page_size token slots; a sequence owns the pages that its
+ * row of the page table lists, in order, so that its token at position j is in
+ * slot j % page_size of page page_table[s][j / page_size].
+ *
+ * One parameter block describes a step for num_seqs sequences.  Sequence s
+ * has seq_lens[s] tokens INCLUDING the n_s new ones of this step; the new
+ * tokens are the rows cu_seqlens_q[s] .. cu_seqlens_q[s+1] - 1 of q / k_new /
+ * v_new / q_rot / o (cu_seqlens_q NULL: one new token per sequence, row s),
+ * and row i of them stands at position seq_lens[s] - n_s + i.  A sequence may
+ * have no new tokens, or no tokens at all (seq_lens[s] = 0: its rows, if any,
+ * are padding; nothing is appended for them and their O is 0).  Rows at and after
+ * cu_seqlens_q[num_seqs] (a padded batch) are neither read nor written.
+ *
+ * attn_paged_append:
+ *   q_rot_i = rotate(q_i),  K_j = rotate(k_new_j),  V_j = v_new_j,
+ *   rotate pairs coordinates a, b of the first rot_dim (the others pass):
+ *     a' = a cos - b sin,  b' = b cos + a sin
+ *   with pair p = (p, p + rot_dim/2), or (2p, 2p+1) when rot_interleaved, and
+ *   cos / sin row p of the tables at the token's position (or rope_pos).
+ *   Computed in fp32 and rounded once, to the 16-bit type or to E4M3.
+ *   E4M3 caches keep one scale per page and head, a power of two:
+ *     K = k_scale * code.  A page written from its slot 0 takes the smallest
+ *   2^e >= 2^-64 with max |K| <= 448 * 2^e over the tokens written to it; a
+ *   page continued at a later slot takes the larger of that and the scale it
+ *   has, and if the scale grows, the codes already there are rounded again
+ *   under the new one (a step is exact unless it reaches E4M3's subnormals).
+ *   Infinities and NaN are stored as NaN and do not enter the scale.
+ *   Slots other than the new tokens', and their pages, are left as they are.
+ *   A page shared by several sequences may be read by all of them, but a call
+ *   that appends to it through more than one sequence gives undefined
+ *   contents (of that page only).
+ *
+ * attn_paged_fwd:
+ *   S_ij = scale * Q_i . K_j,  P = softmax_j(S) over the keys j of the row's
+ *   sequence that the mask keeps,  O_i = sum_j P_ij V_j,
+ *   LSE_i = ln sum_j exp(S_ij);  sink logits join the normaliser as in
+ *   attn_fwd.  Kept: j < seq_lens[s]; with ATTN_MASK_CAUSAL also
+ *   j <= position of i; with window_left >= 0 also j >= position - window_left.
+ *   A row with no kept key gets O = 0 and LSE = -inf (its sink).  What lies in
+ *   slots at or behind seq_lens[s], and in unlisted pages, has no influence,
+ *   NaN included, nor has the value of a key that no row of the sequence
+ *   keeps.  K and V enter the MMAs exactly (E4M3 codes as fp16 values, their
+ *   scales applied in fp32); bf16 queries of an E4M3 cache are multiplied by a
+ *   power of two for each row and enter as fp16, which is exact but for
+ *   elements below 2^-28 of their row's largest; P is rounded to fp16 (to
+ *   bf16 with a bf16 cache); sums and softmax statistics are fp32.  Results do
+ *   not depend on the order in which blocks run.
+ *
+ * Streams, workspaces and errors as above; no call allocates or synchronises,
+ * and all calls can be captured into graphs (lengths, tables and offsets are
+ * read on the device, so a captured call serves later steps).  Device memory
+ * of a call in flight is its own: two calls that may overlap on the GPU need
+ * two workspaces, also across captured graphs.  The workspace needs no
+ * initialisation and carries nothing from call to call.
+ *
+ * Checks on the device: a page id outside [0, num_pages), a position outside
+ * the table's row or below 0, a rotation position outside [0, rope_len) and
+ * offsets outside [0, num_tokens] or decreasing are never used.  The
+ * tokens concerned are not written (append) or count as masked (attention),
+ * and ATTN_ERR_DEVICE_BOUNDS is stored in *status (if given; the library never
+ * clears it). */
+#define ATTN_PAGED_PARAMS_VERSION 1
+typedef struct {
+  int32_t struct_version; /* = ATTN_PAGED_PARAMS_VERSION */
+  int32_t dtype;          /* of q, k_new, v_new, q_rot and o: BF16 or FP16 */
+  int32_t cache_dtype;    /* the same, or ATTN_DTYPE_FP8_E4M3 */
+  int32_t mask;           /* ATTN_MASK_NONE or ATTN_MASK_CAUSAL */
+  int32_t num_seqs;
+  int32_t num_tokens; /* rows of q / k_new / v_new / q_rot / o, padding included */
+  int32_t max_q_len;  /* largest n_s (a hint that chooses the kernel; any value
+                         >= 1 gives right results) */
+  int32_t Hq, Hkv;    /* Hq a multiple of Hkv and at most 256 */
+  int32_t d_qk, d_v;  /* as in attn_params_t */
+  int32_t page_size;  /* 16, 32, 64, 128 or 256 tokens */
+  int32_t num_pages;  /* pages of the pool */
+  int32_t max_pages;  /* columns of the page table; max_pages * page_size < 2^31 */
+  const int32_t* page_table; /* [num_seqs, max_pages], rows table_stride apart */
+  int64_t table_stride;
+  const int32_t* seq_lens;     /* [num_seqs] */
+  const int32_t* cu_seqlens_q; /* [num_seqs + 1] or NULL (num_tokens == num_seqs) */
+  /* Caches, indexed [page][head][slot][dim]: strides in elements of the first
+   * three (any order of memory), dims contiguous.  Each stride is a positive
+   * multiple of 16 bytes. */
+  void* k_cache;
+  void* v_cache;
+  int64_t k_cache_stride[3];
+  int64_t v_cache_stride[3];
+  float* k_scale; /* fp32 [num_pages, Hkv]; E4M3 caches only (NULL otherwise). */
+  float* v_scale; /* Read by attn_paged_fwd: any positive finite values. */
+  int32_t* status; /* optional device word, see above */
+  /* New tokens, rows *_stride elements apart (multiples of 16 bytes), heads
+   * contiguous inside a row: q [num_tokens, Hq, d_qk], k_new [num_tokens, Hkv,
+   * d_qk], v_new [num_tokens, Hkv, d_v].  q_rot: rotated queries, written by
+   * attn_paged_append where q is given (q_rot == q rotates in place; both NULL:
+   * keys and values only) and read by attn_paged_fwd, which reads q when q_rot
+   * is NULL. */
+  const void* q;
+  const void* k_new;
+  const void* v_new;
+  void* q_rot;
+  int64_t q_stride, k_new_stride, v_new_stride, q_rot_stride;
+  int32_t rot_dim; /* a multiple of 16, at most d_qk; 0: no rotation */
+  int32_t rot_interleaved;
+  int32_t rope_len;        /* rows of the tables */
+  const float* rope_cos;   /* fp32 [rope_len, rot_dim / 2], 16-byte aligned */
+  const float* rope_sin;
+  const int32_t* rope_pos; /* int32 [num_tokens], or NULL: the token's position */
+  /* Attention. */
+  float scale;
+  int32_t window_left; /* negative: no window */
+  const float* sink;   /* fp32 [Hq] or NULL */
+} attn_paged_params_t;
+
+/* Workspace bytes attn_paged_fwd needs (0 on invalid parameters; a valid call
+ * needs at least 256).  256-byte aligned. */
+size_t attn_paged_workspace_size(const attn_paged_params_t* p);
+
+/* Rotates the new tokens and writes them into the cache. */
+attn_status_t attn_paged_append(const attn_paged_params_t* p, void* stream);
+
+/* o: [num_tokens, Hq, d_v] of `dtype`; lse: fp32 [Hq, num_tokens] or NULL.
+ * k_new, v_new and the rotation's fields are not read. */
+attn_status_t attn_paged_fwd(const attn_paged_params_t* p, void* o, float* lse, void* ws,
+                             size_t ws_bytes, void* stream);
+
 int32_t attn_abi_version(void);
 
 /* Properties of this build of the library, as bit flags:
