@@ -48,7 +48,7 @@ struct Args {
   float* lse;
   float* part;       // [2 * ctas][rows][d_v] unnormalised O
   float2* part_ml;   // [2 * ctas][rows] (max in log2 units, sum)
-  int4* split_desc;  // [ctas]
+  int4* split_desc;  // [ctas] of an item's first piece: pieces (0: none), sequence, head, rows
   int part_rows;
 };
 
@@ -143,7 +143,14 @@ __device__ __forceinline__ float page_scale(float amax) {
 }
 
 cudaError_t launch_append(const Args& a, int kind, cudaStream_t st);
-cudaError_t launch_attend(const Args& a, int kind, cudaStream_t st);
+
+// Few rows per KV head: `rows` is the expected number of query rows of one
+// KV head (tokens x group); sms the device's SM count.
+constexpr int kMaxCtas = 304;
+inline int decode_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+cudaError_t launch_decode_e4m3(const Args& a, int rows, int sms, cudaStream_t st);
+cudaError_t launch_decode_f16(const Args& a, int rows, int sms, cudaStream_t st);
+cudaError_t launch_decode_bf16(const Args& a, int rows, int sms, cudaStream_t st);
 
 }  // namespace paged
 }  // namespace attn

@@ -127,6 +127,29 @@ void fill(Args& a, const attn_paged_params_t* p) {
   a.d_v = p->d_v;
 }
 
+// Workspace: descriptors of split items, then their partial states.
+struct Plan {
+  size_t desc, ml, part, total;
+};
+Plan make_plan(const attn_paged_params_t* p) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t rows = decode_rows(static_cast<int64_t>(p->max_q_len) * (p->Hq / p->Hkv));
+  Plan pl;
+  pl.desc = 0;
+  pl.ml = up(kMaxCtas * sizeof(int4));
+  pl.part = pl.ml + up(2 * kMaxCtas * rows * sizeof(float2));
+  pl.total = pl.part + 2 * kMaxCtas * rows * p->d_v * sizeof(float);
+  return pl;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return n;
+}
+
 }  // namespace
 }  // namespace paged
 }  // namespace attn
@@ -137,7 +160,7 @@ extern "C" {
 
 size_t attn_paged_workspace_size(const attn_paged_params_t* p) {
   if (validate_fwd(p) != ATTN_OK) return 0;
-  return 256;
+  return make_plan(p).total;
 }
 
 attn_status_t attn_paged_append(const attn_paged_params_t* p, void* stream) {
@@ -172,7 +195,8 @@ attn_status_t attn_paged_fwd(const attn_paged_params_t* p, void* o, float* lse, 
   if (p->num_seqs == 0 || p->num_tokens == 0) return ATTN_OK;
   if (!o || !aligned(o, 16) || !aligned(lse, 4) || !ws || !aligned(ws, 256))
     return ATTN_ERR_INVALID_ARG;
-  if (ws_bytes < attn_paged_workspace_size(p)) return ATTN_ERR_WORKSPACE_TOO_SMALL;
+  const Plan pl = make_plan(p);
+  if (ws_bytes < pl.total) return ATTN_ERR_WORKSPACE_TOO_SMALL;
   Args a;
   fill(a, p);
   a.q = static_cast<const uint16_t*>(p->q_rot ? p->q_rot : p->q);
@@ -180,9 +204,19 @@ attn_status_t attn_paged_fwd(const attn_paged_params_t* p, void* o, float* lse, 
   a.sink = p->sink;
   a.o = static_cast<uint16_t*>(o);
   a.lse = lse;
-  return launch_attend(a, kind_of(p), static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? ATTN_OK
-             : ATTN_ERR_CUDA;
+  char* w = static_cast<char*>(ws);
+  a.split_desc = reinterpret_cast<int4*>(w + pl.desc);
+  a.part_ml = reinterpret_cast<float2*>(w + pl.ml);
+  a.part = reinterpret_cast<float*>(w + pl.part);
+  const int sms = sm_count();
+  if (sms <= 0) return ATTN_ERR_CUDA;
+  const int rows = decode_rows(static_cast<int64_t>(p->max_q_len) * a.group);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int kind = kind_of(p);
+  const cudaError_t e = kind == kCacheE4m3  ? launch_decode_e4m3(a, rows, sms, st)
+                        : kind == kCacheF16 ? launch_decode_f16(a, rows, sms, st)
+                                            : launch_decode_bf16(a, rows, sms, st);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // extern "C"

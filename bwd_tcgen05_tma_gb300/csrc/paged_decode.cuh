@@ -1,0 +1,838 @@
+// Attention over the paged cache for few query rows per KV head: single
+// tokens, drafted tokens, short chunks.
+//
+// Mathematics.  The query rows of one KV head (tokens x heads of the group)
+// are the columns of transposed products, so a group of 4 or 8 heads fills
+// the N = 8 side of an MMA instead of a sixteenth of its M = 128 side:
+//   S^T [16 keys x 8 rows] = K [16 x d] Q^T,   O^T [d_v x 8] += V^T [d_v x 16] P^T
+// with the softmax's running maximum and sum per column (fp32, base 2).
+//
+// What bounds it: every K and V byte is read once from HBM and used for 8
+// rows, 16 or 32 FLOP a byte, so the HBM rate; mma.sync runs far below its
+// peak here and no tensor-memory round trip pays.
+//
+// Layout.  One warp takes 16 keys a step, alone: no barrier between warps
+// until their states are joined.  The order of dims inside S's sum and of rows
+// inside V^T is free, so each lane copies 16 contiguous bytes of a key (four
+// lanes cover 64 bytes of a K row, eight lanes a whole V row) and finds its MMA
+// fragments in what it copied itself.  The copies go through a ring in shared
+// memory (cp.async, 16 bytes, straight past the registers), which keeps
+// 64-128 KB in flight on each SM; rows outside the mask are filled with zeros.
+//   K: lane (g = lane / 4, t = lane % 4) holds keys g and g + 8, dims by t
+//   V: lane (g, t) holds keys 2t, 2t+1, 2t+8, 2t+9, dims by g; pairs of keys
+//      are interleaved by byte permutes (a transpose without shared memory)
+//   P^T: the C fragment of S^T, rounded and transposed 8x8 (movmatrix), is
+//      the B fragment of the second product.
+// E4M3 codes become fp16 exactly; the K scale multiplies the scores, the V
+// scale is added to them as its logarithm (P V s_v = 2^(s + log2 s_v) V) and
+// taken out of the normaliser again, so both cost one multiply-add.
+//
+// Work split.  A tile is 128 keys of one (sequence, KV head, block of rows).
+// All tiles of the batch, in order, are cut into equal shares, one per block
+// of a grid that fills the SMs: long and short sequences balance without a
+// host-side plan, and a single sequence spreads over the whole chip.  A share
+// that covers a whole item writes O; others write partial states (at most two
+// a block), which a second kernel joins in a fixed order.
+#pragma once
+#include <climits>
+
+#include "paged.cuh"
+
+namespace attn {
+namespace paged {
+namespace {
+
+using sm103::ex2_approx;
+using sm103::smem_u32;
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTileKeys = 16 * kWarps;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int KIND, int DQK, int DV, int NT>
+struct Cfg {
+  static constexpr int kCb = KIND == kCacheE4m3 ? 1 : 2;
+  static constexpr int kKch = DQK * kCb / 64;  // 16-byte copies per lane and key
+  static constexpr int kVb = DV * kCb / 8;     // bytes of V per lane and key
+  static constexpr int kStageK = 2 * kKch * 512;
+  static constexpr int kStageV = 4 * kVb * 32;
+  static constexpr int kStage = kStageK + kStageV;
+  static constexpr int kKs = DQK / 16;  // K slices of S^T
+  static constexpr int kMt = DV / 16;   // row tiles of O^T
+  static constexpr int kRows = 8 * NT;
+  // blocks per SM: two where a lane's state leaves them 128 registers each
+  static constexpr int kBlocks = NT == 1 && kStage <= 4096 ? 2 : 1;
+  static constexpr int kBudget = kBlocks == 2 ? 104 * 1024 : 200 * 1024;
+  static constexpr int kFit = kBudget / (kWarps * kStage);
+  static constexpr int kStages = kFit > 4 ? 4 : kFit;
+  static_assert(kStages >= 2, "ring");
+  static constexpr bool kQSmem = NT > 2;
+  static constexpr int kQBytes = kQSmem ? NT * kKs * 256 : 0;
+  static constexpr int kRing = kWarps * kStages * kStage;
+  static constexpr int kMerge = kWarps * 8 * DV * 4;
+  static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + kQBytes;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 8 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t p) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},"
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3},{%4,%5,%6,%7},{%8,%9},"
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Does a word hold an element that is not finite?  (E4M3 has only NaN.)
+template <int KIND>
+__device__ __forceinline__ uint32_t nonfinite(uint32_t w) {
+  if (KIND == kCacheE4m3) return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  if (KIND == kCacheF16) return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+  return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+
+// Share of the batch: sequence `s`, tile `off` of its items, `left` tiles.
+struct Share {
+  int s;
+  int64_t off, begin, end, total;
+  int ctas;
+};
+
+// What a sequence asks for: row blocks, tiles per item, first key.
+struct Need {
+  Seq q;
+  int nrb, tiles, k0, hi;
+};
+__device__ __forceinline__ Need need_of(const Args& a, int s, int rows_per) {
+  Need d;
+  d.q = load_seq(a, s);
+  const int cap = a.max_pages << a.page_shift;
+  if (d.q.len > cap) flag_bounds(a);
+  d.hi = min(d.q.len, cap);
+  int lo = 0;
+  if (a.window >= 0) lo = max(0, d.q.len - d.q.n - a.window);
+  d.k0 = lo & ~15;
+  d.nrb = (d.q.n * a.group + rows_per - 1) / rows_per;
+  d.tiles = max(1, (d.hi - d.k0 + kTileKeys - 1) / kTileKeys);
+  return d;
+}
+
+// This block's share; every thread returns the same values.
+template <int ROWS>
+__device__ __forceinline__ Share find_share(const Args& a) {
+  __shared__ int64_t s_part[kWarps];
+  __shared__ int64_t s_off;
+  __shared__ int s_seq;
+  const int per = (a.num_seqs + kThreads - 1) / kThreads;
+  const int first = threadIdx.x * per, last = min(a.num_seqs, first + per);
+  int64_t mine = 0;
+  for (int s = first; s < last; ++s) {
+    const Need d = need_of(a, s, ROWS);
+    mine += static_cast<int64_t>(d.nrb) * a.Hkv * d.tiles;
+  }
+  int64_t x = mine;
+#pragma unroll
+  for (int i = 1; i < 32; i <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, i);
+    if ((threadIdx.x & 31) >= i) x += y;
+  }
+  if ((threadIdx.x & 31) == 31) s_part[threadIdx.x / 32] = x;
+  __syncthreads();
+  int64_t total = 0, before = x - mine;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int64_t t = s_part[w];
+    if (w < static_cast<int>(threadIdx.x) / 32) before += t;
+    total += t;
+  }
+  Share sh;
+  sh.total = total;
+  sh.ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+  sh.begin = sh.end = 0;
+  if (static_cast<int>(blockIdx.x) < sh.ctas) {
+    sh.begin = blockIdx.x * total / sh.ctas;
+    sh.end = (blockIdx.x + 1) * total / sh.ctas;
+    if (sh.begin >= before && sh.begin < before + mine) {
+      int s = first;
+      int64_t off = sh.begin - before;
+      for (;; ++s) {
+        const Need d = need_of(a, s, ROWS);
+        const int64_t c = static_cast<int64_t>(d.nrb) * a.Hkv * d.tiles;
+        if (off < c) break;
+        off -= c;
+      }
+      s_seq = s;
+      s_off = off;
+    }
+  }
+  __syncthreads();
+  sh.s = s_seq;
+  sh.off = s_off;
+  return sh;
+}
+
+template <int KIND, int DQK, int DV, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
+    decode_kernel(const __grid_constant__ Args a) {
+  using C = Cfg<KIND, DQK, DV, NT>;
+  constexpr bool kBf = KIND == kCacheBf16;
+  // fp16 P is kept at up to 2^14 so that weights down to 2^-28 of the row's
+  // largest are normal numbers
+  constexpr float kShift = kBf ? 0.f : 14.f;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
+  __shared__ float s_sc[kWarps][C::kStages][2];
+  __shared__ int s_ok[kWarps][C::kStages];
+  const int tid = threadIdx.x, w = tid / 32, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const Share sh = find_share<C::kRows>(a);
+  if (tid == 0 && a.split_desc) a.split_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  sm103::grid_dep_launch();  // the joining kernel may be put in place
+  if (sh.begin >= sh.end) return;
+
+  const uint32_t ring = smem_u32(smem) + w * (C::kStages * C::kStage);
+  const uint32_t qs = smem_u32(smem) + (C::kSmem - C::kQBytes);
+  float* const s_o = reinterpret_cast<float*>(smem);
+  const int page_mask = (1 << a.page_shift) - 1;
+
+  int seq = sh.s;
+  int64_t off = sh.off, at = sh.begin;
+  Need nd = need_of(a, seq, C::kRows);
+  while (at < sh.end) {
+    while (off >= static_cast<int64_t>(nd.nrb) * a.Hkv * nd.tiles) {
+      off -= static_cast<int64_t>(nd.nrb) * a.Hkv * nd.tiles;
+      nd = need_of(a, ++seq, C::kRows);
+    }
+    const int item = static_cast<int>(off / nd.tiles), t0 = static_cast<int>(off % nd.tiles);
+    const int t1 = static_cast<int>(min(static_cast<int64_t>(nd.tiles), t0 + (sh.end - at)));
+    const int hk = item / nd.nrb, rb = item % nd.nrb;
+    const int rows = nd.q.n * a.group, r0 = rb * C::kRows;
+    const int pos0 = nd.q.len - nd.q.n;  // position of the sequence's first new row
+    const int tok_lo = r0 / a.group, tok_hi = min(rows - 1, r0 + C::kRows - 1) / a.group;
+    // keys some row of the block keeps, and keys all of them keep
+    const int klo = a.window >= 0 ? max(0, pos0 + tok_lo - a.window) : 0;
+    const int khi = a.causal ? min(nd.hi, pos0 + tok_hi + 1) : nd.hi;
+    const int all_lo = a.window >= 0 ? max(0, pos0 + tok_hi - a.window) : 0;
+    const int all_hi = a.causal ? min(nd.hi, pos0 + tok_lo + 1) : nd.hi;
+    // this piece's 16-key steps
+    const int b_lo = max(nd.k0 + t0 * kTileKeys, klo) >> 4;
+    const int b_hi = (min(nd.k0 + t1 * kTileKeys, khi) + 15) >> 4;
+    const int ns = b_hi - b_lo > w ? (b_hi - b_lo - w + kWarps - 1) / kWarps : 0;
+
+    // ---- page ids: lane i holds step (window * 32 + i)
+    auto load_ids = [&](int window) -> int {
+      const int i = window * 32 + lane;
+      if (i >= ns) return -1;
+      const int col = (b_lo + w + kWarps * i) >> (a.page_shift - 4);
+      int id = col < a.max_pages ? a.table[seq * a.table_stride + col] : -1;
+      if (id < 0 || id >= a.num_pages) {
+        flag_bounds(a);
+        id = -1;
+      }
+      return id;
+    };
+    int ids = load_ids(0), ids_next = ns > 32 ? load_ids(1) : -1;
+    auto issue = [&](int i) {
+      if (i < ns) {
+        if (i > 0 && (i & 31) == 0) {
+          ids = ids_next;
+          ids_next = load_ids((i >> 5) + 1);
+        }
+        const int page = __shfl_sync(0xffffffffu, ids, i & 31);
+        const int key = (b_lo + w + kWarps * i) << 4, slot = key & page_mask;
+        const uint32_t st = ring + (i % C::kStages) * C::kStage;
+        const bool okp = page >= 0;
+        const char* kp = a.kc + (okp ? page * a.k_page + hk * a.k_head + (slot + g) * a.k_tok : 0);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int k = key + g + 8 * r;
+          const bool ok = okp && k >= klo && k < khi;
+          const char* src = ok ? kp + 8 * r * a.k_tok + 16 * t : a.kc;
+#pragma unroll
+          for (int c = 0; c < C::kKch; ++c)
+            cp_async16(st + (r * C::kKch + c) * 512 + lane * 16, src + (ok ? c * 64 : 0), ok);
+        }
+        const char* vp =
+            a.vc + (okp ? page * a.v_page + hk * a.v_head + (slot + 2 * t) * a.v_tok : 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int kk = (j & 1) + 8 * (j >> 1), k = key + 2 * t + kk;
+          const bool ok = okp && k >= klo && k < khi;
+          const uint32_t dst = st + C::kStageK + j * C::kVb * 32;
+          if constexpr (C::kVb == 8) {
+            cp_async8(dst + lane * 8, ok ? vp + kk * a.v_tok + 8 * g : a.vc, ok);
+          } else {
+#pragma unroll
+            for (int c = 0; c < C::kVb / 16; ++c)
+              cp_async16(dst + c * 512 + lane * 16,
+                         ok ? vp + kk * a.v_tok + c * 128 + 16 * g : a.vc, ok);
+          }
+        }
+        if (KIND == kCacheE4m3 && lane < 2 && okp)
+          cp_async4(smem_u32(&s_sc[w][i % C::kStages][lane]),
+                    (lane ? a.v_scale : a.k_scale) + static_cast<int64_t>(page) * a.Hkv + hk);
+        if (lane == 0) s_ok[w][i % C::kStages] = okp;
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) issue(i);
+
+    // ---- queries: column g of each tile as B fragments; factors of columns
+    // 2t and 2t + 1 (base-2 softmax scale, and the row's power of two)
+    uint32_t qf[C::kQSmem ? 1 : NT][C::kKs][2];
+    float fac[NT][2];
+    int cpos[NT][2];  // positions of columns 2t and 2t + 1 (INT_MIN: no row)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = r0 + nt * 8 + g;
+      const bool real = r < rows;
+      const uint16_t* qp = a.q;
+      if (real) {
+        const int tok = r / a.group;
+        qp += (nd.q.row0 + tok) * a.q_stride + (hk * a.group + r % a.group) * DQK;
+      }
+      uint32_t raw[C::kKs][2];
+      // dims of slice ks: E4M3 64 (ks / 4) + 16 t + 4 (ks % 4) + 0..3,
+      // 16-bit 32 (ks / 2) + 8 t + 4 (ks % 2) + 0..3
+#pragma unroll
+      for (int ks = 0; ks < C::kKs; ++ks) {
+        const int d = KIND == kCacheE4m3 ? 64 * (ks / 4) + 16 * t + 4 * (ks % 4)
+                                         : 32 * (ks / 2) + 8 * t + 4 * (ks % 2);
+        uint2 v = make_uint2(0, 0);
+        if (real) v = *reinterpret_cast<const uint2*>(qp + d);
+        raw[ks][0] = v.x;
+        raw[ks][1] = v.y;
+      }
+      float back = 1.f;
+      if (KIND == kCacheE4m3 && !a.f16) {
+        // bf16 row to fp16: its largest element to [2^14, 2^15)
+        uint32_t mx = 0;
+#pragma unroll
+        for (int ks = 0; ks < C::kKs; ++ks)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            mx = max(mx, max(raw[ks][i] & 0x7fffu, (raw[ks][i] >> 16) & 0x7fffu));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        int e = static_cast<int>(mx >> 7);  // biased exponent
+        e = e == 255 ? 127 + 14 : max(e, 27);
+        const float to = __uint_as_float(static_cast<uint32_t>(254 + 14 - e) << 23);
+        back = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+#pragma unroll
+        for (int ks = 0; ks < C::kKs; ++ks)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            raw[ks][i] = sm103::pack_f16x2(__uint_as_float(raw[ks][i] << 16) * to,
+                                           __uint_as_float(raw[ks][i] & 0xffff0000u) * to);
+      }
+      if constexpr (C::kQSmem) {
+        // every warp would write the same: one writes
+        if (w == 0) {
+#pragma unroll
+          for (int ks = 0; ks < C::kKs; ++ks)
+            asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(qs + (nt * C::kKs + ks) * 256 +
+                                                                lane * 8),
+                         "r"(raw[ks][0]), "r"(raw[ks][1])
+                         : "memory");
+        }
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < C::kKs; ++ks) {
+          qf[nt][ks][0] = raw[ks][0];
+          qf[nt][ks][1] = raw[ks][1];
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        fac[nt][c] = a.scale * kLog2e * __shfl_sync(0xffffffffu, back, (2 * t + c) * 4);
+        const int rr = r0 + nt * 8 + 2 * t + c;
+        cpos[nt][c] = rr < rows ? pos0 + rr / a.group : INT_MIN;
+      }
+    }
+    if constexpr (C::kQSmem) __syncthreads();
+
+    float o[NT][C::kMt][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int mt = 0; mt < C::kMt; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[nt][mt][i] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+    auto kept = [&](int nt, int c, int key) -> bool {
+      const int p = cpos[nt][c];
+      return p != INT_MIN && key < nd.hi && (!a.causal || key <= p) &&
+             (a.window < 0 || key >= p - a.window);
+    };
+
+    for (int i = 0; i < ns; ++i) {
+      cp_wait<C::kStages - 2>();
+      __syncwarp();
+      issue(i + C::kStages - 1);
+      const uint32_t st = ring + (i % C::kStages) * C::kStage;
+      const int key = (b_lo + w + kWarps * i) << 4;
+      const bool okp = s_ok[w][i % C::kStages] != 0;
+
+      // S^T
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[nt][j] = 0.f;
+#pragma unroll
+      for (int c = 0; c < C::kKch; ++c) {
+        const uint4 x0 = lds128(st + c * 512 + lane * 16);
+        const uint4 x1 = lds128(st + (C::kKch + c) * 512 + lane * 16);
+        const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+        constexpr int kPer = KIND == kCacheE4m3 ? 4 : 2;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const int ks = c * kPer + j;
+          uint32_t a0, a1, a2, a3;
+          if constexpr (KIND == kCacheE4m3) {
+            a0 = e4m3x2_f16x2(static_cast<uint16_t>(w0[j]));
+            a2 = e4m3x2_f16x2(static_cast<uint16_t>(w0[j] >> 16));
+            a1 = e4m3x2_f16x2(static_cast<uint16_t>(w1[j]));
+            a3 = e4m3x2_f16x2(static_cast<uint16_t>(w1[j] >> 16));
+          } else {
+            a0 = w0[2 * j];
+            a2 = w0[2 * j + 1];
+            a1 = w1[2 * j];
+            a3 = w1[2 * j + 1];
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (C::kQSmem) {
+              const uint2 b = lds64(qs + (nt * C::kKs + ks) * 256 + lane * 8);
+              mma16816<kBf>(s[nt], a0, a1, a2, a3, b.x, b.y);
+            } else {
+              mma16816<kBf>(s[nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+            }
+          }
+        }
+      }
+
+      // softmax in base 2; with E4M3 pages the exponent carries log2 of the V
+      // scale and the sum takes it out
+      float ksc = 1.f, lgv = 0.f, inv_v = 1.f;
+      if (KIND == kCacheE4m3) {
+        ksc = s_sc[w][i % C::kStages][0];
+        const float vsc = fmaxf(s_sc[w][i % C::kStages][1], 0x1p-100f);
+        inv_v = 1.f / vsc;
+        lgv = (__float_as_uint(vsc) & 0x7fffffu) == 0
+                  ? static_cast<float>(static_cast<int>(__float_as_uint(vsc) >> 23) - 127)
+                  : __log2f(vsc);
+      }
+      const bool whole = okp && key >= all_lo && key + 16 <= all_hi;
+      uint32_t pb[NT][2];
+      bool moved = false;
+      float al[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[j] = fmaf(s[nt][j], fac[nt][j & 1] * ksc, lgv);
+        if (!whole) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (!okp || !kept(nt, j & 1, key + g + 8 * (j >> 1))) p[j] = -INFINITY;
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float mx = fmaxf(p[c], p[2 + c]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          mx = fmaxf(mx, m[nt][c]);
+          const float mu = mx == -INFINITY ? 0.f : mx;
+          al[nt][c] = ex2_approx(m[nt][c] - mu);
+          moved |= mx != m[nt][c];
+          m[nt][c] = mx;
+          p[c] = ex2_approx(p[c] - mu + kShift);
+          p[2 + c] = ex2_approx(p[2 + c] - mu + kShift);
+          l[nt][c] = fmaf(l[nt][c], al[nt][c], (p[c] + p[2 + c]) * inv_v);
+        }
+        if constexpr (kBf) {
+          pb[nt][0] = movmatrix(sm103::pack_bf16x2(p[0], p[1]));
+          pb[nt][1] = movmatrix(sm103::pack_bf16x2(p[2], p[3]));
+        } else {
+          pb[nt][0] = movmatrix(sm103::pack_f16x2(p[0], p[1]));
+          pb[nt][1] = movmatrix(sm103::pack_f16x2(p[2], p[3]));
+        }
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int mt = 0; mt < C::kMt; ++mt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[nt][mt][j] *= al[nt][j & 1];
+      }
+
+      // V: four keys, a dim pair per row tile
+      constexpr int kW = C::kVb / 4;  // words per key
+      uint32_t v[4][kW];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t src = st + C::kStageK + j * C::kVb * 32;
+        if constexpr (C::kVb == 8) {
+          const uint2 x = lds64(src + lane * 8);
+          v[j][0] = x.x;
+          v[j][1] = x.y;
+        } else {
+#pragma unroll
+          for (int c = 0; c < C::kVb / 16; ++c) {
+            const uint4 x = lds128(src + c * 512 + lane * 16);
+            v[j][4 * c] = x.x;
+            v[j][4 * c + 1] = x.y;
+            v[j][4 * c + 2] = x.z;
+            v[j][4 * c + 3] = x.w;
+          }
+        }
+      }
+      // A step that some rows keep in part: values that are not finite may
+      // not meet the zero weights of rows that mask them.  They are taken out
+      // of the product and added to the rows that keep them.
+      if (!whole && tok_lo != tok_hi) {
+        uint32_t bad = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int x = 0; x < kW; ++x) bad |= nonfinite<KIND>(v[j][x]);
+        if (__any_sync(0xffffffffu, bad != 0)) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int x = 0; x < kW; ++x) {
+              const uint32_t f = nonfinite<KIND>(v[j][x]);
+              // spread each element's flag (its top bit) over the element
+              const uint32_t mask = KIND == kCacheE4m3 ? (f >> 7) * 255u : (f >> 15) * 65535u;
+              v[j][x] &= ~mask;
+            }
+          for (int r = 0; r < 16; ++r) {
+            const int from = (g << 2) | ((r & 7) >> 1), j = (r & 1) + 2 * (r >> 3);
+#pragma unroll
+            for (int e = 0; e < 2 * C::kMt; ++e) {  // this lane's dims
+              const int byte = e * C::kCb;
+              const uint32_t src = st + C::kStageK + j * C::kVb * 32 +
+                                   (C::kVb == 8 ? from * 8 + byte
+                                                : (byte / 16) * 512 + from * 16 + byte % 16);
+              float x;
+              if constexpr (KIND == kCacheE4m3) {
+                uint32_t b;
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(src) : "memory");
+                x = e4m3_value(static_cast<uint8_t>(b));
+              } else {
+                uint16_t b;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(src) : "memory");
+                x = elem(b, KIND == kCacheF16);
+              }
+              if (!(fabsf(x) < INFINITY)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int c = 0; c < 2; ++c)
+                    if (kept(nt, c, key + r)) o[nt][e / 2][2 * (e & 1) + c] += x;
+              }
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < C::kMt; ++mt) {
+        uint32_t a0, a1, a2, a3;
+        if constexpr (KIND == kCacheE4m3) {
+          const uint32_t sel = (mt & 1) ? 0x7362 : 0x5140;
+          const uint32_t x = __byte_perm(v[0][mt / 2], v[1][mt / 2], sel);
+          const uint32_t y = __byte_perm(v[2][mt / 2], v[3][mt / 2], sel);
+          a0 = e4m3x2_f16x2(static_cast<uint16_t>(x));
+          a1 = e4m3x2_f16x2(static_cast<uint16_t>(x >> 16));
+          a2 = e4m3x2_f16x2(static_cast<uint16_t>(y));
+          a3 = e4m3x2_f16x2(static_cast<uint16_t>(y >> 16));
+        } else {
+          a0 = __byte_perm(v[0][mt], v[1][mt], 0x5410);
+          a1 = __byte_perm(v[0][mt], v[1][mt], 0x7632);
+          a2 = __byte_perm(v[2][mt], v[3][mt], 0x5410);
+          a3 = __byte_perm(v[2][mt], v[3][mt], 0x7632);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma16816<kBf>(o[nt][mt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+      }
+    }
+
+    // ---- join the warps' states.  A column's 16-byte groups are permuted in
+    // shared memory so that the eight lanes of a store (two g, four t) meet
+    // eight different bank groups.
+    auto swz = [](int col) -> int {
+      const int x = (col >> 1) & 3;
+      return DV == 128 && KIND == kCacheE4m3 ? x : (x & 1) | ((x >> 1) << 2);
+    };
+    cp_wait<0>();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float x = l[nt][c];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        if (g == 0) {
+          s_m[w][nt * 8 + 2 * t + c] = m[nt][c];
+          s_l[w][nt * 8 + 2 * t + c] = x;
+        }
+      }
+    const bool complete = t0 == 0 && t1 == nd.tiles;
+    const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      __syncthreads();  // the ring, or the previous tile's sums, are read
+#pragma unroll
+      for (int i = 0; i < DV / 32; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int q4 = DV == 64               ? 2 * g + i
+                         : KIND == kCacheE4m3 ? 4 * g + i
+                                              : (i / 2) * 16 + 2 * g + (i & 1);
+          const int col = 2 * t + c;
+          *reinterpret_cast<float4*>(s_o + (w * 8 + col) * DV + (q4 ^ swz(col)) * 4) =
+              make_float4(o[nt][2 * i][c], o[nt][2 * i][2 + c], o[nt][2 * i + 1][c],
+                          o[nt][2 * i + 1][2 + c]);
+        }
+      __syncthreads();
+      constexpr int kV = DV / 32;  // dims per lane; one warp per column
+      const int r = r0 + nt * 8 + w;
+      if (r < rows) {
+        float mt_ = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) mt_ = fmaxf(mt_, s_m[x][nt * 8 + w]);
+        const int tok = r / a.group, head = hk * a.group + r % a.group;
+        float snk = -INFINITY;
+        const bool none = mt_ == -INFINITY;
+        if (complete && a.sink) {
+          snk = a.sink[head] * kLog2e;
+          mt_ = fmaxf(mt_, snk);
+        }
+        const float mu = mt_ == -INFINITY ? 0.f : mt_;
+        float lt = complete && a.sink ? ex2_approx(snk - mu + kShift) : 0.f;
+        float acc[kV];
+#pragma unroll
+        for (int i = 0; i < kV; ++i) acc[i] = 0.f;
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) {
+          const float mx = s_m[x][nt * 8 + w];
+          if (mx == -INFINITY) continue;  // nothing kept by this warp
+          const float f = ex2_approx(mx - mu);
+          lt = fmaf(s_l[x][nt * 8 + w], f, lt);
+          const float* so = s_o + (x * 8 + w) * DV +
+                            (kV == 4 ? (lane ^ swz(w)) * 4
+                                     : ((lane >> 1) ^ swz(w)) * 4 + 2 * (lane & 1));
+#pragma unroll
+          for (int i = 0; i < kV; ++i) acc[i] = fmaf(so[i], f, acc[i]);
+        }
+        if (complete) {
+          const float inv = lt == 0.f ? 0.f : 1.f / lt;
+          uint16_t* op = a.o + (static_cast<int64_t>(nd.q.row0 + tok) * a.Hq + head) * DV + lane * kV;
+          if constexpr (kV == 4)
+            *reinterpret_cast<uint2*>(op) = make_uint2(pack2(acc[0] * inv, acc[1] * inv, a.f16),
+                                                       pack2(acc[2] * inv, acc[3] * inv, a.f16));
+          else
+            *reinterpret_cast<uint32_t*>(op) = pack2(acc[0] * inv, acc[1] * inv, a.f16);
+          if (a.lse && lane == 0)
+            a.lse[static_cast<int64_t>(head) * a.num_tokens + nd.q.row0 + tok] =
+                none ? (a.sink ? a.sink[head] : -INFINITY) : (mu - kShift) * kLn2 + logf(lt);
+        } else {
+          float* pp = a.part + (static_cast<int64_t>(slot) * a.part_rows + nt * 8 + w) * DV + lane * kV;
+#pragma unroll
+          for (int i = 0; i < kV; ++i) pp[i] = acc[i];
+          if (lane == 0)
+            a.part_ml[static_cast<int64_t>(slot) * a.part_rows + nt * 8 + w] =
+                make_float2(mt_, lt);
+        }
+      }
+    }
+    if (!complete && t0 == 0 && tid == 0) {
+      // first of an item's pieces: blocks up to the one that holds its last tile
+      const int64_t x = at + nd.tiles - 1;
+      const int c1 = static_cast<int>(((x + 1) * sh.ctas + sh.total - 1) / sh.total) - 1;
+      a.split_desc[blockIdx.x] = make_int4(c1 - blockIdx.x + 1, seq, hk, rb);
+    }
+    __syncthreads();  // the sums are read before the next piece fills the ring
+    at += t1 - t0;
+    off += t1 - t0;
+  }
+}
+
+// Joins the pieces of each split item: block (i, y) rows 2y and 2y + 1 of the
+// item whose first piece is block i's, four warps a row.
+template <int DV>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args a, float shift) {
+  __shared__ float s_acc[2][4][DV], s_m[2][4], s_l[2][4];
+  sm103::grid_dep_wait();
+  const int4 d = a.split_desc[blockIdx.x];
+  if (d.x == 0) return;
+  const int w = threadIdx.x / 32, lane = threadIdx.x & 31, rr = w / 4, part = w & 3;
+  const Seq q = load_seq(a, d.y);
+  const int col = 2 * blockIdx.y + rr, r = d.w * a.part_rows + col, rows = q.n * a.group;
+  constexpr int kV = DV / 32;
+  float acc[kV], m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kV; ++i) acc[i] = 0.f;
+  if (r < rows) {
+#pragma unroll 4
+    for (int i = part; i < d.x; i += 4) {
+      const int64_t slot = 2 * (static_cast<int64_t>(blockIdx.x) + i) + (i == 0 ? 1 : 0);
+      const float2 ml = a.part_ml[slot * a.part_rows + col];
+      const float* pp = a.part + (slot * a.part_rows + col) * DV + lane * kV;
+      float x[kV];
+#pragma unroll
+      for (int j = 0; j < kV; ++j) x[j] = pp[j];
+      const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
+      const float f0 = ex2_approx(m - mu), f1 = ex2_approx(ml.x - mu);
+      // a state without keys holds zeros
+#pragma unroll
+      for (int j = 0; j < kV; ++j) acc[j] = acc[j] * f0 + x[j] * f1;
+      l = l * f0 + ml.y * f1;
+      m = mn;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kV; ++j) s_acc[rr][part][lane * kV + j] = acc[j];
+  if (lane == 0) {
+    s_m[rr][part] = m;
+    s_l[rr][part] = l;
+  }
+  __syncthreads();
+  if (part != 0 || r >= rows) return;
+  const int tok = r / a.group, head = d.z * a.group + r % a.group;
+  float mt = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mt = fmaxf(mt, s_m[rr][i]);
+  const bool none = mt == -INFINITY;
+  if (a.sink) mt = fmaxf(mt, a.sink[head] * kLog2e);
+  const float mu = mt == -INFINITY ? 0.f : mt;
+  float lt = a.sink ? ex2_approx(a.sink[head] * kLog2e - mu + shift) : 0.f;
+#pragma unroll
+  for (int j = 0; j < kV; ++j) acc[j] = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float f = ex2_approx(s_m[rr][i] - mu);
+    lt = fmaf(s_l[rr][i], f, lt);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) acc[j] = fmaf(s_acc[rr][i][lane * kV + j], f, acc[j]);
+  }
+  const float inv = lt == 0.f ? 0.f : 1.f / lt;
+  uint16_t* op = a.o + (static_cast<int64_t>(q.row0 + tok) * a.Hq + head) * DV + lane * kV;
+  if constexpr (kV == 4)
+    *reinterpret_cast<uint2*>(op) = make_uint2(pack2(acc[0] * inv, acc[1] * inv, a.f16),
+                                               pack2(acc[2] * inv, acc[3] * inv, a.f16));
+  else
+    *reinterpret_cast<uint32_t*>(op) = pack2(acc[0] * inv, acc[1] * inv, a.f16);
+  if (a.lse && lane == 0)
+    a.lse[static_cast<int64_t>(head) * a.num_tokens + q.row0 + tok] =
+        none ? (a.sink ? a.sink[head] : -INFINITY) : (mu - shift) * kLn2 + logf(lt);
+}
+
+template <int KIND, int DQK, int DV, int NT>
+cudaError_t launch_one(const Args& a0, int sms, cudaStream_t st) {
+  using C = Cfg<KIND, DQK, DV, NT>;
+  Args a = a0;
+  auto kern = decode_kernel<KIND, DQK, DV, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  // as many blocks as can be resident, or as there can be tiles
+  const int64_t most = (static_cast<int64_t>(a.max_pages) << a.page_shift) + kTileKeys - 1;
+  const int64_t tiles = most / kTileKeys + 1;
+  const int64_t items =
+      (static_cast<int64_t>(a.num_tokens) * a.group / C::kRows + a.num_seqs) * a.Hkv;
+  int64_t ctas = static_cast<int64_t>(sms) * C::kBlocks;
+  if (ctas > kMaxCtas) ctas = kMaxCtas;
+  if (tiles < ctas && items * tiles < ctas) ctas = items * tiles;
+  a.part_rows = C::kRows;
+  const bool split = (static_cast<int64_t>(a.max_pages) << a.page_shift) > kTileKeys;
+  if (!split) a.split_desc = nullptr;
+  kern<<<static_cast<unsigned>(ctas), kThreads, C::kSmem, st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !split) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), C::kRows / 2);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<DV>, a, KIND == kCacheBf16 ? 0.f : 14.f);
+}
+
+template <int KIND, int DQK, int DV>
+cudaError_t launch_rows(const Args& a, int rows, int sms, cudaStream_t st) {
+  if (rows <= 8) return launch_one<KIND, DQK, DV, 1>(a, sms, st);
+  if (rows <= 16) return launch_one<KIND, DQK, DV, 2>(a, sms, st);
+  return launch_one<KIND, DQK, DV, 4>(a, sms, st);
+}
+
+template <int KIND>
+cudaError_t launch_dims(const Args& a, int rows, int sms, cudaStream_t st) {
+  if (a.d_v == 64) {
+    if (a.d_qk == 64) return launch_rows<KIND, 64, 64>(a, rows, sms, st);
+    if (a.d_qk == 128) return launch_rows<KIND, 128, 64>(a, rows, sms, st);
+    return launch_rows<KIND, 192, 64>(a, rows, sms, st);
+  }
+  if (a.d_qk == 64) return launch_rows<KIND, 64, 128>(a, rows, sms, st);
+  if (a.d_qk == 128) return launch_rows<KIND, 128, 128>(a, rows, sms, st);
+  return launch_rows<KIND, 192, 128>(a, rows, sms, st);
+}
+
+}  // namespace
+
+}  // namespace paged
+}  // namespace attn

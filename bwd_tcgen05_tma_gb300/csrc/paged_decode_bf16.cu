@@ -1,0 +1,12 @@
+// Few-row attention over a paged bf16 cache.
+#include "paged_decode.cuh"
+
+namespace attn {
+namespace paged {
+
+cudaError_t launch_decode_bf16(const Args& a, int rows, int sms, cudaStream_t st) {
+  return launch_dims<kCacheBf16>(a, rows, sms, st);
+}
+
+}  // namespace paged
+}  // namespace attn
