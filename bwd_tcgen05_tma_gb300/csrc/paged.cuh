@@ -152,5 +152,12 @@ cudaError_t launch_decode_e4m3(const Args& a, int rows, int sms, cudaStream_t st
 cudaError_t launch_decode_f16(const Args& a, int rows, int sms, cudaStream_t st);
 cudaError_t launch_decode_bf16(const Args& a, int rows, int sms, cudaStream_t st);
 
+// Many rows per KV head.
+constexpr int kMaxChunkCtas = 152;
+constexpr int kChunkPartRows = 256;
+cudaError_t launch_chunk_e4m3(const Args& a, int sms, cudaStream_t st);
+cudaError_t launch_chunk_f16(const Args& a, int sms, cudaStream_t st);
+cudaError_t launch_chunk_bf16(const Args& a, int sms, cudaStream_t st);
+
 }  // namespace paged
 }  // namespace attn

@@ -127,18 +127,28 @@ void fill(Args& a, const attn_paged_params_t* p) {
   a.d_v = p->d_v;
 }
 
+// Which kernel: rows of one KV head that make the tensor-memory kernel's 256-row
+// blocks pay.
+constexpr int kManyRows = 64;
+bool many_rows(const attn_paged_params_t* p) {
+  return static_cast<int64_t>(p->max_q_len) * (p->Hq / p->Hkv) > kManyRows;
+}
+
 // Workspace: descriptors of split items, then their partial states.
 struct Plan {
   size_t desc, ml, part, total;
 };
 Plan make_plan(const attn_paged_params_t* p) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t rows = decode_rows(static_cast<int64_t>(p->max_q_len) * (p->Hq / p->Hkv));
+  const int64_t expected = static_cast<int64_t>(p->max_q_len) * (p->Hq / p->Hkv);
+  // partial states: two a block, of all its rows
+  const size_t rows = many_rows(p) ? 2 * kMaxChunkCtas * kChunkPartRows
+                                   : 2 * kMaxCtas * decode_rows(expected);
   Plan pl;
   pl.desc = 0;
   pl.ml = up(kMaxCtas * sizeof(int4));
-  pl.part = pl.ml + up(2 * kMaxCtas * rows * sizeof(float2));
-  pl.total = pl.part + 2 * kMaxCtas * rows * p->d_v * sizeof(float);
+  pl.part = pl.ml + up(rows * sizeof(float2));
+  pl.total = pl.part + rows * p->d_v * sizeof(float);
   return pl;
 }
 
@@ -213,9 +223,15 @@ attn_status_t attn_paged_fwd(const attn_paged_params_t* p, void* o, float* lse, 
   const int rows = decode_rows(static_cast<int64_t>(p->max_q_len) * a.group);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int kind = kind_of(p);
-  const cudaError_t e = kind == kCacheE4m3  ? launch_decode_e4m3(a, rows, sms, st)
-                        : kind == kCacheF16 ? launch_decode_f16(a, rows, sms, st)
-                                            : launch_decode_bf16(a, rows, sms, st);
+  cudaError_t e;
+  if (many_rows(p))
+    e = kind == kCacheE4m3  ? launch_chunk_e4m3(a, sms, st)
+        : kind == kCacheF16 ? launch_chunk_f16(a, sms, st)
+                            : launch_chunk_bf16(a, sms, st);
+  else
+    e = kind == kCacheE4m3  ? launch_decode_e4m3(a, rows, sms, st)
+        : kind == kCacheF16 ? launch_decode_f16(a, rows, sms, st)
+                            : launch_decode_bf16(a, rows, sms, st);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -1,0 +1,921 @@
+// Attention over the paged cache for many query rows per KV head: chunks of
+// prompts behind a cached prefix.
+//
+// Mathematics and tiling.  The rows of one KV head (tokens x heads of its
+// group) are packed, so both heads of a group and short chunks fill the MMA's
+// 128 rows.  A block works on 256 rows in two halves A and B:
+//   S_X = Q_X K^T (tcgen05.mma, both from shared memory), P_X = exp2(S_X - m)
+//   by one thread per row, packed over S_X in tensor memory, O_X += P_X V.
+// A key tile is 128 tokens.  Converter warps bring each tile's pages to
+// shared memory once for both halves, in the 128-byte-swizzled layout the MMA
+// reads: E4M3 codes as fp16 (exact; 16 codes a load, converted in registers),
+// 16-bit caches by 16-byte asynchronous copies; slots outside the mask and
+// pages that are none as zeros.  The scales of 16-key groups (no page is
+// smaller) are applied to the scores: one multiply-add per score as without
+// them, since a group's maximum can be scaled after it is found.
+//
+// What bounds it: at 8 heads a group and more than a few hundred tokens the
+// MMAs (2 x 128 x 128 x 2 d a tile and half); the exponentials and the
+// conversion run beside them on the other warps of the same schedulers.
+//
+// Work split.  As for few rows: all tiles in order (sequence, head, row block,
+// tile) cut into equal shares, one a block, one block an SM; causal row blocks
+// count only the tiles they need.  Pieces of a row block meet in a second
+// kernel.
+//
+// Values that are not finite in a tile that some rows mask in part are taken
+// out of the product (their zero weight would make NaN of them) and added in
+// the epilogue to the rows that keep them.
+#pragma once
+#include <climits>
+
+#include "paged.cuh"
+
+namespace attn {
+namespace paged {
+namespace {
+
+using namespace sm103;
+
+constexpr int kHalf = 128;             // rows per half, keys per tile
+constexpr int kChunkRows = 2 * kHalf;  // rows per block of rows
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// the running maximum follows the true one within a factor of 2^8
+constexpr float kLazy = 8.f;
+
+template <int DQK, int DV>
+struct ChunkCfg {
+  static constexpr int kQTile = kHalf * DQK * 2;  // one half's Q
+  static constexpr int kKV = kHalf * (DQK > DV ? DQK : DV) * 2;
+  static constexpr int kQStages = DQK > 128 ? 1 : 2;
+  static constexpr int kKVStages = DQK > 128 ? 2 : 3;
+  static constexpr int kKVOff = kQStages * 2 * kQTile;
+  static constexpr int kAuxOff = kKVOff + kKVStages * kKV;
+  static constexpr int kSmem = kAuxOff + 3072;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+struct ChunkAux {
+  uint64_t q_full[2], q_empty[2], kv_full[3], kv_empty[3];
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+  uint32_t bad[4];  // by piece: its number + 1 once a value was taken out of the product
+  int ok_mask[4];  // by tile: 16-key groups whose page exists
+  int64_t part[16];
+  int64_t tile0;
+  int seq, head, rb;
+  float4 scale[4][8];     // by tile and group: K scale, log2 V scale, 1 / V scale
+  uint8_t q_exp[4][kChunkRows];  // by piece: biased exponent of the row's power of two
+};
+static_assert(sizeof(ChunkAux) <= 3072, "aux");
+
+template <int KIND>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  if (KIND == kCacheE4m3) return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  if (KIND == kCacheF16) return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+  return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+template <int KIND>
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+  const uint32_t f = not_finite<KIND>(w);
+  return w & ~(KIND == kCacheE4m3 ? (f >> 7) * 255u : (f >> 15) * 65535u);
+}
+
+// A block of rows of one sequence: keys some row keeps, and keys all rows of
+// a range of rows keep.
+struct SeqView {
+  Seq q;
+  int hi, nrb, rows, pos0;
+};
+__device__ __forceinline__ SeqView view_of(const Args& a, int s) {
+  SeqView v;
+  v.q = load_seq(a, s);
+  const int cap = a.max_pages << a.page_shift;
+  if (v.q.len > cap) flag_bounds(a);
+  v.hi = min(v.q.len, cap);
+  v.rows = v.q.n * a.group;
+  v.nrb = (v.rows + kChunkRows - 1) / kChunkRows;
+  v.pos0 = v.q.len - v.q.n;
+  return v;
+}
+// Keys [x, y) that some (any) or every row of rows [r0, r1) keeps.
+__device__ __forceinline__ int2 keys_any(const Args& a, const SeqView& v, int r0, int r1) {
+  const int lo = r0 / a.group, hi = (min(r1, v.rows) - 1) / a.group;
+  return make_int2(a.window >= 0 ? max(0, v.pos0 + lo - a.window) : 0,
+                   a.causal ? min(v.hi, v.pos0 + hi + 1) : v.hi);
+}
+__device__ __forceinline__ int2 keys_all(const Args& a, const SeqView& v, int r0, int r1) {
+  const int lo = r0 / a.group, hi = (min(r1, v.rows) - 1) / a.group;
+  return make_int2(a.window >= 0 ? max(0, v.pos0 + hi - a.window) : 0,
+                   a.causal ? min(v.hi, v.pos0 + lo + 1) : v.hi);
+}
+__device__ __forceinline__ int tiles_of(const Args& a, const SeqView& v, int rb) {
+  const int2 k = keys_any(a, v, rb * kChunkRows, (rb + 1) * kChunkRows);
+  return max(1, (k.y - (k.x & ~15) + kHalf - 1) / kHalf);
+}
+__device__ __forceinline__ int64_t seq_tiles(const Args& a, const SeqView& v) {
+  int64_t n = 0;
+  for (int rb = 0; rb < v.nrb; ++rb) n += tiles_of(a, v, rb);
+  return n;
+}
+
+// Walks the block's pieces; every thread of every role walks the same way.
+struct Walk {
+  int64_t at, end, total;
+  int ctas;
+  int seq, head, rb, t0;
+  SeqView v;
+  // the current piece
+  int t1, nt;
+  int2 any;  // keys some row of the block of rows keeps
+  int k0;    // first key of the row block's tile 0
+  int n;     // key tiles of the piece (0: no row keeps a key)
+};
+__device__ __forceinline__ void walk_piece(const Args& a, Walk& w) {
+  w.nt = tiles_of(a, w.v, w.rb);
+  w.t1 = static_cast<int>(min(static_cast<int64_t>(w.nt), w.t0 + (w.end - w.at)));
+  w.any = keys_any(a, w.v, w.rb * kChunkRows, (w.rb + 1) * kChunkRows);
+  w.k0 = w.any.x & ~15;
+  w.n = w.any.y > w.any.x ? w.t1 - w.t0 : 0;
+}
+__device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
+  w.at += w.t1 - w.t0;
+  if (w.at >= w.end) return false;
+  w.t0 = 0;
+  if (++w.rb >= w.v.nrb) {
+    w.rb = 0;
+    if (++w.head >= a.Hkv) {
+      w.head = 0;
+      do w.v = view_of(a, ++w.seq);
+      while (w.v.nrb == 0);
+    }
+  }
+  walk_piece(a, w);
+  return true;
+}
+
+// This block's share, found by all 512 threads.
+__device__ __forceinline__ void walk_init(const Args& a, ChunkAux* x, Walk& w) {
+  constexpr int kN = 512;
+  const int per = (a.num_seqs + kN - 1) / kN;
+  const int first = threadIdx.x * per, last = min(a.num_seqs, first + per);
+  int64_t mine = 0;
+  for (int s = first; s < last; ++s) mine += a.Hkv * seq_tiles(a, view_of(a, s));
+  int64_t sum = mine;
+#pragma unroll
+  for (int i = 1; i < 32; i <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, sum, i);
+    if ((threadIdx.x & 31) >= i) sum += y;
+  }
+  if ((threadIdx.x & 31) == 31) x->part[threadIdx.x / 32] = sum;
+  __syncthreads();
+  int64_t total = 0, before = sum - mine;
+  for (int i = 0; i < kN / 32; ++i) {
+    if (i < static_cast<int>(threadIdx.x) / 32) before += x->part[i];
+    total += x->part[i];
+  }
+  w.total = total;
+  w.ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+  w.at = w.end = 0;
+  if (static_cast<int>(blockIdx.x) < w.ctas) {
+    w.at = blockIdx.x * total / w.ctas;
+    w.end = (blockIdx.x + 1) * total / w.ctas;
+    if (w.at >= before && w.at < before + mine) {
+      int64_t off = w.at - before;
+      int s = first;
+      for (;; ++s) {
+        const SeqView v = view_of(a, s);
+        const int64_t per_head = seq_tiles(a, v);
+        if (off >= a.Hkv * per_head) {
+          off -= a.Hkv * per_head;
+          continue;
+        }
+        x->seq = s;
+        x->head = static_cast<int>(off / per_head);
+        off %= per_head;
+        int rb = 0;
+        for (int n; off >= (n = tiles_of(a, v, rb)); ++rb) off -= n;
+        x->rb = rb;
+        x->tile0 = off;
+        break;
+      }
+    }
+  }
+  __syncthreads();
+  if (w.at < w.end) {
+    w.seq = x->seq;
+    w.head = x->head;
+    w.rb = x->rb;
+    w.t0 = static_cast<int>(x->tile0);
+    w.v = view_of(a, w.seq);
+    walk_piece(a, w);
+  }
+}
+
+__device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
+
+// Eight E4M3 codes to fp16, stored as one 16-byte unit.
+__device__ __forceinline__ void store_codes(uint32_t dst, uint32_t lo, uint32_t hi) {
+  st_shared_v4(dst, e4m3x2_f16x2(static_cast<uint16_t>(lo)),
+               e4m3x2_f16x2(static_cast<uint16_t>(lo >> 16)),
+               e4m3x2_f16x2(static_cast<uint16_t>(hi)),
+               e4m3x2_f16x2(static_cast<uint16_t>(hi >> 16)));
+}
+
+template <int KIND, int DQK, int DV>
+__global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ Args a) {
+  using L = ChunkCfg<DQK, DV>;
+  constexpr bool kBf = KIND == kCacheBf16;
+  constexpr bool kCodes = KIND == kCacheE4m3;
+  constexpr int NKV = L::kKVStages, NQ = L::kQStages;
+  constexpr float kShift = kBf ? 0.f : 7.f;  // P <= 2^(7 + 8) in fp16
+  constexpr uint32_t kColS = 0, kColO = 256;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  ChunkAux* const x = reinterpret_cast<ChunkAux*>(sm + L::kAuxOff);
+  volatile int* const abort = &x->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (smem_u32(sm) & 1023u) return;  // the swizzle needs it; the window starts aligned
+
+  auto timeout = [&]() {
+    if (a.status) *a.status = ATTN_ERR_DEVICE_TIMEOUT;
+    *abort = 1;
+  };
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&x->q_full[s], 128);
+      mbar_init(&x->q_empty[s], 1);
+      mbar_init(&x->s_full[s], 1);
+      mbar_init(&x->p_full[s], 128);
+      mbar_init(&x->o_full[s], 1);
+      mbar_init(&x->o_empty[s], 128);
+    }
+    for (int s = 0; s < 3; ++s) {
+      mbar_init(&x->kv_full[s], 128);
+      mbar_init(&x->kv_empty[s], 1);
+    }
+    mbar_init(&x->drain, 1);
+    x->abort = 0;
+    for (uint32_t& b : x->bad) b = 0;
+    mbar_fence_init();
+    a.split_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
+  if (warp == 0) {
+    tmem_alloc(&x->tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  Walk w;
+  walk_init(a, x, w);  // two block barriers
+  tc_fence_after();
+  grid_dep_launch();
+  const uint32_t tmem = x->tmem;
+
+  // 512 threads x 128 registers = 65,536: 128 x 56 + 128 x 104 + 256 x 176
+  if (warp < 4) {
+    regs_lower<56>();
+    if (warp == 0 && w.at < w.end) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t id_s = idesc_f32acc(kBf ? 1 : 0, kHalf, kHalf, false, false);
+      constexpr uint32_t id_o = idesc_f32acc(kBf ? 1 : 0, kHalf, DV, false, true);
+      const uint32_t tm = warp_uniform(tmem);
+      const uint64_t q_km = sdesc_sw128(smem_u32(sm), 16, 1024);
+      const uint64_t kv_km = sdesc_sw128(smem_u32(sm + L::kKVOff), 16, 1024);
+      const uint64_t kv_mn = sdesc_sw128(smem_u32(sm + L::kKVOff), 16384, 1024);
+      auto stage = [&](uint32_t c) -> uint32_t { return ((c % NKV) * L::kKV) >> 4; };
+      auto issue_s = [&](int h, uint32_t piece, uint32_t kc) {
+        const uint64_t qd = q_km + ((((piece % NQ) * 2 + h) * L::kQTile) >> 4);
+        mma_ss_warp<DQK / 16, 4, 2, 1018, 2, 1018>(tm + kColS + h * kHalf, qd, kv_km + stage(kc),
+                                                   id_s, 0u);
+        mma_commit_warp(&x->s_full[h]);
+      };
+      uint32_t it = 0, kvc = 0, st = 0;
+      bool ok = true, live = true;
+      while (live && w.n == 0) live = walk_next(a, w);
+      if (live) {
+        if ((ok = mbar_wait_warp(&x->q_full[0], 0) && mbar_wait_warp(&x->kv_full[0], 0))) {
+          tc_fence_after();
+          issue_s(0, 0, 0);
+          issue_s(1, 0, 0);
+          mma_commit_warp(&x->kv_empty[0]);
+          if (w.n == 1) mma_commit_warp(&x->q_empty[0]);
+          kvc = 1;
+        }
+      }
+      // Each step: P_X V, then over P_X's columns the S that comes next, of
+      // this piece or the next one.  The pipe runs in order of issue.
+      while (ok && live) {
+        const int n = w.n;
+        Walk nx = w;
+        for (int j = 0; j < n && ok; ++j) {
+          const uint32_t k = st + j, vc = kvc;
+          const bool more = j + 1 < n;
+          bool go_on = more;
+          if (!more) {
+            do live = walk_next(a, nx);
+            while (live && nx.n == 0);
+            go_on = live;
+          }
+          const uint32_t pc = more ? it : it + 1;
+          if (!(ok = mbar_wait_warp(&x->kv_full[vc % NKV], (vc / NKV) & 1))) break;
+          for (int h = 0; h < 2 && ok; ++h) {
+            if (!(ok = mbar_wait_warp(&x->p_full[h], k & 1))) break;
+            if (j == 0 && it > 0 && !(ok = mbar_wait_warp(&x->o_empty[h], (it - 1) & 1))) break;
+            tc_fence_after();
+            mma_ts_warp<kHalf / 16, 4, 8, 8, 128, 128>(tm + kColO + h * kHalf,
+                                                       tm + kColS + h * kHalf, kv_mn + stage(vc),
+                                                       id_o, j == 0 ? 0u : 1u);
+            if (!more) mma_commit_warp(&x->o_full[h]);
+            if (h == 1) mma_commit_warp(&x->kv_empty[vc % NKV]);
+            if (!go_on) continue;
+            if (h == 0) {
+              if (!more && !(ok = mbar_wait_warp(&x->q_full[pc % NQ], (pc / NQ) & 1))) break;
+              if (!(ok = mbar_wait_warp(&x->kv_full[(vc + 1) % NKV], ((vc + 1) / NKV) & 1))) break;
+            }
+            tc_fence_after();
+            issue_s(h, pc, vc + 1);
+          }
+          if (!ok) break;
+          if (go_on) {
+            mma_commit_warp(&x->kv_empty[(vc + 1) % NKV]);
+            // the last S of a piece: its Q may be replaced
+            if (more ? j + 2 == n : nx.n == 1) mma_commit_warp(&x->q_empty[pc % NQ]);
+          }
+          kvc += go_on ? 2 : 1;
+        }
+        if (!ok) break;
+        st += n;
+        ++it;
+        w = nx;
+      }
+      if (!ok && lane == 0) timeout();
+      mma_commit_warp(&x->drain);
+      mbar_wait(&x->drain, 0, 200000000ull);
+    }
+  } else if (warp < 8) {
+    regs_lower<104>();
+    // ------------------------------------------------------------ converters
+    const int ct = tid - 128;            // 0..127
+    const int c4 = ct & 3, r4 = ct >> 2;  // codes: 16 of a 64-dim chunk, row in 32
+    const int c8 = ct & 7, r8 = ct >> 3;  // 16-bit: 8 of a 64-dim chunk, row in 16
+    const int page_mask = (1 << a.page_shift) - 1;
+    constexpr int kKl = kCodes ? DQK / 16 : 1, kVl = kCodes ? DV / 16 : 1;  // loads per thread
+    uint4 kreg[kKl], vreg[kVl];
+    uint32_t it = 0, kvc = 0, st = 0;
+    bool ok = true, live = w.at < w.end;
+    int pending = -1;  // 16-bit: ring entry copied but not announced
+
+    while (live && ok) {
+      if (w.n == 0) {
+        live = walk_next(a, w);
+        continue;
+      }
+      const int hk = w.head, r0 = w.rb * kChunkRows;
+      const int2 all = keys_all(a, w.v, r0, r0 + kChunkRows);
+      const int kfirst = w.k0 + w.t0 * kHalf;
+      // page and scales of group `lane` (< 8) of tile j
+      struct Ids {
+        int id;
+        float ks, vs;
+      };
+      auto load_ids = [&](int j) -> Ids {
+        Ids r = {-1, 1.f, 1.f};
+        const int key = kfirst + j * kHalf + 16 * (lane & 7);
+        if (j < w.n && key < w.any.y) {
+          const int col = key >> a.page_shift;
+          int id = col < a.max_pages ? a.table[w.seq * a.table_stride + col] : -1;
+          if (id < 0 || id >= a.num_pages) {
+            flag_bounds(a);
+            id = -1;
+          }
+          r.id = id;
+          if (kCodes && id >= 0) {
+            r.ks = a.k_scale[static_cast<int64_t>(id) * a.Hkv + hk];
+            r.vs = a.v_scale[static_cast<int64_t>(id) * a.Hkv + hk];
+          }
+        }
+        return r;
+      };
+      auto load_codes = [&](auto& reg, const Ids& ids, int j, const char* base, int64_t ps,
+                            int64_t hs, int64_t ts, int chunks) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = r4 + 32 * i, key = kfirst + j * kHalf + r;
+          const int page = __shfl_sync(0xffffffffu, ids.id, 2 * i + (ct >> 6));
+          const bool in = page >= 0 && key >= w.any.x && key < w.any.y;
+          const char* p =
+              base + (in ? page * ps + hk * hs + static_cast<int64_t>(key & page_mask) * ts : 0) +
+              c4 * 16;
+#pragma unroll
+          for (int c = 0; c < static_cast<int>(sizeof(reg) / sizeof(reg[0])) / 4; ++c)
+            reg[c * 4 + i] = in ? ld_nc_v4(p + c * 64) : make_uint4(0, 0, 0, 0);
+        }
+      };
+      auto put_codes = [&](const auto& reg, uint32_t dst) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = r4 + 32 * i;
+          const uint32_t row = dst + r * 128, u0 = (2 * c4) ^ (r & 7), u1 = (2 * c4 + 1) ^ (r & 7);
+#pragma unroll
+          for (int c = 0; c < static_cast<int>(sizeof(reg) / sizeof(reg[0])) / 4; ++c) {
+            const uint4 v = reg[c * 4 + i];
+            store_codes(row + c * 16384 + u0 * 16, v.x, v.y);
+            store_codes(row + c * 16384 + u1 * 16, v.z, v.w);
+          }
+        }
+      };
+      auto copy16 = [&](const Ids& ids, int j, const char* base, int64_t ps, int64_t hs, int64_t ts,
+                        int chunks, uint32_t dst) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = r8 + 16 * i, key = kfirst + j * kHalf + r;
+          const int page = __shfl_sync(0xffffffffu, ids.id, i);
+          const bool in = page >= 0 && key >= w.any.x && key < w.any.y;
+          const char* p =
+              base + (in ? page * ps + hk * hs + static_cast<int64_t>(key & page_mask) * ts : 0);
+          for (int c = 0; c < chunks; ++c)
+            cp_async16z(dst + c * 16384 + r * 128 + ((c8 ^ (r & 7)) << 4),
+                        in ? p + c * 128 + c8 * 16 : base, in);
+        }
+      };
+      auto entry = [&](uint32_t c) -> uint32_t {
+        return smem_u32(sm) + L::kKVOff + (c % NKV) * L::kKV;
+      };
+      auto wait_free = [&](uint32_t c) -> bool {
+        return c < NKV || mbar_wait_warp(&x->kv_empty[c % NKV], ((c / NKV) - 1) & 1);
+      };
+      // the entry's last reader is not known to be done (warp-uniform)
+      auto busy = [&](uint32_t c) -> bool {
+        return c >= NKV && !__all_sync(0xffffffffu, mbar_test_wait(&x->kv_empty[c % NKV],
+                                                                  ((c / NKV) - 1) & 1));
+      };
+      // 16-bit copies: announce the entry copied before the last commit
+      auto announce = [&](bool last) {
+        if (last) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        else asm volatile("cp.async.wait_group 1;" ::: "memory");
+        fence_proxy_async_smem();
+        mbar_arrive(&x->kv_full[pending % NKV]);
+      };
+
+      Ids ids = load_ids(0), nxt = load_ids(1);
+      if constexpr (kCodes) {
+        load_codes(kreg, ids, 0, a.kc, a.k_page, a.k_head, a.k_tok, DQK / 64);
+        load_codes(vreg, ids, 0, a.vc, a.v_page, a.v_head, a.v_tok, DV / 64);
+      }
+      // ---- queries: one row a thread and half, to fp16 where the cache is E4M3
+      if (it >= NQ && !mbar_wait_warp(&x->q_empty[it % NQ], ((it / NQ) - 1) & 1)) {
+        ok = false;
+        break;
+      }
+      for (int h = 0; h < 2; ++h) {
+        const int r = r0 + h * kHalf + ct;
+        const bool real = r < w.v.rows;
+        const uint16_t* qp = a.q;
+        if (real) qp += (w.v.q.row0 + r / a.group) * a.q_stride + (hk * a.group + r % a.group) * DQK;
+        float to = 1.f;
+        const bool turn = kCodes && !a.f16;
+        if (turn) {
+          uint32_t mx = 0;
+          if (real) {
+#pragma unroll 4
+            for (int u = 0; u < DQK / 8; ++u) {
+              const uint4 v = *reinterpret_cast<const uint4*>(qp + u * 8);
+              const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mx = max(mx, max(e[i] & 0x7fffu, (e[i] >> 16) & 0x7fffu));
+            }
+          }
+          int e = static_cast<int>(mx >> 7);
+          e = e == 255 ? 127 + 14 : max(e, 27);
+          to = __uint_as_float(static_cast<uint32_t>(254 + 14 - e) << 23);
+          x->q_exp[it & 3][h * kHalf + ct] = static_cast<uint8_t>(e - 14);
+        }
+        const uint32_t row = smem_u32(sm) + ((it % NQ) * 2 + h) * L::kQTile + ct * 128;
+#pragma unroll 4
+        for (int u = 0; u < DQK / 8; ++u) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (real) v = *reinterpret_cast<const uint4*>(qp + u * 8);
+          uint32_t e[4] = {v.x, v.y, v.z, v.w};
+          if (turn) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              e[i] = pack_f16x2(__uint_as_float(e[i] << 16) * to,
+                                __uint_as_float(e[i] & 0xffff0000u) * to);
+          }
+          st_shared_v4(row + (u / 8) * 16384 + (((u & 7) ^ (ct & 7)) << 4), e[0], e[1], e[2], e[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&x->q_full[it % NQ]);
+
+      for (int j = 0; j < w.n && ok; ++j) {
+        const uint32_t k = st + j;
+        const int key = kfirst + j * kHalf;
+        // ---- K
+        if (!kCodes && pending >= 0 && busy(kvc)) {
+          announce(true);
+          pending = -1;
+        }
+        if (!(ok = wait_free(kvc))) break;
+        {
+          const unsigned okm = __ballot_sync(0xffffffffu, ids.id >= 0) & 0xffu;
+          if (ct < 8) {
+            const float vs = fmaxf(ids.vs, 0x1p-100f);
+            const float lg = (__float_as_uint(vs) & 0x7fffffu) == 0
+                                 ? static_cast<float>(
+                                       static_cast<int>(__float_as_uint(vs) >> 23) - 127)
+                                 : __log2f(vs);
+            x->scale[k & 3][ct] = make_float4(ids.ks, lg, 1.f / vs, 0.f);
+            if (ct == 0) x->ok_mask[k & 3] = okm;
+          }
+        }
+        if constexpr (kCodes) {
+          put_codes(kreg, entry(kvc));
+          fence_proxy_async_smem();
+          mbar_arrive(&x->kv_full[kvc % NKV]);
+          if (j + 1 < w.n) load_codes(kreg, nxt, j + 1, a.kc, a.k_page, a.k_head, a.k_tok, DQK / 64);
+        } else {
+          copy16(ids, j, a.kc, a.k_page, a.k_head, a.k_tok, DQK / 64, entry(kvc));
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (pending >= 0) announce(false);
+          pending = kvc;
+        }
+        ++kvc;
+        // ---- V
+        const bool whole = key >= all.x && key + kHalf <= all.y;
+        if (!kCodes && pending >= 0 && busy(kvc)) {
+          announce(true);
+          pending = -1;
+        }
+        if (!(ok = wait_free(kvc))) break;
+        if constexpr (kCodes) {
+          if (!whole) {
+            uint32_t bad = 0;
+#pragma unroll
+            for (int i = 0; i < kVl; ++i)
+              bad |= not_finite<KIND>(vreg[i].x) | not_finite<KIND>(vreg[i].y) |
+                     not_finite<KIND>(vreg[i].z) | not_finite<KIND>(vreg[i].w);
+            if (bad) {
+              x->bad[it & 3] = it + 1;
+#pragma unroll
+              for (int i = 0; i < kVl; ++i)
+                vreg[i] = make_uint4(finite_only<KIND>(vreg[i].x), finite_only<KIND>(vreg[i].y),
+                                     finite_only<KIND>(vreg[i].z), finite_only<KIND>(vreg[i].w));
+            }
+          }
+          put_codes(vreg, entry(kvc));
+          fence_proxy_async_smem();
+          mbar_arrive(&x->kv_full[kvc % NKV]);
+          if (j + 1 < w.n) load_codes(vreg, nxt, j + 1, a.vc, a.v_page, a.v_head, a.v_tok, DV / 64);
+          ++kvc;
+        } else {
+          const uint32_t dst = entry(kvc);
+          copy16(ids, j, a.vc, a.v_page, a.v_head, a.v_tok, DV / 64, dst);
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (pending >= 0) announce(false);
+          pending = kvc++;
+          if (!whole) {
+            // look through what this thread copied itself
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            for (int i = 0; i < 8; ++i)
+              for (int c = 0; c < DV / 64; ++c) {
+                const int r = r8 + 16 * i;
+                const uint32_t p = dst + c * 16384 + r * 128 + ((c8 ^ (r & 7)) << 4);
+                uint32_t e[4];
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(e[0]), "=r"(e[1]), "=r"(e[2]), "=r"(e[3])
+                             : "r"(p)
+                             : "memory");
+                if (not_finite<KIND>(e[0]) | not_finite<KIND>(e[1]) | not_finite<KIND>(e[2]) |
+                    not_finite<KIND>(e[3])) {
+                  x->bad[it & 3] = it + 1;
+                  st_shared_v4(p, finite_only<KIND>(e[0]), finite_only<KIND>(e[1]),
+                               finite_only<KIND>(e[2]), finite_only<KIND>(e[3]));
+                }
+              }
+          }
+        }
+        ids = nxt;
+        nxt = load_ids(j + 2);
+      }
+      if (!ok) break;
+      if (!kCodes && pending >= 0) {
+        announce(true);
+        pending = -1;
+      }
+      st += w.n;
+      ++it;
+      live = walk_next(a, w);
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (!ok && lane == 0) timeout();
+  } else {
+    regs_raise<176>();
+    // ------------------------------------------------------------ softmax
+    const int h = (warp - 8) >> 2, r = tid & 127;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_tm = tmem + lanes + kColS + h * kHalf;
+    const uint32_t o_tm = tmem + lanes + kColO + h * kHalf;
+    uint32_t st = 0, it = 0;
+    bool ok = true, live = w.at < w.end;
+    while (live && ok && !__any_sync(0xffffffffu, *abort != 0)) {
+      const int rr = w.rb * kChunkRows + h * kHalf + r;
+      const bool real = rr < w.v.rows;
+      const int tok = real ? rr / a.group : 0;
+      const int head = w.head * a.group + (real ? rr % a.group : 0);
+      const int pos = w.v.pos0 + tok;
+      const int lo = a.window >= 0 ? max(0, pos - a.window) : 0;
+      const int hi = real ? (a.causal ? min(w.v.hi, pos + 1) : w.v.hi) : 0;
+      const int hr0 = w.rb * kChunkRows + h * kHalf;
+      // a half without rows masks everything
+      const int2 all =
+          hr0 < w.v.rows ? keys_all(a, w.v, hr0, hr0 + kHalf) : make_int2(INT_MAX, INT_MIN);
+      float m = -INFINITY, l = 0.f, fac = a.scale * kLog2e;
+      for (int j = 0; j < w.n; ++j) {
+        const uint32_t k = st + j;
+        const int key = w.k0 + (w.t0 + j) * kHalf;
+        if (!(ok = mbar_wait_warp(&x->s_full[h], k & 1))) break;
+        tc_fence_after();
+        uint32_t u[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32x32b_x32(s_tm + q * 32, u[q]);
+        if (j == 0 && kCodes && !a.f16)
+          fac *= __uint_as_float(static_cast<uint32_t>(x->q_exp[it & 3][h * kHalf + r]) << 23);
+        const unsigned okm = x->ok_mask[k & 3];
+        const bool whole = key >= all.x && key + kHalf <= all.y && okm == 0xffu;
+        tmem_ld_wait(u);
+        if (!whole) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int b = key + 32 * q;
+            const int f = min(max(lo - b, 0), 32), e = min(max(hi - b, 0), 32);
+            uint32_t bits = e > f ? (0xffffffffu >> (32 - (e - f))) << f : 0u;
+            if (!(okm >> (2 * q) & 1)) bits &= 0xffff0000u;
+            if (!(okm >> (2 * q + 1) & 1)) bits &= 0x0000ffffu;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) u[q][i] = (bits >> i & 1) ? u[q][i] : 0xff800000u;
+          }
+        }
+        // the row's maximum: of each group, then scaled
+        float mx = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          const uint32_t* e = &u[g / 2][(g & 1) * 16];
+          float m0 = fmax3(__uint_as_float(e[0]), __uint_as_float(e[1]), __uint_as_float(e[2]));
+          float m1 = fmax3(__uint_as_float(e[3]), __uint_as_float(e[4]), __uint_as_float(e[5]));
+          m0 = fmax3(m0, __uint_as_float(e[6]), __uint_as_float(e[7]));
+          m1 = fmax3(m1, __uint_as_float(e[8]), __uint_as_float(e[9]));
+          m0 = fmax3(m0, __uint_as_float(e[10]), __uint_as_float(e[11]));
+          m1 = fmax3(m1, __uint_as_float(e[12]), __uint_as_float(e[13]));
+          m0 = fmax3(m0, __uint_as_float(e[14]), __uint_as_float(e[15]));
+          m0 = fmaxf(m0, m1);
+          if constexpr (kCodes) {
+            const float4 sc = x->scale[k & 3][g];
+            mx = fmaxf(mx, fmaf(m0, fac * sc.x, sc.y));
+          } else {
+            mx = fmaxf(mx, m0);
+          }
+        }
+        if (!kCodes) mx *= fac;
+        const float mn = fmaxf(m, mx);
+        const bool grow = mn > m + kLazy || (m == -INFINITY && mn > m);
+        const bool again = grow && j > 0 && m > -INFINITY;
+        const float f = again ? ex2_approx(m - mn) : 1.f;
+        if (grow) m = mn;
+        const float base = kShift - (m == -INFINITY ? 0.f : m);
+        float add = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float A = fac, B = base, inv = 1.f;
+            if constexpr (kCodes) {
+              const float4 sc = x->scale[k & 3][2 * q + g];
+              A = fac * sc.x;
+              B = base + sc.y;
+              inv = sc.z;
+            }
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 y = fma_f32x2(make_float2(__uint_as_float(u[q][g * 16 + 2 * i]),
+                                                     __uint_as_float(u[q][g * 16 + 2 * i + 1])),
+                                         make_float2(A, A), make_float2(B, B));
+              const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+              sum = add_f32x2(sum, p);
+              pk[g * 8 + i] = kBf ? pack_bf16x2(p.x, p.y) : pack_f16x2(p.x, p.y);
+            }
+            add = fmaf(sum.x + sum.y, inv, add);
+          }
+          tmem_st32x32b_x16(s_tm + q * 16, pk);
+        }
+        l = fmaf(l, f, add);
+        // S_X(j) was issued after P_X(j-1) V, which is therefore complete
+        if (__any_sync(0xffffffffu, again)) {
+#pragma unroll
+          for (int q = 0; q < DV / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32x32b_x32(o_tm + q * 32, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32x32b_x32(o_tm + q * 32, o);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&x->p_full[h]);
+      }
+      if (!ok) break;
+      // ---- epilogue: O or the piece's partial state
+      const bool complete = w.t0 == 0 && w.t1 == w.nt;
+      const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
+      if (w.n > 0) {
+        if (!(ok = mbar_wait_warp(&x->o_full[h], it & 1))) break;
+        tc_fence_after();
+      }
+      float lt = l, mt = m, keep = 1.f;
+      const bool none = m == -INFINITY;
+      if (complete && a.sink) {
+        const float s2 = a.sink[head] * kLog2e;
+        mt = fmaxf(m, s2);
+        const float mu = mt == -INFINITY ? 0.f : mt;
+        keep = ex2_approx(m - mu);
+        lt = l * keep + ex2_approx(s2 - mu + kShift);
+      }
+      const float inv = complete ? (lt == 0.f ? 0.f : keep / lt) : 1.f;
+      const int64_t prow = static_cast<int64_t>(slot) * kChunkRows + h * kHalf + r;
+      const bool bad = w.n > 0 && x->bad[it & 3] == it + 1;
+      uint16_t* op = a.o + (static_cast<int64_t>(w.v.q.row0 + tok) * a.Hq + head) * DV;
+#pragma unroll
+      for (int q = 0; q < DV / 32; ++q) {
+        uint32_t o[32];
+        if (w.n > 0) {
+          tmem_ld32x32b_x32(o_tm + q * 32, o);
+          tmem_ld_wait(o);
+        }
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          v[i] = w.n > 0 && !none ? __uint_as_float(o[i]) * inv : 0.f;
+        if (bad && real) {
+          // values that are not finite, in tiles the block of rows masks in part
+          const int2 blk = keys_all(a, w.v, w.rb * kChunkRows, (w.rb + 1) * kChunkRows);
+          for (int j = 0; j < w.n; ++j) {
+            const int key = w.k0 + (w.t0 + j) * kHalf;
+            if (key >= blk.x && key + kHalf <= blk.y) continue;
+            for (int kk = max(key, lo); kk < min(key + kHalf, hi); ++kk) {
+              const int page = page_of(a, w.seq, kk);
+              if (page < 0) continue;
+              const char* vp = a.vc + page * a.v_page + w.head * a.v_head +
+                               static_cast<int64_t>(kk & ((1 << a.page_shift) - 1)) * a.v_tok;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float e =
+                    kCodes ? e4m3_value(reinterpret_cast<const uint8_t*>(vp)[q * 32 + i])
+                           : elem(reinterpret_cast<const uint16_t*>(vp)[q * 32 + i], !kBf);
+                if (!(fabsf(e) < INFINITY)) v[i] += e;
+              }
+            }
+          }
+        }
+        if (real && complete) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+            *reinterpret_cast<uint4*>(op + q * 32 + i) =
+                make_uint4(pack2(v[i], v[i + 1], a.f16), pack2(v[i + 2], v[i + 3], a.f16),
+                           pack2(v[i + 4], v[i + 5], a.f16), pack2(v[i + 6], v[i + 7], a.f16));
+        } else if (real) {
+          float* pp = a.part + prow * DV + q * 32;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(pp + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+      }
+      if (w.n > 0) {
+        tc_fence_before();
+        mbar_arrive(&x->o_empty[h]);
+      }
+      if (real && complete && a.lse)
+        a.lse[static_cast<int64_t>(head) * a.num_tokens + w.v.q.row0 + tok] =
+            none ? (a.sink ? a.sink[head] : -INFINITY) : (mt - kShift) * kLn2 + logf(lt);
+      if (real && !complete) a.part_ml[prow] = make_float2(m, l);
+      if (!complete && w.t0 == 0 && h == 0 && r == 0) {
+        const int64_t last = w.at + w.nt - 1;
+        const int c1 = static_cast<int>(((last + 1) * w.ctas + w.total - 1) / w.total) - 1;
+        a.split_desc[blockIdx.x] = make_int4(c1 - blockIdx.x + 1, w.seq, w.head, w.rb);
+      }
+      st += w.n;
+      if (w.n > 0) ++it;
+      live = walk_next(a, w);
+    }
+    if (!ok && lane == 0) timeout();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the pieces of split blocks of rows: block (i, y) 32 of the rows whose
+// first piece is block i's, one warp a row at a time.
+template <int DV>
+__global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ Args a,
+                                                         float shift) {
+  grid_dep_wait();
+  const int4 d = a.split_desc[blockIdx.x];
+  if (d.x == 0) return;
+  const int lane = threadIdx.x & 31;
+  const Seq q = load_seq(a, d.y);
+  const int rows = q.n * a.group;
+  constexpr int kV = DV / 32;
+  for (int i = threadIdx.x / 32; i < 32; i += 8) {
+    const int col = blockIdx.y * 32 + i, r = d.w * kChunkRows + col;
+    if (r >= rows) break;
+    float acc[kV], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int j = 0; j < kV; ++j) acc[j] = 0.f;
+#pragma unroll 2
+    for (int p = 0; p < d.x; ++p) {
+      const int64_t row =
+          (2 * (static_cast<int64_t>(blockIdx.x) + p) + (p == 0 ? 1 : 0)) * kChunkRows + col;
+      const float2 ml = a.part_ml[row];
+      const float* pp = a.part + row * DV + lane * kV;
+      float v[kV];
+#pragma unroll
+      for (int j = 0; j < kV; ++j) v[j] = pp[j];
+      const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
+      const float f0 = ex2_approx(m - mu), f1 = ex2_approx(ml.x - mu);
+#pragma unroll
+      for (int j = 0; j < kV; ++j) acc[j] = acc[j] * f0 + v[j] * f1;
+      l = l * f0 + ml.y * f1;
+      m = mn;
+    }
+    const int tok = r / a.group, head = d.z * a.group + r % a.group;
+    const bool none = m == -INFINITY;
+    float mt = m, lt = l, keep = 1.f;
+    if (a.sink) {
+      const float s2 = a.sink[head] * kLog2e;
+      mt = fmaxf(m, s2);
+      const float mu = mt == -INFINITY ? 0.f : mt;
+      keep = ex2_approx(m - mu);
+      lt = l * keep + ex2_approx(s2 - mu + shift);
+    }
+    const float inv = lt == 0.f ? 0.f : keep / lt;
+    uint16_t* op = a.o + (static_cast<int64_t>(q.row0 + tok) * a.Hq + head) * DV + lane * kV;
+    if constexpr (kV == 4)
+      *reinterpret_cast<uint2*>(op) = make_uint2(pack2(acc[0] * inv, acc[1] * inv, a.f16),
+                                                 pack2(acc[2] * inv, acc[3] * inv, a.f16));
+    else
+      *reinterpret_cast<uint32_t*>(op) = pack2(acc[0] * inv, acc[1] * inv, a.f16);
+    if (a.lse && lane == 0)
+      a.lse[static_cast<int64_t>(head) * a.num_tokens + q.row0 + tok] =
+          none ? (a.sink ? a.sink[head] : -INFINITY) : (mt - shift) * kLn2 + logf(lt);
+  }
+}
+
+template <int KIND, int DQK, int DV>
+cudaError_t chunk_one(const Args& a, int sms, cudaStream_t st) {
+  using L = ChunkCfg<DQK, DV>;
+  auto kern = chunk_kernel<KIND, DQK, DV>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  if (e != cudaSuccess) return e;
+  const unsigned ctas = sms < kMaxChunkCtas ? sms : kMaxChunkCtas;
+  kern<<<ctas, 512, L::kSmem, st>>>(a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(ctas, kChunkRows / 32);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<DV>, a, KIND == kCacheBf16 ? 0.f : 7.f);
+}
+
+template <int KIND>
+cudaError_t chunk_dims(const Args& a, int sms, cudaStream_t st) {
+  if (a.d_v == 64) {
+    if (a.d_qk == 64) return chunk_one<KIND, 64, 64>(a, sms, st);
+    if (a.d_qk == 128) return chunk_one<KIND, 128, 64>(a, sms, st);
+    return chunk_one<KIND, 192, 64>(a, sms, st);
+  }
+  if (a.d_qk == 64) return chunk_one<KIND, 64, 128>(a, sms, st);
+  if (a.d_qk == 128) return chunk_one<KIND, 128, 128>(a, sms, st);
+  return chunk_one<KIND, 192, 128>(a, sms, st);
+}
+
+}  // namespace
+}  // namespace paged
+}  // namespace attn

@@ -207,6 +207,11 @@ ATTEND = {
     "chunk_192_64_bf16": dict(new=[65], ctx=[130], d_qk=192, d_v=64, cache="bf16"),
     "chunk_64_128": dict(new=[65], ctx=[130], d_qk=64, d_v=128, dtype="fp16"),
     "chunk_uneven_group": dict(new=[50, 61], ctx=[30, 0], Hq=6, Hkv=2, layout="nhd", fused=True),
+    "chunk_many_tiles": dict(new=[300, 150], ctx=[1500, 700], Hq=8, Hkv=1, page=64),
+    "chunk_many_tiles_bf16": dict(new=[129, 64], ctx=[1500, 700], Hq=8, Hkv=2, cache="bf16"),
+    "chunk_many_tiles_192": dict(new=[129, 64], ctx=[1500, 700], Hq=4, Hkv=1, d_qk=192, page=128),
+    "chunk_many_seqs": dict(new=[(i * 37) % 90 for i in range(70)],
+                            ctx=[(i * 53) % 200 for i in range(70)], Hq=2, Hkv=1),
     "chunk_mixed_with_decode": dict(new=[1, 200, 1, 0, 3], ctx=[500, 20, 0, 3, 100]),
 }
 MASKS = {"causal": {}, "window": dict(window_left=20), "window0": dict(window_left=0),
