@@ -2,6 +2,7 @@
 // arithmetic of pages, positions and E4M3 scales.
 #pragma once
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -155,6 +156,14 @@ cudaError_t launch_decode_bf16(const Args& a, int rows, int sms, cudaStream_t st
 // Many rows per KV head.
 constexpr int kMaxChunkCtas = 152;
 constexpr int kChunkPartRows = 256;
+struct ChunkMaps {
+  CUtensorMap k, v;
+};
+// Tensor map over a cache, [page][head][slot][dim] by its strides in bytes:
+// boxes of min(page, 128) slots of one head, E4M3 codes as bytes in the order
+// of memory, 16-bit elements 64 at a time in the MMA's swizzle.
+bool cache_map(CUtensorMap* m, int kind, const void* base, int d, const Args& a, int64_t tok,
+               int64_t head, int64_t page);
 cudaError_t launch_chunk_e4m3(const Args& a, int sms, cudaStream_t st);
 cudaError_t launch_chunk_f16(const Args& a, int sms, cudaStream_t st);
 cudaError_t launch_chunk_bf16(const Args& a, int sms, cudaStream_t st);

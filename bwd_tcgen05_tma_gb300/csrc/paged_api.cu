@@ -1,7 +1,10 @@
 // Host side of the paged-cache calls: argument validation, workspace layout
 // and launches.
+#include <cudaTypedefs.h>
+
 #include <cmath>
 #include <cstring>
+#include <mutex>
 
 #include "paged.cuh"
 
@@ -131,7 +134,7 @@ void fill(Args& a, const attn_paged_params_t* p) {
 // blocks pay.
 constexpr int kManyRows = 64;
 bool many_rows(const attn_paged_params_t* p) {
-  return static_cast<int64_t>(p->max_q_len) * (p->Hq / p->Hkv) > kManyRows;
+  return p->num_pages > 0 && static_cast<int64_t>(p->max_q_len) * (p->Hq / p->Hkv) > kManyRows;
 }
 
 // Workspace: descriptors of split items, then their partial states.
@@ -152,6 +155,20 @@ Plan make_plan(const attn_paged_params_t* p) {
   return pl;
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
 int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -161,6 +178,28 @@ int sm_count() {
 }
 
 }  // namespace
+
+bool cache_map(CUtensorMap* m, int kind, const void* base, int d, const Args& a, int64_t tok,
+               int64_t head, int64_t page) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const bool codes = kind == kCacheE4m3;
+  const int slots = 1 << a.page_shift;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)slots, (cuuint64_t)a.Hkv,
+                              (cuuint64_t)a.num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)tok, (cuuint64_t)head, (cuuint64_t)page};
+  const cuuint32_t box[4] = {(cuuint32_t)(codes ? d : 64), (cuuint32_t)(slots < 128 ? slots : 128),
+                             1, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const CUtensorMapDataType type = codes                ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : kind == kCacheF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return fn(m, type, 4, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace paged
 }  // namespace attn
 

@@ -6,13 +6,14 @@
 // 128 rows.  A block works on 256 rows in two halves A and B:
 //   S_X = Q_X K^T (tcgen05.mma, both from shared memory), P_X = exp2(S_X - m)
 //   by one thread per row, packed over S_X in tensor memory, O_X += P_X V.
-// A key tile is 128 tokens.  Converter warps bring each tile's pages to
-// shared memory once for both halves, in the 128-byte-swizzled layout the MMA
-// reads: E4M3 codes as fp16 (exact; 16 codes a load, converted in registers),
-// 16-bit caches by 16-byte asynchronous copies; slots outside the mask and
-// pages that are none as zeros.  The scales of 16-key groups (no page is
-// smaller) are applied to the scores: one multiply-add per score as without
-// them, since a group's maximum can be scaled after it is found.
+// A key tile is 128 tokens, brought to shared memory once for both halves by
+// TMA, a page (or 128 tokens of one) a box.  16-bit caches land in the
+// 128-byte-swizzled layout the MMA reads; E4M3 codes land in a ring of their
+// own, from which converter warps write them as fp16 (exact) into that layout.
+// The converters also write zeros over value slots outside the mask.  The
+// scales of 16-key groups (no page is smaller) are applied to the scores: one
+// multiply-add per score as without them, since a group's maximum can be
+// scaled after it is found.
 //
 // What bounds it: at 8 heads a group and more than a few hundred tokens the
 // MMAs (2 x 128 x 128 x 2 d a tile and half); the exponentials and the
@@ -27,7 +28,10 @@
 // out of the product (their zero weight would make NaN of them) and added in
 // the epilogue to the rows that keep them.
 #pragma once
+#include <cuda.h>
+
 #include <climits>
+#include <type_traits>
 
 #include "paged.cuh"
 
@@ -44,30 +48,45 @@ constexpr float kLn2 = 0.6931471805599453f;
 // the running maximum follows the true one within a factor of 2^8
 constexpr float kLazy = 8.f;
 
-template <int DQK, int DV>
+template <int KIND, int DQK, int DV>
 struct ChunkCfg {
+  static constexpr bool kCodes = KIND == kCacheE4m3;
+  static constexpr bool kWide = DQK > 128;
   static constexpr int kQTile = kHalf * DQK * 2;  // one half's Q
-  static constexpr int kKV = kHalf * (DQK > DV ? DQK : DV) * 2;
-  static constexpr int kQStages = DQK > 128 ? 1 : 2;
-  static constexpr int kKVStages = DQK > 128 ? 2 : 3;
+  // K and V tiles take turns in the rings; with two stages K has the first
+  static constexpr int kK = kHalf * DQK * 2, kV = kHalf * DV * 2;
+  static constexpr int kKV = kK > kV ? kK : kV;
+  static constexpr int kQStages = kWide || kCodes ? 1 : 2;
+  static constexpr int kKVStages = kWide ? 2 : 3;
+  static constexpr int kCodeStages = !kCodes ? 0 : kWide ? 2 : 4;
   static constexpr int kKVOff = kQStages * 2 * kQTile;
-  static constexpr int kAuxOff = kKVOff + kKVStages * kKV;
+  static constexpr int kCodeOff = kKVOff + (kWide ? kK + kV : kKVStages * kKV);
+  static constexpr int kAuxOff =
+      kCodeOff + (!kCodes ? 0 : kWide ? (kK + kV) / 2 : kCodeStages * kKV / 2);
   static constexpr int kSmem = kAuxOff + 3072;
   static_assert(kSmem <= 227 * 1024, "shared memory");
+  static __device__ __forceinline__ uint32_t kv(uint32_t e) {
+    return kKVOff + (kWide ? (e & 1) * kK : (e % kKVStages) * kKV);
+  }
+  static __device__ __forceinline__ uint32_t code(uint32_t e) {
+    return kCodeOff + (kWide ? (e & 1) * (kK / 2) : (e & 3) * (kKV / 2));
+  }
 };
 
 struct ChunkAux {
   uint64_t q_full[2], q_empty[2], kv_full[3], kv_empty[3];
+  uint64_t raw_full[4], raw_empty[4];  // TMA: of the code ring, or of the K / V ring
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
   uint64_t drain;
   uint32_t tmem;
   int abort;
   uint32_t bad[4];  // by piece: its number + 1 once a value was taken out of the product
-  int ok_mask[4];  // by tile: 16-key groups whose page exists
+  int ok_mask[8];  // by tile (the producer runs up to four tiles ahead of the softmax): 16-key groups whose page exists
   int64_t part[16];
-  int64_t tile0;
+  int64_t begin, total;  // the block's first tile, all tiles
+  int ctas, tile0;
   int seq, head, rb;
-  float4 scale[4][8];     // by tile and group: K scale, log2 V scale, 1 / V scale
+  float4 scale[8][8];     // by tile and group: K scale, log2 V scale, 1 / V scale
   uint8_t q_exp[4][kChunkRows];  // by piece: biased exponent of the row's power of two
 };
 static_assert(sizeof(ChunkAux) <= 3072, "aux");
@@ -84,11 +103,9 @@ __device__ __forceinline__ uint32_t finite_only(uint32_t w) {
   return w & ~(KIND == kCacheE4m3 ? (f >> 7) * 255u : (f >> 15) * 65535u);
 }
 
-// A block of rows of one sequence: keys some row keeps, and keys all rows of
-// a range of rows keep.
 struct SeqView {
   Seq q;
-  int hi, nrb, rows, pos0;
+  int hi;  // keys it has in the cache
 };
 __device__ __forceinline__ SeqView view_of(const Args& a, int s) {
   SeqView v;
@@ -96,61 +113,65 @@ __device__ __forceinline__ SeqView view_of(const Args& a, int s) {
   const int cap = a.max_pages << a.page_shift;
   if (v.q.len > cap) flag_bounds(a);
   v.hi = min(v.q.len, cap);
-  v.rows = v.q.n * a.group;
-  v.nrb = (v.rows + kChunkRows - 1) / kChunkRows;
-  v.pos0 = v.q.len - v.q.n;
   return v;
+}
+__device__ __forceinline__ int rows_of(const Args& a, const SeqView& v) { return v.q.n * a.group; }
+__device__ __forceinline__ int blocks_of(const Args& a, const SeqView& v) {
+  return (v.q.n * a.group + kChunkRows - 1) / kChunkRows;
 }
 // Keys [x, y) that some (any) or every row of rows [r0, r1) keeps.
 __device__ __forceinline__ int2 keys_any(const Args& a, const SeqView& v, int r0, int r1) {
-  const int lo = r0 / a.group, hi = (min(r1, v.rows) - 1) / a.group;
-  return make_int2(a.window >= 0 ? max(0, v.pos0 + lo - a.window) : 0,
-                   a.causal ? min(v.hi, v.pos0 + hi + 1) : v.hi);
+  const int pos0 = v.q.len - v.q.n;
+  const int lo = r0 / a.group, hi = (min(r1, rows_of(a, v)) - 1) / a.group;
+  return make_int2(a.window >= 0 ? max(0, pos0 + lo - a.window) : 0,
+                   a.causal ? min(v.hi, pos0 + hi + 1) : v.hi);
 }
 __device__ __forceinline__ int2 keys_all(const Args& a, const SeqView& v, int r0, int r1) {
-  const int lo = r0 / a.group, hi = (min(r1, v.rows) - 1) / a.group;
-  return make_int2(a.window >= 0 ? max(0, v.pos0 + hi - a.window) : 0,
-                   a.causal ? min(v.hi, v.pos0 + lo + 1) : v.hi);
+  const int pos0 = v.q.len - v.q.n;
+  const int lo = r0 / a.group, hi = (min(r1, rows_of(a, v)) - 1) / a.group;
+  return make_int2(a.window >= 0 ? max(0, pos0 + hi - a.window) : 0,
+                   a.causal ? min(v.hi, pos0 + lo + 1) : v.hi);
 }
+// Tiles start at multiples of 128 keys, so that a tile is a whole number of
+// pages or inside one.
 __device__ __forceinline__ int tiles_of(const Args& a, const SeqView& v, int rb) {
   const int2 k = keys_any(a, v, rb * kChunkRows, (rb + 1) * kChunkRows);
-  return max(1, (k.y - (k.x & ~15) + kHalf - 1) / kHalf);
+  return max(1, (k.y - (k.x & ~(kHalf - 1)) + kHalf - 1) / kHalf);
 }
 __device__ __forceinline__ int64_t seq_tiles(const Args& a, const SeqView& v) {
   int64_t n = 0;
-  for (int rb = 0; rb < v.nrb; ++rb) n += tiles_of(a, v, rb);
+  const int nrb = blocks_of(a, v);
+  for (int rb = 0; rb < nrb; ++rb) n += tiles_of(a, v, rb);
   return n;
 }
 
-// Walks the block's pieces; every thread of every role walks the same way.
+// Walks the block's pieces; every warp of every role walks the same way.
 struct Walk {
-  int64_t at, end, total;
-  int ctas;
+  int done, share;  // tiles behind the current piece's first, and in all
   int seq, head, rb, t0;
   SeqView v;
   // the current piece
   int t1, nt;
-  int2 any;  // keys some row of the block of rows keeps
-  int k0;    // first key of the row block's tile 0
-  int n;     // key tiles of the piece (0: no row keeps a key)
+  int2 any;    // keys some row of the block of rows keeps
+  int n, key;  // key tiles (0: no row keeps a key), first key of the first
 };
 __device__ __forceinline__ void walk_piece(const Args& a, Walk& w) {
   w.nt = tiles_of(a, w.v, w.rb);
-  w.t1 = static_cast<int>(min(static_cast<int64_t>(w.nt), w.t0 + (w.end - w.at)));
+  w.t1 = min(w.nt, w.t0 + (w.share - w.done));
   w.any = keys_any(a, w.v, w.rb * kChunkRows, (w.rb + 1) * kChunkRows);
-  w.k0 = w.any.x & ~15;
+  w.key = (w.any.x & ~(kHalf - 1)) + w.t0 * kHalf;
   w.n = w.any.y > w.any.x ? w.t1 - w.t0 : 0;
 }
 __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
-  w.at += w.t1 - w.t0;
-  if (w.at >= w.end) return false;
+  w.done += w.t1 - w.t0;
+  if (w.done >= w.share) return false;
   w.t0 = 0;
-  if (++w.rb >= w.v.nrb) {
+  if (++w.rb >= blocks_of(a, w.v)) {
     w.rb = 0;
     if (++w.head >= a.Hkv) {
       w.head = 0;
       do w.v = view_of(a, ++w.seq);
-      while (w.v.nrb == 0);
+      while (w.v.q.n == 0);
     }
   }
   walk_piece(a, w);
@@ -177,14 +198,13 @@ __device__ __forceinline__ void walk_init(const Args& a, ChunkAux* x, Walk& w) {
     if (i < static_cast<int>(threadIdx.x) / 32) before += x->part[i];
     total += x->part[i];
   }
-  w.total = total;
-  w.ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
-  w.at = w.end = 0;
-  if (static_cast<int>(blockIdx.x) < w.ctas) {
-    w.at = blockIdx.x * total / w.ctas;
-    w.end = (blockIdx.x + 1) * total / w.ctas;
-    if (w.at >= before && w.at < before + mine) {
-      int64_t off = w.at - before;
+  const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+  w.done = w.share = 0;
+  if (static_cast<int>(blockIdx.x) < ctas) {
+    const int64_t begin = blockIdx.x * total / ctas;
+    w.share = static_cast<int>((blockIdx.x + 1) * total / ctas - begin);
+    if (begin >= before && begin < before + mine) {
+      int64_t off = begin - before;
       int s = first;
       for (;; ++s) {
         const SeqView v = view_of(a, s);
@@ -199,26 +219,40 @@ __device__ __forceinline__ void walk_init(const Args& a, ChunkAux* x, Walk& w) {
         int rb = 0;
         for (int n; off >= (n = tiles_of(a, v, rb)); ++rb) off -= n;
         x->rb = rb;
-        x->tile0 = off;
+        x->tile0 = static_cast<int>(off);
+        x->begin = begin;
+        x->total = total;
+        x->ctas = ctas;
         break;
       }
     }
   }
   __syncthreads();
-  if (w.at < w.end) {
+  if (w.share > 0) {
     w.seq = x->seq;
     w.head = x->head;
     w.rb = x->rb;
-    w.t0 = static_cast<int>(x->tile0);
+    w.t0 = x->tile0;
     w.v = view_of(a, w.seq);
     walk_piece(a, w);
   }
 }
 
-__device__ __forceinline__ void cp_async16z(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(ok ? 16 : 0)
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, uint64_t* bar, int x,
+                                            int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(p)
                : "memory");
+  return v;
 }
 
 // Eight E4M3 codes to fp16, stored as one 16-byte unit.
@@ -230,8 +264,9 @@ __device__ __forceinline__ void store_codes(uint32_t dst, uint32_t lo, uint32_t 
 }
 
 template <int KIND, int DQK, int DV>
-__global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ Args a) {
-  using L = ChunkCfg<DQK, DV>;
+__global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ Args a,
+                                                       const __grid_constant__ ChunkMaps maps) {
+  using L = ChunkCfg<KIND, DQK, DV>;
   constexpr bool kBf = KIND == kCacheBf16;
   constexpr bool kCodes = KIND == kCacheE4m3;
   constexpr int NKV = L::kKVStages, NQ = L::kQStages;
@@ -260,6 +295,10 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
       mbar_init(&x->kv_full[s], 128);
       mbar_init(&x->kv_empty[s], 1);
     }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&x->raw_full[s], 1);
+      mbar_init(&x->raw_empty[s], 128);
+    }
     mbar_init(&x->drain, 1);
     x->abort = 0;
     for (uint32_t& b : x->bad) b = 0;
@@ -277,10 +316,10 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
   grid_dep_launch();
   const uint32_t tmem = x->tmem;
 
-  // 512 threads x 128 registers = 65,536: 128 x 56 + 128 x 104 + 256 x 176
+  // 512 threads x 128 registers = 65,536 >= 128 x 56 + 128 x 80 + 256 x 184
   if (warp < 4) {
     regs_lower<56>();
-    if (warp == 0 && w.at < w.end) {
+    if (warp == 0 && w.share > 0) {
       // ------------------------------------------------------------ MMA issuer
       constexpr uint32_t id_s = idesc_f32acc(kBf ? 1 : 0, kHalf, kHalf, false, false);
       constexpr uint32_t id_o = idesc_f32acc(kBf ? 1 : 0, kHalf, DV, false, true);
@@ -288,7 +327,7 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
       const uint64_t q_km = sdesc_sw128(smem_u32(sm), 16, 1024);
       const uint64_t kv_km = sdesc_sw128(smem_u32(sm + L::kKVOff), 16, 1024);
       const uint64_t kv_mn = sdesc_sw128(smem_u32(sm + L::kKVOff), 16384, 1024);
-      auto stage = [&](uint32_t c) -> uint32_t { return ((c % NKV) * L::kKV) >> 4; };
+      auto stage = [&](uint32_t c) -> uint32_t { return (L::kv(c) - L::kKVOff) >> 4; };
       auto issue_s = [&](int h, uint32_t piece, uint32_t kc) {
         const uint64_t qd = q_km + ((((piece % NQ) * 2 + h) * L::kQTile) >> 4);
         mma_ss_warp<DQK / 16, 4, 2, 1018, 2, 1018>(tm + kColS + h * kHalf, qd, kv_km + stage(kc),
@@ -300,6 +339,7 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
       while (live && w.n == 0) live = walk_next(a, w);
       if (live) {
         if ((ok = mbar_wait_warp(&x->q_full[0], 0) && mbar_wait_warp(&x->kv_full[0], 0))) {
+          fence_proxy_async_smem();
           tc_fence_after();
           issue_s(0, 0, 0);
           issue_s(1, 0, 0);
@@ -324,6 +364,7 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
           }
           const uint32_t pc = more ? it : it + 1;
           if (!(ok = mbar_wait_warp(&x->kv_full[vc % NKV], (vc / NKV) & 1))) break;
+          fence_proxy_async_smem();
           for (int h = 0; h < 2 && ok; ++h) {
             if (!(ok = mbar_wait_warp(&x->p_full[h], k & 1))) break;
             if (j == 0 && it > 0 && !(ok = mbar_wait_warp(&x->o_empty[h], (it - 1) & 1))) break;
@@ -337,6 +378,7 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
             if (h == 0) {
               if (!more && !(ok = mbar_wait_warp(&x->q_full[pc % NQ], (pc / NQ) & 1))) break;
               if (!(ok = mbar_wait_warp(&x->kv_full[(vc + 1) % NKV], ((vc + 1) / NKV) & 1))) break;
+              fence_proxy_async_smem();
             }
             tc_fence_after();
             issue_s(h, pc, vc + 1);
@@ -358,116 +400,120 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
       mma_commit_warp(&x->drain);
       mbar_wait(&x->drain, 0, 200000000ull);
     }
+    if (warp == 1 && w.share > 0) {
+      // ------------------------------------------------------------ TMA producer
+      // Lane i looks after box i of a tile: a page, or 128 tokens of one.  The
+      // table is read two tiles ahead and the scales one, so that no load of a
+      // tile waits for another of the same tile.
+      const int rows_log = min(a.page_shift, 7), boxes = kHalf >> rows_log;
+      const int page_mask = (1 << a.page_shift) - 1;
+      uint32_t st = 0, e = 0;  // tiles and ring entries so far
+      bool ok = true, live = true;
+      while (live && ok) {
+        if (w.n == 0) {
+          live = walk_next(a, w);
+          continue;
+        }
+        const int hk = w.head;
+        auto key_of = [&](int j) -> int { return w.key + j * kHalf + (lane << rows_log); };
+        auto load_entry = [&](int j) -> int {
+          if (j >= w.n || lane >= boxes || key_of(j) >= w.any.y) return INT_MIN;
+          const int col = key_of(j) >> a.page_shift;
+          return col < a.max_pages ? a.table[w.seq * a.table_stride + col] : -1;
+        };
+        struct Ids {
+          int id;
+          float ks, vs;
+        };
+        auto load_ids = [&](int p) -> Ids {
+          Ids r = {p, 1.f, 1.f};
+          if (p < 0 || p >= a.num_pages) {
+            if (p != INT_MIN) flag_bounds(a);
+            r.id = -1;
+          } else if (kCodes) {
+            r.ks = a.k_scale[static_cast<int64_t>(p) * a.Hkv + hk];
+            r.vs = a.v_scale[static_cast<int64_t>(p) * a.Hkv + hk];
+          }
+          return r;
+        };
+        int ahead = load_entry(1);
+        Ids ids = load_ids(load_entry(0));
+        for (int j = 0; j < w.n && ok; ++j) {
+          const uint32_t k = st + j;
+          const Ids nxt = load_ids(ahead);
+          ahead = load_entry(j + 2);
+          const unsigned okm = __ballot_sync(0xffffffffu, ids.id >= 0);
+          const uint32_t count = __popc(okm);
+          const int slot = key_of(j) & page_mask;
+          for (int m = 0; m < 2 && ok; ++m, ++e) {
+            const int d = m == 0 ? DQK : DV;
+            const uint32_t rs = kCodes ? e % (L::kCodeStages + !kCodes) : e % NKV;
+            if (e >= (kCodes ? L::kCodeStages : NKV)) {
+              const uint32_t ph = (e / (kCodes ? L::kCodeStages + !kCodes : NKV) - 1) & 1;
+              if (!(ok = mbar_wait_warp(kCodes ? &x->raw_empty[rs] : &x->kv_empty[rs], ph))) break;
+            }
+            if (m == 0) {
+              const int box = (16 * (lane & 7)) >> rows_log;
+              const float ks = __shfl_sync(0xffffffffu, ids.ks, box);
+              const float vs = fmaxf(__shfl_sync(0xffffffffu, ids.vs, box), 0x1p-100f);
+              const unsigned groups = __ballot_sync(0xffffffffu, okm >> box & 1) & 0xffu;
+              if (lane < 8) {
+                const float lg = (__float_as_uint(vs) & 0x7fffffu) == 0
+                                     ? static_cast<float>(
+                                           static_cast<int>(__float_as_uint(vs) >> 23) - 127)
+                                     : __log2f(vs);
+                x->scale[k & 7][lane] = make_float4(ks, lg, 1.f / vs, 0.f);
+                if (lane == 0) x->ok_mask[k & 7] = groups;
+              }
+            }
+            // the arrival (release) publishes the scales; the loads follow it
+            __syncwarp();
+            if (lane == 0)
+              mbar_arrive_expect_tx(&x->raw_full[rs],
+                                    (count << rows_log) * d * (kCodes ? 1 : 2));
+            __syncwarp();
+            if (ids.id >= 0) {
+              const void* map = m == 0 ? &maps.k : &maps.v;
+              const uint32_t dst = smem_u32(sm);
+              if constexpr (kCodes) {
+                tma_load_4d(dst + L::code(e) + (lane << rows_log) * d, map, &x->raw_full[rs], 0,
+                            slot, hk, ids.id);
+              } else {
+                for (int c = 0; c < d / 64; ++c)
+                  tma_load_4d(dst + L::kv(e) + c * 16384 + (lane << rows_log) * 128, map,
+                              &x->raw_full[rs], c * 64, slot, hk, ids.id);
+              }
+            }
+            __syncwarp();
+          }
+          ids = nxt;
+        }
+        st += w.n;
+        if (ok) live = walk_next(a, w);
+      }
+      if (!ok) {
+        if (lane == 0) timeout();
+      }
+      // copies in flight land before the block may leave
+      const uint32_t depth = kCodes ? L::kCodeStages : NKV;
+      for (uint32_t i = e > depth ? e - depth : 0; i < e; ++i)
+        mbar_wait(&x->raw_full[i % depth], (i / depth) & 1, 100000000ull);
+    }
   } else if (warp < 8) {
-    regs_lower<104>();
+    regs_lower<80>();
     // ------------------------------------------------------------ converters
-    const int ct = tid - 128;            // 0..127
-    const int c4 = ct & 3, r4 = ct >> 2;  // codes: 16 of a 64-dim chunk, row in 32
-    const int c8 = ct & 7, r8 = ct >> 3;  // 16-bit: 8 of a 64-dim chunk, row in 16
-    const int page_mask = (1 << a.page_shift) - 1;
-    constexpr int kKl = kCodes ? DQK / 16 : 1, kVl = kCodes ? DV / 16 : 1;  // loads per thread
-    uint4 kreg[kKl], vreg[kVl];
-    uint32_t it = 0, kvc = 0, st = 0;
-    bool ok = true, live = w.at < w.end;
-    int pending = -1;  // 16-bit: ring entry copied but not announced
-
+    // Their shared-memory writes are ordered before the MMA's reads by the
+    // issuer's proxy fence behind its wait.
+    const int ct = tid - 128;  // 0..127
+    uint32_t it = 0, e = 0, st = 0;
+    bool ok = true, live = w.share > 0;
     while (live && ok) {
       if (w.n == 0) {
         live = walk_next(a, w);
         continue;
       }
-      const int hk = w.head, r0 = w.rb * kChunkRows;
+      const int r0 = w.rb * kChunkRows, rows = rows_of(a, w.v);
       const int2 all = keys_all(a, w.v, r0, r0 + kChunkRows);
-      const int kfirst = w.k0 + w.t0 * kHalf;
-      // page and scales of group `lane` (< 8) of tile j
-      struct Ids {
-        int id;
-        float ks, vs;
-      };
-      auto load_ids = [&](int j) -> Ids {
-        Ids r = {-1, 1.f, 1.f};
-        const int key = kfirst + j * kHalf + 16 * (lane & 7);
-        if (j < w.n && key < w.any.y) {
-          const int col = key >> a.page_shift;
-          int id = col < a.max_pages ? a.table[w.seq * a.table_stride + col] : -1;
-          if (id < 0 || id >= a.num_pages) {
-            flag_bounds(a);
-            id = -1;
-          }
-          r.id = id;
-          if (kCodes && id >= 0) {
-            r.ks = a.k_scale[static_cast<int64_t>(id) * a.Hkv + hk];
-            r.vs = a.v_scale[static_cast<int64_t>(id) * a.Hkv + hk];
-          }
-        }
-        return r;
-      };
-      auto load_codes = [&](auto& reg, const Ids& ids, int j, const char* base, int64_t ps,
-                            int64_t hs, int64_t ts, int chunks) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = r4 + 32 * i, key = kfirst + j * kHalf + r;
-          const int page = __shfl_sync(0xffffffffu, ids.id, 2 * i + (ct >> 6));
-          const bool in = page >= 0 && key >= w.any.x && key < w.any.y;
-          const char* p =
-              base + (in ? page * ps + hk * hs + static_cast<int64_t>(key & page_mask) * ts : 0) +
-              c4 * 16;
-#pragma unroll
-          for (int c = 0; c < static_cast<int>(sizeof(reg) / sizeof(reg[0])) / 4; ++c)
-            reg[c * 4 + i] = in ? ld_nc_v4(p + c * 64) : make_uint4(0, 0, 0, 0);
-        }
-      };
-      auto put_codes = [&](const auto& reg, uint32_t dst) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = r4 + 32 * i;
-          const uint32_t row = dst + r * 128, u0 = (2 * c4) ^ (r & 7), u1 = (2 * c4 + 1) ^ (r & 7);
-#pragma unroll
-          for (int c = 0; c < static_cast<int>(sizeof(reg) / sizeof(reg[0])) / 4; ++c) {
-            const uint4 v = reg[c * 4 + i];
-            store_codes(row + c * 16384 + u0 * 16, v.x, v.y);
-            store_codes(row + c * 16384 + u1 * 16, v.z, v.w);
-          }
-        }
-      };
-      auto copy16 = [&](const Ids& ids, int j, const char* base, int64_t ps, int64_t hs, int64_t ts,
-                        int chunks, uint32_t dst) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = r8 + 16 * i, key = kfirst + j * kHalf + r;
-          const int page = __shfl_sync(0xffffffffu, ids.id, i);
-          const bool in = page >= 0 && key >= w.any.x && key < w.any.y;
-          const char* p =
-              base + (in ? page * ps + hk * hs + static_cast<int64_t>(key & page_mask) * ts : 0);
-          for (int c = 0; c < chunks; ++c)
-            cp_async16z(dst + c * 16384 + r * 128 + ((c8 ^ (r & 7)) << 4),
-                        in ? p + c * 128 + c8 * 16 : base, in);
-        }
-      };
-      auto entry = [&](uint32_t c) -> uint32_t {
-        return smem_u32(sm) + L::kKVOff + (c % NKV) * L::kKV;
-      };
-      auto wait_free = [&](uint32_t c) -> bool {
-        return c < NKV || mbar_wait_warp(&x->kv_empty[c % NKV], ((c / NKV) - 1) & 1);
-      };
-      // the entry's last reader is not known to be done (warp-uniform)
-      auto busy = [&](uint32_t c) -> bool {
-        return c >= NKV && !__all_sync(0xffffffffu, mbar_test_wait(&x->kv_empty[c % NKV],
-                                                                  ((c / NKV) - 1) & 1));
-      };
-      // 16-bit copies: announce the entry copied before the last commit
-      auto announce = [&](bool last) {
-        if (last) asm volatile("cp.async.wait_group 0;" ::: "memory");
-        else asm volatile("cp.async.wait_group 1;" ::: "memory");
-        fence_proxy_async_smem();
-        mbar_arrive(&x->kv_full[pending % NKV]);
-      };
-
-      Ids ids = load_ids(0), nxt = load_ids(1);
-      if constexpr (kCodes) {
-        load_codes(kreg, ids, 0, a.kc, a.k_page, a.k_head, a.k_tok, DQK / 64);
-        load_codes(vreg, ids, 0, a.vc, a.v_page, a.v_head, a.v_tok, DV / 64);
-      }
       // ---- queries: one row a thread and half, to fp16 where the cache is E4M3
       if (it >= NQ && !mbar_wait_warp(&x->q_empty[it % NQ], ((it / NQ) - 1) & 1)) {
         ok = false;
@@ -475,171 +521,153 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
       }
       for (int h = 0; h < 2; ++h) {
         const int r = r0 + h * kHalf + ct;
-        const bool real = r < w.v.rows;
+        const bool real = r < rows;
         const uint16_t* qp = a.q;
-        if (real) qp += (w.v.q.row0 + r / a.group) * a.q_stride + (hk * a.group + r % a.group) * DQK;
+        if (real)
+          qp += (w.v.q.row0 + r / a.group) * a.q_stride + (w.head * a.group + r % a.group) * DQK;
         float to = 1.f;
         const bool turn = kCodes && !a.f16;
         if (turn) {
           uint32_t mx = 0;
           if (real) {
-#pragma unroll 4
+#pragma unroll 8
             for (int u = 0; u < DQK / 8; ++u) {
               const uint4 v = *reinterpret_cast<const uint4*>(qp + u * 8);
-              const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+              const uint32_t b[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-              for (int i = 0; i < 4; ++i) mx = max(mx, max(e[i] & 0x7fffu, (e[i] >> 16) & 0x7fffu));
+              for (int i = 0; i < 4; ++i) mx = max(mx, max(b[i] & 0x7fffu, (b[i] >> 16) & 0x7fffu));
             }
           }
-          int e = static_cast<int>(mx >> 7);
-          e = e == 255 ? 127 + 14 : max(e, 27);
-          to = __uint_as_float(static_cast<uint32_t>(254 + 14 - e) << 23);
-          x->q_exp[it & 3][h * kHalf + ct] = static_cast<uint8_t>(e - 14);
+          int ex = static_cast<int>(mx >> 7);
+          ex = ex == 255 ? 127 + 14 : max(ex, 27);
+          to = __uint_as_float(static_cast<uint32_t>(254 + 14 - ex) << 23);
+          x->q_exp[it & 3][h * kHalf + ct] = static_cast<uint8_t>(ex - 14);
         }
         const uint32_t row = smem_u32(sm) + ((it % NQ) * 2 + h) * L::kQTile + ct * 128;
-#pragma unroll 4
+#pragma unroll 8
         for (int u = 0; u < DQK / 8; ++u) {
           uint4 v = make_uint4(0, 0, 0, 0);
           if (real) v = *reinterpret_cast<const uint4*>(qp + u * 8);
-          uint32_t e[4] = {v.x, v.y, v.z, v.w};
+          uint32_t b[4] = {v.x, v.y, v.z, v.w};
           if (turn) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              e[i] = pack_f16x2(__uint_as_float(e[i] << 16) * to,
-                                __uint_as_float(e[i] & 0xffff0000u) * to);
+              b[i] = pack_f16x2(__uint_as_float(b[i] << 16) * to,
+                                __uint_as_float(b[i] & 0xffff0000u) * to);
           }
-          st_shared_v4(row + (u / 8) * 16384 + (((u & 7) ^ (ct & 7)) << 4), e[0], e[1], e[2], e[3]);
+          st_shared_v4(row + (u / 8) * 16384 + (((u & 7) ^ (ct & 7)) << 4), b[0], b[1], b[2], b[3]);
         }
       }
-      fence_proxy_async_smem();
       mbar_arrive(&x->q_full[it % NQ]);
 
-      for (int j = 0; j < w.n && ok; ++j) {
-        const uint32_t k = st + j;
-        const int key = kfirst + j * kHalf;
-        // ---- K
-        if (!kCodes && pending >= 0 && busy(kvc)) {
-          announce(true);
-          pending = -1;
-        }
-        if (!(ok = wait_free(kvc))) break;
-        {
-          const unsigned okm = __ballot_sync(0xffffffffu, ids.id >= 0) & 0xffu;
-          if (ct < 8) {
-            const float vs = fmaxf(ids.vs, 0x1p-100f);
-            const float lg = (__float_as_uint(vs) & 0x7fffffu) == 0
-                                 ? static_cast<float>(
-                                       static_cast<int>(__float_as_uint(vs) >> 23) - 127)
-                                 : __log2f(vs);
-            x->scale[k & 3][ct] = make_float4(ids.ks, lg, 1.f / vs, 0.f);
-            if (ct == 0) x->ok_mask[k & 3] = okm;
-          }
-        }
+      // One ring entry: K (no row is ever masked by its content) or V, whose
+      // slots outside the mask become zeros.
+      auto convert = [&](auto dim, bool value, int key, uint32_t k) -> bool {
+        constexpr int D = decltype(dim)::value;
+        constexpr uint32_t kDepth = kCodes ? L::kCodeStages + !kCodes : NKV;
+        if (!mbar_wait_warp(&x->raw_full[e % kDepth], (e / kDepth) & 1)) return false;
+        const bool whole = key >= all.x && key + kHalf <= all.y && x->ok_mask[k & 7] == 0xff;
+        const int okm = x->ok_mask[k & 7];
+        auto in = [&](int r) -> bool {
+          return (okm >> (r >> 4) & 1) && key + r >= w.any.x && key + r < w.any.y;
+        };
         if constexpr (kCodes) {
-          put_codes(kreg, entry(kvc));
-          fence_proxy_async_smem();
-          mbar_arrive(&x->kv_full[kvc % NKV]);
-          if (j + 1 < w.n) load_codes(kreg, nxt, j + 1, a.kc, a.k_page, a.k_head, a.k_tok, DQK / 64);
-        } else {
-          copy16(ids, j, a.kc, a.k_page, a.k_head, a.k_tok, DQK / 64, entry(kvc));
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          if (pending >= 0) announce(false);
-          pending = kvc;
-        }
-        ++kvc;
-        // ---- V
-        const bool whole = key >= all.x && key + kHalf <= all.y;
-        if (!kCodes && pending >= 0 && busy(kvc)) {
-          announce(true);
-          pending = -1;
-        }
-        if (!(ok = wait_free(kvc))) break;
-        if constexpr (kCodes) {
-          if (!whole) {
+          // D / 16 units of 16 codes a row, in the order of memory
+          constexpr int kU = D / 16;
+          const uint32_t src = smem_u32(sm) + L::code(e) + ct * 16;
+          uint4 v[kU];
+#pragma unroll
+          for (int i = 0; i < kU; ++i) v[i] = lds128(src + i * 2048);
+          mbar_arrive(&x->raw_empty[e % kDepth]);
+          if (value && !whole) {
             uint32_t bad = 0;
 #pragma unroll
-            for (int i = 0; i < kVl; ++i)
-              bad |= not_finite<KIND>(vreg[i].x) | not_finite<KIND>(vreg[i].y) |
-                     not_finite<KIND>(vreg[i].z) | not_finite<KIND>(vreg[i].w);
+            for (int i = 0; i < kU; ++i) {
+              if (!in((ct + 128 * i) / kU)) v[i] = make_uint4(0, 0, 0, 0);
+              bad |= not_finite<KIND>(v[i].x) | not_finite<KIND>(v[i].y) |
+                     not_finite<KIND>(v[i].z) | not_finite<KIND>(v[i].w);
+            }
             if (bad) {
               x->bad[it & 3] = it + 1;
 #pragma unroll
-              for (int i = 0; i < kVl; ++i)
-                vreg[i] = make_uint4(finite_only<KIND>(vreg[i].x), finite_only<KIND>(vreg[i].y),
-                                     finite_only<KIND>(vreg[i].z), finite_only<KIND>(vreg[i].w));
+              for (int i = 0; i < kU; ++i)
+                v[i] = make_uint4(finite_only<KIND>(v[i].x), finite_only<KIND>(v[i].y),
+                                  finite_only<KIND>(v[i].z), finite_only<KIND>(v[i].w));
             }
           }
-          put_codes(vreg, entry(kvc));
-          fence_proxy_async_smem();
-          mbar_arrive(&x->kv_full[kvc % NKV]);
-          if (j + 1 < w.n) load_codes(vreg, nxt, j + 1, a.vc, a.v_page, a.v_head, a.v_tok, DV / 64);
-          ++kvc;
-        } else {
-          const uint32_t dst = entry(kvc);
-          copy16(ids, j, a.vc, a.v_page, a.v_head, a.v_tok, DV / 64, dst);
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          if (pending >= 0) announce(false);
-          pending = kvc++;
-          if (!whole) {
-            // look through what this thread copied itself
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            for (int i = 0; i < 8; ++i)
-              for (int c = 0; c < DV / 64; ++c) {
-                const int r = r8 + 16 * i;
-                const uint32_t p = dst + c * 16384 + r * 128 + ((c8 ^ (r & 7)) << 4);
-                uint32_t e[4];
-                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(e[0]), "=r"(e[1]), "=r"(e[2]), "=r"(e[3])
-                             : "r"(p)
-                             : "memory");
-                if (not_finite<KIND>(e[0]) | not_finite<KIND>(e[1]) | not_finite<KIND>(e[2]) |
-                    not_finite<KIND>(e[3])) {
-                  x->bad[it & 3] = it + 1;
-                  st_shared_v4(p, finite_only<KIND>(e[0]), finite_only<KIND>(e[1]),
-                               finite_only<KIND>(e[2]), finite_only<KIND>(e[3]));
-                }
+          if (e >= NKV && !mbar_wait_warp(&x->kv_empty[e % NKV], ((e / NKV) - 1) & 1)) return false;
+          const uint32_t dst = smem_u32(sm) + L::kv(e);
+#pragma unroll
+          for (int i = 0; i < kU; ++i) {
+            const int q = ct + 128 * i, r = q / kU, u = q % kU;
+            // lanes with u >= 4 (the second 64 dims) store their second half
+            // first: eight lanes then meet eight bank groups
+            const uint32_t row = dst + (u >> 2) * 16384 + r * 128;
+            const int f = (u >> 2) & 1, u0 = 2 * (u & 3) + f, u1 = u0 ^ 1;
+            store_codes(row + ((u0 ^ (r & 7)) << 4), f ? v[i].z : v[i].x, f ? v[i].w : v[i].y);
+            store_codes(row + ((u1 ^ (r & 7)) << 4), f ? v[i].x : v[i].z, f ? v[i].y : v[i].w);
+          }
+        } else if (value && !whole) {
+          const uint32_t at = smem_u32(sm) + L::kv(e);
+          for (int i = 0; i < 8; ++i) {
+            const int r = (ct >> 3) + 16 * i;
+            for (int c = 0; c < D / 64; ++c) {
+              const uint32_t p = at + c * 16384 + r * 128 + (ct & 7) * 16;
+              if (!in(r)) {
+                st_shared_v4(p, 0, 0, 0, 0);
+                continue;
               }
+              const uint4 v = lds128(p);
+              if (not_finite<KIND>(v.x) | not_finite<KIND>(v.y) | not_finite<KIND>(v.z) |
+                  not_finite<KIND>(v.w)) {
+                x->bad[it & 3] = it + 1;
+                st_shared_v4(p, finite_only<KIND>(v.x), finite_only<KIND>(v.y),
+                             finite_only<KIND>(v.z), finite_only<KIND>(v.w));
+              }
+            }
           }
         }
-        ids = nxt;
-        nxt = load_ids(j + 2);
+        mbar_arrive(&x->kv_full[e % NKV]);
+        ++e;
+        return true;
+      };
+      for (int j = 0; j < w.n && ok; ++j) {
+        const int key = w.key + j * kHalf;
+        ok = convert(std::integral_constant<int, DQK>{}, false, key, st + j) &&
+             convert(std::integral_constant<int, DV>{}, true, key, st + j);
       }
       if (!ok) break;
-      if (!kCodes && pending >= 0) {
-        announce(true);
-        pending = -1;
-      }
       st += w.n;
       ++it;
       live = walk_next(a, w);
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!ok && lane == 0) timeout();
   } else {
-    regs_raise<176>();
+    regs_raise<184>();
     // ------------------------------------------------------------ softmax
     const int h = (warp - 8) >> 2, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_tm = tmem + lanes + kColS + h * kHalf;
     const uint32_t o_tm = tmem + lanes + kColO + h * kHalf;
     uint32_t st = 0, it = 0;
-    bool ok = true, live = w.at < w.end;
+    bool ok = true, live = w.share > 0;
     while (live && ok && !__any_sync(0xffffffffu, *abort != 0)) {
       const int rr = w.rb * kChunkRows + h * kHalf + r;
-      const bool real = rr < w.v.rows;
+      const int rows = rows_of(a, w.v);
+      const bool real = rr < rows;
       const int tok = real ? rr / a.group : 0;
       const int head = w.head * a.group + (real ? rr % a.group : 0);
-      const int pos = w.v.pos0 + tok;
+      const int pos = w.v.q.len - w.v.q.n + tok;
       const int lo = a.window >= 0 ? max(0, pos - a.window) : 0;
       const int hi = real ? (a.causal ? min(w.v.hi, pos + 1) : w.v.hi) : 0;
       const int hr0 = w.rb * kChunkRows + h * kHalf;
       // a half without rows masks everything
       const int2 all =
-          hr0 < w.v.rows ? keys_all(a, w.v, hr0, hr0 + kHalf) : make_int2(INT_MAX, INT_MIN);
+          hr0 < rows ? keys_all(a, w.v, hr0, hr0 + kHalf) : make_int2(INT_MAX, INT_MIN);
       float m = -INFINITY, l = 0.f, fac = a.scale * kLog2e;
       for (int j = 0; j < w.n; ++j) {
         const uint32_t k = st + j;
-        const int key = w.k0 + (w.t0 + j) * kHalf;
+        const int key = w.key + j * kHalf;
         if (!(ok = mbar_wait_warp(&x->s_full[h], k & 1))) break;
         tc_fence_after();
         uint32_t u[4][32];
@@ -647,7 +675,7 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
         for (int q = 0; q < 4; ++q) tmem_ld32x32b_x32(s_tm + q * 32, u[q]);
         if (j == 0 && kCodes && !a.f16)
           fac *= __uint_as_float(static_cast<uint32_t>(x->q_exp[it & 3][h * kHalf + r]) << 23);
-        const unsigned okm = x->ok_mask[k & 3];
+        const unsigned okm = x->ok_mask[k & 7];
         const bool whole = key >= all.x && key + kHalf <= all.y && okm == 0xffu;
         tmem_ld_wait(u);
         if (!whole) {
@@ -676,7 +704,7 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
           m0 = fmax3(m0, __uint_as_float(e[14]), __uint_as_float(e[15]));
           m0 = fmaxf(m0, m1);
           if constexpr (kCodes) {
-            const float4 sc = x->scale[k & 3][g];
+            const float4 sc = x->scale[k & 7][g];
             mx = fmaxf(mx, fmaf(m0, fac * sc.x, sc.y));
           } else {
             mx = fmaxf(mx, m0);
@@ -697,7 +725,7 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
           for (int g = 0; g < 2; ++g) {
             float A = fac, B = base, inv = 1.f;
             if constexpr (kCodes) {
-              const float4 sc = x->scale[k & 3][2 * q + g];
+              const float4 sc = x->scale[k & 7][2 * q + g];
               A = fac * sc.x;
               B = base + sc.y;
               inv = sc.z;
@@ -769,7 +797,7 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
           // values that are not finite, in tiles the block of rows masks in part
           const int2 blk = keys_all(a, w.v, w.rb * kChunkRows, (w.rb + 1) * kChunkRows);
           for (int j = 0; j < w.n; ++j) {
-            const int key = w.k0 + (w.t0 + j) * kHalf;
+            const int key = w.key + j * kHalf;
             if (key >= blk.x && key + kHalf <= blk.y) continue;
             for (int kk = max(key, lo); kk < min(key + kHalf, hi); ++kk) {
               const int page = page_of(a, w.seq, kk);
@@ -808,8 +836,8 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
             none ? (a.sink ? a.sink[head] : -INFINITY) : (mt - kShift) * kLn2 + logf(lt);
       if (real && !complete) a.part_ml[prow] = make_float2(m, l);
       if (!complete && w.t0 == 0 && h == 0 && r == 0) {
-        const int64_t last = w.at + w.nt - 1;
-        const int c1 = static_cast<int>(((last + 1) * w.ctas + w.total - 1) / w.total) - 1;
+        const int64_t end = x->begin + w.done + w.nt;  // of the row block's tiles
+        const int c1 = static_cast<int>((end * x->ctas + x->total - 1) / x->total) - 1;
         a.split_desc[blockIdx.x] = make_int4(c1 - blockIdx.x + 1, w.seq, w.head, w.rb);
       }
       st += w.n;
@@ -885,12 +913,16 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
 
 template <int KIND, int DQK, int DV>
 cudaError_t chunk_one(const Args& a, int sms, cudaStream_t st) {
-  using L = ChunkCfg<DQK, DV>;
+  using L = ChunkCfg<KIND, DQK, DV>;
   auto kern = chunk_kernel<KIND, DQK, DV>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
+  ChunkMaps maps;
+  if (!cache_map(&maps.k, KIND, a.kc, DQK, a, a.k_tok, a.k_head, a.k_page) ||
+      !cache_map(&maps.v, KIND, a.vc, DV, a, a.v_tok, a.v_head, a.v_page))
+    return cudaErrorInvalidValue;
   const unsigned ctas = sms < kMaxChunkCtas ? sms : kMaxChunkCtas;
-  kern<<<ctas, 512, L::kSmem, st>>>(a);
+  kern<<<ctas, 512, L::kSmem, st>>>(a, maps);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
