@@ -18,6 +18,8 @@ enum CacheKind { kCacheBf16 = 0, kCacheF16 = 1, kCacheE4m3 = 2 };
 
 struct Args {
   int num_seqs, num_tokens, Hq, Hkv, group;
+  uint32_t group_mul;  // multiplier and shift of a division by `group`
+  int group_shift;
   int page_shift, num_pages, max_pages;
   int f16;     // 16-bit tensors are fp16 (else bf16)
   int causal;  // attention: keys behind the row's position are masked
@@ -51,6 +53,7 @@ struct Args {
   float2* part_ml;   // [2 * ctas][rows] (max in log2 units, sum)
   int4* split_desc;  // [ctas] of an item's first piece: pieces (0: none), sequence, head, rows
   int part_rows;
+  int o_st32;  // O may be stored 32 bytes at a time
 };
 
 // One sequence: its new rows and its length.
@@ -60,6 +63,13 @@ struct Seq {
 
 __device__ __forceinline__ void flag_bounds(const Args& a) {
   if (a.status) *a.status = ATTN_ERR_DEVICE_BOUNDS;
+}
+
+// n / group for n >= 0 (multiplication by a rounded-up reciprocal of 33 bits,
+// after Granlund and Montgomery's division by invariant integers).
+__device__ __forceinline__ int div_group(const Args& a, int n) {
+  const uint32_t u = static_cast<uint32_t>(n), t = __umulhi(a.group_mul, u);
+  return a.group == 1 ? n : static_cast<int>((t + ((u - t) >> 1)) >> (a.group_shift - 1));
 }
 
 // Rows and length of sequence s.  Offsets outside [0, num_tokens] or

@@ -104,6 +104,9 @@ void fill(Args& a, const attn_paged_params_t* p) {
   a.Hq = p->Hq;
   a.Hkv = p->Hkv;
   a.group = p->Hq / p->Hkv;
+  while ((1 << a.group_shift) < a.group) ++a.group_shift;
+  a.group_mul = static_cast<uint32_t>(
+      ((1ull << 32) * ((1ull << a.group_shift) - a.group)) / a.group + 1);
   while ((1 << a.page_shift) < p->page_size) ++a.page_shift;
   a.num_pages = p->num_pages;
   a.max_pages = p->max_pages;
@@ -253,6 +256,7 @@ attn_status_t attn_paged_fwd(const attn_paged_params_t* p, void* o, float* lse, 
   a.sink = p->sink;
   a.o = static_cast<uint16_t*>(o);
   a.lse = lse;
+  a.o_st32 = aligned(o, 32);
   char* w = static_cast<char*>(ws);
   a.split_desc = reinterpret_cast<int4*>(w + pl.desc);
   a.part_ml = reinterpret_cast<float2*>(w + pl.ml);

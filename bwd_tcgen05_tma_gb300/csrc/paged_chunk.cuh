@@ -122,13 +122,13 @@ __device__ __forceinline__ int blocks_of(const Args& a, const SeqView& v) {
 // Keys [x, y) that some (any) or every row of rows [r0, r1) keeps.
 __device__ __forceinline__ int2 keys_any(const Args& a, const SeqView& v, int r0, int r1) {
   const int pos0 = v.q.len - v.q.n;
-  const int lo = r0 / a.group, hi = (min(r1, rows_of(a, v)) - 1) / a.group;
+  const int lo = div_group(a, r0), hi = div_group(a, min(r1, rows_of(a, v)) - 1);
   return make_int2(a.window >= 0 ? max(0, pos0 + lo - a.window) : 0,
                    a.causal ? min(v.hi, pos0 + hi + 1) : v.hi);
 }
 __device__ __forceinline__ int2 keys_all(const Args& a, const SeqView& v, int r0, int r1) {
   const int pos0 = v.q.len - v.q.n;
-  const int lo = r0 / a.group, hi = (min(r1, rows_of(a, v)) - 1) / a.group;
+  const int lo = div_group(a, r0), hi = div_group(a, min(r1, rows_of(a, v)) - 1);
   return make_int2(a.window >= 0 ? max(0, pos0 + hi - a.window) : 0,
                    a.causal ? min(v.hi, pos0 + lo + 1) : v.hi);
 }
@@ -316,9 +316,7 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
   grid_dep_launch();
   const uint32_t tmem = x->tmem;
 
-  // 512 threads x 128 registers = 65,536 >= 128 x 56 + 128 x 80 + 256 x 184
   if (warp < 4) {
-    regs_lower<56>();
     if (warp == 0 && w.share > 0) {
       // ------------------------------------------------------------ MMA issuer
       constexpr uint32_t id_s = idesc_f32acc(kBf ? 1 : 0, kHalf, kHalf, false, false);
@@ -339,7 +337,6 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
       while (live && w.n == 0) live = walk_next(a, w);
       if (live) {
         if ((ok = mbar_wait_warp(&x->q_full[0], 0) && mbar_wait_warp(&x->kv_full[0], 0))) {
-          fence_proxy_async_smem();
           tc_fence_after();
           issue_s(0, 0, 0);
           issue_s(1, 0, 0);
@@ -364,7 +361,6 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
           }
           const uint32_t pc = more ? it : it + 1;
           if (!(ok = mbar_wait_warp(&x->kv_full[vc % NKV], (vc / NKV) & 1))) break;
-          fence_proxy_async_smem();
           for (int h = 0; h < 2 && ok; ++h) {
             if (!(ok = mbar_wait_warp(&x->p_full[h], k & 1))) break;
             if (j == 0 && it > 0 && !(ok = mbar_wait_warp(&x->o_empty[h], (it - 1) & 1))) break;
@@ -378,7 +374,6 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
             if (h == 0) {
               if (!more && !(ok = mbar_wait_warp(&x->q_full[pc % NQ], (pc / NQ) & 1))) break;
               if (!(ok = mbar_wait_warp(&x->kv_full[(vc + 1) % NKV], ((vc + 1) / NKV) & 1))) break;
-              fence_proxy_async_smem();
             }
             tc_fence_after();
             issue_s(h, pc, vc + 1);
@@ -500,10 +495,9 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
         mbar_wait(&x->raw_full[i % depth], (i / depth) & 1, 100000000ull);
     }
   } else if (warp < 8) {
-    regs_lower<80>();
     // ------------------------------------------------------------ converters
-    // Their shared-memory writes are ordered before the MMA's reads by the
-    // issuer's proxy fence behind its wait.
+    // They hold no global loads in flight at their proxy fences (a fence waits
+    // for them): the codes come by TMA.
     const int ct = tid - 128;  // 0..127
     uint32_t it = 0, e = 0, st = 0;
     bool ok = true, live = w.share > 0;
@@ -512,52 +506,76 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
         live = walk_next(a, w);
         continue;
       }
-      const int r0 = w.rb * kChunkRows, rows = rows_of(a, w.v);
+      const int r0 = w.rb * kChunkRows;
       const int2 all = keys_all(a, w.v, r0, r0 + kChunkRows);
       // ---- queries: one row a thread and half, to fp16 where the cache is E4M3
       if (it >= NQ && !mbar_wait_warp(&x->q_empty[it % NQ], ((it / NQ) - 1) & 1)) {
         ok = false;
         break;
       }
-      for (int h = 0; h < 2; ++h) {
-        const int r = r0 + h * kHalf + ct;
-        const bool real = r < rows;
-        const uint16_t* qp = a.q;
-        if (real)
-          qp += (w.v.q.row0 + r / a.group) * a.q_stride + (w.head * a.group + r % a.group) * DQK;
-        float to = 1.f;
-        const bool turn = kCodes && !a.f16;
-        if (turn) {
-          uint32_t mx = 0;
-          if (real) {
-#pragma unroll 8
-            for (int u = 0; u < DQK / 8; ++u) {
-              const uint4 v = *reinterpret_cast<const uint4*>(qp + u * 8);
-              const uint32_t b[4] = {v.x, v.y, v.z, v.w};
+      {
+        // Lanes of a group copy one row together, 16 bytes each, to where the
+        // MMA reads it; what a lane copied it turns to fp16 in place.  Small
+        // rolled loops: this code runs once a piece and is fetched anew.
+        constexpr int kL = DQK == 64 ? 8 : 16, kPer = 32 / kL;  // lanes a row, rows a load
+        constexpr int kU = DQK == 192 ? 2 : 1;                  // units a lane (192: 16 + 8)
+        constexpr int kSteps = 2 * 32 / kPer;                   // this warp's rows of both halves
+        const int sub = lane % kL, first = (warp - 4) * 32 + lane / kL;
+        const uint32_t qs = smem_u32(sm) + (it % NQ) * 2 * L::kQTile;
+        auto place = [&](int b, int u) -> uint32_t {
+          const int n = b * kPer, rr = first + n % 32, unit = sub + kL * u;
+          return qs + (n / 32) * L::kQTile + rr * 128 + (unit / 8) * 16384 +
+                 (((unit & 7) ^ (rr & 7)) << 4);
+        };
+#pragma unroll 4
+        for (int b = 0; b < kSteps; ++b) {
+          const int n = b * kPer, r = r0 + (n / 32) * kHalf + first + n % 32;
+          const int tok = div_group(a, r);
+          const bool real = tok < w.v.q.n;
+          const uint16_t* qp = a.q + (real ? (w.v.q.row0 + tok) * a.q_stride +
+                                                 (w.head * a.group + r - tok * a.group) * DQK +
+                                                 sub * 8
+                                           : 0);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) mx = max(mx, max(b[i] & 0x7fffu, (b[i] >> 16) & 0x7fffu));
-            }
-          }
-          int ex = static_cast<int>(mx >> 7);
-          ex = ex == 255 ? 127 + 14 : max(ex, 27);
-          to = __uint_as_float(static_cast<uint32_t>(254 + 14 - ex) << 23);
-          x->q_exp[it & 3][h * kHalf + ct] = static_cast<uint8_t>(ex - 14);
+          for (int u = 0; u < kU; ++u)
+            if (u == 0 || sub < 8)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(place(b, u)),
+                           "l"(qp + (real ? kL * u * 8 : 0)), "r"(real ? 16 : 0)
+                           : "memory");
         }
-        const uint32_t row = smem_u32(sm) + ((it % NQ) * 2 + h) * L::kQTile + ct * 128;
-#pragma unroll 8
-        for (int u = 0; u < DQK / 8; ++u) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (real) v = *reinterpret_cast<const uint4*>(qp + u * 8);
-          uint32_t b[4] = {v.x, v.y, v.z, v.w};
-          if (turn) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (kCodes && !a.f16) {
+#pragma unroll 4
+          for (int b = 0; b < kSteps; ++b) {
+            uint4 v[kU];
+            uint32_t mx = 0;  // two 16-bit magnitudes
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              b[i] = pack_f16x2(__uint_as_float(b[i] << 16) * to,
-                                __uint_as_float(b[i] & 0xffff0000u) * to);
+            for (int u = 0; u < kU; ++u) {
+              v[u] = u == 0 || sub < 8 ? lds128(place(b, u)) : make_uint4(0, 0, 0, 0);
+              mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v[u].x & 0x7fff7fffu, v[u].y & 0x7fff7fffu),
+                                         __vmaxu2(v[u].z & 0x7fff7fffu, v[u].w & 0x7fff7fffu)));
+            }
+#pragma unroll
+            for (int k = 1; k < kL; k <<= 1)
+              mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+            int ex = static_cast<int>(max(mx & 0xffffu, mx >> 16) >> 7);
+            ex = ex == 255 ? 127 + 14 : max(ex, 27);
+            const float to = __uint_as_float(static_cast<uint32_t>(254 + 14 - ex) << 23);
+            const int n = b * kPer;
+            if (sub == 0)
+              x->q_exp[it & 3][(n / 32) * kHalf + first + n % 32] = static_cast<uint8_t>(ex - 14);
+            auto turn = [&](uint32_t e) -> uint32_t {
+              return pack_f16x2(__uint_as_float(e << 16) * to,
+                                __uint_as_float(e & 0xffff0000u) * to);
+            };
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+              if (u == 0 || sub < 8)
+                st_shared_v4(place(b, u), turn(v[u].x), turn(v[u].y), turn(v[u].z), turn(v[u].w));
           }
-          st_shared_v4(row + (u / 8) * 16384 + (((u & 7) ^ (ct & 7)) << 4), b[0], b[1], b[2], b[3]);
         }
       }
+      fence_proxy_async_smem();
       mbar_arrive(&x->q_full[it % NQ]);
 
       // One ring entry: K (no row is ever masked by its content) or V, whose
@@ -627,6 +645,7 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
             }
           }
         }
+        fence_proxy_async_smem();
         mbar_arrive(&x->kv_full[e % NKV]);
         ++e;
         return true;
@@ -643,7 +662,6 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
     }
     if (!ok && lane == 0) timeout();
   } else {
-    regs_raise<184>();
     // ------------------------------------------------------------ softmax
     const int h = (warp - 8) >> 2, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -655,8 +673,8 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
       const int rr = w.rb * kChunkRows + h * kHalf + r;
       const int rows = rows_of(a, w.v);
       const bool real = rr < rows;
-      const int tok = real ? rr / a.group : 0;
-      const int head = w.head * a.group + (real ? rr % a.group : 0);
+      const int tok = real ? div_group(a, rr) : 0;
+      const int head = w.head * a.group + (real ? rr - tok * a.group : 0);
       const int pos = w.v.q.len - w.v.q.n + tok;
       const int lo = a.window >= 0 ? max(0, pos - a.window) : 0;
       const int hi = real ? (a.causal ? min(w.v.hi, pos + 1) : w.v.hi) : 0;
@@ -670,31 +688,32 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
         const int key = w.key + j * kHalf;
         if (!(ok = mbar_wait_warp(&x->s_full[h], k & 1))) break;
         tc_fence_after();
-        uint32_t u[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32x32b_x32(s_tm + q * 32, u[q]);
         if (j == 0 && kCodes && !a.f16)
           fac *= __uint_as_float(static_cast<uint32_t>(x->q_exp[it & 3][h * kHalf + r]) << 23);
-        const unsigned okm = x->ok_mask[k & 7];
-        const bool whole = key >= all.x && key + kHalf <= all.y && okm == 0xffu;
-        tmem_ld_wait(u);
-        if (!whole) {
+        const int okm = x->ok_mask[k & 7];
+        // The row's scores are read twice, a group at a time and the next group
+        // while this one is worked on: held whole they would cost 128
+        // registers, and spills meet an L1 that shared memory has left small.
+        auto pass = [&](auto masked, auto&& body) {
+          uint32_t u[2][16];
+          tmem_ld32x32b_x16(s_tm, u[0]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int b = key + 32 * q;
-            const int f = min(max(lo - b, 0), 32), e = min(max(hi - b, 0), 32);
-            uint32_t bits = e > f ? (0xffffffffu >> (32 - (e - f))) << f : 0u;
-            if (!(okm >> (2 * q) & 1)) bits &= 0xffff0000u;
-            if (!(okm >> (2 * q + 1) & 1)) bits &= 0x0000ffffu;
+          for (int g = 0; g < 8; ++g) {
+            tmem_ld_wait(u[g & 1]);
+            if (g < 7) tmem_ld32x32b_x16(s_tm + (g + 1) * 16, u[(g + 1) & 1]);
+            if constexpr (decltype(masked)::value) {
+              const int b = key + 16 * g;
+              const int f = min(max(lo - b, 0), 16), e = min(max(hi - b, 0), 16);
+              uint32_t bits = (okm >> g & 1) && e > f ? (0xffffu >> (16 - (e - f))) << f : 0u;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) u[q][i] = (bits >> i & 1) ? u[q][i] : 0xff800000u;
+              for (int i = 0; i < 16; ++i) u[g & 1][i] = (bits >> i & 1) ? u[g & 1][i] : 0xff800000u;
+            }
+            body(g, u[g & 1]);
           }
-        }
+        };
         // the row's maximum: of each group, then scaled
         float mx = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          const uint32_t* e = &u[g / 2][(g & 1) * 16];
+        auto largest = [&](int g, const uint32_t (&e)[16]) {
           float m0 = fmax3(__uint_as_float(e[0]), __uint_as_float(e[1]), __uint_as_float(e[2]));
           float m1 = fmax3(__uint_as_float(e[3]), __uint_as_float(e[4]), __uint_as_float(e[5]));
           m0 = fmax3(m0, __uint_as_float(e[6]), __uint_as_float(e[7]));
@@ -702,14 +721,16 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
           m0 = fmax3(m0, __uint_as_float(e[10]), __uint_as_float(e[11]));
           m1 = fmax3(m1, __uint_as_float(e[12]), __uint_as_float(e[13]));
           m0 = fmax3(m0, __uint_as_float(e[14]), __uint_as_float(e[15]));
-          m0 = fmaxf(m0, m1);
           if constexpr (kCodes) {
             const float4 sc = x->scale[k & 7][g];
-            mx = fmaxf(mx, fmaf(m0, fac * sc.x, sc.y));
+            mx = fmaxf(mx, fmaf(fmaxf(m0, m1), fac * sc.x, sc.y));
           } else {
-            mx = fmaxf(mx, m0);
+            mx = fmax3(mx, m0, m1);
           }
-        }
+        };
+        const bool whole = key >= all.x && key + kHalf <= all.y && okm == 0xff;
+        if (whole) pass(std::false_type{}, largest);
+        else pass(std::true_type{}, largest);
         if (!kCodes) mx *= fac;
         const float mn = fmaxf(m, mx);
         const bool grow = mn > m + kLazy || (m == -INFINITY && mn > m);
@@ -718,32 +739,31 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
         if (grow) m = mn;
         const float base = kShift - (m == -INFINITY ? 0.f : m);
         float add = 0.f;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            float A = fac, B = base, inv = 1.f;
-            if constexpr (kCodes) {
-              const float4 sc = x->scale[k & 7][2 * q + g];
-              A = fac * sc.x;
-              B = base + sc.y;
-              inv = sc.z;
-            }
-            float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 y = fma_f32x2(make_float2(__uint_as_float(u[q][g * 16 + 2 * i]),
-                                                     __uint_as_float(u[q][g * 16 + 2 * i + 1])),
-                                         make_float2(A, A), make_float2(B, B));
-              const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-              sum = add_f32x2(sum, p);
-              pk[g * 8 + i] = kBf ? pack_bf16x2(p.x, p.y) : pack_f16x2(p.x, p.y);
-            }
-            add = fmaf(sum.x + sum.y, inv, add);
+        // P over the columns of scores that have been read
+        uint32_t pk[16];
+        auto exps = [&](int g, const uint32_t (&u)[16]) {
+          float A = fac, B = base, inv = 1.f;
+          if constexpr (kCodes) {
+            const float4 sc = x->scale[k & 7][g];
+            A = fac * sc.x;
+            B = base + sc.y;
+            inv = sc.z;
           }
-          tmem_st32x32b_x16(s_tm + q * 16, pk);
-        }
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 y =
+                fma_f32x2(make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])),
+                          make_float2(A, A), make_float2(B, B));
+            const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            sum = add_f32x2(sum, p);
+            pk[(g & 1) * 8 + i] = kBf ? pack_bf16x2(p.x, p.y) : pack_f16x2(p.x, p.y);
+          }
+          add = fmaf(sum.x + sum.y, inv, add);
+          if (g & 1) tmem_st32x32b_x16(s_tm + (g >> 1) * 16, pk);
+        };
+        if (whole) pass(std::false_type{}, exps);
+        else pass(std::true_type{}, exps);
         l = fmaf(l, f, add);
         // S_X(j) was issued after P_X(j-1) V, which is therefore complete
         if (__any_sync(0xffffffffu, again)) {
@@ -779,10 +799,14 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
         lt = l * keep + ex2_approx(s2 - mu + kShift);
       }
       const float inv = complete ? (lt == 0.f ? 0.f : keep / lt) : 1.f;
+      // partial states lie [slot][16-byte column][row], so that a warp's
+      // stores (a row a lane) are contiguous
       const int64_t prow = static_cast<int64_t>(slot) * kChunkRows + h * kHalf + r;
+      float4* const pbase = reinterpret_cast<float4*>(a.part) +
+                            static_cast<int64_t>(slot) * (DV / 4) * kChunkRows + h * kHalf + r;
       const bool bad = w.n > 0 && x->bad[it & 3] == it + 1;
       uint16_t* op = a.o + (static_cast<int64_t>(w.v.q.row0 + tok) * a.Hq + head) * DV;
-#pragma unroll
+#pragma unroll 1
       for (int q = 0; q < DV / 32; ++q) {
         uint32_t o[32];
         if (w.n > 0) {
@@ -815,16 +839,24 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
           }
         }
         if (real && complete) {
+          uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(op + q * 32 + i) =
-                make_uint4(pack2(v[i], v[i + 1], a.f16), pack2(v[i + 2], v[i + 3], a.f16),
-                           pack2(v[i + 4], v[i + 5], a.f16), pack2(v[i + 6], v[i + 7], a.f16));
+          for (int i = 0; i < 16; ++i) pk[i] = pack2(v[2 * i], v[2 * i + 1], a.f16);
+          if (a.o_st32) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 8)
+              st_global_v8(op + q * 32 + 2 * i, pk[i], pk[i + 1], pk[i + 2], pk[i + 3], pk[i + 4],
+                           pk[i + 5], pk[i + 6], pk[i + 7]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<uint4*>(op + q * 32 + 2 * i) =
+                  make_uint4(pk[i], pk[i + 1], pk[i + 2], pk[i + 3]);
+          }
         } else if (real) {
-          float* pp = a.part + prow * DV + q * 32;
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(pp + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            pbase[(q * 8 + i / 4) * kChunkRows] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
       }
       if (w.n > 0) {
@@ -854,60 +886,75 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
   }
 }
 
-// Joins the pieces of split blocks of rows: block (i, y) 32 of the rows whose
-// first piece is block i's, one warp a row at a time.
+// Joins the pieces of split blocks of rows: block (i, y) rows 32 y .. 32 y + 31
+// of the block of rows whose first piece is block i's.  A lane reads a row's
+// 16-byte columns (a warp's reads are contiguous), its eight warps share the
+// columns; O goes through shared memory so that its rows are written whole.
 template <int DV>
 __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__ Args a,
                                                          float shift) {
+  __shared__ uint2 s_o[32][DV / 4 + 1];
   grid_dep_wait();
   const int4 d = a.split_desc[blockIdx.x];
   if (d.x == 0) return;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, wp = threadIdx.x / 32;
   const Seq q = load_seq(a, d.y);
-  const int rows = q.n * a.group;
-  constexpr int kV = DV / 32;
-  for (int i = threadIdx.x / 32; i < 32; i += 8) {
-    const int col = blockIdx.y * 32 + i, r = d.w * kChunkRows + col;
-    if (r >= rows) break;
-    float acc[kV], m = -INFINITY, l = 0.f;
+  const int rows = q.n * a.group, r0 = d.w * kChunkRows + blockIdx.y * 32;
+  if (r0 >= rows) return;
+  constexpr int kC = DV / 4 / 8;  // 16-byte columns per warp
+  const int col = blockIdx.y * 32 + lane, r = r0 + lane;
+  const int rc = min(r, rows - 1), tok = div_group(a, rc);
+  const int head = d.z * a.group + rc - tok * a.group;
+  float4 acc[kC];
+  float m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int j = 0; j < kV; ++j) acc[j] = 0.f;
+  for (int j = 0; j < kC; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (r < rows) {
 #pragma unroll 2
     for (int p = 0; p < d.x; ++p) {
-      const int64_t row =
-          (2 * (static_cast<int64_t>(blockIdx.x) + p) + (p == 0 ? 1 : 0)) * kChunkRows + col;
-      const float2 ml = a.part_ml[row];
-      const float* pp = a.part + row * DV + lane * kV;
-      float v[kV];
+      const int64_t slot = 2 * (static_cast<int64_t>(blockIdx.x) + p) + (p == 0 ? 1 : 0);
+      const float2 ml = a.part_ml[slot * kChunkRows + col];
+      const float4* pp = reinterpret_cast<const float4*>(a.part) + slot * (DV / 4) * kChunkRows +
+                         wp * kC * kChunkRows + col;
+      float4 v[kC];
 #pragma unroll
-      for (int j = 0; j < kV; ++j) v[j] = pp[j];
+      for (int j = 0; j < kC; ++j) v[j] = pp[j * kChunkRows];
       const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
       const float f0 = ex2_approx(m - mu), f1 = ex2_approx(ml.x - mu);
 #pragma unroll
-      for (int j = 0; j < kV; ++j) acc[j] = acc[j] * f0 + v[j] * f1;
+      for (int j = 0; j < kC; ++j)
+        acc[j] = make_float4(acc[j].x * f0 + v[j].x * f1, acc[j].y * f0 + v[j].y * f1,
+                             acc[j].z * f0 + v[j].z * f1, acc[j].w * f0 + v[j].w * f1);
       l = l * f0 + ml.y * f1;
       m = mn;
     }
-    const int tok = r / a.group, head = d.z * a.group + r % a.group;
-    const bool none = m == -INFINITY;
-    float mt = m, lt = l, keep = 1.f;
-    if (a.sink) {
-      const float s2 = a.sink[head] * kLog2e;
-      mt = fmaxf(m, s2);
-      const float mu = mt == -INFINITY ? 0.f : mt;
-      keep = ex2_approx(m - mu);
-      lt = l * keep + ex2_approx(s2 - mu + shift);
-    }
-    const float inv = lt == 0.f ? 0.f : keep / lt;
-    uint16_t* op = a.o + (static_cast<int64_t>(q.row0 + tok) * a.Hq + head) * DV + lane * kV;
-    if constexpr (kV == 4)
-      *reinterpret_cast<uint2*>(op) = make_uint2(pack2(acc[0] * inv, acc[1] * inv, a.f16),
-                                                 pack2(acc[2] * inv, acc[3] * inv, a.f16));
-    else
-      *reinterpret_cast<uint32_t*>(op) = pack2(acc[0] * inv, acc[1] * inv, a.f16);
-    if (a.lse && lane == 0)
-      a.lse[static_cast<int64_t>(head) * a.num_tokens + q.row0 + tok] =
-          none ? (a.sink ? a.sink[head] : -INFINITY) : (mt - shift) * kLn2 + logf(lt);
+  }
+  const bool none = m == -INFINITY;
+  float mt = m, lt = l, keep = 1.f;
+  if (a.sink) {
+    const float s2 = a.sink[head] * kLog2e;
+    mt = fmaxf(m, s2);
+    const float mu = mt == -INFINITY ? 0.f : mt;
+    keep = ex2_approx(m - mu);
+    lt = l * keep + ex2_approx(s2 - mu + shift);
+  }
+  const float inv = lt == 0.f ? 0.f : keep / lt;
+#pragma unroll
+  for (int j = 0; j < kC; ++j)
+    s_o[lane][wp * kC + j] = make_uint2(pack2(acc[j].x * inv, acc[j].y * inv, a.f16),
+                                        pack2(acc[j].z * inv, acc[j].w * inv, a.f16));
+  if (a.lse && wp == 0 && r < rows)
+    a.lse[static_cast<int64_t>(head) * a.num_tokens + q.row0 + tok] =
+        none ? (a.sink ? a.sink[head] : -INFINITY) : (mt - shift) * kLn2 + logf(lt);
+  __syncthreads();
+  constexpr int kPer = 128 / DV;  // rows a warp writes at once
+  for (int i = wp * kPer + lane / (DV / 4); i < 32; i += 8 * kPer) {
+    const int rr = r0 + i;
+    if (rr >= rows) break;
+    const int tk = div_group(a, rr);
+    uint16_t* op = a.o + (static_cast<int64_t>(q.row0 + tk) * a.Hq + d.z * a.group + rr -
+                          tk * a.group) * DV;
+    reinterpret_cast<uint2*>(op)[lane % (DV / 4)] = s_o[i][lane % (DV / 4)];
   }
 }
 
