@@ -590,41 +590,46 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
           return (okm >> (r >> 4) & 1) && key + r >= w.any.x && key + r < w.any.y;
         };
         if constexpr (kCodes) {
-          // D / 16 units of 16 codes a row, in the order of memory
+          // D / 16 units of 16 codes a row, in the order of memory, four a
+          // round.  (The stage's last reader is waited for first: the codes
+          // are turned as they are read.)
           constexpr int kU = D / 16;
-          const uint32_t src = smem_u32(sm) + L::code(e) + ct * 16;
-          uint4 v[kU];
-#pragma unroll
-          for (int i = 0; i < kU; ++i) v[i] = lds128(src + i * 2048);
-          mbar_arrive(&x->raw_empty[e % kDepth]);
-          if (value && !whole) {
-            uint32_t bad = 0;
-#pragma unroll
-            for (int i = 0; i < kU; ++i) {
-              if (!in((ct + 128 * i) / kU)) v[i] = make_uint4(0, 0, 0, 0);
-              bad |= not_finite<KIND>(v[i].x) | not_finite<KIND>(v[i].y) |
-                     not_finite<KIND>(v[i].z) | not_finite<KIND>(v[i].w);
-            }
-            if (bad) {
-              x->bad[it & 3] = it + 1;
-#pragma unroll
-              for (int i = 0; i < kU; ++i)
-                v[i] = make_uint4(finite_only<KIND>(v[i].x), finite_only<KIND>(v[i].y),
-                                  finite_only<KIND>(v[i].z), finite_only<KIND>(v[i].w));
-            }
-          }
           if (e >= NKV && !mbar_wait_warp(&x->kv_empty[e % NKV], ((e / NKV) - 1) & 1)) return false;
+          const uint32_t src = smem_u32(sm) + L::code(e) + ct * 16;
           const uint32_t dst = smem_u32(sm) + L::kv(e);
+#pragma unroll 1
+          for (int i0 = 0; i0 < kU; i0 += 4) {
+            uint4 v[4];
 #pragma unroll
-          for (int i = 0; i < kU; ++i) {
-            const int q = ct + 128 * i, r = q / kU, u = q % kU;
-            // lanes with u >= 4 (the second 64 dims) store their second half
-            // first: eight lanes then meet eight bank groups
-            const uint32_t row = dst + (u >> 2) * 16384 + r * 128;
-            const int f = (u >> 2) & 1, u0 = 2 * (u & 3) + f, u1 = u0 ^ 1;
-            store_codes(row + ((u0 ^ (r & 7)) << 4), f ? v[i].z : v[i].x, f ? v[i].w : v[i].y);
-            store_codes(row + ((u1 ^ (r & 7)) << 4), f ? v[i].x : v[i].z, f ? v[i].y : v[i].w);
+            for (int i = 0; i < 4; ++i) v[i] = lds128(src + (i0 + i) * 2048);
+            if (value && !whole) {
+              uint32_t bad = 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (!in((ct + 128 * (i0 + i)) / kU)) v[i] = make_uint4(0, 0, 0, 0);
+                bad |= not_finite<KIND>(v[i].x) | not_finite<KIND>(v[i].y) |
+                       not_finite<KIND>(v[i].z) | not_finite<KIND>(v[i].w);
+              }
+              if (bad) {
+                x->bad[it & 3] = it + 1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  v[i] = make_uint4(finite_only<KIND>(v[i].x), finite_only<KIND>(v[i].y),
+                                    finite_only<KIND>(v[i].z), finite_only<KIND>(v[i].w));
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int q = ct + 128 * (i0 + i), r = q / kU, u = q % kU;
+              // lanes with u >= 4 (the second 64 dims) store their second half
+              // first: eight lanes then meet eight bank groups
+              const uint32_t row = dst + (u >> 2) * 16384 + r * 128;
+              const int f = (u >> 2) & 1, u0 = 2 * (u & 3) + f, u1 = u0 ^ 1;
+              store_codes(row + ((u0 ^ (r & 7)) << 4), f ? v[i].z : v[i].x, f ? v[i].w : v[i].y);
+              store_codes(row + ((u1 ^ (r & 7)) << 4), f ? v[i].x : v[i].z, f ? v[i].y : v[i].w);
+            }
           }
+          mbar_arrive(&x->raw_empty[e % kDepth]);
         } else if (value && !whole) {
           const uint32_t at = smem_u32(sm) + L::kv(e);
           for (int i = 0; i < 8; ++i) {
@@ -652,8 +657,14 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
       };
       for (int j = 0; j < w.n && ok; ++j) {
         const int key = w.key + j * kHalf;
-        ok = convert(std::integral_constant<int, DQK>{}, false, key, st + j) &&
-             convert(std::integral_constant<int, DV>{}, true, key, st + j);
+        if constexpr (DQK == DV) {
+#pragma unroll 1
+          for (int m = 0; m < 2 && ok; ++m)
+            ok = convert(std::integral_constant<int, DV>{}, m == 1, key, st + j);
+        } else {
+          ok = convert(std::integral_constant<int, DQK>{}, false, key, st + j) &&
+               convert(std::integral_constant<int, DV>{}, true, key, st + j);
+        }
       }
       if (!ok) break;
       st += w.n;
@@ -694,26 +705,35 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
         // The row's scores are read twice, a group at a time and the next group
         // while this one is worked on: held whole they would cost 128
         // registers, and spills meet an L1 that shared memory has left small.
+        // Two groups an iteration and no further unrolled: the roles' loops
+        // share a scheduler's instruction cache.
         auto pass = [&](auto masked, auto&& body) {
-          uint32_t u[2][16];
-          tmem_ld32x32b_x16(s_tm, u[0]);
-#pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            tmem_ld_wait(u[g & 1]);
-            if (g < 7) tmem_ld32x32b_x16(s_tm + (g + 1) * 16, u[(g + 1) & 1]);
+          uint32_t u0[16], u1[16];
+          auto mask = [&](int g, uint32_t(&u)[16]) {
             if constexpr (decltype(masked)::value) {
               const int b = key + 16 * g;
               const int f = min(max(lo - b, 0), 16), e = min(max(hi - b, 0), 16);
-              uint32_t bits = (okm >> g & 1) && e > f ? (0xffffu >> (16 - (e - f))) << f : 0u;
+              const uint32_t bits = (okm >> g & 1) && e > f ? (0xffffu >> (16 - (e - f))) << f : 0u;
 #pragma unroll
-              for (int i = 0; i < 16; ++i) u[g & 1][i] = (bits >> i & 1) ? u[g & 1][i] : 0xff800000u;
+              for (int i = 0; i < 16; ++i) u[i] = (bits >> i & 1) ? u[i] : 0xff800000u;
             }
-            body(g, u[g & 1]);
+          };
+          tmem_ld32x32b_x16(s_tm, u0);
+#pragma unroll 1
+          for (int g = 0; g < 8; g += 2) {
+            tmem_ld_wait(u0);
+            tmem_ld32x32b_x16(s_tm + g * 16 + 16, u1);
+            mask(g, u0);
+            body(g, std::integral_constant<int, 0>{}, u0);
+            tmem_ld_wait(u1);
+            if (g < 6) tmem_ld32x32b_x16(s_tm + g * 16 + 32, u0);
+            mask(g + 1, u1);
+            body(g + 1, std::integral_constant<int, 1>{}, u1);
           }
         };
         // the row's maximum: of each group, then scaled
         float mx = -INFINITY;
-        auto largest = [&](int g, const uint32_t (&e)[16]) {
+        auto largest = [&](int g, auto, const uint32_t (&e)[16]) {
           float m0 = fmax3(__uint_as_float(e[0]), __uint_as_float(e[1]), __uint_as_float(e[2]));
           float m1 = fmax3(__uint_as_float(e[3]), __uint_as_float(e[4]), __uint_as_float(e[5]));
           m0 = fmax3(m0, __uint_as_float(e[6]), __uint_as_float(e[7]));
@@ -741,7 +761,8 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
         float add = 0.f;
         // P over the columns of scores that have been read
         uint32_t pk[16];
-        auto exps = [&](int g, const uint32_t (&u)[16]) {
+        auto exps = [&](int g, auto odd, const uint32_t (&u)[16]) {
+          constexpr int kOdd = decltype(odd)::value;
           float A = fac, B = base, inv = 1.f;
           if constexpr (kCodes) {
             const float4 sc = x->scale[k & 7][g];
@@ -757,10 +778,10 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
                           make_float2(A, A), make_float2(B, B));
             const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
             sum = add_f32x2(sum, p);
-            pk[(g & 1) * 8 + i] = kBf ? pack_bf16x2(p.x, p.y) : pack_f16x2(p.x, p.y);
+            pk[kOdd * 8 + i] = kBf ? pack_bf16x2(p.x, p.y) : pack_f16x2(p.x, p.y);
           }
           add = fmaf(sum.x + sum.y, inv, add);
-          if (g & 1) tmem_st32x32b_x16(s_tm + (g >> 1) * 16, pk);
+          if constexpr (kOdd) tmem_st32x32b_x16(s_tm + (g >> 1) * 16, pk);
         };
         if (whole) pass(std::false_type{}, exps);
         else pass(std::true_type{}, exps);
