@@ -73,19 +73,32 @@ struct ChunkCfg {
   }
 };
 
+// A piece of a block of rows, as the scheduler warp hands it to the others.
+struct Piece {
+  int n, key;        // key tiles (0: no row keeps a key, < 0: the end), first key
+  int seq, head, rb; // sequence, KV head, block of rows
+  int first, whole;  // begins with the block's first tile; holds all its tiles
+  int pieces;        // of a split block, in its first piece: how many there are
+  int row0, new_rows, pos0, hi;  // of the sequence: first row, tokens, first position, keys
+  int2 any, all;     // keys some row, and every row, of the block keeps
+  int2 half[2];      // keys every row of a half keeps
+};
+
 struct ChunkAux {
   uint64_t q_full[2], q_empty[2], kv_full[3], kv_empty[3];
   uint64_t raw_full[4], raw_empty[4];  // TMA: of the code ring, or of the K / V ring
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t piece_full[4], piece_empty[4];
   uint64_t drain;
   uint32_t tmem;
   int abort;
   uint32_t bad[4];  // by piece: its number + 1 once a value was taken out of the product
   int ok_mask[8];  // by tile (the producer runs up to four tiles ahead of the softmax): 16-key groups whose page exists
   int64_t part[16];
-  int64_t begin, total;  // the block's first tile, all tiles
-  int ctas, tile0;
+  int64_t begin, total;  // the block's first unit, all units
+  int ctas, unit0;
   int seq, head, rb;
+  Piece piece[4];
   float4 scale[8][8];     // by tile and group: K scale, log2 V scale, 1 / V scale
   uint8_t q_exp[4][kChunkRows];  // by piece: biased exponent of the row's power of two
 };
@@ -132,49 +145,58 @@ __device__ __forceinline__ int2 keys_all(const Args& a, const SeqView& v, int r0
   return make_int2(a.window >= 0 ? max(0, pos0 + hi - a.window) : 0,
                    a.causal ? min(v.hi, pos0 + lo + 1) : v.hi);
 }
+// A block of rows costs its tiles and about as much as this many more: queries
+// to load, a pipeline to fill, O to write.  Shares are cut by that sum.
+constexpr int kStart = 3;
 // Tiles start at multiples of 128 keys, so that a tile is a whole number of
 // pages or inside one.
 __device__ __forceinline__ int tiles_of(const Args& a, const SeqView& v, int rb) {
   const int2 k = keys_any(a, v, rb * kChunkRows, (rb + 1) * kChunkRows);
   return max(1, (k.y - (k.x & ~(kHalf - 1)) + kHalf - 1) / kHalf);
 }
-__device__ __forceinline__ int64_t seq_tiles(const Args& a, const SeqView& v) {
+__device__ __forceinline__ int64_t seq_units(const Args& a, const SeqView& v) {
   int64_t n = 0;
   const int nrb = blocks_of(a, v);
-  for (int rb = 0; rb < nrb; ++rb) n += tiles_of(a, v, rb);
+  for (int rb = 0; rb < nrb; ++rb) n += kStart + tiles_of(a, v, rb);
   return n;
 }
 
-// Walks the block's pieces; every warp of every role walks the same way.
+// Walks the block's pieces (the scheduler warp does).  Units
+// [0, kStart) of a block of rows are its start, the others its tiles.
 struct Walk {
-  int done, share;  // tiles behind the current piece's first, and in all
-  int seq, head, rb, t0;
+  int done, share;  // units behind the current piece's first, and in all
+  int seq, head, rb, u0;
   SeqView v;
-  // the current piece
-  int t1, nt;
+  // the current piece: tiles [t0, t1) of nt
+  int u1, t0, t1, nt;
   int2 any;    // keys some row of the block of rows keeps
   int n, key;  // key tiles (0: no row keeps a key), first key of the first
 };
-__device__ __forceinline__ void walk_piece(const Args& a, Walk& w) {
+__device__ __forceinline__ bool walk_piece(const Args& a, Walk& w) {
   w.nt = tiles_of(a, w.v, w.rb);
-  w.t1 = min(w.nt, w.t0 + (w.share - w.done));
+  w.u1 = min(w.nt + kStart, w.u0 + (w.share - w.done));
+  w.t0 = max(0, w.u0 - kStart);
+  w.t1 = max(0, w.u1 - kStart);
   w.any = keys_any(a, w.v, w.rb * kChunkRows, (w.rb + 1) * kChunkRows);
   w.key = (w.any.x & ~(kHalf - 1)) + w.t0 * kHalf;
   w.n = w.any.y > w.any.x ? w.t1 - w.t0 : 0;
+  return w.t1 > w.t0;
 }
+// The next piece with tiles.
 __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
-  w.done += w.t1 - w.t0;
-  if (w.done >= w.share) return false;
-  w.t0 = 0;
-  if (++w.rb >= blocks_of(a, w.v)) {
-    w.rb = 0;
-    if (++w.head >= a.Hkv) {
-      w.head = 0;
-      do w.v = view_of(a, ++w.seq);
-      while (w.v.q.n == 0);
+  do {
+    w.done += w.u1 - w.u0;
+    if (w.done >= w.share) return false;
+    w.u0 = 0;
+    if (++w.rb >= blocks_of(a, w.v)) {
+      w.rb = 0;
+      if (++w.head >= a.Hkv) {
+        w.head = 0;
+        do w.v = view_of(a, ++w.seq);
+        while (w.v.q.n == 0);
+      }
     }
-  }
-  walk_piece(a, w);
+  } while (!walk_piece(a, w));
   return true;
 }
 
@@ -184,7 +206,7 @@ __device__ __forceinline__ void walk_init(const Args& a, ChunkAux* x, Walk& w) {
   const int per = (a.num_seqs + kN - 1) / kN;
   const int first = threadIdx.x * per, last = min(a.num_seqs, first + per);
   int64_t mine = 0;
-  for (int s = first; s < last; ++s) mine += a.Hkv * seq_tiles(a, view_of(a, s));
+  for (int s = first; s < last; ++s) mine += a.Hkv * seq_units(a, view_of(a, s));
   int64_t sum = mine;
 #pragma unroll
   for (int i = 1; i < 32; i <<= 1) {
@@ -208,7 +230,7 @@ __device__ __forceinline__ void walk_init(const Args& a, ChunkAux* x, Walk& w) {
       int s = first;
       for (;; ++s) {
         const SeqView v = view_of(a, s);
-        const int64_t per_head = seq_tiles(a, v);
+        const int64_t per_head = seq_units(a, v);
         if (off >= a.Hkv * per_head) {
           off -= a.Hkv * per_head;
           continue;
@@ -217,9 +239,9 @@ __device__ __forceinline__ void walk_init(const Args& a, ChunkAux* x, Walk& w) {
         x->head = static_cast<int>(off / per_head);
         off %= per_head;
         int rb = 0;
-        for (int n; off >= (n = tiles_of(a, v, rb)); ++rb) off -= n;
+        for (int n; off >= (n = kStart + tiles_of(a, v, rb)); ++rb) off -= n;
         x->rb = rb;
-        x->tile0 = static_cast<int>(off);
+        x->unit0 = static_cast<int>(off);
         x->begin = begin;
         x->total = total;
         x->ctas = ctas;
@@ -232,9 +254,10 @@ __device__ __forceinline__ void walk_init(const Args& a, ChunkAux* x, Walk& w) {
     w.seq = x->seq;
     w.head = x->head;
     w.rb = x->rb;
-    w.t0 = x->tile0;
+    w.u0 = x->unit0;
     w.v = view_of(a, w.seq);
-    walk_piece(a, w);
+    // a share that ends inside its only start has no piece
+    if (!walk_piece(a, w) && !walk_next(a, w)) w.share = 0;
   }
 }
 
@@ -299,6 +322,10 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
       mbar_init(&x->raw_full[s], 1);
       mbar_init(&x->raw_empty[s], 128);
     }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&x->piece_full[s], 1);
+      mbar_init(&x->piece_empty[s], 1 + 1 + 4 + 8);  // MMA, producer, converter, softmax warps
+    }
     mbar_init(&x->drain, 1);
     x->abort = 0;
     for (uint32_t& b : x->bad) b = 0;
@@ -316,8 +343,59 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
   grid_dep_launch();
   const uint32_t tmem = x->tmem;
 
+  // The i-th piece (in shared memory), and this warp's release of it.
+  auto take = [&](uint32_t i, bool* ok) -> const Piece* {
+    *ok = mbar_wait_warp(&x->piece_full[i & 3], (i >> 2) & 1);
+    return &x->piece[i & 3];
+  };
+  auto release = [&](uint32_t i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&x->piece_empty[i & 3]);
+  };
+
   if (warp < 4) {
-    if (warp == 0 && w.share > 0) {
+    if (warp == 2) {
+      // ------------------------------------------------------------ scheduler
+      // Keeps the walk's state and divisions out of the other roles' registers
+      // and code.
+      bool ok = true, live = w.share > 0;
+      for (uint32_t i = 0; ok; ++i) {
+        if (i >= 4 && !(ok = mbar_wait_warp(&x->piece_empty[i & 3], ((i >> 2) - 1) & 1))) break;
+        if (lane == 0) {
+          Piece& p = x->piece[i & 3];
+          if (live) {
+            const int r0 = w.rb * kChunkRows, rows = rows_of(a, w.v);
+            p.n = w.n;
+            p.key = w.key;
+            p.seq = w.seq;
+            p.head = w.head;
+            p.rb = w.rb;
+            p.first = w.t0 == 0;
+            p.whole = w.t0 == 0 && w.t1 == w.nt;
+            const int64_t end = x->begin + w.done + (w.nt + kStart - w.u0);  // of the block's units
+            p.pieces = static_cast<int>((end * x->ctas + x->total - 1) / x->total) -
+                       static_cast<int>(blockIdx.x);
+            p.row0 = w.v.q.row0;
+            p.new_rows = w.v.q.n;
+            p.pos0 = w.v.q.len - w.v.q.n;
+            p.hi = w.v.hi;
+            p.any = w.any;
+            p.all = keys_all(a, w.v, r0, r0 + kChunkRows);
+            for (int h = 0; h < 2; ++h)  // a half without rows masks everything
+              p.half[h] = r0 + h * kHalf < rows
+                              ? keys_all(a, w.v, r0 + h * kHalf, r0 + (h + 1) * kHalf)
+                              : make_int2(INT_MAX, INT_MIN);
+          } else {
+            p.n = -1;
+          }
+          mbar_arrive(&x->piece_full[i & 3]);
+        }
+        if (__any_sync(0xffffffffu, !live || *abort != 0)) break;
+        live = walk_next(a, w);
+      }
+      if (!ok && lane == 0) timeout();
+    }
+    if (warp == 0) {
       // ------------------------------------------------------------ MMA issuer
       constexpr uint32_t id_s = idesc_f32acc(kBf ? 1 : 0, kHalf, kHalf, false, false);
       constexpr uint32_t id_o = idesc_f32acc(kBf ? 1 : 0, kHalf, DV, false, true);
@@ -332,33 +410,38 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
                                                    id_s, 0u);
         mma_commit_warp(&x->s_full[h]);
       };
-      uint32_t it = 0, kvc = 0, st = 0;
-      bool ok = true, live = true;
-      while (live && w.n == 0) live = walk_next(a, w);
-      if (live) {
+      uint32_t it = 0, kvc = 0, st = 0, pi = 0;
+      bool ok = true;
+      // tiles of the next piece that has some, or -1 behind the last
+      auto next = [&]() -> int {
+        for (;;) {
+          const Piece* p = take(pi, &ok);
+          const int n = ok ? p->n : -1;
+          release(pi++);
+          if (n != 0) return n;
+        }
+      };
+      int n = next();
+      if (ok && n > 0) {
         if ((ok = mbar_wait_warp(&x->q_full[0], 0) && mbar_wait_warp(&x->kv_full[0], 0))) {
           tc_fence_after();
           issue_s(0, 0, 0);
           issue_s(1, 0, 0);
           mma_commit_warp(&x->kv_empty[0]);
-          if (w.n == 1) mma_commit_warp(&x->q_empty[0]);
+          if (n == 1) mma_commit_warp(&x->q_empty[0]);
           kvc = 1;
         }
       }
       // Each step: P_X V, then over P_X's columns the S that comes next, of
       // this piece or the next one.  The pipe runs in order of issue.
-      while (ok && live) {
-        const int n = w.n;
-        Walk nx = w;
+      while (ok && n > 0) {
+        int nx = -1;
         for (int j = 0; j < n && ok; ++j) {
           const uint32_t k = st + j, vc = kvc;
           const bool more = j + 1 < n;
-          bool go_on = more;
-          if (!more) {
-            do live = walk_next(a, nx);
-            while (live && nx.n == 0);
-            go_on = live;
-          }
+          if (!more) nx = next();
+          if (!ok) break;
+          const bool go_on = more || nx > 0;
           const uint32_t pc = more ? it : it + 1;
           if (!(ok = mbar_wait_warp(&x->kv_full[vc % NKV], (vc / NKV) & 1))) break;
           for (int h = 0; h < 2 && ok; ++h) {
@@ -382,20 +465,20 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
           if (go_on) {
             mma_commit_warp(&x->kv_empty[(vc + 1) % NKV]);
             // the last S of a piece: its Q may be replaced
-            if (more ? j + 2 == n : nx.n == 1) mma_commit_warp(&x->q_empty[pc % NQ]);
+            if (more ? j + 2 == n : nx == 1) mma_commit_warp(&x->q_empty[pc % NQ]);
           }
           kvc += go_on ? 2 : 1;
         }
         if (!ok) break;
         st += n;
         ++it;
-        w = nx;
+        n = nx;
       }
       if (!ok && lane == 0) timeout();
       mma_commit_warp(&x->drain);
       mbar_wait(&x->drain, 0, 200000000ull);
     }
-    if (warp == 1 && w.share > 0) {
+    if (warp == 1) {
       // ------------------------------------------------------------ TMA producer
       // Lane i looks after box i of a tile: a page, or 128 tokens of one.  The
       // table is read two tiles ahead and the scales one, so that no load of a
@@ -403,37 +486,37 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
       const int rows_log = min(a.page_shift, 7), boxes = kHalf >> rows_log;
       const int page_mask = (1 << a.page_shift) - 1;
       uint32_t st = 0, e = 0;  // tiles and ring entries so far
-      bool ok = true, live = true;
-      while (live && ok) {
-        if (w.n == 0) {
-          live = walk_next(a, w);
-          continue;
-        }
-        const int hk = w.head;
-        auto key_of = [&](int j) -> int { return w.key + j * kHalf + (lane << rows_log); };
+      bool ok = true;
+      for (uint32_t pi = 0;; ++pi) {
+        const Piece* const p = take(pi, &ok);
+        if (!ok || p->n < 0) break;
+        const int n = p->n, hk = p->head, key0 = p->key, last = p->any.y;
+        const int32_t* const table = a.table + p->seq * a.table_stride;
+        release(pi);
+        auto key_of = [&](int j) -> int { return key0 + j * kHalf + (lane << rows_log); };
         auto load_entry = [&](int j) -> int {
-          if (j >= w.n || lane >= boxes || key_of(j) >= w.any.y) return INT_MIN;
+          if (j >= n || lane >= boxes || key_of(j) >= last) return INT_MIN;
           const int col = key_of(j) >> a.page_shift;
-          return col < a.max_pages ? a.table[w.seq * a.table_stride + col] : -1;
+          return col < a.max_pages ? table[col] : -1;
         };
         struct Ids {
           int id;
           float ks, vs;
         };
-        auto load_ids = [&](int p) -> Ids {
-          Ids r = {p, 1.f, 1.f};
-          if (p < 0 || p >= a.num_pages) {
-            if (p != INT_MIN) flag_bounds(a);
+        auto load_ids = [&](int id) -> Ids {
+          Ids r = {id, 1.f, 1.f};
+          if (id < 0 || id >= a.num_pages) {
+            if (id != INT_MIN) flag_bounds(a);
             r.id = -1;
           } else if (kCodes) {
-            r.ks = a.k_scale[static_cast<int64_t>(p) * a.Hkv + hk];
-            r.vs = a.v_scale[static_cast<int64_t>(p) * a.Hkv + hk];
+            r.ks = a.k_scale[static_cast<int64_t>(id) * a.Hkv + hk];
+            r.vs = a.v_scale[static_cast<int64_t>(id) * a.Hkv + hk];
           }
           return r;
         };
         int ahead = load_entry(1);
         Ids ids = load_ids(load_entry(0));
-        for (int j = 0; j < w.n && ok; ++j) {
+        for (int j = 0; j < n && ok; ++j) {
           const uint32_t k = st + j;
           const Ids nxt = load_ids(ahead);
           ahead = load_entry(j + 2);
@@ -483,12 +566,10 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
           }
           ids = nxt;
         }
-        st += w.n;
-        if (ok) live = walk_next(a, w);
+        if (!ok) break;
+        st += n;
       }
-      if (!ok) {
-        if (lane == 0) timeout();
-      }
+      if (!ok && lane == 0) timeout();
       // copies in flight land before the block may leave
       const uint32_t depth = kCodes ? L::kCodeStages : NKV;
       for (uint32_t i = e > depth ? e - depth : 0; i < e; ++i)
@@ -500,14 +581,15 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
     // for them): the codes come by TMA.
     const int ct = tid - 128;  // 0..127
     uint32_t it = 0, e = 0, st = 0;
-    bool ok = true, live = w.share > 0;
-    while (live && ok) {
-      if (w.n == 0) {
-        live = walk_next(a, w);
-        continue;
-      }
-      const int r0 = w.rb * kChunkRows;
-      const int2 all = keys_all(a, w.v, r0, r0 + kChunkRows);
+    bool ok = true;
+    for (uint32_t pi = 0;; ++pi) {
+      const Piece* const p = take(pi, &ok);
+      if (!ok || p->n < 0) break;
+      const int n = p->n, r0 = p->rb * kChunkRows, head = p->head, key0 = p->key;
+      const int row0 = p->row0, new_rows = p->new_rows;
+      const int2 any = p->any, all = p->all;
+      release(pi);
+      if (n == 0) continue;
       // ---- queries: one row a thread and half, to fp16 where the cache is E4M3
       if (it >= NQ && !mbar_wait_warp(&x->q_empty[it % NQ], ((it / NQ) - 1) & 1)) {
         ok = false;
@@ -523,17 +605,17 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
         const int sub = lane % kL, first = (warp - 4) * 32 + lane / kL;
         const uint32_t qs = smem_u32(sm) + (it % NQ) * 2 * L::kQTile;
         auto place = [&](int b, int u) -> uint32_t {
-          const int n = b * kPer, rr = first + n % 32, unit = sub + kL * u;
-          return qs + (n / 32) * L::kQTile + rr * 128 + (unit / 8) * 16384 +
+          const int nr = b * kPer, rr = first + nr % 32, unit = sub + kL * u;
+          return qs + (nr / 32) * L::kQTile + rr * 128 + (unit / 8) * 16384 +
                  (((unit & 7) ^ (rr & 7)) << 4);
         };
 #pragma unroll 4
         for (int b = 0; b < kSteps; ++b) {
-          const int n = b * kPer, r = r0 + (n / 32) * kHalf + first + n % 32;
+          const int nr = b * kPer, r = r0 + (nr / 32) * kHalf + first + nr % 32;
           const int tok = div_group(a, r);
-          const bool real = tok < w.v.q.n;
-          const uint16_t* qp = a.q + (real ? (w.v.q.row0 + tok) * a.q_stride +
-                                                 (w.head * a.group + r - tok * a.group) * DQK +
+          const bool real = tok < new_rows;
+          const uint16_t* qp = a.q + (real ? (row0 + tok) * a.q_stride +
+                                                 (head * a.group + r - tok * a.group) * DQK +
                                                  sub * 8
                                            : 0);
 #pragma unroll
@@ -561,9 +643,9 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
             int ex = static_cast<int>(max(mx & 0xffffu, mx >> 16) >> 7);
             ex = ex == 255 ? 127 + 14 : max(ex, 27);
             const float to = __uint_as_float(static_cast<uint32_t>(254 + 14 - ex) << 23);
-            const int n = b * kPer;
+            const int nr = b * kPer;
             if (sub == 0)
-              x->q_exp[it & 3][(n / 32) * kHalf + first + n % 32] = static_cast<uint8_t>(ex - 14);
+              x->q_exp[it & 3][(nr / 32) * kHalf + first + nr % 32] = static_cast<uint8_t>(ex - 14);
             auto turn = [&](uint32_t e) -> uint32_t {
               return pack_f16x2(__uint_as_float(e << 16) * to,
                                 __uint_as_float(e & 0xffff0000u) * to);
@@ -587,7 +669,7 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
         const bool whole = key >= all.x && key + kHalf <= all.y && x->ok_mask[k & 7] == 0xff;
         const int okm = x->ok_mask[k & 7];
         auto in = [&](int r) -> bool {
-          return (okm >> (r >> 4) & 1) && key + r >= w.any.x && key + r < w.any.y;
+          return (okm >> (r >> 4) & 1) && key + r >= any.x && key + r < any.y;
         };
         if constexpr (kCodes) {
           // D / 16 units of 16 codes a row, in the order of memory, four a
@@ -655,8 +737,8 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
         ++e;
         return true;
       };
-      for (int j = 0; j < w.n && ok; ++j) {
-        const int key = w.key + j * kHalf;
+      for (int j = 0; j < n && ok; ++j) {
+        const int key = key0 + j * kHalf;
         if constexpr (DQK == DV) {
 #pragma unroll 1
           for (int m = 0; m < 2 && ok; ++m)
@@ -667,9 +749,8 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
         }
       }
       if (!ok) break;
-      st += w.n;
+      st += n;
       ++it;
-      live = walk_next(a, w);
     }
     if (!ok && lane == 0) timeout();
   } else {
@@ -679,78 +760,83 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
     const uint32_t s_tm = tmem + lanes + kColS + h * kHalf;
     const uint32_t o_tm = tmem + lanes + kColO + h * kHalf;
     uint32_t st = 0, it = 0;
-    bool ok = true, live = w.share > 0;
-    while (live && ok && !__any_sync(0xffffffffu, *abort != 0)) {
-      const int rr = w.rb * kChunkRows + h * kHalf + r;
-      const int rows = rows_of(a, w.v);
-      const bool real = rr < rows;
-      const int tok = real ? div_group(a, rr) : 0;
-      const int head = w.head * a.group + (real ? rr - tok * a.group : 0);
-      const int pos = w.v.q.len - w.v.q.n + tok;
-      const int lo = a.window >= 0 ? max(0, pos - a.window) : 0;
-      const int hi = real ? (a.causal ? min(w.v.hi, pos + 1) : w.v.hi) : 0;
-      const int hr0 = w.rb * kChunkRows + h * kHalf;
-      // a half without rows masks everything
-      const int2 all =
-          hr0 < rows ? keys_all(a, w.v, hr0, hr0 + kHalf) : make_int2(INT_MAX, INT_MIN);
+    bool ok = true;
+    for (uint32_t pi = 0;; ++pi) {
+      const Piece* const p = take(pi, &ok);
+      if (!ok || p->n < 0 || __any_sync(0xffffffffu, *abort != 0)) break;
+      const int n = p->n, key0 = p->key;
+      const int2 all = p->half[h];
+      int lo, hi;  // keys the row keeps
+      {
+        const int rr = p->rb * kChunkRows + h * kHalf + r, tok = div_group(a, rr);
+        const int pos = p->pos0 + tok;
+        lo = a.window >= 0 ? max(0, pos - a.window) : 0;
+        hi = tok < p->new_rows ? (a.causal ? min(p->hi, pos + 1) : p->hi) : 0;
+      }
       float m = -INFINITY, l = 0.f, fac = a.scale * kLog2e;
-      for (int j = 0; j < w.n; ++j) {
+      for (int j = 0; j < n; ++j) {
         const uint32_t k = st + j;
-        const int key = w.key + j * kHalf;
+        const int key = key0 + j * kHalf;
         if (!(ok = mbar_wait_warp(&x->s_full[h], k & 1))) break;
         tc_fence_after();
         if (j == 0 && kCodes && !a.f16)
           fac *= __uint_as_float(static_cast<uint32_t>(x->q_exp[it & 3][h * kHalf + r]) << 23);
         const int okm = x->ok_mask[k & 7];
-        // The row's scores are read twice, a group at a time and the next group
-        // while this one is worked on: held whole they would cost 128
-        // registers, and spills meet an L1 that shared memory has left small.
-        // Two groups an iteration and no further unrolled: the roles' loops
-        // share a scheduler's instruction cache.
-        auto pass = [&](auto masked, auto&& body) {
-          uint32_t u0[16], u1[16];
-          auto mask = [&](int g, uint32_t(&u)[16]) {
-            if constexpr (decltype(masked)::value) {
-              const int b = key + 16 * g;
-              const int f = min(max(lo - b, 0), 16), e = min(max(hi - b, 0), 16);
-              const uint32_t bits = (okm >> g & 1) && e > f ? (0xffffu >> (16 - (e - f))) << f : 0u;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) u[i] = (bits >> i & 1) ? u[i] : 0xff800000u;
-            }
-          };
-          tmem_ld32x32b_x16(s_tm, u0);
+        // The row's scores are read twice, 32 at a time and the next 32 while
+        // these are worked on: held whole they would cost 128 registers, and
+        // spills meet an L1 that shared memory has left small.  (1024 tokens
+        // over 31744 cached ones, 64 query heads: 784 us; 16 at a time 818,
+        // 64 at a time without reading ahead 880, rolled loops 825-916.)
+        const bool whole = key >= all.x && key + kHalf <= all.y && okm == 0xff;
+        if (!whole) {
+          // masked scores to -inf where they lie, so that one copy of the
+          // passes serves every tile
 #pragma unroll 1
+          for (int g = 0; g < 8; ++g) {
+            uint32_t u[16];
+            tmem_ld32x32b_x16(s_tm + g * 16, u);
+            const int b = key + 16 * g;
+            const int f = min(max(lo - b, 0), 16), e = min(max(hi - b, 0), 16);
+            const uint32_t bits = (okm >> g & 1) && e > f ? (0xffffu >> (16 - (e - f))) << f : 0u;
+            tmem_ld_wait(u);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[i] = (bits >> i & 1) ? u[i] : 0xff800000u;
+            tmem_st32x32b_x16(s_tm + g * 16, u);
+          }
+          tmem_st_wait();
+        }
+        auto pass = [&](auto&& body) {
+          uint32_t u[2][32];
+          tmem_ld32x32b_x32(s_tm, u[0]);
+#pragma unroll
           for (int g = 0; g < 8; g += 2) {
-            tmem_ld_wait(u0);
-            tmem_ld32x32b_x16(s_tm + g * 16 + 16, u1);
-            mask(g, u0);
-            body(g, std::integral_constant<int, 0>{}, u0);
-            tmem_ld_wait(u1);
-            if (g < 6) tmem_ld32x32b_x16(s_tm + g * 16 + 32, u0);
-            mask(g + 1, u1);
-            body(g + 1, std::integral_constant<int, 1>{}, u1);
+            tmem_ld_wait(u[(g >> 1) & 1]);
+            if (g < 6) tmem_ld32x32b_x32(s_tm + g * 16 + 32, u[((g >> 1) + 1) & 1]);
+            body(g, u[(g >> 1) & 1]);
           }
         };
         // the row's maximum: of each group, then scaled
         float mx = -INFINITY;
-        auto largest = [&](int g, auto, const uint32_t (&e)[16]) {
-          float m0 = fmax3(__uint_as_float(e[0]), __uint_as_float(e[1]), __uint_as_float(e[2]));
-          float m1 = fmax3(__uint_as_float(e[3]), __uint_as_float(e[4]), __uint_as_float(e[5]));
-          m0 = fmax3(m0, __uint_as_float(e[6]), __uint_as_float(e[7]));
-          m1 = fmax3(m1, __uint_as_float(e[8]), __uint_as_float(e[9]));
-          m0 = fmax3(m0, __uint_as_float(e[10]), __uint_as_float(e[11]));
-          m1 = fmax3(m1, __uint_as_float(e[12]), __uint_as_float(e[13]));
-          m0 = fmax3(m0, __uint_as_float(e[14]), __uint_as_float(e[15]));
-          if constexpr (kCodes) {
-            const float4 sc = x->scale[k & 7][g];
-            mx = fmaxf(mx, fmaf(fmaxf(m0, m1), fac * sc.x, sc.y));
-          } else {
-            mx = fmax3(mx, m0, m1);
+        auto largest = [&](int g, const uint32_t (&u)[32]) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t* e = u + 16 * q;
+            float m0 = fmax3(__uint_as_float(e[0]), __uint_as_float(e[1]), __uint_as_float(e[2]));
+            float m1 = fmax3(__uint_as_float(e[3]), __uint_as_float(e[4]), __uint_as_float(e[5]));
+            m0 = fmax3(m0, __uint_as_float(e[6]), __uint_as_float(e[7]));
+            m1 = fmax3(m1, __uint_as_float(e[8]), __uint_as_float(e[9]));
+            m0 = fmax3(m0, __uint_as_float(e[10]), __uint_as_float(e[11]));
+            m1 = fmax3(m1, __uint_as_float(e[12]), __uint_as_float(e[13]));
+            m0 = fmax3(m0, __uint_as_float(e[14]), __uint_as_float(e[15]));
+            if constexpr (kCodes) {
+              const float4 sc = x->scale[k & 7][g + q];
+              mx = fmaxf(mx, fmaf(fmaxf(m0, m1), fac * sc.x, sc.y));
+            } else {
+              mx = fmax3(mx, m0, m1);
+            }
           }
         };
-        const bool whole = key >= all.x && key + kHalf <= all.y && okm == 0xff;
-        if (whole) pass(std::false_type{}, largest);
-        else pass(std::true_type{}, largest);
+        pass(largest);
         if (!kCodes) mx *= fac;
         const float mn = fmaxf(m, mx);
         const bool grow = mn > m + kLazy || (m == -INFINITY && mn > m);
@@ -760,31 +846,32 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
         const float base = kShift - (m == -INFINITY ? 0.f : m);
         float add = 0.f;
         // P over the columns of scores that have been read
-        uint32_t pk[16];
-        auto exps = [&](int g, auto odd, const uint32_t (&u)[16]) {
-          constexpr int kOdd = decltype(odd)::value;
-          float A = fac, B = base, inv = 1.f;
-          if constexpr (kCodes) {
-            const float4 sc = x->scale[k & 7][g];
-            A = fac * sc.x;
-            B = base + sc.y;
-            inv = sc.z;
-          }
-          float2 sum = make_float2(0.f, 0.f);
+        auto exps = [&](int g, const uint32_t (&u)[32]) {
+          uint32_t pk[16];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 y =
-                fma_f32x2(make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])),
-                          make_float2(A, A), make_float2(B, B));
-            const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-            sum = add_f32x2(sum, p);
-            pk[kOdd * 8 + i] = kBf ? pack_bf16x2(p.x, p.y) : pack_f16x2(p.x, p.y);
+          for (int q = 0; q < 2; ++q) {
+            float A = fac, B = base, inv = 1.f;
+            if constexpr (kCodes) {
+              const float4 sc = x->scale[k & 7][g + q];
+              A = fac * sc.x;
+              B = base + sc.y;
+              inv = sc.z;
+            }
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 y = fma_f32x2(make_float2(__uint_as_float(u[16 * q + 2 * i]),
+                                                     __uint_as_float(u[16 * q + 2 * i + 1])),
+                                         make_float2(A, A), make_float2(B, B));
+              const float2 p = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+              sum = add_f32x2(sum, p);
+              pk[8 * q + i] = kBf ? pack_bf16x2(p.x, p.y) : pack_f16x2(p.x, p.y);
+            }
+            add = fmaf(sum.x + sum.y, inv, add);
           }
-          add = fmaf(sum.x + sum.y, inv, add);
-          if constexpr (kOdd) tmem_st32x32b_x16(s_tm + (g >> 1) * 16, pk);
+          tmem_st32x32b_x16(s_tm + g * 8, pk);
         };
-        if (whole) pass(std::false_type{}, exps);
-        else pass(std::true_type{}, exps);
+        pass(exps);
         l = fmaf(l, f, add);
         // S_X(j) was issued after P_X(j-1) V, which is therefore complete
         if (__any_sync(0xffffffffu, again)) {
@@ -804,9 +891,12 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
       }
       if (!ok) break;
       // ---- epilogue: O or the piece's partial state
-      const bool complete = w.t0 == 0 && w.t1 == w.nt;
-      const int slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
-      if (w.n > 0) {
+      const int rr = p->rb * kChunkRows + h * kHalf + r, tk = div_group(a, rr);
+      const bool real = tk < p->new_rows;
+      const int tok = real ? tk : 0, head = p->head * a.group + (real ? rr - tk * a.group : 0);
+      const bool complete = p->whole;
+      const int slot = 2 * blockIdx.x + p->first;
+      if (n > 0) {
         if (!(ok = mbar_wait_warp(&x->o_full[h], it & 1))) break;
         tc_fence_after();
       }
@@ -825,29 +915,29 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
       const int64_t prow = static_cast<int64_t>(slot) * kChunkRows + h * kHalf + r;
       float4* const pbase = reinterpret_cast<float4*>(a.part) +
                             static_cast<int64_t>(slot) * (DV / 4) * kChunkRows + h * kHalf + r;
-      const bool bad = w.n > 0 && x->bad[it & 3] == it + 1;
-      uint16_t* op = a.o + (static_cast<int64_t>(w.v.q.row0 + tok) * a.Hq + head) * DV;
+      const bool bad = n > 0 && x->bad[it & 3] == it + 1;
+      uint16_t* op = a.o + (static_cast<int64_t>(p->row0 + tok) * a.Hq + head) * DV;
 #pragma unroll 1
       for (int q = 0; q < DV / 32; ++q) {
         uint32_t o[32];
-        if (w.n > 0) {
+        if (n > 0) {
           tmem_ld32x32b_x32(o_tm + q * 32, o);
           tmem_ld_wait(o);
         }
         float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          v[i] = w.n > 0 && !none ? __uint_as_float(o[i]) * inv : 0.f;
+          v[i] = n > 0 && !none ? __uint_as_float(o[i]) * inv : 0.f;
         if (bad && real) {
           // values that are not finite, in tiles the block of rows masks in part
-          const int2 blk = keys_all(a, w.v, w.rb * kChunkRows, (w.rb + 1) * kChunkRows);
-          for (int j = 0; j < w.n; ++j) {
-            const int key = w.key + j * kHalf;
+          const int2 blk = p->all;
+          for (int j = 0; j < n; ++j) {
+            const int key = key0 + j * kHalf;
             if (key >= blk.x && key + kHalf <= blk.y) continue;
             for (int kk = max(key, lo); kk < min(key + kHalf, hi); ++kk) {
-              const int page = page_of(a, w.seq, kk);
+              const int page = page_of(a, p->seq, kk);
               if (page < 0) continue;
-              const char* vp = a.vc + page * a.v_page + w.head * a.v_head +
+              const char* vp = a.vc + page * a.v_page + p->head * a.v_head +
                                static_cast<int64_t>(kk & ((1 << a.page_shift) - 1)) * a.v_tok;
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
@@ -880,22 +970,19 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
             pbase[(q * 8 + i / 4) * kChunkRows] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
       }
-      if (w.n > 0) {
+      if (n > 0) {
         tc_fence_before();
         mbar_arrive(&x->o_empty[h]);
       }
       if (real && complete && a.lse)
-        a.lse[static_cast<int64_t>(head) * a.num_tokens + w.v.q.row0 + tok] =
+        a.lse[static_cast<int64_t>(head) * a.num_tokens + p->row0 + tok] =
             none ? (a.sink ? a.sink[head] : -INFINITY) : (mt - kShift) * kLn2 + logf(lt);
       if (real && !complete) a.part_ml[prow] = make_float2(m, l);
-      if (!complete && w.t0 == 0 && h == 0 && r == 0) {
-        const int64_t end = x->begin + w.done + w.nt;  // of the row block's tiles
-        const int c1 = static_cast<int>((end * x->ctas + x->total - 1) / x->total) - 1;
-        a.split_desc[blockIdx.x] = make_int4(c1 - blockIdx.x + 1, w.seq, w.head, w.rb);
-      }
-      st += w.n;
-      if (w.n > 0) ++it;
-      live = walk_next(a, w);
+      if (!complete && p->first && h == 0 && r == 0)
+        a.split_desc[blockIdx.x] = make_int4(p->pieces, p->seq, p->head, p->rb);
+      release(pi);
+      st += n;
+      if (n > 0) ++it;
     }
     if (!ok && lane == 0) timeout();
   }
