@@ -85,8 +85,17 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool ok
                "r"(ok ? 8 : 0)
                : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+// Whole copies at constant offsets from a stage and a row.
+template <int DST, int SRC>
+__device__ __forceinline__ void cp_async16_at(uint32_t dst, const char* src) {
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(DST),
+               "n"(SRC)
+               : "memory");
+}
+template <int DST>
+__device__ __forceinline__ void cp_async8_at(uint32_t dst, const char* src) {
+  asm volatile("cp.async.ca.shared.global [%0 + %2], [%1], 8;" ::"r"(dst), "l"(src), "n"(DST)
+               : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -226,8 +235,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
   constexpr float kShift = kBf ? 0.f : 14.f;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
-  __shared__ float s_sc[kWarps][C::kStages][2];
-  __shared__ int s_ok[kWarps][C::kStages];
   const int tid = threadIdx.x, w = tid / 32, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const Share sh = find_share<C::kRows>(a);
   if (tid == 0 && a.split_desc) a.split_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -252,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
     const int hk = item / nd.nrb, rb = item % nd.nrb;
     const int rows = nd.q.n * a.group, r0 = rb * C::kRows;
     const int pos0 = nd.q.len - nd.q.n;  // position of the sequence's first new row
-    const int tok_lo = r0 / a.group, tok_hi = min(rows - 1, r0 + C::kRows - 1) / a.group;
+    const int tok_lo = div_group(a, r0), tok_hi = div_group(a, min(rows - 1, r0 + C::kRows - 1));
     // keys some row of the block keeps, and keys all of them keep
     const int klo = a.window >= 0 ? max(0, pos0 + tok_lo - a.window) : 0;
     const int khi = a.causal ? min(nd.hi, pos0 + tok_hi + 1) : nd.hi;
@@ -263,7 +270,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
     const int b_hi = (min(nd.k0 + t1 * kTileKeys, khi) + 15) >> 4;
     const int ns = b_hi - b_lo > w ? (b_hi - b_lo - w + kWarps - 1) / kWarps : 0;
 
-    // ---- page ids: lane i holds step (window * 32 + i)
+    // ---- page ids and scales: lane i holds those of step (window * 32 + i).
+    // Ids are read two windows of 32 steps ahead and scales one, so that no
+    // load waits for another in the loop.
     auto load_ids = [&](int window) -> int {
       const int i = window * 32 + lane;
       if (i >= ns) return -1;
@@ -275,48 +284,91 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
       }
       return id;
     };
-    int ids = load_ids(0), ids_next = ns > 32 ? load_ids(1) : -1;
+    struct Scales {
+      float k, v;
+    };
+    auto load_scales = [&](int id) -> Scales {
+      Scales r = {1.f, 1.f};
+      if (KIND == kCacheE4m3 && id >= 0) {
+        r.k = a.k_scale[static_cast<int64_t>(id) * a.Hkv + hk];
+        r.v = fmaxf(a.v_scale[static_cast<int64_t>(id) * a.Hkv + hk], 0x1p-100f);
+      }
+      return r;
+    };
+    int ids = load_ids(0), ids1 = ns > 32 ? load_ids(1) : -1, ids2 = ns > 64 ? load_ids(2) : -1;
+    Scales sc = load_scales(ids), sc1 = load_scales(ids1);
+    // of the window being computed: K scale, log2 of the V scale, its inverse,
+    // and whether the page exists
+    float w_k = 1.f, w_lg = 0.f, w_inv = 1.f;
+    int w_id = ids;
+    const char* const k_lane = a.kc + hk * a.k_head + g * a.k_tok + 16 * t;
+    const char* const v_lane =
+        a.vc + hk * a.v_head + 2 * t * a.v_tok + (C::kVb == 8 ? 8 * g : 16 * g);
+    uint32_t st_in = ring;  // stage of the next copy
     auto issue = [&](int i) {
       if (i < ns) {
         if (i > 0 && (i & 31) == 0) {
-          ids = ids_next;
-          ids_next = load_ids((i >> 5) + 1);
+          ids = ids1;
+          ids1 = ids2;
+          ids2 = load_ids((i >> 5) + 2);
         }
         const int page = __shfl_sync(0xffffffffu, ids, i & 31);
         const int key = (b_lo + w + kWarps * i) << 4, slot = key & page_mask;
-        const uint32_t st = ring + (i % C::kStages) * C::kStage;
-        const bool okp = page >= 0;
-        const char* kp = a.kc + (okp ? page * a.k_page + hk * a.k_head + (slot + g) * a.k_tok : 0);
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int k = key + g + 8 * r;
-          const bool ok = okp && k >= klo && k < khi;
-          const char* src = ok ? kp + 8 * r * a.k_tok + 16 * t : a.kc;
-#pragma unroll
-          for (int c = 0; c < C::kKch; ++c)
-            cp_async16(st + (r * C::kKch + c) * 512 + lane * 16, src + (ok ? c * 64 : 0), ok);
-        }
-        const char* vp =
-            a.vc + (okp ? page * a.v_page + hk * a.v_head + (slot + 2 * t) * a.v_tok : 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int kk = (j & 1) + 8 * (j >> 1), k = key + 2 * t + kk;
-          const bool ok = okp && k >= klo && k < khi;
-          const uint32_t dst = st + C::kStageK + j * C::kVb * 32;
+        const uint32_t dst = st_in + lane * 16;
+        if (page >= 0 && key >= klo && key + 16 <= khi) {
+          const char* const kp = k_lane + page * a.k_page + slot * a.k_tok;
+          const char* const kp8 = kp + 8 * a.k_tok;
+          const char* const vp = v_lane + page * a.v_page + slot * a.v_tok;
+          const char* const vp8 = vp + 8 * a.v_tok;
+#define PAGED_K(c)                                             \
+  if constexpr (C::kKch > (c)) {                               \
+    cp_async16_at<(c)*512, (c)*64>(dst, kp);                   \
+    cp_async16_at<(C::kKch + (c)) * 512, (c)*64>(dst, kp8);    \
+  }
+          PAGED_K(0) PAGED_K(1) PAGED_K(2) PAGED_K(3) PAGED_K(4) PAGED_K(5)
+#undef PAGED_K
           if constexpr (C::kVb == 8) {
-            cp_async8(dst + lane * 8, ok ? vp + kk * a.v_tok + 8 * g : a.vc, ok);
+            const uint32_t d8 = st_in + lane * 8;
+            cp_async8_at<C::kStageK>(d8, vp);
+            cp_async8_at<C::kStageK + 256>(d8, vp + a.v_tok);
+            cp_async8_at<C::kStageK + 512>(d8, vp8);
+            cp_async8_at<C::kStageK + 768>(d8, vp8 + a.v_tok);
           } else {
-#pragma unroll
-            for (int c = 0; c < C::kVb / 16; ++c)
-              cp_async16(dst + c * 512 + lane * 16,
-                         ok ? vp + kk * a.v_tok + c * 128 + 16 * g : a.vc, ok);
+#define PAGED_V(j, p)                                                                 \
+  cp_async16_at<C::kStageK + (j)*C::kVb * 32, 0>(dst, p);                             \
+  if constexpr (C::kVb == 32) cp_async16_at<C::kStageK + (j)*1024 + 512, 128>(dst, p);
+            PAGED_V(0, vp) PAGED_V(1, vp + a.v_tok) PAGED_V(2, vp8) PAGED_V(3, vp8 + a.v_tok)
+#undef PAGED_V
+          }
+        } else {  // a step at the mask's edge, or without a page: zeros outside
+          const char* kp = page >= 0 ? k_lane + page * a.k_page + slot * a.k_tok : a.kc;
+#pragma unroll 1
+          for (int r = 0; r < 2; ++r) {
+            const int k = key + g + 8 * r;
+            const bool ok = page >= 0 && k >= klo && k < khi;
+            const char* src = ok ? kp + 8 * r * a.k_tok : a.kc;
+#pragma unroll 1
+            for (int c = 0; c < C::kKch; ++c)
+              cp_async16(dst + (r * C::kKch + c) * 512, src + (ok ? c * 64 : 0), ok);
+          }
+          const char* vp = page >= 0 ? v_lane + page * a.v_page + slot * a.v_tok : a.vc;
+#pragma unroll 1
+          for (int j = 0; j < 4; ++j) {
+            const int kk = (j & 1) + 8 * (j >> 1), k = key + 2 * t + kk;
+            const bool ok = page >= 0 && k >= klo && k < khi;
+            const uint32_t vd = st_in + C::kStageK + j * C::kVb * 32;
+            const char* src = ok ? vp + kk * a.v_tok : a.vc;
+            if constexpr (C::kVb == 8) {
+              cp_async8(vd + lane * 8, src, ok);
+            } else {
+#pragma unroll 1
+              for (int c = 0; c < C::kVb / 16; ++c)
+                cp_async16(vd + c * 512 + lane * 16, src + (ok ? c * 128 : 0), ok);
+            }
           }
         }
-        if (KIND == kCacheE4m3 && lane < 2 && okp)
-          cp_async4(smem_u32(&s_sc[w][i % C::kStages][lane]),
-                    (lane ? a.v_scale : a.k_scale) + static_cast<int64_t>(page) * a.Hkv + hk);
-        if (lane == 0) s_ok[w][i % C::kStages] = okp;
       }
+      st_in = st_in + C::kStage == ring + C::kStages * C::kStage ? ring : st_in + C::kStage;
       cp_commit();
     };
 #pragma unroll
@@ -333,8 +385,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
       const bool real = r < rows;
       const uint16_t* qp = a.q;
       if (real) {
-        const int tok = r / a.group;
-        qp += (nd.q.row0 + tok) * a.q_stride + (hk * a.group + r % a.group) * DQK;
+        const int tok = div_group(a, r);
+        qp += (nd.q.row0 + tok) * a.q_stride + (hk * a.group + r - tok * a.group) * DQK;
       }
       uint32_t raw[C::kKs][2];
       // dims of slice ks: E4M3 64 (ks / 4) + 16 t + 4 (ks % 4) + 0..3,
@@ -391,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
       for (int c = 0; c < 2; ++c) {
         fac[nt][c] = a.scale * kLog2e * __shfl_sync(0xffffffffu, back, (2 * t + c) * 4);
         const int rr = r0 + nt * 8 + 2 * t + c;
-        cpos[nt][c] = rr < rows ? pos0 + rr / a.group : INT_MIN;
+        cpos[nt][c] = rr < rows ? pos0 + div_group(a, rr) : INT_MIN;
       }
     }
     if constexpr (C::kQSmem) __syncthreads();
@@ -412,13 +464,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
              (a.window < 0 || key >= p - a.window);
     };
 
+    uint32_t st = ring;  // stage being computed
     for (int i = 0; i < ns; ++i) {
+      if ((i & 31) == 0) {  // a new window; copies are less than one ahead
+        w_id = ids;
+        if (i > 0) {
+          sc = sc1;
+          sc1 = load_scales(ids1);
+        }
+        w_k = sc.k;
+        w_inv = 1.f / sc.v;
+        w_lg = (__float_as_uint(sc.v) & 0x7fffffu) == 0
+                   ? static_cast<float>(static_cast<int>(__float_as_uint(sc.v) >> 23) - 127)
+                   : __log2f(sc.v);
+      }
       cp_wait<C::kStages - 2>();
       __syncwarp();
       issue(i + C::kStages - 1);
-      const uint32_t st = ring + (i % C::kStages) * C::kStage;
       const int key = (b_lo + w + kWarps * i) << 4;
-      const bool okp = s_ok[w][i % C::kStages] != 0;
+      const bool okp = __shfl_sync(0xffffffffu, w_id, i & 31) >= 0;
 
       // S^T
       float s[NT][4];
@@ -463,12 +527,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
       // scale and the sum takes it out
       float ksc = 1.f, lgv = 0.f, inv_v = 1.f;
       if (KIND == kCacheE4m3) {
-        ksc = s_sc[w][i % C::kStages][0];
-        const float vsc = fmaxf(s_sc[w][i % C::kStages][1], 0x1p-100f);
-        inv_v = 1.f / vsc;
-        lgv = (__float_as_uint(vsc) & 0x7fffffu) == 0
-                  ? static_cast<float>(static_cast<int>(__float_as_uint(vsc) >> 23) - 127)
-                  : __log2f(vsc);
+        ksc = __shfl_sync(0xffffffffu, w_k, i & 31);
+        lgv = __shfl_sync(0xffffffffu, w_lg, i & 31);
+        inv_v = __shfl_sync(0xffffffffu, w_inv, i & 31);
       }
       const bool whole = okp && key >= all_lo && key + 16 <= all_hi;
       uint32_t pb[NT][2];
@@ -606,6 +667,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
         for (int nt = 0; nt < NT; ++nt)
           mma16816<kBf>(o[nt][mt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
       }
+      st = st + C::kStage == ring + C::kStages * C::kStage ? ring : st + C::kStage;
     }
 
     // ---- join the warps' states.  A column's 16-byte groups are permuted in
@@ -653,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
         float mt_ = -INFINITY;
 #pragma unroll
         for (int x = 0; x < kWarps; ++x) mt_ = fmaxf(mt_, s_m[x][nt * 8 + w]);
-        const int tok = r / a.group, head = hk * a.group + r % a.group;
+        const int tok = div_group(a, r), head = hk * a.group + r - tok * a.group;
         float snk = -INFINITY;
         const bool none = mt_ == -INFINITY;
         if (complete && a.sink) {
@@ -751,7 +813,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
   }
   __syncthreads();
   if (part != 0 || r >= rows) return;
-  const int tok = r / a.group, head = d.z * a.group + r % a.group;
+  const int tok = div_group(a, r), head = d.z * a.group + r - tok * a.group;
   float mt = -INFINITY;
 #pragma unroll
   for (int i = 0; i < 4; ++i) mt = fmaxf(mt, s_m[rr][i]);
