@@ -27,7 +27,7 @@
 // scale is added to them as its logarithm (P V s_v = 2^(s + log2 s_v) V) and
 // taken out of the normaliser again, so both cost one multiply-add.
 //
-// Work split.  A tile is 128 keys of one (sequence, KV head, block of rows).
+// Work split.  A tile is one step of each of a block's warps, of one (sequence, KV head, block of rows).
 // All tiles of the batch, in order, are cut into equal shares, one per block
 // of a grid that fills the SMs: long and short sequences balance without a
 // host-side plan, and a single sequence spreads over the whole chip.  A share
@@ -45,9 +45,6 @@ namespace {
 using sm103::ex2_approx;
 using sm103::smem_u32;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kTileKeys = 16 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -62,12 +59,22 @@ struct Cfg {
   static constexpr int kKs = DQK / 16;  // K slices of S^T
   static constexpr int kMt = DV / 16;   // row tiles of O^T
   static constexpr int kRows = 8 * NT;
-  // blocks per SM: two where a lane's state leaves them 128 registers each
+  // Steps a warp takes together: with one tile of rows a step is a chain of
+  // dependent short operations, and two chains hide each other's latency (and
+  // share the maximum's shuffles); more rows are independent work already.
+  static constexpr int kTogether = NT == 1 ? 2 : 1;
+  // blocks per SM: two where a stage is small, so that one streams while the
+  // other joins its warps' states
   static constexpr int kBlocks = NT == 1 && kStage <= 4096 ? 2 : 1;
-  static constexpr int kBudget = kBlocks == 2 ? 104 * 1024 : 200 * 1024;
+  static constexpr int kBudget = kBlocks == 2 ? 100 * 1024 : 200 * 1024;
+  // the steps in hand, and as many on their way
+  static constexpr int kFitWarps = kBudget / (2 * kTogether * kStage);
+  static constexpr int kWarps = kFitWarps > 8 ? 8 : kFitWarps;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kTileKeys = 16 * kWarps;
   static constexpr int kFit = kBudget / (kWarps * kStage);
-  static constexpr int kStages = kFit > 4 ? 4 : kFit;
-  static_assert(kStages >= 2, "ring");
+  static constexpr int kStages = kFit > 4 * kTogether ? 4 * kTogether : kFit;
+  static_assert(kStages >= 2 * kTogether && kWarps >= 4, "ring");
   static constexpr bool kQSmem = NT > 2;
   static constexpr int kQBytes = kQSmem ? NT * kKs * 256 : 0;
   static constexpr int kRing = kWarps * kStages * kStage;
@@ -157,7 +164,7 @@ struct Need {
   Seq q;
   int nrb, tiles, k0, hi;
 };
-__device__ __forceinline__ Need need_of(const Args& a, int s, int rows_per) {
+__device__ __forceinline__ Need need_of(const Args& a, int s, int rows_per, int tile_keys) {
   Need d;
   d.q = load_seq(a, s);
   const int cap = a.max_pages << a.page_shift;
@@ -167,13 +174,14 @@ __device__ __forceinline__ Need need_of(const Args& a, int s, int rows_per) {
   if (a.window >= 0) lo = max(0, d.q.len - d.q.n - a.window);
   d.k0 = lo & ~15;
   d.nrb = (d.q.n * a.group + rows_per - 1) / rows_per;
-  d.tiles = max(1, (d.hi - d.k0 + kTileKeys - 1) / kTileKeys);
+  d.tiles = max(1, (d.hi - d.k0 + tile_keys - 1) / tile_keys);
   return d;
 }
 
 // This block's share; every thread returns the same values.
-template <int ROWS>
+template <class C>
 __device__ __forceinline__ Share find_share(const Args& a) {
+  constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
   __shared__ int64_t s_part[kWarps];
   __shared__ int64_t s_off;
   __shared__ int s_seq;
@@ -181,7 +189,7 @@ __device__ __forceinline__ Share find_share(const Args& a) {
   const int first = threadIdx.x * per, last = min(a.num_seqs, first + per);
   int64_t mine = 0;
   for (int s = first; s < last; ++s) {
-    const Need d = need_of(a, s, ROWS);
+    const Need d = need_of(a, s, C::kRows, C::kTileKeys);
     mine += static_cast<int64_t>(d.nrb) * a.Hkv * d.tiles;
   }
   int64_t x = mine;
@@ -210,7 +218,7 @@ __device__ __forceinline__ Share find_share(const Args& a) {
       int s = first;
       int64_t off = sh.begin - before;
       for (;; ++s) {
-        const Need d = need_of(a, s, ROWS);
+        const Need d = need_of(a, s, C::kRows, C::kTileKeys);
         const int64_t c = static_cast<int64_t>(d.nrb) * a.Hkv * d.tiles;
         if (off < c) break;
         off -= c;
@@ -226,17 +234,18 @@ __device__ __forceinline__ Share find_share(const Args& a) {
 }
 
 template <int KIND, int DQK, int DV, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
+__global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
     decode_kernel(const __grid_constant__ Args a) {
   using C = Cfg<KIND, DQK, DV, NT>;
   constexpr bool kBf = KIND == kCacheBf16;
+  constexpr int kWarps = C::kWarps, kTileKeys = C::kTileKeys, U = C::kTogether;
   // fp16 P is kept at up to 2^14 so that weights down to 2^-28 of the row's
   // largest are normal numbers
   constexpr float kShift = kBf ? 0.f : 14.f;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
   const int tid = threadIdx.x, w = tid / 32, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const Share sh = find_share<C::kRows>(a);
+  const Share sh = find_share<C>(a);
   if (tid == 0 && a.split_desc) a.split_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   sm103::grid_dep_launch();  // the joining kernel may be put in place
   if (sh.begin >= sh.end) return;
@@ -248,11 +257,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
 
   int seq = sh.s;
   int64_t off = sh.off, at = sh.begin;
-  Need nd = need_of(a, seq, C::kRows);
+  Need nd = need_of(a, seq, C::kRows, C::kTileKeys);
   while (at < sh.end) {
     while (off >= static_cast<int64_t>(nd.nrb) * a.Hkv * nd.tiles) {
       off -= static_cast<int64_t>(nd.nrb) * a.Hkv * nd.tiles;
-      nd = need_of(a, ++seq, C::kRows);
+      nd = need_of(a, ++seq, C::kRows, C::kTileKeys);
     }
     const int item = static_cast<int>(off / nd.tiles), t0 = static_cast<int>(off % nd.tiles);
     const int t1 = static_cast<int>(min(static_cast<int64_t>(nd.tiles), t0 + (sh.end - at)));
@@ -372,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
       cp_commit();
     };
 #pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) issue(i);
+    for (int i = 0; i < C::kStages - U; ++i) issue(i);
 
     // ---- queries: column g of each tile as B fragments; factors of columns
     // 2t and 2t + 1 (base-2 softmax scale, and the row's power of two)
@@ -465,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
     };
 
     uint32_t st = ring;  // stage being computed
-    for (int i = 0; i < ns; ++i) {
+    for (int i = 0; i < ns; i += U) {
       if ((i & 31) == 0) {  // a new window; copies are less than one ahead
         w_id = ids;
         if (i > 0) {
@@ -478,46 +487,59 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
                    ? static_cast<float>(static_cast<int>(__float_as_uint(sc.v) >> 23) - 127)
                    : __log2f(sc.v);
       }
-      cp_wait<C::kStages - 2>();
+      cp_wait<C::kStages - 2 * U>();
       __syncwarp();
-      issue(i + C::kStages - 1);
-      const int key = (b_lo + w + kWarps * i) << 4;
-      const bool okp = __shfl_sync(0xffffffffu, w_id, i & 31) >= 0;
+#pragma unroll
+      for (int x = 0; x < U; ++x) issue(i + C::kStages - U + x);
+      const bool two = U == 1 || i + 1 < ns;  // the second step exists
 
       // S^T
-      float s[NT][4];
+      float s[U][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int x = 0; x < U; ++x)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[nt][j] = 0.f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[x][nt][j] = 0.f;
+      uint32_t at_stage[U];
+#pragma unroll
+      for (int x = 0; x < U; ++x) {
+        at_stage[x] = st;
+        st = st + C::kStage == ring + C::kStages * C::kStage ? ring : st + C::kStage;
+      }
 #pragma unroll
       for (int c = 0; c < C::kKch; ++c) {
-        const uint4 x0 = lds128(st + c * 512 + lane * 16);
-        const uint4 x1 = lds128(st + (C::kKch + c) * 512 + lane * 16);
-        const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
-        constexpr int kPer = KIND == kCacheE4m3 ? 4 : 2;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const int ks = c * kPer + j;
-          uint32_t a0, a1, a2, a3;
-          if constexpr (KIND == kCacheE4m3) {
-            a0 = e4m3x2_f16x2(static_cast<uint16_t>(w0[j]));
-            a2 = e4m3x2_f16x2(static_cast<uint16_t>(w0[j] >> 16));
-            a1 = e4m3x2_f16x2(static_cast<uint16_t>(w1[j]));
-            a3 = e4m3x2_f16x2(static_cast<uint16_t>(w1[j] >> 16));
-          } else {
-            a0 = w0[2 * j];
-            a2 = w0[2 * j + 1];
-            a1 = w1[2 * j];
-            a3 = w1[2 * j + 1];
-          }
+        for (int x = 0; x < U; ++x) {
+          // (a second step that does not exist multiplies what its stage held;
+          // its scores are masked)
+          const uint4 x0 = lds128(at_stage[x] + c * 512 + lane * 16);
+          const uint4 x1 = lds128(at_stage[x] + (C::kKch + c) * 512 + lane * 16);
+          const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+          constexpr int kPer = KIND == kCacheE4m3 ? 4 : 2;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if constexpr (C::kQSmem) {
-              const uint2 b = lds64(qs + (nt * C::kKs + ks) * 256 + lane * 8);
-              mma16816<kBf>(s[nt], a0, a1, a2, a3, b.x, b.y);
+          for (int j = 0; j < kPer; ++j) {
+            const int ks = c * kPer + j;
+            uint32_t a0, a1, a2, a3;
+            if constexpr (KIND == kCacheE4m3) {
+              a0 = e4m3x2_f16x2(static_cast<uint16_t>(w0[j]));
+              a2 = e4m3x2_f16x2(static_cast<uint16_t>(w0[j] >> 16));
+              a1 = e4m3x2_f16x2(static_cast<uint16_t>(w1[j]));
+              a3 = e4m3x2_f16x2(static_cast<uint16_t>(w1[j] >> 16));
             } else {
-              mma16816<kBf>(s[nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+              a0 = w0[2 * j];
+              a2 = w0[2 * j + 1];
+              a1 = w1[2 * j];
+              a3 = w1[2 * j + 1];
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (C::kQSmem) {
+                const uint2 b = lds64(qs + (nt * C::kKs + ks) * 256 + lane * 8);
+                mma16816<kBf>(s[x][nt], a0, a1, a2, a3, b.x, b.y);
+              } else {
+                mma16816<kBf>(s[x][nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+              }
             }
           }
         }
@@ -525,29 +547,44 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
 
       // softmax in base 2; with E4M3 pages the exponent carries log2 of the V
       // scale and the sum takes it out
-      float ksc = 1.f, lgv = 0.f, inv_v = 1.f;
-      if (KIND == kCacheE4m3) {
-        ksc = __shfl_sync(0xffffffffu, w_k, i & 31);
-        lgv = __shfl_sync(0xffffffffu, w_lg, i & 31);
-        inv_v = __shfl_sync(0xffffffffu, w_inv, i & 31);
+      float ksc[U], lgv[U], inv_v[U];
+      bool okp[U], whole[U];
+      int key[U];
+#pragma unroll
+      for (int x = 0; x < U; ++x) {
+        const int from = (i + x) & 31;
+        key[x] = (b_lo + w + kWarps * (i + x)) << 4;
+        okp[x] = (x == 0 || two) && __shfl_sync(0xffffffffu, w_id, from) >= 0;
+        whole[x] = okp[x] && key[x] >= all_lo && key[x] + 16 <= all_hi;
+        ksc[x] = inv_v[x] = 1.f;
+        lgv[x] = 0.f;
+        if (KIND == kCacheE4m3) {
+          ksc[x] = __shfl_sync(0xffffffffu, w_k, from);
+          lgv[x] = __shfl_sync(0xffffffffu, w_lg, from);
+          inv_v[x] = __shfl_sync(0xffffffffu, w_inv, from);
+        }
       }
-      const bool whole = okp && key >= all_lo && key + 16 <= all_hi;
-      uint32_t pb[NT][2];
+      uint32_t pb[U][NT][2];
       bool moved = false;
       float al[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float p[4];
+        float p[U][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = fmaf(s[nt][j], fac[nt][j & 1] * ksc, lgv);
-        if (!whole) {
+        for (int x = 0; x < U; ++x) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (!okp || !kept(nt, j & 1, key + g + 8 * (j >> 1))) p[j] = -INFINITY;
+            p[x][j] = fmaf(s[x][nt][j], fac[nt][j & 1] * ksc[x], lgv[x]);
+          if (!whole[x]) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (!okp[x] || !kept(nt, j & 1, key[x] + g + 8 * (j >> 1))) p[x][j] = -INFINITY;
+          }
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float mx = fmaxf(p[c], p[2 + c]);
+          float mx = fmaxf(p[0][c], p[0][2 + c]);
+          if constexpr (U == 2) mx = sm103::fmax3(mx, p[U - 1][c], p[U - 1][2 + c]);
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -556,16 +593,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
           al[nt][c] = ex2_approx(m[nt][c] - mu);
           moved |= mx != m[nt][c];
           m[nt][c] = mx;
-          p[c] = ex2_approx(p[c] - mu + kShift);
-          p[2 + c] = ex2_approx(p[2 + c] - mu + kShift);
-          l[nt][c] = fmaf(l[nt][c], al[nt][c], (p[c] + p[2 + c]) * inv_v);
+          l[nt][c] *= al[nt][c];
+#pragma unroll
+          for (int x = 0; x < U; ++x) {
+            p[x][c] = ex2_approx(p[x][c] - mu + kShift);
+            p[x][2 + c] = ex2_approx(p[x][2 + c] - mu + kShift);
+            l[nt][c] = fmaf(p[x][c] + p[x][2 + c], inv_v[x], l[nt][c]);
+          }
         }
-        if constexpr (kBf) {
-          pb[nt][0] = movmatrix(sm103::pack_bf16x2(p[0], p[1]));
-          pb[nt][1] = movmatrix(sm103::pack_bf16x2(p[2], p[3]));
-        } else {
-          pb[nt][0] = movmatrix(sm103::pack_f16x2(p[0], p[1]));
-          pb[nt][1] = movmatrix(sm103::pack_f16x2(p[2], p[3]));
+#pragma unroll
+        for (int x = 0; x < U; ++x) {
+          if constexpr (kBf) {
+            pb[x][nt][0] = movmatrix(sm103::pack_bf16x2(p[x][0], p[x][1]));
+            pb[x][nt][1] = movmatrix(sm103::pack_bf16x2(p[x][2], p[x][3]));
+          } else {
+            pb[x][nt][0] = movmatrix(sm103::pack_f16x2(p[x][0], p[x][1]));
+            pb[x][nt][1] = movmatrix(sm103::pack_f16x2(p[x][2], p[x][3]));
+          }
         }
       }
       if (__any_sync(0xffffffffu, moved)) {
@@ -577,70 +621,73 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
             for (int j = 0; j < 4; ++j) o[nt][mt][j] *= al[nt][j & 1];
       }
 
+#pragma unroll
+      for (int x = 0; x < U; ++x) {
+        if (x > 0 && !two) break;  // weights of 0 do not undo a NaN of an old stage
       // V: four keys, a dim pair per row tile
       constexpr int kW = C::kVb / 4;  // words per key
       uint32_t v[4][kW];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t src = st + C::kStageK + j * C::kVb * 32;
+        const uint32_t src = at_stage[x] + C::kStageK + j * C::kVb * 32;
         if constexpr (C::kVb == 8) {
-          const uint2 x = lds64(src + lane * 8);
-          v[j][0] = x.x;
-          v[j][1] = x.y;
+          const uint2 q = lds64(src + lane * 8);
+          v[j][0] = q.x;
+          v[j][1] = q.y;
         } else {
 #pragma unroll
           for (int c = 0; c < C::kVb / 16; ++c) {
-            const uint4 x = lds128(src + c * 512 + lane * 16);
-            v[j][4 * c] = x.x;
-            v[j][4 * c + 1] = x.y;
-            v[j][4 * c + 2] = x.z;
-            v[j][4 * c + 3] = x.w;
+            const uint4 q = lds128(src + c * 512 + lane * 16);
+            v[j][4 * c] = q.x;
+            v[j][4 * c + 1] = q.y;
+            v[j][4 * c + 2] = q.z;
+            v[j][4 * c + 3] = q.w;
           }
         }
       }
       // A step that some rows keep in part: values that are not finite may
       // not meet the zero weights of rows that mask them.  They are taken out
       // of the product and added to the rows that keep them.
-      if (!whole && tok_lo != tok_hi) {
+      if (!whole[x] && tok_lo != tok_hi) {
         uint32_t bad = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int x = 0; x < kW; ++x) bad |= nonfinite<KIND>(v[j][x]);
+          for (int z = 0; z < kW; ++z) bad |= nonfinite<KIND>(v[j][z]);
         if (__any_sync(0xffffffffu, bad != 0)) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int x = 0; x < kW; ++x) {
-              const uint32_t f = nonfinite<KIND>(v[j][x]);
+            for (int z = 0; z < kW; ++z) {
+              const uint32_t f = nonfinite<KIND>(v[j][z]);
               // spread each element's flag (its top bit) over the element
               const uint32_t mask = KIND == kCacheE4m3 ? (f >> 7) * 255u : (f >> 15) * 65535u;
-              v[j][x] &= ~mask;
+              v[j][z] &= ~mask;
             }
           for (int r = 0; r < 16; ++r) {
             const int from = (g << 2) | ((r & 7) >> 1), j = (r & 1) + 2 * (r >> 3);
 #pragma unroll
             for (int e = 0; e < 2 * C::kMt; ++e) {  // this lane's dims
               const int byte = e * C::kCb;
-              const uint32_t src = st + C::kStageK + j * C::kVb * 32 +
+              const uint32_t src = at_stage[x] + C::kStageK + j * C::kVb * 32 +
                                    (C::kVb == 8 ? from * 8 + byte
                                                 : (byte / 16) * 512 + from * 16 + byte % 16);
-              float x;
+              float y;
               if constexpr (KIND == kCacheE4m3) {
                 uint32_t b;
                 asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(src) : "memory");
-                x = e4m3_value(static_cast<uint8_t>(b));
+                y = e4m3_value(static_cast<uint8_t>(b));
               } else {
                 uint16_t b;
                 asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(src) : "memory");
-                x = elem(b, KIND == kCacheF16);
+                y = elem(b, KIND == kCacheF16);
               }
-              if (!(fabsf(x) < INFINITY)) {
+              if (!(fabsf(y) < INFINITY)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                   for (int c = 0; c < 2; ++c)
-                    if (kept(nt, c, key + r)) o[nt][e / 2][2 * (e & 1) + c] += x;
+                    if (kept(nt, c, key[x] + r)) o[nt][e / 2][2 * (e & 1) + c] += y;
               }
             }
           }
@@ -651,12 +698,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
         uint32_t a0, a1, a2, a3;
         if constexpr (KIND == kCacheE4m3) {
           const uint32_t sel = (mt & 1) ? 0x7362 : 0x5140;
-          const uint32_t x = __byte_perm(v[0][mt / 2], v[1][mt / 2], sel);
-          const uint32_t y = __byte_perm(v[2][mt / 2], v[3][mt / 2], sel);
-          a0 = e4m3x2_f16x2(static_cast<uint16_t>(x));
-          a1 = e4m3x2_f16x2(static_cast<uint16_t>(x >> 16));
-          a2 = e4m3x2_f16x2(static_cast<uint16_t>(y));
-          a3 = e4m3x2_f16x2(static_cast<uint16_t>(y >> 16));
+          const uint32_t lo = __byte_perm(v[0][mt / 2], v[1][mt / 2], sel);
+          const uint32_t hi = __byte_perm(v[2][mt / 2], v[3][mt / 2], sel);
+          a0 = e4m3x2_f16x2(static_cast<uint16_t>(lo));
+          a1 = e4m3x2_f16x2(static_cast<uint16_t>(lo >> 16));
+          a2 = e4m3x2_f16x2(static_cast<uint16_t>(hi));
+          a3 = e4m3x2_f16x2(static_cast<uint16_t>(hi >> 16));
         } else {
           a0 = __byte_perm(v[0][mt], v[1][mt], 0x5410);
           a1 = __byte_perm(v[0][mt], v[1][mt], 0x7632);
@@ -665,9 +712,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          mma16816<kBf>(o[nt][mt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+          mma16816<kBf>(o[nt][mt], a0, a1, a2, a3, pb[x][nt][0], pb[x][nt][1]);
       }
-      st = st + C::kStage == ring + C::kStages * C::kStage ? ring : st + C::kStage;
+      }
     }
 
     // ---- join the warps' states.  A column's 16-byte groups are permuted in
@@ -709,12 +756,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
                           o[nt][2 * i + 1][2 + c]);
         }
       __syncthreads();
-      constexpr int kV = DV / 32;  // dims per lane; one warp per column
-      const int r = r0 + nt * 8 + w;
-      if (r < rows) {
+      constexpr int kV = DV / 32;  // dims per lane; one warp a column at a time
+      for (int cw = w; cw < 8; cw += kWarps) {
+        const int r = r0 + nt * 8 + cw;
+        if (r >= rows) break;
         float mt_ = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < kWarps; ++x) mt_ = fmaxf(mt_, s_m[x][nt * 8 + w]);
+        for (int x = 0; x < kWarps; ++x) mt_ = fmaxf(mt_, s_m[x][nt * 8 + cw]);
         const int tok = div_group(a, r), head = hk * a.group + r - tok * a.group;
         float snk = -INFINITY;
         const bool none = mt_ == -INFINITY;
@@ -729,13 +777,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
         for (int i = 0; i < kV; ++i) acc[i] = 0.f;
 #pragma unroll
         for (int x = 0; x < kWarps; ++x) {
-          const float mx = s_m[x][nt * 8 + w];
+          const float mx = s_m[x][nt * 8 + cw];
           if (mx == -INFINITY) continue;  // nothing kept by this warp
           const float f = ex2_approx(mx - mu);
-          lt = fmaf(s_l[x][nt * 8 + w], f, lt);
-          const float* so = s_o + (x * 8 + w) * DV +
-                            (kV == 4 ? (lane ^ swz(w)) * 4
-                                     : ((lane >> 1) ^ swz(w)) * 4 + 2 * (lane & 1));
+          lt = fmaf(s_l[x][nt * 8 + cw], f, lt);
+          const float* so = s_o + (x * 8 + cw) * DV +
+                            (kV == 4 ? (lane ^ swz(cw)) * 4
+                                     : ((lane >> 1) ^ swz(cw)) * 4 + 2 * (lane & 1));
 #pragma unroll
           for (int i = 0; i < kV; ++i) acc[i] = fmaf(so[i], f, acc[i]);
         }
@@ -751,11 +799,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
             a.lse[static_cast<int64_t>(head) * a.num_tokens + nd.q.row0 + tok] =
                 none ? (a.sink ? a.sink[head] : -INFINITY) : (mu - kShift) * kLn2 + logf(lt);
         } else {
-          float* pp = a.part + (static_cast<int64_t>(slot) * a.part_rows + nt * 8 + w) * DV + lane * kV;
+          float* pp = a.part + (static_cast<int64_t>(slot) * a.part_rows + nt * 8 + cw) * DV + lane * kV;
 #pragma unroll
           for (int i = 0; i < kV; ++i) pp[i] = acc[i];
           if (lane == 0)
-            a.part_ml[static_cast<int64_t>(slot) * a.part_rows + nt * 8 + w] =
+            a.part_ml[static_cast<int64_t>(slot) * a.part_rows + nt * 8 + cw] =
                 make_float2(mt_, lt);
         }
       }
@@ -850,17 +898,17 @@ cudaError_t launch_one(const Args& a0, int sms, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   // as many blocks as can be resident, or as there can be tiles
-  const int64_t most = (static_cast<int64_t>(a.max_pages) << a.page_shift) + kTileKeys - 1;
-  const int64_t tiles = most / kTileKeys + 1;
+  const int64_t most = (static_cast<int64_t>(a.max_pages) << a.page_shift) + C::kTileKeys - 1;
+  const int64_t tiles = most / C::kTileKeys + 1;
   const int64_t items =
       (static_cast<int64_t>(a.num_tokens) * a.group / C::kRows + a.num_seqs) * a.Hkv;
   int64_t ctas = static_cast<int64_t>(sms) * C::kBlocks;
   if (ctas > kMaxCtas) ctas = kMaxCtas;
   if (tiles < ctas && items * tiles < ctas) ctas = items * tiles;
   a.part_rows = C::kRows;
-  const bool split = (static_cast<int64_t>(a.max_pages) << a.page_shift) > kTileKeys;
+  const bool split = (static_cast<int64_t>(a.max_pages) << a.page_shift) > C::kTileKeys;
   if (!split) a.split_desc = nullptr;
-  kern<<<static_cast<unsigned>(ctas), kThreads, C::kSmem, st>>>(a);
+  kern<<<static_cast<unsigned>(ctas), C::kThreads, C::kSmem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || !split) return e;
   cudaLaunchConfig_t cfg = {};
