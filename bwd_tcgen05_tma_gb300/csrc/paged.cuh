@@ -143,6 +143,25 @@ __device__ __forceinline__ uint16_t f32x2_e4m3x2(float lo, float hi) {
   return r;
 }
 
+// Launches a kernel that may be put in place while the one before it on the
+// stream still runs; it waits for that one (grid_dep_wait) before it reads
+// anything.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                         A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 constexpr int kMinExp = -64;
 // Smallest power of two s >= 2^-64 with amax <= 448 s (amax finite): with
 // amax = 1.f * 2^x, 448 = 1.75 * 2^8, so e = x - 8, or one more if 1.f > 1.75.

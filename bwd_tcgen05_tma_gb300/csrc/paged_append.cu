@@ -184,6 +184,7 @@ __device__ __forceinline__ bool find_run(const Args& a, int c, Run* out) {
 // kind: CacheKind
 template <int kKind>
 __global__ void __launch_bounds__(kThreads) append_kernel(Args a) {
+  sm103::grid_dep_wait();
   Run run;
   if (!find_run(a, blockIdx.x, &run)) return;
   const int h = blockIdx.y, tid = threadIdx.x;
@@ -344,10 +345,10 @@ cudaError_t launch_append(const Args& a, int kind, cudaStream_t st) {
     if (runs > a.num_tokens) runs = a.num_tokens;
   }
   const dim3 grid(static_cast<unsigned>(runs), a.Hkv);
-  if (kind == kCacheE4m3) append_kernel<kCacheE4m3><<<grid, kThreads, 0, st>>>(a);
-  else if (kind == kCacheF16) append_kernel<kCacheF16><<<grid, kThreads, 0, st>>>(a);
-  else append_kernel<kCacheBf16><<<grid, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  auto kern = kind == kCacheE4m3  ? append_kernel<kCacheE4m3>
+              : kind == kCacheF16 ? append_kernel<kCacheF16>
+                                  : append_kernel<kCacheBf16>;
+  return launch_early(kern, grid, dim3(kThreads), 0, st, a);
 }
 
 }  // namespace paged

@@ -330,13 +330,14 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
     x->abort = 0;
     for (uint32_t& b : x->bad) b = 0;
     mbar_fence_init();
-    a.split_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
   if (warp == 0) {
     tmem_alloc(&x->tmem, 512);
     tmem_relinquish();
   }
   tc_fence_before();
+  grid_dep_wait();
+  if (tid == 0) a.split_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   Walk w;
   walk_init(a, x, w);  // two block barriers
   tc_fence_after();
@@ -1077,18 +1078,10 @@ cudaError_t chunk_one(const Args& a, int sms, cudaStream_t st) {
       !cache_map(&maps.v, KIND, a.vc, DV, a, a.v_tok, a.v_head, a.v_page))
     return cudaErrorInvalidValue;
   const unsigned ctas = sms < kMaxChunkCtas ? sms : kMaxChunkCtas;
-  kern<<<ctas, 512, L::kSmem, st>>>(a, maps);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(ctas, kChunkRows / 32);
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<DV>, a, KIND == kCacheBf16 ? 0.f : 7.f);
+  e = launch_early(kern, dim3(ctas), dim3(512), L::kSmem, st, a, maps);
+  if (e != cudaSuccess) return e;
+  return launch_early(chunk_join_kernel<DV>, dim3(ctas, kChunkRows / 32), dim3(256), 0, st, a,
+                      KIND == kCacheBf16 ? 0.f : 7.f);
 }
 
 template <int KIND>

@@ -152,19 +152,19 @@ __device__ __forceinline__ uint32_t nonfinite(uint32_t w) {
   return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
 }
 
-// Share of the batch: sequence `s`, tile `off` of its items, `left` tiles.
-struct Share {
-  int s;
-  int64_t off, begin, end, total;
-  int ctas;
-};
+// An item costs its tiles and about as much as this many more (its queries, a
+// pipeline to fill, a state to join): shares are cut by that sum.
+constexpr int kStart = 3;
 
-// What a sequence asks for: row blocks, tiles per item, first key.
+// What a sequence asks for: row blocks, first key, end.
 struct Need {
   Seq q;
-  int nrb, tiles, k0, hi;
+  int nrb, k0, hi;
+  __device__ __forceinline__ int tiles(int tile_keys) const {
+    return max(1, (hi - k0 + tile_keys - 1) / tile_keys);
+  }
 };
-__device__ __forceinline__ Need need_of(const Args& a, int s, int rows_per, int tile_keys) {
+__device__ __forceinline__ Need need_of(const Args& a, int s, int rows_per) {
   Need d;
   d.q = load_seq(a, s);
   const int cap = a.max_pages << a.page_shift;
@@ -174,62 +174,103 @@ __device__ __forceinline__ Need need_of(const Args& a, int s, int rows_per, int 
   if (a.window >= 0) lo = max(0, d.q.len - d.q.n - a.window);
   d.k0 = lo & ~15;
   d.nrb = (d.q.n * a.group + rows_per - 1) / rows_per;
-  d.tiles = max(1, (d.hi - d.k0 + tile_keys - 1) / tile_keys);
   return d;
 }
 
-// This block's share; every thread returns the same values.
+// A block's or a warp's share of the batch: units [begin, end) of all, the
+// first one unit `off` of sequence `s`.
+struct Share {
+  int64_t off, begin, end, total;
+  int s, ctas;
+  bool solo;
+};
+
+// Every thread of the block (solo: of the warp) returns the same values.
+//
+// Solo: a warp takes whole items alone and nothing is joined.  That is the
+// better half where no item is much larger than a warp's average share (many
+// short sequences: 256 of up to 256 keys take 62 us when a block's warps share
+// each item); otherwise blocks share items, cut anywhere.
 template <class C>
 __device__ __forceinline__ Share find_share(const Args& a) {
   constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
-  __shared__ int64_t s_part[kWarps];
-  __shared__ int64_t s_off;
-  __shared__ int s_seq;
+  __shared__ int64_t s_sum[2][kWarps], s_off[kWarps];
+  __shared__ int s_max[kWarps], s_seq[kWarps];
+  const int w = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int per = (a.num_seqs + kThreads - 1) / kThreads;
   const int first = threadIdx.x * per, last = min(a.num_seqs, first + per);
-  int64_t mine = 0;
+  int64_t mine[2] = {0, 0}, sum[2];
+  int most = 0;
   for (int s = first; s < last; ++s) {
-    const Need d = need_of(a, s, C::kRows, C::kTileKeys);
-    mine += static_cast<int64_t>(d.nrb) * a.Hkv * d.tiles;
+    const Need d = need_of(a, s, C::kRows);
+    const int64_t items = static_cast<int64_t>(d.nrb) * a.Hkv;
+    const int steps = d.tiles(16);
+    mine[0] += items * (kStart + d.tiles(C::kTileKeys));
+    mine[1] += items * (kStart + steps);
+    if (items) most = max(most, kStart + steps);
   }
-  int64_t x = mine;
+  sum[0] = mine[0];
+  sum[1] = mine[1];
 #pragma unroll
   for (int i = 1; i < 32; i <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, i);
-    if ((threadIdx.x & 31) >= i) x += y;
+    const int64_t y0 = __shfl_up_sync(0xffffffffu, sum[0], i);
+    const int64_t y1 = __shfl_up_sync(0xffffffffu, sum[1], i);
+    if (lane >= i) {
+      sum[0] += y0;
+      sum[1] += y1;
+    }
   }
-  if ((threadIdx.x & 31) == 31) s_part[threadIdx.x / 32] = x;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) {
+    s_sum[0][w] = sum[0];
+    s_sum[1][w] = sum[1];
+    s_max[w] = most;
+  }
   __syncthreads();
-  int64_t total = 0, before = x - mine;
+  int64_t total[2] = {0, 0}, before[2] = {sum[0] - mine[0], sum[1] - mine[1]};
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int64_t t = s_part[w];
-    if (w < static_cast<int>(threadIdx.x) / 32) before += t;
-    total += t;
+  for (int x = 0; x < kWarps; ++x) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      if (x < w) before[m] += s_sum[m][x];
+      total[m] += s_sum[m][x];
+    }
+    most = max(most, s_max[x]);
   }
   Share sh;
-  sh.total = total;
-  sh.ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
-  sh.begin = sh.end = 0;
-  if (static_cast<int>(blockIdx.x) < sh.ctas) {
-    sh.begin = blockIdx.x * total / sh.ctas;
-    sh.end = (blockIdx.x + 1) * total / sh.ctas;
-    if (sh.begin >= before && sh.begin < before + mine) {
+  sh.solo = !C::kQSmem && static_cast<int64_t>(most) * gridDim.x * kWarps <= 2 * total[1];
+  sh.total = total[sh.solo];
+  sh.ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), sh.total));
+  const int64_t lo = before[sh.solo], hi = lo + mine[sh.solo];
+  const int64_t workers = sh.solo ? static_cast<int64_t>(gridDim.x) * kWarps : sh.ctas;
+  const int me = sh.solo ? blockIdx.x * kWarps + w : blockIdx.x;
+#pragma unroll 1
+  for (int x = 0; x < (sh.solo ? kWarps : 1); ++x) {
+    const int64_t k = sh.solo ? static_cast<int64_t>(blockIdx.x) * kWarps + x : blockIdx.x;
+    if (k >= workers) break;
+    const int64_t begin = k * sh.total / workers;
+    if (begin >= lo && begin < hi) {
       int s = first;
-      int64_t off = sh.begin - before;
+      int64_t off = begin - lo;
       for (;; ++s) {
-        const Need d = need_of(a, s, C::kRows, C::kTileKeys);
-        const int64_t c = static_cast<int64_t>(d.nrb) * a.Hkv * d.tiles;
+        const Need d = need_of(a, s, C::kRows);
+        const int64_t c = static_cast<int64_t>(d.nrb) * a.Hkv *
+                          (kStart + d.tiles(sh.solo ? 16 : C::kTileKeys));
         if (off < c) break;
         off -= c;
       }
-      s_seq = s;
-      s_off = off;
+      s_seq[x] = s;
+      s_off[x] = off;
     }
   }
   __syncthreads();
-  sh.s = s_seq;
-  sh.off = s_off;
+  sh.begin = sh.end = 0;
+  if (me < workers) {
+    sh.begin = me * sh.total / workers;
+    sh.end = (me + 1) * sh.total / workers;
+  }
+  sh.s = s_seq[sh.solo ? w : 0];
+  sh.off = s_off[sh.solo ? w : 0];
   return sh;
 }
 
@@ -238,13 +279,14 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
     decode_kernel(const __grid_constant__ Args a) {
   using C = Cfg<KIND, DQK, DV, NT>;
   constexpr bool kBf = KIND == kCacheBf16;
-  constexpr int kWarps = C::kWarps, kTileKeys = C::kTileKeys, U = C::kTogether;
+  constexpr int kWarps = C::kWarps, U = C::kTogether;
   // fp16 P is kept at up to 2^14 so that weights down to 2^-28 of the row's
   // largest are normal numbers
   constexpr float kShift = kBf ? 0.f : 14.f;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
   const int tid = threadIdx.x, w = tid / 32, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  sm103::grid_dep_wait();
   const Share sh = find_share<C>(a);
   if (tid == 0 && a.split_desc) a.split_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   sm103::grid_dep_launch();  // the joining kernel may be put in place
@@ -255,16 +297,29 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
   float* const s_o = reinterpret_cast<float*>(smem);
   const int page_mask = (1 << a.page_shift) - 1;
 
+  // the warps that share an item, and this one among them
+  const int nw = sh.solo ? 1 : kWarps, wi = sh.solo ? 0 : w;
+  const int tile_keys = 16 * nw;
   int seq = sh.s;
   int64_t off = sh.off, at = sh.begin;
-  Need nd = need_of(a, seq, C::kRows, C::kTileKeys);
+  Need nd = need_of(a, seq, C::kRows);
   while (at < sh.end) {
-    while (off >= static_cast<int64_t>(nd.nrb) * a.Hkv * nd.tiles) {
-      off -= static_cast<int64_t>(nd.nrb) * a.Hkv * nd.tiles;
-      nd = need_of(a, ++seq, C::kRows, C::kTileKeys);
+    const int tiles = nd.tiles(tile_keys), cost = kStart + tiles;
+    if (off >= static_cast<int64_t>(nd.nrb) * a.Hkv * cost) {
+      off -= static_cast<int64_t>(nd.nrb) * a.Hkv * cost;
+      nd = need_of(a, ++seq, C::kRows);
+      continue;
     }
-    const int item = static_cast<int>(off / nd.tiles), t0 = static_cast<int>(off % nd.tiles);
-    const int t1 = static_cast<int>(min(static_cast<int64_t>(nd.tiles), t0 + (sh.end - at)));
+    const int item = static_cast<int>(off / cost), u0 = static_cast<int>(off - static_cast<int64_t>(item) * cost);
+    // units [u0, u1): an item's start, then its tiles [t0, t1)
+    const int u1 = sh.solo ? cost
+                           : static_cast<int>(min(static_cast<int64_t>(cost), u0 + (sh.end - at)));
+    const int t0 = max(0, u0 - kStart), t1 = max(0, u1 - kStart);
+    const int64_t here = at;
+    at += u1 - u0;
+    off += u1 - u0;
+    // solo, an item is its first unit's; a share may end inside a start
+    if (sh.solo ? u0 > 0 : t1 <= t0) continue;
     const int hk = item / nd.nrb, rb = item % nd.nrb;
     const int rows = nd.q.n * a.group, r0 = rb * C::kRows;
     const int pos0 = nd.q.len - nd.q.n;  // position of the sequence's first new row
@@ -275,9 +330,9 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
     const int all_lo = a.window >= 0 ? max(0, pos0 + tok_hi - a.window) : 0;
     const int all_hi = a.causal ? min(nd.hi, pos0 + tok_lo + 1) : nd.hi;
     // this piece's 16-key steps
-    const int b_lo = max(nd.k0 + t0 * kTileKeys, klo) >> 4;
-    const int b_hi = (min(nd.k0 + t1 * kTileKeys, khi) + 15) >> 4;
-    const int ns = b_hi - b_lo > w ? (b_hi - b_lo - w + kWarps - 1) / kWarps : 0;
+    const int b_lo = max(nd.k0 + t0 * tile_keys, klo) >> 4;
+    const int b_hi = (min(nd.k0 + t1 * tile_keys, khi) + 15) >> 4;
+    const int ns = b_hi - b_lo > wi ? (b_hi - b_lo - wi + nw - 1) / nw : 0;
 
     // ---- page ids and scales: lane i holds those of step (window * 32 + i).
     // Ids are read two windows of 32 steps ahead and scales one, so that no
@@ -285,7 +340,7 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
     auto load_ids = [&](int window) -> int {
       const int i = window * 32 + lane;
       if (i >= ns) return -1;
-      const int col = (b_lo + w + kWarps * i) >> (a.page_shift - 4);
+      const int col = (b_lo + wi + nw * i) >> (a.page_shift - 4);
       int id = col < a.max_pages ? a.table[seq * a.table_stride + col] : -1;
       if (id < 0 || id >= a.num_pages) {
         flag_bounds(a);
@@ -322,7 +377,7 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
           ids2 = load_ids((i >> 5) + 2);
         }
         const int page = __shfl_sync(0xffffffffu, ids, i & 31);
-        const int key = (b_lo + w + kWarps * i) << 4, slot = key & page_mask;
+        const int key = (b_lo + wi + nw * i) << 4, slot = key & page_mask;
         const uint32_t dst = st_in + lane * 16;
         if (page >= 0 && key >= klo && key + 16 <= khi) {
           const char* const kp = k_lane + page * a.k_page + slot * a.k_tok;
@@ -553,7 +608,7 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
 #pragma unroll
       for (int x = 0; x < U; ++x) {
         const int from = (i + x) & 31;
-        key[x] = (b_lo + w + kWarps * (i + x)) << 4;
+        key[x] = (b_lo + wi + nw * (i + x)) << 4;
         okp[x] = (x == 0 || two) && __shfl_sync(0xffffffffu, w_id, from) >= 0;
         whole[x] = okp[x] && key[x] >= all_lo && key[x] + 16 <= all_hi;
         ksc[x] = inv_v[x] = 1.f;
@@ -733,12 +788,50 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
         x += __shfl_xor_sync(0xffffffffu, x, 4);
         x += __shfl_xor_sync(0xffffffffu, x, 8);
         x += __shfl_xor_sync(0xffffffffu, x, 16);
+        l[nt][c] = x;
         if (g == 0) {
           s_m[w][nt * 8 + 2 * t + c] = m[nt][c];
           s_l[w][nt * 8 + 2 * t + c] = x;
         }
       }
-    const bool complete = t0 == 0 && t1 == nd.tiles;
+    if (sh.solo) {
+      // the warp's own state is the item's
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int r = r0 + nt * 8 + 2 * t + c;
+          if (r >= rows) continue;
+          const int tok = div_group(a, r), head = hk * a.group + r - tok * a.group;
+          const bool none = m[nt][c] == -INFINITY;
+          float mt = m[nt][c], lt = l[nt][c], keep = 1.f;
+          if (a.sink) {
+            const float s2 = a.sink[head] * kLog2e;
+            mt = fmaxf(mt, s2);
+            const float mu = mt == -INFINITY ? 0.f : mt;
+            keep = ex2_approx(m[nt][c] - mu);
+            lt = fmaf(lt, keep, ex2_approx(s2 - mu + kShift));
+          }
+          const float inv = none || lt == 0.f ? 0.f : keep / lt;
+          uint16_t* const op = a.o + (static_cast<int64_t>(nd.q.row0 + tok) * a.Hq + head) * DV;
+#pragma unroll
+          for (int e = 0; e < 2 * C::kMt; e += 8) {  // eight dims a store
+            const int d = KIND == kCacheE4m3 ? C::kVb * g + e : 64 * (e / 8) + 8 * g;
+            auto at_dim = [&](int z) { return none ? 0.f : o[nt][z / 2][2 * (z & 1) + c] * inv; };
+            *reinterpret_cast<uint4*>(op + d) =
+                make_uint4(pack2(at_dim(e), at_dim(e + 1), a.f16),
+                           pack2(at_dim(e + 2), at_dim(e + 3), a.f16),
+                           pack2(at_dim(e + 4), at_dim(e + 5), a.f16),
+                           pack2(at_dim(e + 6), at_dim(e + 7), a.f16));
+          }
+          if (a.lse && g == 0)
+            a.lse[static_cast<int64_t>(head) * a.num_tokens + nd.q.row0 + tok] =
+                none ? (a.sink ? a.sink[head] : -INFINITY) : (mt - kShift) * kLn2 + logf(lt);
+        }
+      __syncwarp();
+      continue;
+    }
+    const bool complete = t0 == 0 && t1 == tiles;
     const int slot = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -810,13 +903,11 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
     }
     if (!complete && t0 == 0 && tid == 0) {
       // first of an item's pieces: blocks up to the one that holds its last tile
-      const int64_t x = at + nd.tiles - 1;
-      const int c1 = static_cast<int>(((x + 1) * sh.ctas + sh.total - 1) / sh.total) - 1;
+      const int64_t end = here + cost - u0;  // of the item's units
+      const int c1 = static_cast<int>((end * sh.ctas + sh.total - 1) / sh.total) - 1;
       a.split_desc[blockIdx.x] = make_int4(c1 - blockIdx.x + 1, seq, hk, rb);
     }
     __syncthreads();  // the sums are read before the next piece fills the ring
-    at += t1 - t0;
-    off += t1 - t0;
   }
 }
 
@@ -908,19 +999,10 @@ cudaError_t launch_one(const Args& a0, int sms, cudaStream_t st) {
   a.part_rows = C::kRows;
   const bool split = (static_cast<int64_t>(a.max_pages) << a.page_shift) > C::kTileKeys;
   if (!split) a.split_desc = nullptr;
-  kern<<<static_cast<unsigned>(ctas), C::kThreads, C::kSmem, st>>>(a);
-  e = cudaGetLastError();
+  e = launch_early(kern, dim3(static_cast<unsigned>(ctas)), dim3(C::kThreads), C::kSmem, st, a);
   if (e != cudaSuccess || !split) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), C::kRows / 2);
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<DV>, a, KIND == kCacheBf16 ? 0.f : 14.f);
+  return launch_early(join_kernel<DV>, dim3(static_cast<unsigned>(ctas), C::kRows / 2), dim3(256),
+                      0, st, a, KIND == kCacheBf16 ? 0.f : 14.f);
 }
 
 template <int KIND, int DQK, int DV>
