@@ -123,6 +123,23 @@ __device__ __forceinline__ uint16_t round16(float x, int f16) {
   return static_cast<uint16_t>(pack2(x, 0.f, f16));
 }
 
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, uint64_t* bar, int x,
+                                            int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(map), "r"(sm103::smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(p)
+               : "memory");
+  return v;
+}
+
 // Two E4M3 codes (low byte first) to a pair of fp16 values, exactly.
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t c) {
   uint32_t d;
@@ -178,6 +195,14 @@ cudaError_t launch_append(const Args& a, int kind, cudaStream_t st);
 // KV head (tokens x group); sms the device's SM count.
 constexpr int kMaxCtas = 304;
 inline int decode_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+struct CacheMaps {
+  CUtensorMap k, v;
+};
+// Tensor map over a cache, [page][head][slot][dim] by its strides in bytes:
+// boxes of `slots` slots of one head and `width` bytes of their dims, in the
+// swizzle of that many bytes (0: in the order of memory).
+bool cache_map(CUtensorMap* m, int kind, const void* base, int d, const Args& a, int64_t tok,
+               int64_t head, int64_t page, int slots, int width, int swizzle);
 cudaError_t launch_decode_e4m3(const Args& a, int rows, int sms, cudaStream_t st);
 cudaError_t launch_decode_f16(const Args& a, int rows, int sms, cudaStream_t st);
 cudaError_t launch_decode_bf16(const Args& a, int rows, int sms, cudaStream_t st);
@@ -185,14 +210,6 @@ cudaError_t launch_decode_bf16(const Args& a, int rows, int sms, cudaStream_t st
 // Many rows per KV head.
 constexpr int kMaxChunkCtas = 152;
 constexpr int kChunkPartRows = 256;
-struct ChunkMaps {
-  CUtensorMap k, v;
-};
-// Tensor map over a cache, [page][head][slot][dim] by its strides in bytes:
-// boxes of min(page, 128) slots of one head, E4M3 codes as bytes in the order
-// of memory, 16-bit elements 64 at a time in the MMA's swizzle.
-bool cache_map(CUtensorMap* m, int kind, const void* base, int d, const Args& a, int64_t tok,
-               int64_t head, int64_t page);
 cudaError_t launch_chunk_e4m3(const Args& a, int sms, cudaStream_t st);
 cudaError_t launch_chunk_f16(const Args& a, int sms, cudaStream_t st);
 cudaError_t launch_chunk_bf16(const Args& a, int sms, cudaStream_t st);

@@ -183,24 +183,26 @@ int sm_count() {
 }  // namespace
 
 bool cache_map(CUtensorMap* m, int kind, const void* base, int d, const Args& a, int64_t tok,
-               int64_t head, int64_t page) {
+               int64_t head, int64_t page, int slots, int width, int swizzle) {
   auto fn = encode_fn();
   if (!fn) return false;
   const bool codes = kind == kCacheE4m3;
-  const int slots = 1 << a.page_shift;
-  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)slots, (cuuint64_t)a.Hkv,
-                              (cuuint64_t)a.num_pages};
+  // a pool without pages has no memory; no box of it is ever asked for
+  const void* mem = a.num_pages > 0 ? base : static_cast<const void*>(a.q);
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)1 << a.page_shift, (cuuint64_t)a.Hkv,
+                              (cuuint64_t)(a.num_pages > 0 ? a.num_pages : 1)};
   const cuuint64_t strides[3] = {(cuuint64_t)tok, (cuuint64_t)head, (cuuint64_t)page};
-  const cuuint32_t box[4] = {(cuuint32_t)(codes ? d : 64), (cuuint32_t)(slots < 128 ? slots : 128),
-                             1, 1};
+  const cuuint32_t box[4] = {(cuuint32_t)(codes ? width : width / 2), (cuuint32_t)slots, 1, 1};
   const cuuint32_t es[4] = {1, 1, 1, 1};
   const CUtensorMapDataType type = codes                ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                    : kind == kCacheF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  return fn(m, type, 4, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE,
-            codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const CUtensorMapSwizzle sw = swizzle == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                : CU_TENSOR_MAP_SWIZZLE_NONE;
+  return fn(m, type, 4, const_cast<void*>(mem), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace paged

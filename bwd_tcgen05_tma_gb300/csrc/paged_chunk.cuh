@@ -261,23 +261,6 @@ __device__ __forceinline__ void walk_init(const Args& a, ChunkAux* x, Walk& w) {
   }
 }
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, uint64_t* bar, int x,
-                                            int y, int z, int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
-      : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t p) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(p)
-               : "memory");
-  return v;
-}
-
 // Eight E4M3 codes to fp16, stored as one 16-byte unit.
 __device__ __forceinline__ void store_codes(uint32_t dst, uint32_t lo, uint32_t hi) {
   st_shared_v4(dst, e4m3x2_f16x2(static_cast<uint16_t>(lo)),
@@ -288,7 +271,7 @@ __device__ __forceinline__ void store_codes(uint32_t dst, uint32_t lo, uint32_t 
 
 template <int KIND, int DQK, int DV>
 __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ Args a,
-                                                       const __grid_constant__ ChunkMaps maps) {
+                                                       const __grid_constant__ CacheMaps maps) {
   using L = ChunkCfg<KIND, DQK, DV>;
   constexpr bool kBf = KIND == kCacheBf16;
   constexpr bool kCodes = KIND == kCacheE4m3;
@@ -1073,9 +1056,13 @@ cudaError_t chunk_one(const Args& a, int sms, cudaStream_t st) {
   auto kern = chunk_kernel<KIND, DQK, DV>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
-  ChunkMaps maps;
-  if (!cache_map(&maps.k, KIND, a.kc, DQK, a, a.k_tok, a.k_head, a.k_page) ||
-      !cache_map(&maps.v, KIND, a.vc, DV, a, a.v_tok, a.v_head, a.v_page))
+  CacheMaps maps;
+  const int slots = a.page_shift < 7 ? 1 << a.page_shift : 128;
+  const bool codes = KIND == kCacheE4m3;
+  if (!cache_map(&maps.k, KIND, a.kc, DQK, a, a.k_tok, a.k_head, a.k_page, slots,
+                 codes ? DQK : 128, codes ? 0 : 128) ||
+      !cache_map(&maps.v, KIND, a.vc, DV, a, a.v_tok, a.v_head, a.v_page, slots, codes ? DV : 128,
+                 codes ? 0 : 128))
     return cudaErrorInvalidValue;
   const unsigned ctas = sms < kMaxChunkCtas ? sms : kMaxChunkCtas;
   e = launch_early(kern, dim3(ctas), dim3(512), L::kSmem, st, a, maps);

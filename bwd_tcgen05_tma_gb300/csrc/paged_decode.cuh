@@ -51,10 +51,12 @@ constexpr float kLn2 = 0.6931471805599453f;
 template <int KIND, int DQK, int DV, int NT>
 struct Cfg {
   static constexpr int kCb = KIND == kCacheE4m3 ? 1 : 2;
-  static constexpr int kKch = DQK * kCb / 64;  // 16-byte copies per lane and key
+  static constexpr int kKch = DQK * kCb / 64;  // 16-byte units of K per lane and key
   static constexpr int kVb = DV * kCb / 8;     // bytes of V per lane and key
-  static constexpr int kStageK = 2 * kKch * 512;
-  static constexpr int kStageV = 4 * kVb * 32;
+  // boxes of 16 slots, this many bytes wide, in the swizzle of that width
+  static constexpr int kKw = DQK * kCb % 128 ? 64 : 128, kVw = DV * kCb % 128 ? 64 : 128;
+  static constexpr int kStageK = 16 * DQK * kCb;
+  static constexpr int kStageV = 16 * DV * kCb;
   static constexpr int kStage = kStageK + kStageV;
   static constexpr int kKs = DQK / 16;  // K slices of S^T
   static constexpr int kMt = DV / 16;   // row tiles of O^T
@@ -79,44 +81,10 @@ struct Cfg {
   static constexpr int kQBytes = kQSmem ? NT * kKs * 256 : 0;
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kMerge = kWarps * 8 * DV * 4;
-  static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + kQBytes;
+  static constexpr int kBody = (kRing > kMerge ? kRing : kMerge);
+  static constexpr int kSmem = 1024 + kBody + kQBytes;  // the ring starts at a multiple of 1024
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(ok ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
-               "r"(ok ? 8 : 0)
-               : "memory");
-}
-// Whole copies at constant offsets from a stage and a row.
-template <int DST, int SRC>
-__device__ __forceinline__ void cp_async16_at(uint32_t dst, const char* src) {
-  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(DST),
-               "n"(SRC)
-               : "memory");
-}
-template <int DST>
-__device__ __forceinline__ void cp_async8_at(uint32_t dst, const char* src) {
-  asm volatile("cp.async.ca.shared.global [%0 + %2], [%1], 8;" ::"r"(dst), "l"(src), "n"(DST)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t p) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(p)
-               : "memory");
-  return v;
-}
 __device__ __forceinline__ uint2 lds64(uint32_t p) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(p) : "memory");
@@ -150,6 +118,16 @@ __device__ __forceinline__ uint32_t nonfinite(uint32_t w) {
   if (KIND == kCacheE4m3) return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
   if (KIND == kCacheF16) return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
   return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+
+// The four dims of slice ks that lane t holds, in the order of its 16-byte units
+// (two neighbouring ones of each 128-byte box, or one of each 64-byte box).
+template <class C>
+__device__ __forceinline__ constexpr int k_dim(int ks, int t) {
+  constexpr int kE = 16 / C::kCb, kPer = kE / 4;  // elements, slices of a unit
+  const int c = ks / kPer;
+  return (C::kKw == 128 ? (c / 2) * (8 * kE) + (2 * t + c % 2) * kE : c * (4 * kE) + t * kE) +
+         4 * (ks % kPer);
 }
 
 // An item costs its tiles and about as much as this many more (its queries, a
@@ -276,7 +254,7 @@ __device__ __forceinline__ Share find_share(const Args& a) {
 
 template <int KIND, int DQK, int DV, int NT>
 __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQK, DV, NT>::kBlocks)
-    decode_kernel(const __grid_constant__ Args a) {
+    decode_kernel(const __grid_constant__ Args a, const __grid_constant__ CacheMaps maps) {
   using C = Cfg<KIND, DQK, DV, NT>;
   constexpr bool kBf = KIND == kCacheBf16;
   constexpr int kWarps = C::kWarps, U = C::kTogether;
@@ -286,15 +264,29 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
   const int tid = threadIdx.x, w = tid / 32, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  // a barrier for each warp's each stage
+  __shared__ uint64_t s_full[kWarps][C::kStages];
+  if (lane == 0) {
+    for (int i = 0; i < C::kStages; ++i) sm103::mbar_init(&s_full[w][i], 1);
+    sm103::mbar_fence_init();
+    sm103::prefetch_tensormap(&maps.k);
+    sm103::prefetch_tensormap(&maps.v);
+  }
   sm103::grid_dep_wait();
   const Share sh = find_share<C>(a);
   if (tid == 0 && a.split_desc) a.split_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   sm103::grid_dep_launch();  // the joining kernel may be put in place
   if (sh.begin >= sh.end) return;
 
-  const uint32_t ring = smem_u32(smem) + w * (C::kStages * C::kStage);
-  const uint32_t qs = smem_u32(smem) + (C::kSmem - C::kQBytes);
-  float* const s_o = reinterpret_cast<float*>(smem);
+  uint8_t* const body = smem + (-smem_u32(smem) & 1023u);
+  const uint32_t ring = smem_u32(body) + w * (C::kStages * C::kStage);
+  const uint32_t qs = smem_u32(body) + C::kBody;
+  float* const s_o = reinterpret_cast<float*>(body);
+  // the ring runs on from item to item: stage and phase of the next copy, and
+  // of the next step to compute
+  int in_stage = 0, out_stage = 0;
+  uint32_t out_phase = 0;
+  bool dead = false;
   const int page_mask = (1 << a.page_shift) - 1;
 
   // the warps that share an item, and this one among them
@@ -365,75 +357,34 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
     // and whether the page exists
     float w_k = 1.f, w_lg = 0.f, w_inv = 1.f;
     int w_id = ids;
-    const char* const k_lane = a.kc + hk * a.k_head + g * a.k_tok + 16 * t;
-    const char* const v_lane =
-        a.vc + hk * a.v_head + 2 * t * a.v_tok + (C::kVb == 8 ? 8 * g : 16 * g);
-    uint32_t st_in = ring;  // stage of the next copy
+    // Step i's 16 slots of K and V, by TMA: whole boxes, whatever the mask
+    // keeps of them; nothing where there is no page.
     auto issue = [&](int i) {
-      if (i < ns) {
-        if (i > 0 && (i & 31) == 0) {
-          ids = ids1;
-          ids1 = ids2;
-          ids2 = load_ids((i >> 5) + 2);
-        }
-        const int page = __shfl_sync(0xffffffffu, ids, i & 31);
-        const int key = (b_lo + wi + nw * i) << 4, slot = key & page_mask;
-        const uint32_t dst = st_in + lane * 16;
-        if (page >= 0 && key >= klo && key + 16 <= khi) {
-          const char* const kp = k_lane + page * a.k_page + slot * a.k_tok;
-          const char* const kp8 = kp + 8 * a.k_tok;
-          const char* const vp = v_lane + page * a.v_page + slot * a.v_tok;
-          const char* const vp8 = vp + 8 * a.v_tok;
-#define PAGED_K(c)                                             \
-  if constexpr (C::kKch > (c)) {                               \
-    cp_async16_at<(c)*512, (c)*64>(dst, kp);                   \
-    cp_async16_at<(C::kKch + (c)) * 512, (c)*64>(dst, kp8);    \
-  }
-          PAGED_K(0) PAGED_K(1) PAGED_K(2) PAGED_K(3) PAGED_K(4) PAGED_K(5)
-#undef PAGED_K
-          if constexpr (C::kVb == 8) {
-            const uint32_t d8 = st_in + lane * 8;
-            cp_async8_at<C::kStageK>(d8, vp);
-            cp_async8_at<C::kStageK + 256>(d8, vp + a.v_tok);
-            cp_async8_at<C::kStageK + 512>(d8, vp8);
-            cp_async8_at<C::kStageK + 768>(d8, vp8 + a.v_tok);
-          } else {
-#define PAGED_V(j, p)                                                                 \
-  cp_async16_at<C::kStageK + (j)*C::kVb * 32, 0>(dst, p);                             \
-  if constexpr (C::kVb == 32) cp_async16_at<C::kStageK + (j)*1024 + 512, 128>(dst, p);
-            PAGED_V(0, vp) PAGED_V(1, vp + a.v_tok) PAGED_V(2, vp8) PAGED_V(3, vp8 + a.v_tok)
-#undef PAGED_V
-          }
-        } else {  // a step at the mask's edge, or without a page: zeros outside
-          const char* kp = page >= 0 ? k_lane + page * a.k_page + slot * a.k_tok : a.kc;
-#pragma unroll 1
-          for (int r = 0; r < 2; ++r) {
-            const int k = key + g + 8 * r;
-            const bool ok = page >= 0 && k >= klo && k < khi;
-            const char* src = ok ? kp + 8 * r * a.k_tok : a.kc;
-#pragma unroll 1
-            for (int c = 0; c < C::kKch; ++c)
-              cp_async16(dst + (r * C::kKch + c) * 512, src + (ok ? c * 64 : 0), ok);
-          }
-          const char* vp = page >= 0 ? v_lane + page * a.v_page + slot * a.v_tok : a.vc;
-#pragma unroll 1
-          for (int j = 0; j < 4; ++j) {
-            const int kk = (j & 1) + 8 * (j >> 1), k = key + 2 * t + kk;
-            const bool ok = page >= 0 && k >= klo && k < khi;
-            const uint32_t vd = st_in + C::kStageK + j * C::kVb * 32;
-            const char* src = ok ? vp + kk * a.v_tok : a.vc;
-            if constexpr (C::kVb == 8) {
-              cp_async8(vd + lane * 8, src, ok);
-            } else {
-#pragma unroll 1
-              for (int c = 0; c < C::kVb / 16; ++c)
-                cp_async16(vd + c * 512 + lane * 16, src + (ok ? c * 128 : 0), ok);
-            }
-          }
+      if (i >= ns || dead) return;
+      if (i > 0 && (i & 31) == 0) {
+        ids = ids1;
+        ids1 = ids2;
+        ids2 = load_ids((i >> 5) + 2);
+      }
+      const int page = __shfl_sync(0xffffffffu, ids, i & 31);
+      if (lane == 0) {
+        uint64_t* const bar = &s_full[w][in_stage];
+        if (page >= 0) {
+          const int slot = ((b_lo + wi + nw * i) << 4) & page_mask;
+          const uint32_t dst = ring + in_stage * C::kStage;
+          sm103::mbar_arrive_expect_tx(bar, C::kStage);
+#pragma unroll
+          for (int c = 0; c < DQK * C::kCb / C::kKw; ++c)
+            tma_load_4d(dst + c * 16 * C::kKw, &maps.k, bar, c * C::kKw / C::kCb, slot, hk, page);
+#pragma unroll
+          for (int c = 0; c < DV * C::kCb / C::kVw; ++c)
+            tma_load_4d(dst + C::kStageK + c * 16 * C::kVw, &maps.v, bar, c * C::kVw / C::kCb, slot,
+                        hk, page);
+        } else {
+          sm103::mbar_arrive(bar);
         }
       }
-      st_in = st_in + C::kStage == ring + C::kStages * C::kStage ? ring : st_in + C::kStage;
-      cp_commit();
+      in_stage = in_stage + 1 == C::kStages ? 0 : in_stage + 1;
     };
 #pragma unroll
     for (int i = 0; i < C::kStages - U; ++i) issue(i);
@@ -453,12 +404,9 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
         qp += (nd.q.row0 + tok) * a.q_stride + (hk * a.group + r - tok * a.group) * DQK;
       }
       uint32_t raw[C::kKs][2];
-      // dims of slice ks: E4M3 64 (ks / 4) + 16 t + 4 (ks % 4) + 0..3,
-      // 16-bit 32 (ks / 2) + 8 t + 4 (ks % 2) + 0..3
 #pragma unroll
       for (int ks = 0; ks < C::kKs; ++ks) {
-        const int d = KIND == kCacheE4m3 ? 64 * (ks / 4) + 16 * t + 4 * (ks % 4)
-                                         : 32 * (ks / 2) + 8 * t + 4 * (ks % 2);
+        const int d = k_dim<C>(ks, t);
         uint2 v = make_uint2(0, 0);
         if (real) v = *reinterpret_cast<const uint2*>(qp + d);
         raw[ks][0] = v.x;
@@ -528,7 +476,15 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
              (a.window < 0 || key >= p - a.window);
     };
 
-    uint32_t st = ring;  // stage being computed
+    // this lane's places in a stage: K rows g (and g + 8, 8 rows on) for its
+    // units of a box, V rows 2t, 2t + 1 (and 8 rows on)
+    uint32_t k_at[2], v_at[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      k_at[c] = C::kKw == 128 ? g * 128 + (((2 * t + c) ^ g) << 4) : g * 64 + ((t ^ (g >> 1)) << 4);
+      v_at[c] = C::kStageK + (C::kVw == 128 ? (2 * t + c) * 128 + ((g ^ (2 * t + c)) << 4)
+                                            : (2 * t + c) * 64 + (((g >> 1) ^ t) << 4) + 8 * (g & 1));
+    }
     for (int i = 0; i < ns; i += U) {
       if ((i & 31) == 0) {  // a new window; copies are less than one ahead
         w_id = ids;
@@ -542,11 +498,24 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
                    ? static_cast<float>(static_cast<int>(__float_as_uint(sc.v) >> 23) - 127)
                    : __log2f(sc.v);
       }
-      cp_wait<C::kStages - 2 * U>();
-      __syncwarp();
+      const bool two = U == 1 || i + 1 < ns;  // the second step exists
+      uint32_t at_stage[U];
+#pragma unroll
+      for (int x = 0; x < U; ++x) {
+        at_stage[x] = ring + out_stage * C::kStage;
+        if (x > 0 && !two) break;
+        if (!dead && !sm103::mbar_wait_warp(&s_full[w][out_stage], out_phase)) {
+          if (a.status) *a.status = ATTN_ERR_DEVICE_TIMEOUT;
+          dead = true;
+        }
+        if (++out_stage == C::kStages) {
+          out_stage = 0;
+          out_phase ^= 1;
+        }
+      }
+      __syncwarp();  // the stages filled next are read by every lane
 #pragma unroll
       for (int x = 0; x < U; ++x) issue(i + C::kStages - U + x);
-      const bool two = U == 1 || i + 1 < ns;  // the second step exists
 
       // S^T
       float s[U][NT][4];
@@ -556,20 +525,16 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[x][nt][j] = 0.f;
-      uint32_t at_stage[U];
-#pragma unroll
-      for (int x = 0; x < U; ++x) {
-        at_stage[x] = st;
-        st = st + C::kStage == ring + C::kStages * C::kStage ? ring : st + C::kStage;
-      }
 #pragma unroll
       for (int c = 0; c < C::kKch; ++c) {
 #pragma unroll
         for (int x = 0; x < U; ++x) {
           // (a second step that does not exist multiplies what its stage held;
           // its scores are masked)
-          const uint4 x0 = lds128(at_stage[x] + c * 512 + lane * 16);
-          const uint4 x1 = lds128(at_stage[x] + (C::kKch + c) * 512 + lane * 16);
+          constexpr int kBox = 16 * C::kKw;
+          const uint32_t from =
+              at_stage[x] + (C::kKw == 128 ? (c / 2) * kBox + k_at[c & 1] : c * kBox + k_at[0]);
+          const uint4 x0 = lds128(from), x1 = lds128(from + 8 * C::kKw);
           const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
           constexpr int kPer = KIND == kCacheE4m3 ? 4 : 2;
 #pragma unroll
@@ -684,19 +649,26 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
       uint32_t v[4][kW];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t src = at_stage[x] + C::kStageK + j * C::kVb * 32;
+        const uint32_t src = at_stage[x] + v_at[j & 1] + (j >> 1) * 8 * C::kVw;
         if constexpr (C::kVb == 8) {
-          const uint2 q = lds64(src + lane * 8);
+          const uint2 q = lds64(src);
           v[j][0] = q.x;
           v[j][1] = q.y;
         } else {
 #pragma unroll
           for (int c = 0; c < C::kVb / 16; ++c) {
-            const uint4 q = lds128(src + c * 512 + lane * 16);
+            const uint4 q = lds128(src + c * 16 * C::kVw);
             v[j][4 * c] = q.x;
             v[j][4 * c + 1] = q.y;
             v[j][4 * c + 2] = q.z;
             v[j][4 * c + 3] = q.w;
+          }
+        }
+        if (!whole[x]) {  // what lies in slots that no row keeps, NaN included
+          const int kk = key[x] + 2 * t + (j & 1) + 8 * (j >> 1);
+          if (!okp[x] || kk < klo || kk >= khi) {
+#pragma unroll
+            for (int z = 0; z < kW; ++z) v[j][z] = 0;
           }
         }
       }
@@ -720,13 +692,14 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
               v[j][z] &= ~mask;
             }
           for (int r = 0; r < 16; ++r) {
-            const int from = (g << 2) | ((r & 7) >> 1), j = (r & 1) + 2 * (r >> 3);
+            if (!okp[x] || key[x] + r < klo || key[x] + r >= khi) continue;
+            const uint32_t row = at_stage[x] + C::kStageK + r * C::kVw;
 #pragma unroll
             for (int e = 0; e < 2 * C::kMt; ++e) {  // this lane's dims
               const int byte = e * C::kCb;
-              const uint32_t src = at_stage[x] + C::kStageK + j * C::kVb * 32 +
-                                   (C::kVb == 8 ? from * 8 + byte
-                                                : (byte / 16) * 512 + from * 16 + byte % 16);
+              const uint32_t src =
+                  C::kVb == 8 ? row + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + 8 * (g & 1) + byte
+                              : row + (byte / 16) * 16 * C::kVw + ((g ^ (r & 7)) << 4) + byte % 16;
               float y;
               if constexpr (KIND == kCacheE4m3) {
                 uint32_t b;
@@ -779,7 +752,6 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
       const int x = (col >> 1) & 3;
       return DV == 128 && KIND == kCacheE4m3 ? x : (x & 1) | ((x >> 1) << 2);
     };
-    cp_wait<0>();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -907,8 +879,11 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
       const int c1 = static_cast<int>((end * sh.ctas + sh.total - 1) / sh.total) - 1;
       a.split_desc[blockIdx.x] = make_int4(c1 - blockIdx.x + 1, seq, hk, rb);
     }
-    __syncthreads();  // the sums are read before the next piece fills the ring
+    sm103::fence_proxy_async_smem();
+    __syncthreads();  // the sums are read before the next piece's copies fill the ring
   }
+  if (dead)  // copies in flight land before the block may leave
+    for (int i = 0; i < C::kStages; ++i) sm103::mbar_wait(&s_full[w][i], out_phase, 100000000ull);
 }
 
 // Joins the pieces of each split item: block (i, y) rows 2y and 2y + 1 of the
@@ -999,7 +974,12 @@ cudaError_t launch_one(const Args& a0, int sms, cudaStream_t st) {
   a.part_rows = C::kRows;
   const bool split = (static_cast<int64_t>(a.max_pages) << a.page_shift) > C::kTileKeys;
   if (!split) a.split_desc = nullptr;
-  e = launch_early(kern, dim3(static_cast<unsigned>(ctas)), dim3(C::kThreads), C::kSmem, st, a);
+  CacheMaps maps;
+  if (!cache_map(&maps.k, KIND, a.kc, DQK, a, a.k_tok, a.k_head, a.k_page, 16, C::kKw, C::kKw) ||
+      !cache_map(&maps.v, KIND, a.vc, DV, a, a.v_tok, a.v_head, a.v_page, 16, C::kVw, C::kVw))
+    return cudaErrorInvalidValue;
+  e = launch_early(kern, dim3(static_cast<unsigned>(ctas)), dim3(C::kThreads), C::kSmem, st, a,
+                   maps);
   if (e != cudaSuccess || !split) return e;
   return launch_early(join_kernel<DV>, dim3(static_cast<unsigned>(ctas), C::kRows / 2), dim3(256),
                       0, st, a, KIND == kCacheBf16 ? 0.f : 14.f);
