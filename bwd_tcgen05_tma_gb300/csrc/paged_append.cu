@@ -1,16 +1,21 @@
 // Appending new tokens to the paged cache.
 //
-// One block per (run of new tokens inside one page, KV head): it rotates the
-// head's new keys and the queries of its group, and writes keys and values
-// into the page.  With an E4M3 cache the block owns the page's two scales of
-// that head, so the scale, the codes already there and the new ones are
-// settled in one place without atomics: the result does not depend on the
-// order of blocks.
+// Two kinds of blocks in one launch.
+//
+// Keys and values: one block per (run of new tokens inside one page, KV head).
+// With an E4M3 cache it owns the page's two scales of that head, so the scale,
+// the codes already there and the new ones are settled in one place without
+// atomics: the result does not depend on the order of blocks.  The values stay
+// in registers from the load over the block's maximum to the store (up to
+// kHold units a thread; pages of more read them twice).
+//
+// Queries: a thread takes one unit of a token (its cosines and sines stay in
+// registers) through several heads, four in flight.
 //
 // Work goes in units of 16 elements, two 16-byte loads: the eight pairs of a
 // rotation (halves rot/2 apart, or neighbours), or sixteen values that pass.
-// The values stay in registers from the load over the block's maximum to the
-// store (up to kHold units a thread; pages of more read them twice).
+// Bound by HBM: two bytes a query element each way, a key or value element
+// read as two bytes and written as one or two.
 #include "paged.cuh"
 
 namespace attn {
@@ -45,31 +50,43 @@ __device__ __forceinline__ void unpack8(uint4 v, float* x, int f16) {
   }
 }
 
-// Unit u of a head at `src`, rotated where u < rot / 16 by row `cs` of the
-// tables.  a' = a c - b s and b' = b c + a s, each product and the sum rounded
-// in fp32.
-__device__ __forceinline__ void load_unit(const Args& a, const uint16_t* src, int u, int rot,
-                                          int64_t cs, Unit& r) {
-  const int2 at = unit_at(u, rot, a.interleaved);
-  const uint4 lo = *reinterpret_cast<const uint4*>(src + at.x);
-  const uint4 hi = *reinterpret_cast<const uint4*>(src + at.y);
-  unpack8(lo, r.x, a.f16);
-  unpack8(hi, r.x + 8, a.f16);
-  if (u < rot / 16) {
-    float c[8], s[8];
-    const float4* cp = reinterpret_cast<const float4*>(a.cos + cs * (rot / 2) + 8 * u);
-    const float4* sp = reinterpret_cast<const float4*>(a.sin + cs * (rot / 2) + 8 * u);
-    *reinterpret_cast<float4*>(c) = __ldg(cp);
-    *reinterpret_cast<float4*>(c + 4) = __ldg(cp + 1);
-    *reinterpret_cast<float4*>(s) = __ldg(sp);
-    *reinterpret_cast<float4*>(s + 4) = __ldg(sp + 1);
+// The two 16-byte halves of a unit as they lie in memory.
+struct Raw {
+  uint4 lo, hi;
+};
+__device__ __forceinline__ Raw load_raw(const uint16_t* src, int2 at) {
+  return {*reinterpret_cast<const uint4*>(src + at.x), *reinterpret_cast<const uint4*>(src + at.y)};
+}
+__device__ __forceinline__ void unpack(const Raw& v, Unit& r, int f16) {
+  unpack8(v.lo, r.x, f16);
+  unpack8(v.hi, r.x + 8, f16);
+}
+
+// A unit's cosines and sines: row `cs` of the tables, columns 8 u .. 8 u + 7.
+struct Turn {
+  float c[8], s[8];
+};
+__device__ __forceinline__ void load_turn(const Args& a, int u, int64_t cs, Turn& t) {
+  const float4* cp = reinterpret_cast<const float4*>(a.cos + cs * (a.rot / 2) + 8 * u);
+  const float4* sp = reinterpret_cast<const float4*>(a.sin + cs * (a.rot / 2) + 8 * u);
+  *reinterpret_cast<float4*>(t.c) = __ldg(cp);
+  *reinterpret_cast<float4*>(t.c + 4) = __ldg(cp + 1);
+  *reinterpret_cast<float4*>(t.s) = __ldg(sp);
+  *reinterpret_cast<float4*>(t.s + 4) = __ldg(sp + 1);
+}
+// a' = a c - b s and b' = b c + a s, each product and the sum rounded in fp32.
+__device__ __forceinline__ void turn_pair(float& x, float& y, float c, float s) {
+  const float a = x, b = y;
+  x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  y = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+}
+__device__ __forceinline__ void turn(Unit& r, const Turn& t, int interleaved) {
+  if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int p = a.interleaved ? 2 * i : i, q = a.interleaved ? 2 * i + 1 : i + 8;
-      const float x = r.x[p], y = r.x[q];
-      r.x[p] = __fsub_rn(__fmul_rn(x, c[i]), __fmul_rn(y, s[i]));
-      r.x[q] = __fadd_rn(__fmul_rn(y, c[i]), __fmul_rn(x, s[i]));
-    }
+    for (int i = 0; i < 8; ++i) turn_pair(r.x[2 * i], r.x[2 * i + 1], t.c[i], t.s[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turn_pair(r.x[i], r.x[i + 8], t.c[i], t.s[i]);
   }
 }
 
@@ -181,101 +198,181 @@ __device__ __forceinline__ bool find_run(const Args& a, int c, Run* out) {
   return out->page >= 0;
 }
 
-// kind: CacheKind
+// Row of the rotation tables for a token, or -1 (reported).
+__device__ __forceinline__ int table_row(const Args& a, int row, int pos) {
+  const int p = a.rope_pos ? a.rope_pos[row] : pos;
+  if (p < 0 || p >= a.rope_len) {
+    flag_bounds(a);
+    return -1;
+  }
+  return p;
+}
+
+// Queries: this block's tokens and eight heads.
+constexpr int kHeads = 8;
+__device__ __forceinline__ void turn_queries(const Args& a, int block) {
+  const int units = a.d_qk / 16, tokens = kThreads / units;
+  const int groups = (a.Hq + kHeads - 1) / kHeads;
+  const int u = threadIdx.x % units, i = threadIdx.x / units;
+  const int t = (block / groups) * tokens + i, h0 = (block % groups) * kHeads;
+  if (i >= tokens || t >= a.num_tokens) return;
+  const int2 at = unit_at(u, a.rot, a.interleaved);
+  const int heads = min(kHeads, a.Hq - h0);
+  const uint16_t* src = a.q + t * a.q_stride + h0 * a.d_qk;
+  uint16_t* dst = a.q_rot + t * a.q_rot_stride + h0 * a.d_qk;
+  Raw raw[4];  // on their way while the token's place is looked up
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < heads) raw[j] = load_raw(src + j * a.d_qk, at);
+  // the token's sequence: the last one that starts at or before it
+  int s = t;
+  if (a.cu) {
+    int lo = 0, hi = a.num_seqs;  // cu[lo] <= t < cu[hi], where it is anywhere
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (a.cu[mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    s = lo;
+  }
+  const Seq q = load_seq(a, s);
+  if (t < q.row0 || t >= q.row0 + q.n || q.len <= 0) return;  // padding
+  const bool turns = u < a.rot / 16;
+  Turn cs;
+  if (a.rot > 0) {
+    const int row = table_row(a, t, q.len - q.n + t - q.row0);
+    if (row < 0) return;
+    if (turns) load_turn(a, u, row, cs);
+  }
+#pragma unroll
+  for (int b = 0; b < kHeads; b += 4) {
+    if (b > 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (b + j < heads) raw[j] = load_raw(src + (b + j) * a.d_qk, at);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (b + j >= heads) continue;
+      uint16_t* const to = dst + (b + j) * a.d_qk;
+      if (turns) {
+        Unit r;
+        unpack(raw[j], r, a.f16);
+        turn(r, cs, a.interleaved);
+        store16(to, at, r, a.f16);
+      } else {
+        *reinterpret_cast<uint4*>(to + at.x) = raw[j].lo;
+        *reinterpret_cast<uint4*>(to + at.y) = raw[j].hi;
+      }
+    }
+  }
+}
+
+// Blocks [0, runs * groups) write keys and values, of `per_block` heads (one
+// with an E4M3 cache), the others turn queries.
 template <int kKind>
-__global__ void __launch_bounds__(kThreads) append_kernel(Args a) {
+__global__ void __launch_bounds__(kThreads)
+    append_kernel(const __grid_constant__ Args a, int runs, int per_block) {
   sm103::grid_dep_wait();
+  const int groups = (a.Hkv + per_block - 1) / per_block;
+  if (static_cast<int>(blockIdx.x) >= runs * groups) {
+    turn_queries(a, blockIdx.x - runs * groups);
+    return;
+  }
   Run run;
-  if (!find_run(a, blockIdx.x, &run)) return;
-  const int h = blockIdx.y, tid = threadIdx.x;
+  if (!find_run(a, blockIdx.x / groups, &run)) return;
+  const int h = (blockIdx.x % groups) * per_block, tid = threadIdx.x;
   const int uk = a.d_qk / 16, uv = a.d_v / 16;
-  const int nk = run.n * uk, nkv = nk + run.n * uv;
-  const int rot = a.rot;
+  const int nk = run.n * uk, each = nk + run.n * uv;
+  const int nkv = each * min(per_block, a.Hkv - h);
   char* kdst = a.kc + run.page * a.k_page + h * a.k_head + run.slot0 * a.k_tok;
   char* vdst = a.vc + run.page * a.v_page + h * a.v_head + run.slot0 * a.v_tok;
 
-  // Row of the rotation tables for token i of the run, or -1 (reported).
-  auto table_row = [&](int i) -> int {
-    const int p = a.rope_pos ? a.rope_pos[run.row0 + i] : run.pos0 + i;
-    if (p < 0 || p >= a.rope_len) {
-      flag_bounds(a);
-      return -1;
-    }
-    return p;
+  // Unit e of the run's keys, then values.
+  struct Place {
+    int h, i, u;
+    bool key;
   };
-  // Unit e of the run's keys, then values: false if it is not to be written.
-  auto load_kv = [&](int e, Unit& r) -> bool {
+  auto place = [&](int e) -> Place {
+    int hh = 0;
+    if (kKind != kCacheE4m3) {
+      hh = e / each;
+      e -= hh * each;
+    }
     const bool key = e < nk;
-    const int i = key ? e / uk : (e - nk) / uv, u = key ? e % uk : (e - nk) % uv;
+    const int i = key ? e / uk : (e - nk) / uv;
+    return {hh, i, key ? e - i * uk : e - nk - i * uv, key};
+  };
+  auto fetch = [&](const Place& p) -> Raw {
+    const int64_t t = run.row0 + p.i;
+    return p.key ? load_raw(a.k_new + t * a.k_new_stride + (h + p.h) * a.d_qk,
+                            unit_at(p.u, a.rot, a.interleaved))
+                 : load_raw(a.v_new + t * a.v_new_stride + (h + p.h) * a.d_v, unit_at(p.u, 0, 0));
+  };
+  // its values, turned; false if the token is not to be written
+  auto finish = [&](const Place& p, const Raw& raw, Unit& r) -> bool {
     int row = 0;
-    if (rot > 0 && (row = table_row(i)) < 0) return false;
-    const int64_t t = run.row0 + i;
-    if (key)
-      load_unit(a, a.k_new + t * a.k_new_stride + h * a.d_qk, u, rot, row, r);
-    else
-      load_unit(a, a.v_new + t * a.v_new_stride + h * a.d_v, u, 0, 0, r);
+    if (a.rot > 0 && (row = table_row(a, run.row0 + p.i, run.pos0 + p.i)) < 0) return false;
+    unpack(raw, r, a.f16);
+    if (p.key && p.u < a.rot / 16) {
+      Turn cs;
+      load_turn(a, p.u, row, cs);
+      turn(r, cs, a.interleaved);
+    }
     return true;
   };
-  auto store_kv = [&](int e, const Unit& r, float inv_k, float inv_v) {
-    const bool key = e < nk;
-    const int i = key ? e / uk : (e - nk) / uv, u = key ? e % uk : (e - nk) % uv;
-    char* dst = key ? kdst + i * a.k_tok : vdst + i * a.v_tok;
-    const int2 at = unit_at(u, key ? rot : 0, a.interleaved);
+  auto store = [&](const Place& p, const Unit& r, float inv_k, float inv_v) {
+    char* dst = p.key ? kdst + p.h * a.k_head + p.i * a.k_tok : vdst + p.h * a.v_head + p.i * a.v_tok;
+    const int2 at = unit_at(p.u, p.key ? a.rot : 0, a.interleaved);
     if (kKind == kCacheE4m3)
-      store8(reinterpret_cast<uint8_t*>(dst), at, r, key ? inv_k : inv_v);
+      store8(reinterpret_cast<uint8_t*>(dst), at, r, p.key ? inv_k : inv_v);
     else
       store16(reinterpret_cast<uint16_t*>(dst), at, r, kKind == kCacheF16);
   };
-  auto turn_queries = [&]() {
-    if (!a.q) return;
-    const int per = a.group * uk;
-    for (int e = tid; e < run.n * per; e += kThreads) {
-      const int i = e / per, hu = e % per;
-      int row = 0;
-      if (rot > 0 && (row = table_row(i)) < 0) continue;
-      const int64_t t = run.row0 + i;
-      const int head = (h * a.group + hu / uk) * a.d_qk;
-      Unit r;
-      load_unit(a, a.q + t * a.q_stride + head, hu % uk, rot, row, r);
-      store16(a.q_rot + t * a.q_rot_stride + head, unit_at(hu % uk, rot, a.interleaved), r, a.f16);
-    }
-  };
 
   if (kKind != kCacheE4m3) {
-    for (int e = tid; e < nkv; e += kThreads) {
-      Unit r;
-      if (load_kv(e, r)) store_kv(e, r, 1.f, 1.f);
+    for (int e0 = tid; e0 < nkv; e0 += 4 * kThreads) {
+      Raw raw[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (e0 + j * kThreads < nkv) raw[j] = fetch(place(e0 + j * kThreads));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int e = e0 + j * kThreads;
+        Unit r;
+        if (e < nkv && finish(place(e), raw[j], r)) store(place(e), r, 1.f, 1.f);
+      }
     }
-    turn_queries();
     return;
   }
 
   // E4M3: the maxima first
   Unit hold[kHold];
+  Raw raw[kHold];
   float mk = 0.f, mv = 0.f;
   unsigned ok = 0;
   bool any = false;  // some token is written
+  auto largest = [&](const Place& p, const Unit& r) {
+    const float m = unit_amax(r);
+    if (p.key) mk = fmaxf(mk, m);
+    else mv = fmaxf(mv, m);
+    any = true;
+  };
+#pragma unroll
+  for (int j = 0; j < kHold; ++j)
+    if (tid + j * kThreads < nkv) raw[j] = fetch(place(tid + j * kThreads));
 #pragma unroll
   for (int j = 0; j < kHold; ++j) {
     const int e = tid + j * kThreads;
-    if (e < nkv && load_kv(e, hold[j])) {
+    if (e < nkv && finish(place(e), raw[j], hold[j])) {
       ok |= 1u << j;
-      any = true;
-      const float m = unit_amax(hold[j]);
-      if (e < nk) mk = fmaxf(mk, m);
-      else mv = fmaxf(mv, m);
+      largest(place(e), hold[j]);
     }
   }
   for (int e = tid + kHold * kThreads; e < nkv; e += kThreads) {
     Unit r;
-    if (load_kv(e, r)) {
-      any = true;
-      const float m = unit_amax(r);
-      if (e < nk) mk = fmaxf(mk, m);
-      else mv = fmaxf(mv, m);
-    }
+    if (finish(place(e), fetch(place(e)), r)) largest(place(e), r);
   }
-  turn_queries();
   __shared__ float s_mk[kThreads / 32], s_mv[kThreads / 32];
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) {
@@ -324,10 +421,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Args a) {
   const float inv_k = 1.f / new_k, inv_v = 1.f / new_v;
 #pragma unroll
   for (int j = 0; j < kHold; ++j)
-    if (ok >> j & 1) store_kv(tid + j * kThreads, hold[j], inv_k, inv_v);
+    if (ok >> j & 1) store(place(tid + j * kThreads), hold[j], inv_k, inv_v);
   for (int e = tid + kHold * kThreads; e < nkv; e += kThreads) {
     Unit r;
-    if (load_kv(e, r)) store_kv(e, r, inv_k, inv_v);
+    if (finish(place(e), fetch(place(e)), r)) store(place(e), r, inv_k, inv_v);
   }
   if (tid == 0) {
     *pk = new_k;
@@ -344,11 +441,24 @@ cudaError_t launch_append(const Args& a, int kind, cudaStream_t st) {
     runs = (static_cast<int64_t>(a.num_tokens) >> a.page_shift) + 2ll * a.num_seqs;
     if (runs > a.num_tokens) runs = a.num_tokens;
   }
-  const dim3 grid(static_cast<unsigned>(runs), a.Hkv);
+  // heads of a 16-bit cache's block: about 1024 units of a whole page
+  int per_block = 1;
+  if (kind != kCacheE4m3)
+    while (per_block < a.Hkv &&
+           (2 * per_block * (a.d_qk + a.d_v) / 16 << (a.cu ? a.page_shift : 0)) <= 1024)
+      per_block *= 2;
+  int64_t blocks = runs * ((a.Hkv + per_block - 1) / per_block);
+  if (a.q) {
+    const int tokens = kThreads / (a.d_qk / 16);
+    blocks += (static_cast<int64_t>(a.num_tokens) + tokens - 1) / tokens *
+              ((a.Hq + kHeads - 1) / kHeads);
+  }
+  if (blocks >= 1ll << 31) return cudaErrorInvalidValue;
   auto kern = kind == kCacheE4m3  ? append_kernel<kCacheE4m3>
               : kind == kCacheF16 ? append_kernel<kCacheF16>
                                   : append_kernel<kCacheBf16>;
-  return launch_early(kern, grid, dim3(kThreads), 0, st, a);
+  return launch_early(kern, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, a,
+                      static_cast<int>(runs), per_block);
 }
 
 }  // namespace paged
