@@ -129,73 +129,61 @@ __device__ __forceinline__ float unit_amax(const Unit& r) {
 
 // The run of new tokens a block works on.
 struct Run {
-  int seq, page, slot0, n, row0, pos0;
+  int seq, col, slot0, n, row0, pos0;  // sequence, page's column of the table, slots, rows, position
 };
 
 // Block `c`'s run: the runs of all sequences in order, each sequence's new
 // positions cut at page borders.  With one token per sequence run c is
-// sequence c; otherwise every block sums the sequences' run counts.
+// sequence c; otherwise every block sums the sequences' run counts, and the
+// thread that finds run c among its sequence's hands it to the others.
 __device__ __forceinline__ bool find_run(const Args& a, int c, Run* out) {
   __shared__ int s_sum[kThreads / 32];
-  __shared__ int s_seq, s_left;
-  if (threadIdx.x == 0) s_seq = -1;
-  int base = 0;
-  if (a.cu) {
-    for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
-      const int s = s0 + threadIdx.x;
-      int cnt = 0;
-      if (s < a.num_seqs) {
-        const Seq q = load_seq(a, s);
-        if (q.n > 0) {
-          const int first = max(0, q.len - q.n);
-          if (q.len > 0) cnt = ((q.len - 1) >> a.page_shift) - (first >> a.page_shift) + 1;
-        }
-      }
-      int x = cnt;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, d);
-        if ((threadIdx.x & 31) >= d) x += y;
-      }
-      if ((threadIdx.x & 31) == 31) s_sum[threadIdx.x / 32] = x;
-      __syncthreads();
-      int before = base;
-      for (int w = 0; w < kThreads / 32; ++w) {
-        const int t = s_sum[w];
-        if (w < static_cast<int>(threadIdx.x) / 32) before += t;
-        base += t;
-      }
-      if (c >= before + x - cnt && c < before + x) {
-        s_seq = s;
-        s_left = c - (before + x - cnt);
-      }
-      __syncthreads();
-      if (s_seq >= 0 || c < base) break;
-    }
-  } else {
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      s_seq = c;
-      s_left = 0;
-    }
-    __syncthreads();
+  __shared__ Run s_run;
+  auto cut = [&](int s, const Seq& q, int left) -> Run {
+    const int first = q.len - q.n, lo = max(0, first);  // first < 0: those tokens have no slot
+    if (first < 0) flag_bounds(a);
+    const int col = (lo >> a.page_shift) + left;
+    const int p0 = max(lo, col << a.page_shift), p1 = min(q.len, (col + 1) << a.page_shift);
+    return {s, col, p0 & ((1 << a.page_shift) - 1), p1 - p0, q.row0 + (p0 - first), p0};
+  };
+  if (!a.cu) {
+    const Seq q = load_seq(a, c);
+    if (q.len <= 0) return false;  // length 0: the row is padding
+    *out = cut(c, q, 0);
+    return true;
   }
-  if (s_seq < 0) return false;
-  const Seq q = load_seq(a, s_seq);
-  const int first = q.len - q.n;  // may be negative: those tokens have no slot
-  const int lo = max(0, first);
-  if (q.n <= 0 || q.len <= 0) return false;  // length 0: the rows are padding
-  if (first < 0 && threadIdx.x == 0) flag_bounds(a);
-  const int col = (lo >> a.page_shift) + s_left;
-  const int p0 = max(lo, col << a.page_shift);
-  const int p1 = min(q.len, (col + 1) << a.page_shift);
-  out->seq = s_seq;
-  out->page = page_of(a, s_seq, p0);
-  out->slot0 = p0 & ((1 << a.page_shift) - 1);
-  out->n = p1 - p0;
-  out->row0 = q.row0 + (p0 - first);
-  out->pos0 = p0;
-  return out->page >= 0;
+  if (threadIdx.x == 0) s_run.seq = -1;
+  int base = 0;
+  for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
+    const int s = s0 + threadIdx.x;
+    Seq q = {0, 0, 0};
+    int cnt = 0;
+    if (s < a.num_seqs) {
+      q = load_seq(a, s);
+      if (q.n > 0 && q.len > 0)
+        cnt = ((q.len - 1) >> a.page_shift) - (max(0, q.len - q.n) >> a.page_shift) + 1;
+    }
+    int x = cnt;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, d);
+      if ((threadIdx.x & 31) >= d) x += y;
+    }
+    if ((threadIdx.x & 31) == 31) s_sum[threadIdx.x / 32] = x;
+    __syncthreads();
+    int before = base;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const int t = s_sum[w];
+      if (w < static_cast<int>(threadIdx.x) / 32) before += t;
+      base += t;
+    }
+    before += x - cnt;
+    if (c >= before && c < before + cnt) s_run = cut(s, q, c - before);
+    __syncthreads();
+    if (s_run.seq >= 0 || c < base) break;
+  }
+  *out = s_run;
+  return out->seq >= 0;
 }
 
 // Row of the rotation tables for a token, or -1 (reported).
@@ -271,7 +259,7 @@ __device__ __forceinline__ void turn_queries(const Args& a, int block) {
 // Blocks [0, runs * groups) write keys and values, of `per_block` heads (one
 // with an E4M3 cache), the others turn queries.
 template <int kKind>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     append_kernel(const __grid_constant__ Args a, int runs, int per_block) {
   sm103::grid_dep_wait();
   const int groups = (a.Hkv + per_block - 1) / per_block;
@@ -285,8 +273,7 @@ __global__ void __launch_bounds__(kThreads)
   const int uk = a.d_qk / 16, uv = a.d_v / 16;
   const int nk = run.n * uk, each = nk + run.n * uv;
   const int nkv = each * min(per_block, a.Hkv - h);
-  char* kdst = a.kc + run.page * a.k_page + h * a.k_head + run.slot0 * a.k_tok;
-  char* vdst = a.vc + run.page * a.v_page + h * a.v_head + run.slot0 * a.v_tok;
+  char *kdst, *vdst;  // the run's first slot of head h
 
   // Unit e of the run's keys, then values.
   struct Place {
@@ -330,14 +317,24 @@ __global__ void __launch_bounds__(kThreads)
       store16(reinterpret_cast<uint16_t*>(dst), at, r, kKind == kCacheF16);
   };
 
+  // The first units are on their way while the page is looked up.
+  Raw raw[kHold];
+  auto fetch_from = [&](int e0) {
+#pragma unroll
+    for (int j = 0; j < kHold; ++j)
+      if (e0 + j * kThreads < nkv) raw[j] = fetch(place(e0 + j * kThreads));
+  };
+  fetch_from(tid);
+  const int page = page_of(a, run.seq, run.pos0);
+  if (page < 0) return;
+  kdst = a.kc + page * a.k_page + h * a.k_head + run.slot0 * a.k_tok;
+  vdst = a.vc + page * a.v_page + h * a.v_head + run.slot0 * a.v_tok;
+
   if (kKind != kCacheE4m3) {
-    for (int e0 = tid; e0 < nkv; e0 += 4 * kThreads) {
-      Raw raw[4];
+    for (int e0 = tid; e0 < nkv; e0 += kHold * kThreads) {
+      if (e0 != tid) fetch_from(e0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (e0 + j * kThreads < nkv) raw[j] = fetch(place(e0 + j * kThreads));
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kHold; ++j) {
         const int e = e0 + j * kThreads;
         Unit r;
         if (e < nkv && finish(place(e), raw[j], r)) store(place(e), r, 1.f, 1.f);
@@ -346,9 +343,9 @@ __global__ void __launch_bounds__(kThreads)
     return;
   }
 
-  // E4M3: the maxima first
-  Unit hold[kHold];
-  Raw raw[kHold];
+  // E4M3: the maxima first.  What is held is the unit as loaded; it is turned
+  // again at the store (its cosines are in L1 by then), which leaves the
+  // registers to a third block.
   float mk = 0.f, mv = 0.f;
   unsigned ok = 0;
   bool any = false;  // some token is written
@@ -359,14 +356,12 @@ __global__ void __launch_bounds__(kThreads)
     any = true;
   };
 #pragma unroll
-  for (int j = 0; j < kHold; ++j)
-    if (tid + j * kThreads < nkv) raw[j] = fetch(place(tid + j * kThreads));
-#pragma unroll
   for (int j = 0; j < kHold; ++j) {
     const int e = tid + j * kThreads;
-    if (e < nkv && finish(place(e), raw[j], hold[j])) {
+    Unit r;
+    if (e < nkv && finish(place(e), raw[j], r)) {
       ok |= 1u << j;
-      largest(place(e), hold[j]);
+      largest(place(e), r);
     }
   }
   for (int e = tid + kHold * kThreads; e < nkv; e += kThreads) {
@@ -383,8 +378,8 @@ __global__ void __launch_bounds__(kThreads)
     s_mk[tid / 32] = mk;
     s_mv[tid / 32] = mv;
   }
-  float* pk = a.k_scale + static_cast<int64_t>(run.page) * a.Hkv + h;
-  float* pv = a.v_scale + static_cast<int64_t>(run.page) * a.Hkv + h;
+  float* pk = a.k_scale + static_cast<int64_t>(page) * a.Hkv + h;
+  float* pv = a.v_scale + static_cast<int64_t>(page) * a.Hkv + h;
   const float old_k = run.slot0 ? *pk : 0.f, old_v = run.slot0 ? *pv : 0.f;
   if (!__syncthreads_or(any)) return;
 #pragma unroll
@@ -421,7 +416,12 @@ __global__ void __launch_bounds__(kThreads)
   const float inv_k = 1.f / new_k, inv_v = 1.f / new_v;
 #pragma unroll
   for (int j = 0; j < kHold; ++j)
-    if (ok >> j & 1) store(place(tid + j * kThreads), hold[j], inv_k, inv_v);
+    if (ok >> j & 1) {
+      const Place p = place(tid + j * kThreads);
+      Unit r;
+      finish(p, raw[j], r);
+      store(p, r, inv_k, inv_v);
+    }
   for (int e = tid + kHold * kThreads; e < nkv; e += kThreads) {
     Unit r;
     if (finish(place(e), fetch(place(e)), r)) store(place(e), r, inv_k, inv_v);
