@@ -149,12 +149,8 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t c) {
 __device__ __forceinline__ float e4m3_value(uint8_t c) {
   return __half2float(__ushort_as_half(static_cast<uint16_t>(e4m3x2_f16x2(c))));
 }
-// Two values to E4M3 codes, nearest even; the callers' values are at most 448
-// in magnitude but for infinities, which become NaN here like NaN itself.
+// Two values of at most 448 in magnitude, or NaN, to E4M3 codes, nearest even.
 __device__ __forceinline__ uint16_t f32x2_e4m3x2(float lo, float hi) {
-  const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fc00000);
-  lo = fabsf(lo) == inf ? nan : lo;
-  hi = fabsf(hi) == inf ? nan : hi;
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;

@@ -104,7 +104,15 @@ __device__ __forceinline__ void store16(uint16_t* dst, int2 at, const Unit& r, i
   *reinterpret_cast<uint4*>(dst + at.y) = hi;
 }
 
-__device__ __forceinline__ void store8(uint8_t* dst, int2 at, const Unit& r, float inv) {
+__device__ __forceinline__ void store8(uint8_t* dst, int2 at, Unit r, float inv) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) m = sm103::fmax3(m, fabsf(r.x[i]), fabsf(r.x[i + 1]));
+  if (m == __int_as_float(0x7f800000)) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (fabsf(r.x[i]) == __int_as_float(0x7f800000)) r.x[i] = __int_as_float(0x7fc00000);
+  }
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -116,9 +124,14 @@ __device__ __forceinline__ void store8(uint8_t* dst, int2 at, const Unit& r, flo
   *reinterpret_cast<uint2*>(dst + at.y) = make_uint2(w[2], w[3]);
 }
 
-// Largest finite magnitude (infinities and NaN become NaN codes).
+// Largest finite magnitude (infinities and NaN become NaN codes and are left
+// out; fmax leaves NaN out by itself).
 __device__ __forceinline__ float unit_amax(const Unit& r) {
   float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) m = sm103::fmax3(m, fabsf(r.x[i]), fabsf(r.x[i + 1]));
+  if (m < __int_as_float(0x7f800000)) return m;
+  m = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const float x = fabsf(r.x[i]);
@@ -198,8 +211,9 @@ __device__ __forceinline__ int table_row(const Args& a, int row, int pos) {
 
 // Queries: this block's tokens and eight heads.
 constexpr int kHeads = 8;
+template <int units>
 __device__ __forceinline__ void turn_queries(const Args& a, int block) {
-  const int units = a.d_qk / 16, tokens = kThreads / units;
+  constexpr int tokens = kThreads / units;
   const int groups = (a.Hq + kHeads - 1) / kHeads;
   const int u = threadIdx.x % units, i = threadIdx.x / units;
   const int t = (block / groups) * tokens + i, h0 = (block % groups) * kHeads;
@@ -258,19 +272,18 @@ __device__ __forceinline__ void turn_queries(const Args& a, int block) {
 
 // Blocks [0, runs * groups) write keys and values, of `per_block` heads (one
 // with an E4M3 cache), the others turn queries.
-template <int kKind>
+template <int kKind, int uk, int uv>
 __global__ void __launch_bounds__(kThreads, 3)
     append_kernel(const __grid_constant__ Args a, int runs, int per_block) {
   sm103::grid_dep_wait();
   const int groups = (a.Hkv + per_block - 1) / per_block;
   if (static_cast<int>(blockIdx.x) >= runs * groups) {
-    turn_queries(a, blockIdx.x - runs * groups);
+    turn_queries<uk>(a, blockIdx.x - runs * groups);
     return;
   }
   Run run;
   if (!find_run(a, blockIdx.x / groups, &run)) return;
   const int h = (blockIdx.x % groups) * per_block, tid = threadIdx.x;
-  const int uk = a.d_qk / 16, uv = a.d_v / 16;
   const int nk = run.n * uk, each = nk + run.n * uv;
   const int nkv = each * min(per_block, a.Hkv - h);
   char *kdst, *vdst;  // the run's first slot of head h
@@ -432,6 +445,21 @@ __global__ void __launch_bounds__(kThreads, 3)
   }
 }
 
+template <int kKind, int uk>
+cudaError_t launch_width(const Args& a, dim3 grid, int runs, int per_block, cudaStream_t st) {
+  return a.d_v == 64
+             ? launch_early(append_kernel<kKind, uk, 4>, grid, dim3(kThreads), 0, st, a, runs,
+                            per_block)
+             : launch_early(append_kernel<kKind, uk, 8>, grid, dim3(kThreads), 0, st, a, runs,
+                            per_block);
+}
+template <int kKind>
+cudaError_t launch_dims(const Args& a, dim3 grid, int runs, int per_block, cudaStream_t st) {
+  return a.d_qk == 64    ? launch_width<kKind, 4>(a, grid, runs, per_block, st)
+         : a.d_qk == 128 ? launch_width<kKind, 8>(a, grid, runs, per_block, st)
+                         : launch_width<kKind, 12>(a, grid, runs, per_block, st);
+}
+
 }  // namespace
 
 cudaError_t launch_append(const Args& a, int kind, cudaStream_t st) {
@@ -454,11 +482,11 @@ cudaError_t launch_append(const Args& a, int kind, cudaStream_t st) {
               ((a.Hq + kHeads - 1) / kHeads);
   }
   if (blocks >= 1ll << 31) return cudaErrorInvalidValue;
-  auto kern = kind == kCacheE4m3  ? append_kernel<kCacheE4m3>
-              : kind == kCacheF16 ? append_kernel<kCacheF16>
-                                  : append_kernel<kCacheBf16>;
-  return launch_early(kern, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, a,
-                      static_cast<int>(runs), per_block);
+  const dim3 grid(static_cast<unsigned>(blocks));
+  const int n = static_cast<int>(runs);
+  return kind == kCacheE4m3  ? launch_dims<kCacheE4m3>(a, grid, n, per_block, st)
+         : kind == kCacheF16 ? launch_dims<kCacheF16>(a, grid, n, per_block, st)
+                             : launch_dims<kCacheBf16>(a, grid, n, per_block, st);
 }
 
 }  // namespace paged
