@@ -427,11 +427,14 @@ attn_status_t attn_fwd_noalloc(const attn_params_t* p, void* o, float* lse, void
  * initialisation and carries nothing from call to call.
  *
  * Checks on the device: a page id outside [0, num_pages), a position outside
- * the table's row or below 0, a rotation position outside [0, rope_len) and
- * offsets outside [0, num_tokens] or decreasing are never used.  The
- * tokens concerned are not written (append) or count as masked (attention),
- * and ATTN_ERR_DEVICE_BOUNDS is stored in *status (if given; the library never
- * clears it). */
+ * the table's row or below 0, a rotation position outside [0, rope_len),
+ * a negative length, and offsets outside [0, num_tokens] or decreasing are
+ * never used.  The keys and values concerned are not written (append; a query
+ * is left out only for its offsets, length or rotation position) or count as
+ * masked (attention), and ATTN_ERR_DEVICE_BOUNDS is stored in *status, if
+ * given; the library never clears it.  A wait of the attention kernels that
+ * runs past its limit (2 s) stores ATTN_ERR_DEVICE_TIMEOUT there and the
+ * kernel ends. */
 #define ATTN_PAGED_PARAMS_VERSION 1
 typedef struct {
   int32_t struct_version; /* = ATTN_PAGED_PARAMS_VERSION */
