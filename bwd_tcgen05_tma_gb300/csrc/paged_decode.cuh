@@ -58,9 +58,6 @@ struct Cfg {
   static constexpr int kStageK = 16 * DQK * kCb;
   static constexpr int kStageV = 16 * DV * kCb;
   static constexpr int kStage = kStageK + kStageV;
-  static constexpr int kKs = DQK / 16;  // K slices of S^T
-  static constexpr int kMt = DV / 16;   // row tiles of O^T
-  static constexpr int kRows = 8 * NT;
   // Steps a warp takes together: with one tile of rows a step is a chain of
   // dependent short operations, and two chains hide each other's latency (and
   // share the maximum's shuffles); more rows are independent work already.
@@ -69,20 +66,24 @@ struct Cfg {
   // other joins its warps' states
   static constexpr int kBlocks = NT == 1 && kStage <= 4096 ? 2 : 1;
   static constexpr int kBudget = kBlocks == 2 ? 100 * 1024 : 200 * 1024;
+  static constexpr int kKs = DQK / 16;  // K slices of S^T
+  static constexpr int kMt = DV / 16;   // row tiles of O^T
+  static constexpr int kRows = 8 * NT;
+  // queries of more rows than registers hold, a copy for each warp
+  static constexpr bool kQSmem = NT > 2;
+  static constexpr int kQBytes = kQSmem ? NT * kKs * 256 : 0;
   // the steps in hand, and as many on their way
-  static constexpr int kFitWarps = kBudget / (2 * kTogether * kStage);
+  static constexpr int kFitWarps = kBudget / (2 * kTogether * kStage + kQBytes);
   static constexpr int kWarps = kFitWarps > 8 ? 8 : kFitWarps;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kTileKeys = 16 * kWarps;
-  static constexpr int kFit = kBudget / (kWarps * kStage);
+  static constexpr int kFit = (kBudget - kWarps * kQBytes) / (kWarps * kStage);
   static constexpr int kStages = kFit > 4 * kTogether ? 4 * kTogether : kFit;
   static_assert(kStages >= 2 * kTogether && kWarps >= 4, "ring");
-  static constexpr bool kQSmem = NT > 2;
-  static constexpr int kQBytes = kQSmem ? NT * kKs * 256 : 0;
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kMerge = kWarps * 8 * DV * 4;
   static constexpr int kBody = (kRing > kMerge ? kRing : kMerge);
-  static constexpr int kSmem = 1024 + kBody + kQBytes;  // the ring starts at a multiple of 1024
+  static constexpr int kSmem = 1024 + kBody + kWarps * kQBytes;  // the ring starts at a multiple of 1024
 };
 
 __device__ __forceinline__ uint2 lds64(uint32_t p) {
@@ -159,8 +160,17 @@ __device__ __forceinline__ Need need_of(const Args& a, int s, int rows_per) {
 // first one unit `off` of sequence `s`.
 struct Share {
   int64_t off, begin, end, total;
-  int s, ctas;
+  int64_t base;  // units of a share; the first `more` shares have one more
+  int s, more;
   bool solo;
+  __device__ __forceinline__ int64_t start(int64_t k) const {
+    return k * base + (k < more ? k : more);
+  }
+  // the share that unit x is in
+  __device__ __forceinline__ int of(int64_t x) const {
+    const int64_t cut = more * (base + 1);
+    return static_cast<int>(x < cut ? x / (base + 1) : more + (x - cut) / base);
+  }
 };
 
 // Every thread of the block (solo: of the warp) returns the same values.
@@ -216,17 +226,24 @@ __device__ __forceinline__ Share find_share(const Args& a) {
     most = max(most, s_max[x]);
   }
   Share sh;
-  sh.solo = !C::kQSmem && static_cast<int64_t>(most) * gridDim.x * kWarps <= 2 * total[1];
+  sh.solo = static_cast<int64_t>(most) * gridDim.x * kWarps <= 2 * total[1];
   sh.total = total[sh.solo];
-  sh.ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), sh.total));
   const int64_t lo = before[sh.solo], hi = lo + mine[sh.solo];
-  const int64_t workers = sh.solo ? static_cast<int64_t>(gridDim.x) * kWarps : sh.ctas;
+  const int workers =
+      static_cast<int>(min(static_cast<int64_t>(gridDim.x) * (sh.solo ? kWarps : 1), sh.total));
   const int me = sh.solo ? blockIdx.x * kWarps + w : blockIdx.x;
+  sh.base = 0;
+  sh.more = 0;
+  if (workers > 0) {
+    sh.base = (sh.total >> 31) ? sh.total / workers
+                               : static_cast<uint32_t>(sh.total) / static_cast<uint32_t>(workers);
+    sh.more = static_cast<int>(sh.total - sh.base * workers);
+  }
 #pragma unroll 1
   for (int x = 0; x < (sh.solo ? kWarps : 1); ++x) {
-    const int64_t k = sh.solo ? static_cast<int64_t>(blockIdx.x) * kWarps + x : blockIdx.x;
+    const int k = sh.solo ? blockIdx.x * kWarps + x : blockIdx.x;
     if (k >= workers) break;
-    const int64_t begin = k * sh.total / workers;
+    const int64_t begin = sh.start(k);
     if (begin >= lo && begin < hi) {
       int s = first;
       int64_t off = begin - lo;
@@ -244,8 +261,8 @@ __device__ __forceinline__ Share find_share(const Args& a) {
   __syncthreads();
   sh.begin = sh.end = 0;
   if (me < workers) {
-    sh.begin = me * sh.total / workers;
-    sh.end = (me + 1) * sh.total / workers;
+    sh.begin = sh.start(me);
+    sh.end = sh.start(me + 1);
   }
   sh.s = s_seq[sh.solo ? w : 0];
   sh.off = s_off[sh.solo ? w : 0];
@@ -280,7 +297,7 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
 
   uint8_t* const body = smem + (-smem_u32(smem) & 1023u);
   const uint32_t ring = smem_u32(body) + w * (C::kStages * C::kStage);
-  const uint32_t qs = smem_u32(body) + C::kBody;
+  const uint32_t qs = smem_u32(body) + C::kBody + w * C::kQBytes;
   float* const s_o = reinterpret_cast<float*>(body);
   // the ring runs on from item to item: stage and phase of the next copy, and
   // of the next step to compute
@@ -302,7 +319,9 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
       nd = need_of(a, ++seq, C::kRows);
       continue;
     }
-    const int item = static_cast<int>(off / cost), u0 = static_cast<int>(off - static_cast<int64_t>(item) * cost);
+    const int item = static_cast<int>((off >> 31) ? off / cost
+                                                  : static_cast<uint32_t>(off) / static_cast<uint32_t>(cost));
+    const int u0 = static_cast<int>(off - static_cast<int64_t>(item) * cost);
     // units [u0, u1): an item's start, then its tiles [t0, t1)
     const int u1 = sh.solo ? cost
                            : static_cast<int>(min(static_cast<int64_t>(cost), u0 + (sh.end - at)));
@@ -435,15 +454,13 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
                                            __uint_as_float(raw[ks][i] & 0xffff0000u) * to);
       }
       if constexpr (C::kQSmem) {
-        // every warp would write the same: one writes
-        if (w == 0) {
+        // (a lane reads back what it wrote itself)
 #pragma unroll
-          for (int ks = 0; ks < C::kKs; ++ks)
-            asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(qs + (nt * C::kKs + ks) * 256 +
-                                                                lane * 8),
-                         "r"(raw[ks][0]), "r"(raw[ks][1])
-                         : "memory");
-        }
+        for (int ks = 0; ks < C::kKs; ++ks)
+          asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(qs + (nt * C::kKs + ks) * 256 +
+                                                              lane * 8),
+                       "r"(raw[ks][0]), "r"(raw[ks][1])
+                       : "memory");
       } else {
 #pragma unroll
         for (int ks = 0; ks < C::kKs; ++ks) {
@@ -458,7 +475,6 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
         cpos[nt][c] = rr < rows ? pos0 + div_group(a, rr) : INT_MIN;
       }
     }
-    if constexpr (C::kQSmem) __syncthreads();
 
     float o[NT][C::kMt][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -876,8 +892,7 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
     if (!complete && t0 == 0 && tid == 0) {
       // first of an item's pieces: blocks up to the one that holds its last tile
       const int64_t end = here + cost - u0;  // of the item's units
-      const int c1 = static_cast<int>((end * sh.ctas + sh.total - 1) / sh.total) - 1;
-      a.split_desc[blockIdx.x] = make_int4(c1 - blockIdx.x + 1, seq, hk, rb);
+      a.split_desc[blockIdx.x] = make_int4(sh.of(end - 1) - blockIdx.x + 1, seq, hk, rb);
     }
     sm103::fence_proxy_async_smem();
     __syncthreads();  // the sums are read before the next piece's copies fill the ring
