@@ -304,10 +304,9 @@ def make_paged_params(*, dtype, cache_dtype, k_cache, v_cache, page_table, seq_l
     max_pages]; seq_lens: int32 [num_seqs], new tokens included; q, q_rot
     [tokens, Hq, d_qk], k_new, v_new [tokens, Hkv, dim]; rope_cos, rope_sin:
     fp32 [rope_len, rot_dim / 2] (None: no rotation); scale: softmax scale
-    (None: d_qk ** -0.5).  The block holds the tensors' addresses, so they must
-    outlive its calls; their contents may change between calls.  All tensors
-    are on the device that is current when the block is made, which is also
-    the one its calls must be made on."""
+    (None: d_qk ** -0.5).  The block holds the tensors' addresses and keeps them
+    alive; their contents may change between calls.  All tensors are on the
+    device that is current when the block is made and when it is used."""
     import torch
 
     if q is None and q_rot is None and k_new is None:
@@ -360,6 +359,7 @@ def make_paged_params(*, dtype, cache_dtype, k_cache, v_cache, page_table, seq_l
             raise ValueError(f"{name}: [num_pages, Hkv]")
 
     p = attn_paged_params_t()
+    p.tensors, p.device = given, device.index
     p.struct_version = ATTN_PAGED_PARAMS_VERSION
     p.dtype, p.cache_dtype, p.mask = DTYPES[dtype], DTYPES[cache_dtype], MASKS[mask]
     rows = next(t for t in (q, q_rot, k_new) if t is not None)
@@ -407,8 +407,17 @@ def attn_paged_workspace_size(p):
     return int(load_library().attn_paged_workspace_size(ctypes.byref(p)))
 
 
+def _on_device(p):
+    import torch
+
+    if torch.cuda.current_device() != p.device:
+        raise ValueError(f"tensors on cuda:{p.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
 def attn_paged_append(p, stream=None):
     """Enqueue the append on `stream` (default: torch's current stream)."""
+    _on_device(p)
     s = load_library().attn_paged_append(ctypes.byref(p), _stream(stream))
     if s != 0:
         raise AttnError(s, "attn_paged_append")
@@ -416,7 +425,15 @@ def attn_paged_append(p, stream=None):
 
 def attn_paged_fwd(p, o, lse, ws, stream=None):
     """Enqueue the attention over the cache on `stream` (default: torch's
-    current stream).  o: [tokens, Hq, d_v]; lse: fp32 [Hq, tokens] or None."""
+    current stream).  o: [tokens, Hq, d_v]; lse: fp32 [Hq, tokens] or None;
+    both contiguous."""
+    _on_device(p)
+    for name, t, n in (("o", o, p.num_tokens * p.Hq * p.d_v),
+                       ("lse", lse, p.num_tokens * p.Hq)):
+        if t is not None and (t.numel() != n or not t.is_contiguous() or
+                              t.element_size() != (2 if name == "o" else 4)):
+            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected a contiguous tensor of "
+                             f"{n} elements")
     s = load_library().attn_paged_fwd(ctypes.byref(p), _ptr(o), _ptr(lse), _ptr(ws),
                                       ws.numel() * ws.element_size(), _stream(stream))
     if s != 0:

@@ -45,7 +45,10 @@ attn_status_t validate(const attn_paged_params_t* p) {
   if (p->d_v != 64 && p->d_v != 128) return ATTN_ERR_UNSUPPORTED;
   if (p->page_size < 16 || p->page_size > 256 || (p->page_size & (p->page_size - 1)))
     return ATTN_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(p->max_pages) * p->page_size >= (1ll << 31)) return ATTN_ERR_UNSUPPORTED;
+  // positions and packed rows are 32-bit, with room for a window or a tile beyond
+  if (static_cast<int64_t>(p->max_pages) * p->page_size > (1ll << 30) ||
+      static_cast<int64_t>(p->num_tokens) * (p->Hq / p->Hkv) > (1ll << 30))
+    return ATTN_ERR_UNSUPPORTED;
   if (!p->cu_seqlens_q && p->num_tokens != p->num_seqs) return ATTN_ERR_SHAPE_MISMATCH;
   const bool none = p->num_seqs == 0 || p->num_tokens == 0;
   if (!none && (!p->seq_lens || (!p->page_table && p->max_pages > 0) ||
@@ -112,7 +115,7 @@ void fill(Args& a, const attn_paged_params_t* p) {
   a.max_pages = p->max_pages;
   a.f16 = p->dtype == ATTN_DTYPE_FP16;
   a.causal = p->mask == ATTN_MASK_CAUSAL;
-  a.window = p->window_left < 0 ? -1 : p->window_left;
+  a.window = p->window_left < 0 ? -1 : p->window_left < (1 << 30) ? p->window_left : 1 << 30;
   a.scale = p->scale;
   a.table = p->page_table;
   a.table_stride = p->table_stride;

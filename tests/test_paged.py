@@ -261,6 +261,46 @@ def test_attend_any_length_hint(hint):
     _attend(c, max_q_len=hint)
 
 
+def test_shared_prefix_and_strided_table():
+    """Two sequences that list the same pages for their first 48 tokens, tables
+    with rows further apart than their columns, windows of any size."""
+    from bwd_tcgen05_tma_gb300 import attn as A
+
+    c = Paged([3, 20], [60, 90], seed=41)
+    c.table[1, :3] = c.table[0, :3]
+    wide = torch.full((2, c.table.shape[1] + 5), -7, dtype=torch.int32, device="cuda")
+    wide[:, :c.table.shape[1]] = torch.tensor(c.table, dtype=torch.int32)
+    c.t["table"] = wide[:, :c.table.shape[1]]
+    A.attn_paged_append(c.params())
+    for window in (None, 2 ** 31 - 1, 70):
+        p = c.params(q_rot=None, window_left=window)
+        o, lse = c.attend(p)
+        assert c.status() == 0
+        check_attend(c, o, lse, c.oracle_attend(c.q, window=-1 if window is None else window))
+
+
+def test_lengths_behind_the_table_are_reported():
+    """A length beyond the table's row: what the table has counts, the rest is
+    masked, and the status says so (few rows and many)."""
+    from bwd_tcgen05_tma_gb300 import attn as A
+
+    for new in (1, 80):
+        c = Paged([new], [100], seed=42, spare=0)
+        A.attn_paged_append(c.params())
+        assert c.status() == 0
+        full = c.t["table"]
+        c.t["table"] = full[:, :5].contiguous()  # 80 of the tokens
+        o, lse = c.attend(c.params(q_rot=None, mask="NONE"))
+        assert c.status() == 7
+        lens, c.lens = c.lens, [80]
+        src = {n: c.cache_host(n) for n in ("k", "v")}
+        ref = P.attend(c.q, lambda s: P.gather(*src["k"], c.table[s], 16, 80),
+                       lambda s: P.gather(*src["v"], c.table[s], 16, 80), [80], c.cu,
+                       c.d_qk ** -0.5, causal=False)
+        check_attend(c, o, lse, ref)
+        c.lens = lens
+
+
 def test_attend_without_lse():
     from bwd_tcgen05_tma_gb300 import attn as A
 

@@ -67,7 +67,8 @@ BOTH = [
     (dict(d_qk=96), UNSUPPORTED), (dict(d_v=192), UNSUPPORTED),
     (dict(page_size=8), UNSUPPORTED), (dict(page_size=48), UNSUPPORTED),
     (dict(page_size=512), UNSUPPORTED),
-    (dict(max_pages=1 << 25, table_stride=1 << 25), UNSUPPORTED),  # 2^31 positions
+    (dict(max_pages=(1 << 24) + 1, table_stride=1 << 25), UNSUPPORTED),  # over 2^30 positions
+    (dict(num_seqs=(1 << 28) + 1, num_tokens=(1 << 28) + 1), UNSUPPORTED),  # over 2^30 rows
     (dict(num_tokens=5), SHAPE),  # one token per sequence without offsets
     (dict(seq_lens=None), INVALID), (dict(page_table=None), INVALID),
     (dict(k_cache=None), INVALID), (dict(v_cache=None), INVALID),
