@@ -17,7 +17,8 @@ VALUES = P.e4m3_values()
 class Paged:
     """new[s] new tokens behind ctx[s] cached ones for each sequence.
 
-    layout "hnd" keeps a page as [Hkv, page, dim], "nhd" as [page, Hkv, dim];
+    layout "hnd" keeps a page as [Hkv, page, dim], "nhd" as [page, Hkv, dim],
+    "packed" leaves room for another cache between pages and behind dims;
     fused: q, k_new, v_new are slices of one projection; pad: rows behind the
     last sequence; one: no offsets (one new token each)."""
 
@@ -90,7 +91,16 @@ class Paged:
             vals, scale = self.host[name]
             x = torch.from_numpy(vals).to(device)
             x = x.float().to(TORCH[cache])
-            if layout == "nhd":
+            d = x.shape[3]
+            if layout == "packed":  # K and V of a page side by side
+                both = torch.zeros(pages, 2, *x.shape[1:3], max(d_qk, d_v), dtype=torch.uint8,
+                                   device=device)
+                if cache != "fp8_e4m3":
+                    both = both.to(torch.int16)
+                side = both[:, 0 if name == "k" else 1, :, :, :d]
+                side.copy_(x.view(both.dtype))
+                x = both.view(TORCH[cache])[:, 0 if name == "k" else 1, :, :, :d]
+            elif layout == "nhd":
                 x = x.view(torch.uint8 if cache == "fp8_e4m3" else torch.int16)
                 x = x.transpose(1, 2).contiguous().view(TORCH[cache]).transpose(1, 2)
             t[name + "_cache"] = x

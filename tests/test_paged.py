@@ -43,6 +43,7 @@ APPEND = {
     "nhd": dict(new=[18, 2], ctx=[15, 16], layout="nhd", grow=20.0),
     "nhd_fused_bf16": dict(new=[18, 2], ctx=[15, 16], layout="nhd", fused=True, cache="bf16"),
     "fused_shifted": dict(new=[18, 2], ctx=[15, 16], fused=True, pos_shift=100),
+    "packed": dict(new=[18, 2], ctx=[15, 16], layout="packed", d_qk=192, grow=20.0),
     "many_seqs": dict(new=[i % 3 for i in range(600)], ctx=[i % 7 for i in range(600)], Hq=2,
                       Hkv=1, d_qk=64, d_v=64),
 }
@@ -194,6 +195,14 @@ ATTEND = {
     "decode_64_128_bf16": dict(new=[1] * 2, ctx=[33, 300], one=True, d_qk=64, cache="bf16"),
     "decode_nhd": dict(new=[1] * 3, ctx=[33, 300, 64], one=True, layout="nhd"),
     "decode_many": dict(new=[1] * 300, ctx=[i % 40 for i in range(300)], one=True, Hq=2, Hkv=1),
+    "decode_group64": dict(new=[1] * 3, ctx=[33, 300, 0], one=True, Hq=64, Hkv=1),
+    "decode_group256": dict(new=[1] * 2, ctx=[200, 0], one=True, Hq=256, Hkv=1, d_qk=64, d_v=64),
+    "decode_page256": dict(new=[1] * 3, ctx=[255, 700, 256], one=True, page=256),
+    "decode_packed_192": dict(new=[1] * 2, ctx=[33, 300], one=True, d_qk=192, layout="packed"),
+    "decode_nhd_bf16": dict(new=[1] * 2, ctx=[33, 300], one=True, layout="nhd", cache="bf16",
+                            page=128),
+    "verify_many": dict(new=[1 + i % 5 for i in range(200)], ctx=[i % 60 for i in range(200)],
+                        Hq=8, Hkv=1, d_qk=64, d_v=64),
     "padded": dict(new=[1, 0, 1], ctx=[20, 30, 0], pad=5),
     "verify": dict(new=[4, 1, 0, 5, 2], ctx=[100, 0, 50, 16, 31]),
     "verify_fp16_64": dict(new=[3, 2], ctx=[150, 40], d_qk=64, d_v=64, dtype="fp16", page=32),
@@ -207,6 +216,10 @@ ATTEND = {
     "chunk_192_64_bf16": dict(new=[65], ctx=[130], d_qk=192, d_v=64, cache="bf16"),
     "chunk_64_128": dict(new=[65], ctx=[130], d_qk=64, d_v=128, dtype="fp16"),
     "chunk_uneven_group": dict(new=[50, 61], ctx=[30, 0], Hq=6, Hkv=2, layout="nhd", fused=True),
+    "chunk_page256": dict(new=[100, 33], ctx=[500, 200], page=256),
+    "chunk_page256_bf16": dict(new=[100, 33], ctx=[500, 200], page=256, cache="bf16"),
+    "chunk_packed": dict(new=[100], ctx=[130], layout="packed", d_qk=192, page=32),
+    "chunk_packed_fp16": dict(new=[100], ctx=[130], layout="packed", cache="fp16", dtype="fp16"),
     "chunk_many_tiles": dict(new=[300, 150], ctx=[1500, 700], Hq=8, Hkv=1, page=64),
     "chunk_many_tiles_bf16": dict(new=[129, 64], ctx=[1500, 700], Hq=8, Hkv=2, cache="bf16"),
     "chunk_many_tiles_192": dict(new=[129, 64], ctx=[1500, 700], Hq=4, Hkv=1, d_qk=192, page=128),
@@ -242,8 +255,8 @@ def test_attend(name):
 
 
 @pytest.mark.parametrize("mask", list(MASKS))
-@pytest.mark.parametrize("name", ["decode", "verify", "chunk", "chunk_bf16",
-                                  "chunk_mixed_with_decode"])
+@pytest.mark.parametrize("name", ["decode", "verify", "verify_many", "chunk", "chunk_bf16",
+                                  "chunk_page256", "chunk_mixed_with_decode"])
 def test_attend_masks(name, mask):
     _attend(Paged(seed=22, **ATTEND[name]), **MASKS[mask])
 
@@ -378,6 +391,32 @@ def test_masked_values_have_no_influence(cache, new):
     # the rows that keep one: NaN scores and NaN or infinite values
     for r in {0, new - 1}:
         assert not torch.isfinite(lse[:, r]).any() or not torch.isfinite(o[r]).all()
+
+
+@pytest.mark.parametrize("cache", ["fp8_e4m3", "bf16"])
+@pytest.mark.parametrize("Hq", [2, 16])
+def test_masked_values_in_a_wide_batch(cache, Hq):
+    """As above where a warp takes whole sequences: a NaN in the last token's
+    value reaches the last row of its sequence only."""
+    from bwd_tcgen05_tma_gb300 import attn as A
+
+    n = 300
+    c = Paged([3] * n, [20 + i % 17 for i in range(n)], seed=43, cache=cache, Hq=Hq, Hkv=1)
+    A.attn_paged_append(c.params())
+    p = c.params(q_rot=None)
+    ref, ref_lse = (x.clone() for x in c.attend(p))
+    v = c.t["v_cache"].view(torch.uint8 if cache == "fp8_e4m3" else torch.int16)
+    hit = list(range(0, n, 7))
+    for s in hit:
+        j = c.lens[s] - 1
+        v[c.table[s, j // 16], 0, j % 16, 5] = 0x7F if cache == "fp8_e4m3" else 0x7FC0
+    o, lse = c.attend(p)
+    assert torch.equal(bits(lse), bits(ref_lse))
+    got, want = o.float().cpu(), ref.float().cpu()
+    rows = [3 * s + 2 for s in hit]
+    assert torch.isnan(got[rows, :, 5]).all()
+    want[rows, :, 5] = got[rows, :, 5]
+    assert torch.equal(bits(got), bits(want))
 
 
 @pytest.mark.parametrize("new", [1, 4, 60, 140])
