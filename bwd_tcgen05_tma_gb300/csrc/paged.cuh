@@ -190,7 +190,9 @@ cudaError_t launch_append(const Args& a, int kind, cudaStream_t st);
 // Few rows per KV head: `rows` is the expected number of query rows of one
 // KV head (tokens x group); sms the device's SM count.
 constexpr int kMaxCtas = 304;
-inline int decode_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+inline int decode_rows(int64_t rows) {
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : 32;
+}
 struct CacheMaps {
   CUtensorMap k, v;
 };
