@@ -2,6 +2,7 @@
 // and launches.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -136,11 +137,26 @@ void fill(Args& a, const attn_paged_params_t* p) {
   a.d_v = p->d_v;
 }
 
-// Which kernel: rows of one KV head that make the tensor-memory kernel's 256-row
-// blocks pay.
-constexpr int kManyRows = 64;
+// Which kernel, by the rows expected for a KV head and the keys a row can see.
+// The many-row kernel's time hardly depends on the rows up to 256, the few-row
+// kernel's grows with them.  d 128, 8 KV heads, us, few against many rows:
+//   16 x 4096 keys, E4M3: 32 rows 80 : 96, 48 rows 136 : 96, 128 rows 257 : 97;
+//     bf16: 88 : 85, 148 : 85, 279 : 87.
+//   1 x 32768 keys, E4M3: 32 rows 45 : 60, 48 rows 67 : 61; bf16: 51 : 56,
+//     75 : 56.
+// With few keys a row block's start weighs more than a second pass, and more
+// so in E4M3, whose pages are converted.  64 rows of each of 64 sequences:
+//   E4M3: 256 keys 46 : 68, 512 keys 76 : 84, 1024 keys 132 : 120;
+//   bf16: 256 keys 51 : 52, 512 keys 85 : 69; a window of 10 keys 20 : 44.
+// (Of 16 sequences of 256 keys: E4M3 43 : 30, bf16 40 : 22; the batch's size
+// moves the point, the keys a row sees move it more.)
+// 96 rows of 64 x 512 keys: E4M3 142 : 85, bf16 158 : 70.
 bool many_rows(const attn_paged_params_t* p) {
-  return p->num_pages > 0 && static_cast<int64_t>(p->max_q_len) * (p->Hq / p->Hkv) > kManyRows;
+  const int64_t rows = static_cast<int64_t>(p->max_q_len) * (p->Hq / p->Hkv);
+  int64_t keys = static_cast<int64_t>(p->max_pages) * p->page_size;
+  if (p->window_left >= 0) keys = std::min<int64_t>(keys, int64_t{p->window_left} + p->max_q_len);
+  const int64_t few_keys = p->cache_dtype == ATTN_DTYPE_FP8_E4M3 ? 768 : 192;
+  return p->num_pages > 0 && (rows > 64 || (rows > 32 && keys > few_keys));
 }
 
 // Workspace: descriptors of split items, then their partial states.

@@ -15,14 +15,21 @@
 // multiply-add per score as without them, since a group's maximum can be
 // scaled after it is found.
 //
-// What bounds it: at 8 heads a group and more than a few hundred tokens the
-// MMAs (2 x 128 x 128 x 2 d a tile and half); the exponentials and the
-// conversion run beside them on the other warps of the same schedulers.
+// What bounds it (1024 tokens over 31744 cached ones, 64 query heads, E4M3:
+// 784 us, 1.38 PFLOP/s, tensor pipe 58 % busy): S, P and O of two halves fill
+// tensor memory, so a half's MMAs and its softmax take turns, with only the
+// other half beside them; and shared memory, which the MMAs read at 192 KB a
+// tile of 2048 MMA clocks while the conversion reads 32 and writes 64.
 //
 // Work split.  As for few rows: all tiles in order (sequence, head, row block,
 // tile) cut into equal shares, one a block, one block an SM; causal row blocks
 // count only the tiles they need.  Pieces of a row block meet in a second
 // kernel.
+//
+// Roles: MMA issuer, TMA producer and scheduler (a warp each), four converter
+// warps, four softmax warps a half.  The scheduler hands out pieces so that the
+// walk's state stays out of the other roles' registers; loops that run once a
+// piece are rolled, since the roles share instruction caches.
 //
 // Values that are not finite in a tile that some rows mask in part are taken
 // out of the product (their zero weight would make NaN of them) and added in

@@ -489,8 +489,9 @@ typedef struct {
 } attn_paged_params_t;
 
 /* Workspace bytes attn_paged_fwd needs (0 on invalid parameters): 2.5 to 11 MB
- * for few query rows, 41 MB where max_q_len * Hq / Hkv > 64 (d_v = 128).
- * 256-byte aligned. */
+ * for few query rows, 41 MB (d_v = 128) where max_q_len * Hq / Hkv > 64, or > 32
+ * with more keys to see than some hundreds.  Depends on no device data; ask it
+ * again when a field changes.  256-byte aligned. */
 size_t attn_paged_workspace_size(const attn_paged_params_t* p);
 
 /* Rotates the new tokens and writes them into the cache. */
