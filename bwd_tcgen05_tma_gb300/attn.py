@@ -426,14 +426,20 @@ def attn_paged_append(p, stream=None):
 def attn_paged_fwd(p, o, lse, ws, stream=None):
     """Enqueue the attention over the cache on `stream` (default: torch's
     current stream).  o: [tokens, Hq, d_v]; lse: fp32 [Hq, tokens] or None;
-    both contiguous."""
+    both contiguous, as is ws, and all on the block's device."""
+    import torch
+
     _on_device(p)
-    for name, t, n in (("o", o, p.num_tokens * p.Hq * p.d_v),
-                       ("lse", lse, p.num_tokens * p.Hq)):
-        if t is not None and (t.numel() != n or not t.is_contiguous() or
-                              t.element_size() != (2 if name == "o" else 4)):
-            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, expected a contiguous tensor of "
-                             f"{n} elements")
+    want = torch.bfloat16 if p.dtype == DTYPES["bf16"] else torch.float16
+    for name, t, n, dt in (("o", o, p.num_tokens * p.Hq * p.d_v, want),
+                           ("lse", lse, p.num_tokens * p.Hq, torch.float32)):
+        if t is not None and (t.numel() != n or not t.is_contiguous() or t.dtype != dt or
+                              t.get_device() != p.device):
+            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected a "
+                             f"contiguous {dt} tensor of {n} elements on cuda:{p.device}")
+    if ws.get_device() != p.device or not ws.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{p.device}, got one "
+                         f"on {ws.device}")
     s = load_library().attn_paged_fwd(ctypes.byref(p), _ptr(o), _ptr(lse), _ptr(ws),
                                       ws.numel() * ws.element_size(), _stream(stream))
     if s != 0:

@@ -197,3 +197,23 @@ def test_binding_refuses(kw):
     t.update(kw)
     with pytest.raises(ValueError):
         A.make_paged_params(**t)
+
+
+def test_fwd_refuses_outputs_of_another_type_or_device(monkeypatch):
+    """Raised before the library is called: nothing is launched."""
+    p = A.attn_paged_params_t()
+    p.device, p.num_tokens, p.Hq, p.d_v, p.dtype = 0, 2, 4, 64, A.DTYPES["bf16"]
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(A, "load_library", lambda: pytest.fail("the library was called"))
+    meta = dict(device="meta")
+    o, lse = torch.empty(2, 4, 64, dtype=torch.bfloat16), torch.empty(4, 2)
+    ws = torch.empty(1 << 20, dtype=torch.uint8)
+    for bad in ((o, lse, ws), (o.half(), lse, ws), (o, lse.int(), ws),
+                (o.to(**meta), lse.to(**meta), ws.to(**meta))):
+        with pytest.raises(ValueError):
+            A.attn_paged_fwd(p, *bad)
+    # as if on the device: the types alone are wrong, or the workspace lies in parts
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    for bad in ((o.half(), lse, ws), (o, lse.int(), ws), (o, lse, ws[::2])):
+        with pytest.raises(ValueError):
+            A.attn_paged_fwd(p, *bad)
