@@ -274,6 +274,16 @@ def test_attend_any_length_hint(hint):
     _attend(c, max_q_len=hint)
 
 
+@pytest.mark.parametrize("window", [None, 20])
+@pytest.mark.parametrize("cache", ["fp8_e4m3", "bf16"])
+@pytest.mark.parametrize("new", [8, 9, 16, 17])
+def test_attend_on_both_sides_of_the_choice(new, cache, window):
+    """32, 36, 64 and 68 rows a KV head over a long table and inside a narrow
+    window: the last sizes of one kernel and the first of the other."""
+    _attend(Paged([new, 1, new - 3], [900, 300, 40], seed=25, Hq=8, Hkv=2, cache=cache),
+            window_left=window)
+
+
 def test_shared_prefix_and_strided_table():
     """Two sequences that list the same pages for their first 48 tokens, tables
     with rows further apart than their columns, windows of any size."""
