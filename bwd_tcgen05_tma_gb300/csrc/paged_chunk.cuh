@@ -55,31 +55,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 // the running maximum follows the true one within a factor of 2^8
 constexpr float kLazy = 8.f;
 
-template <int KIND, int DQK, int DV>
-struct ChunkCfg {
-  static constexpr bool kCodes = KIND == kCacheE4m3;
-  static constexpr bool kWide = DQK > 128;
-  static constexpr int kQTile = kHalf * DQK * 2;  // one half's Q
-  // K and V tiles take turns in the rings; with two stages K has the first
-  static constexpr int kK = kHalf * DQK * 2, kV = kHalf * DV * 2;
-  static constexpr int kKV = kK > kV ? kK : kV;
-  static constexpr int kQStages = kWide || kCodes ? 1 : 2;
-  static constexpr int kKVStages = kWide ? 2 : 3;
-  static constexpr int kCodeStages = !kCodes ? 0 : kWide ? 2 : 4;
-  static constexpr int kKVOff = kQStages * 2 * kQTile;
-  static constexpr int kCodeOff = kKVOff + (kWide ? kK + kV : kKVStages * kKV);
-  static constexpr int kAuxOff =
-      kCodeOff + (!kCodes ? 0 : kWide ? (kK + kV) / 2 : kCodeStages * kKV / 2);
-  static constexpr int kSmem = kAuxOff + 3072;
-  static_assert(kSmem <= 227 * 1024, "shared memory");
-  static __device__ __forceinline__ uint32_t kv(uint32_t e) {
-    return kKVOff + (kWide ? (e & 1) * kK : (e % kKVStages) * kKV);
-  }
-  static __device__ __forceinline__ uint32_t code(uint32_t e) {
-    return kCodeOff + (kWide ? (e & 1) * (kK / 2) : (e & 3) * (kKV / 2));
-  }
-};
-
 // A piece of a block of rows, as the scheduler warp hands it to the others.
 struct Piece {
   int n, key;        // key tiles (0: no row keeps a key, < 0: the end), first key
@@ -100,7 +75,8 @@ struct ChunkAux {
   uint32_t tmem;
   int abort;
   uint32_t bad[4];  // by piece: its number + 1 once a value was taken out of the product
-  int ok_mask[8];  // by tile (the producer runs up to four tiles ahead of the softmax): 16-key groups whose page exists
+  int ok_mask[8];   // by tile (the producer runs up to four tiles ahead of the
+                    // softmax): 16-key groups whose page exists
   int64_t part[16];
   int64_t begin, total;  // the block's first unit, all units
   int ctas, unit0;
@@ -109,7 +85,31 @@ struct ChunkAux {
   float4 scale[8][8];     // by tile and group: K scale, log2 V scale, 1 / V scale
   uint8_t q_exp[4][kChunkRows];  // by piece: biased exponent of the row's power of two
 };
-static_assert(sizeof(ChunkAux) <= 3072, "aux");
+
+template <int KIND, int DQK, int DV>
+struct ChunkCfg {
+  static constexpr bool kCodes = KIND == kCacheE4m3;
+  static constexpr bool kWide = DQK > 128;
+  static constexpr int kQTile = kHalf * DQK * 2;  // one half's Q
+  // K and V tiles take turns in the rings; with two stages K has the first
+  static constexpr int kK = kHalf * DQK * 2, kV = kHalf * DV * 2;
+  static constexpr int kKV = kK > kV ? kK : kV;
+  static constexpr int kQStages = kWide || kCodes ? 1 : 2;
+  static constexpr int kKVStages = kWide ? 2 : 3;
+  static constexpr int kCodeStages = !kCodes ? 0 : kWide ? 2 : 4;
+  static constexpr int kKVOff = kQStages * 2 * kQTile;
+  static constexpr int kCodeOff = kKVOff + (kWide ? kK + kV : kKVStages * kKV);
+  static constexpr int kAuxOff =
+      kCodeOff + (!kCodes ? 0 : kWide ? (kK + kV) / 2 : kCodeStages * kKV / 2);
+  static constexpr int kSmem = kAuxOff + (static_cast<int>(sizeof(ChunkAux)) + 127) / 128 * 128;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static __device__ __forceinline__ uint32_t kv(uint32_t e) {
+    return kKVOff + (kWide ? (e & 1) * kK : (e % kKVStages) * kKV);
+  }
+  static __device__ __forceinline__ uint32_t code(uint32_t e) {
+    return kCodeOff + (kWide ? (e & 1) * (kK / 2) : (e & 3) * (kKV / 2));
+  }
+};
 
 template <int KIND>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
