@@ -156,6 +156,13 @@ __device__ __forceinline__ uint16_t f32x2_e4m3x2(float lo, float hi) {
   return r;
 }
 
+// Did a row (or a part of it) keep no key?  Its running maximum alone does not
+// tell: maxima leave NaN out, so a row of NaN scores has -inf there too, but
+// NaN in its sum.
+__device__ __forceinline__ bool no_key(float max, float sum) {
+  return max == -INFINITY && sum == 0.f;
+}
+
 // Launches a kernel that may be put in place while the one before it on the
 // stream still runs; it waits for that one (grid_dep_wait) before it reads
 // anything.

@@ -892,7 +892,7 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
         tc_fence_after();
       }
       float lt = l, mt = m, keep = 1.f;
-      const bool none = m == -INFINITY;
+      const bool none = no_key(m, l);
       if (complete && a.sink) {
         const float s2 = a.sink[head] * kLog2e;
         mt = fmaxf(m, s2);
@@ -1028,7 +1028,7 @@ __global__ void __launch_bounds__(256) chunk_join_kernel(const __grid_constant__
       m = mn;
     }
   }
-  const bool none = m == -INFINITY;
+  const bool none = no_key(m, l);
   float mt = m, lt = l, keep = 1.f;
   if (a.sink) {
     const float s2 = a.sink[head] * kLog2e;

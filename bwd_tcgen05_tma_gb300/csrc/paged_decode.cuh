@@ -793,7 +793,7 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
           const int r = r0 + nt * 8 + 2 * t + c;
           if (r >= rows) continue;
           const int tok = div_group(a, r), head = hk * a.group + r - tok * a.group;
-          const bool none = m[nt][c] == -INFINITY;
+          const bool none = no_key(m[nt][c], l[nt][c]);
           float mt = m[nt][c], lt = l[nt][c], keep = 1.f;
           if (a.sink) {
             const float s2 = a.sink[head] * kLog2e;
@@ -844,11 +844,15 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
         const int r = r0 + nt * 8 + cw;
         if (r >= rows) break;
         float mt_ = -INFINITY;
+        bool none = true;
 #pragma unroll
-        for (int x = 0; x < kWarps; ++x) mt_ = fmaxf(mt_, s_m[x][nt * 8 + cw]);
+        for (int x = 0; x < kWarps; ++x) {
+          const float mx = s_m[x][nt * 8 + cw];
+          mt_ = fmaxf(mt_, mx);
+          none &= no_key(mx, s_l[x][nt * 8 + cw]);
+        }
         const int tok = div_group(a, r), head = hk * a.group + r - tok * a.group;
         float snk = -INFINITY;
-        const bool none = mt_ == -INFINITY;
         if (complete && a.sink) {
           snk = a.sink[head] * kLog2e;
           mt_ = fmaxf(mt_, snk);
@@ -861,7 +865,7 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
 #pragma unroll
         for (int x = 0; x < kWarps; ++x) {
           const float mx = s_m[x][nt * 8 + cw];
-          if (mx == -INFINITY) continue;  // nothing kept by this warp
+          if (no_key(mx, s_l[x][nt * 8 + cw])) continue;  // nothing kept by this warp
           const float f = ex2_approx(mx - mu);
           lt = fmaf(s_l[x][nt * 8 + cw], f, lt);
           const float* so = s_o + (x * 8 + cw) * DV +
@@ -948,7 +952,9 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Args 
   float mt = -INFINITY;
 #pragma unroll
   for (int i = 0; i < 4; ++i) mt = fmaxf(mt, s_m[rr][i]);
-  const bool none = mt == -INFINITY;
+  bool none = true;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) none &= no_key(s_m[rr][i], s_l[rr][i]);
   if (a.sink) mt = fmaxf(mt, a.sink[head] * kLog2e);
   const float mu = mt == -INFINITY ? 0.f : mt;
   float lt = a.sink ? ex2_approx(a.sink[head] * kLog2e - mu + shift) : 0.f;

@@ -409,7 +409,9 @@ attn_status_t attn_fwd_noalloc(const attn_params_t* p, void* o, float* lse, void
  *   LSE_i = ln sum_j exp(S_ij);  sink logits join the normaliser as in
  *   attn_fwd.  Kept: j < seq_lens[s]; with ATTN_MASK_CAUSAL also
  *   j <= position of i; with window_left >= 0 also j >= position - window_left.
- *   A row with no kept key gets O = 0 and LSE = -inf (its sink).  What lies in
+ *   A row with no kept key, or with none whose score is above -inf, gets O = 0
+ *   and LSE = -inf (its sink); a score that is NaN (a NaN in the query, or in a
+ *   key that the row keeps) makes both NaN.  What lies in
  *   slots at or behind seq_lens[s], and in unlisted pages, has no influence,
  *   NaN included, nor has the value of a key that no row of the sequence
  *   keeps.  K and V enter the MMAs exactly (E4M3 codes as fp16 values, their
