@@ -156,6 +156,13 @@ __device__ __forceinline__ uint16_t f32x2_e4m3x2(float lo, float hi) {
   return r;
 }
 
+// The larger of two, or NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // Did a row (or a part of it) keep no key?  Its running maximum alone does not
 // tell: maxima leave NaN out, so a row of NaN scores has -inf there too, but
 // NaN in its sum.

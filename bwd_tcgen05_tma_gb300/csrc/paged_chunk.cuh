@@ -806,6 +806,11 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
             body(g, u[(g >> 1) & 1]);
           }
         };
+        // A group's factor on the scores.  It may underflow (a query of zeros
+        // over a page of zeros: 2^-117 * 2^-64) but not to 0, which would make
+        // NaN of the -inf of masked scores; the others are below 2^33, so that
+        // the bound moves them by less than 2^-93.
+        auto factor = [&](float ks) -> float { return max_nan(fac * ks, 0x1p-126f); };
         // the row's maximum: of each group, then scaled
         float mx = -INFINITY;
         auto largest = [&](int g, const uint32_t (&u)[32]) {
@@ -821,7 +826,7 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
             m0 = fmax3(m0, __uint_as_float(e[14]), __uint_as_float(e[15]));
             if constexpr (kCodes) {
               const float4 sc = x->scale[k & 7][g + q];
-              mx = fmaxf(mx, fmaf(fmaxf(m0, m1), fac * sc.x, sc.y));
+              mx = fmaxf(mx, fmaf(fmaxf(m0, m1), factor(sc.x), sc.y));
             } else {
               mx = fmax3(mx, m0, m1);
             }
@@ -844,7 +849,7 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
             float A = fac, B = base, inv = 1.f;
             if constexpr (kCodes) {
               const float4 sc = x->scale[k & 7][g + q];
-              A = fac * sc.x;
+              A = factor(sc.x);
               B = base + sc.y;
               inv = sc.z;
             }
