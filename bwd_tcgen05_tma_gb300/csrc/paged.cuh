@@ -190,6 +190,9 @@ cudaError_t launch_early(void (*kern)(P...), dim3 grid, dim3 block, size_t smem,
 }
 
 constexpr int kMinExp = -64;
+// Smallest V scale the attention tells from 0: its inverse times the largest P
+// (2^15) times the most keys (2^30) is still a number in the normaliser.
+constexpr float kMinVScale = 0x1p-80f;
 // Smallest power of two s >= 2^-64 with amax <= 448 s (amax finite): with
 // amax = 1.f * 2^x, 448 = 1.75 * 2^8, so e = x - 8, or one more if 1.f > 1.75.
 __device__ __forceinline__ float page_scale(float amax) {

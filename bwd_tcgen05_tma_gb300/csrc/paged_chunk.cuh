@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
             if (m == 0) {
               const int box = (16 * (lane & 7)) >> rows_log;
               const float ks = __shfl_sync(0xffffffffu, ids.ks, box);
-              const float vs = fmaxf(__shfl_sync(0xffffffffu, ids.vs, box), 0x1p-100f);
+              const float vs = fmaxf(__shfl_sync(0xffffffffu, ids.vs, box), kMinVScale);
               const unsigned groups = __ballot_sync(0xffffffffu, okm >> box & 1) & 0xffu;
               if (lane < 8) {
                 const float lg = (__float_as_uint(vs) & 0x7fffffu) == 0

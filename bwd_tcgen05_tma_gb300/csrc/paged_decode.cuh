@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
       Scales r = {1.f, 1.f};
       if (KIND == kCacheE4m3 && id >= 0) {
         r.k = a.k_scale[static_cast<int64_t>(id) * a.Hkv + hk];
-        r.v = fmaxf(a.v_scale[static_cast<int64_t>(id) * a.Hkv + hk], 0x1p-100f);
+        r.v = fmaxf(a.v_scale[static_cast<int64_t>(id) * a.Hkv + hk], kMinVScale);
       }
       return r;
     };

@@ -465,7 +465,11 @@ typedef struct {
   int64_t k_cache_stride[3];
   int64_t v_cache_stride[3];
   float* k_scale; /* fp32 [num_pages, Hkv]; E4M3 caches only (NULL otherwise). */
-  float* v_scale; /* Read by attn_paged_fwd: any positive finite values. */
+  float* v_scale; /* Read by attn_paged_fwd: positive finite values, a V scale
+                     below 2^-80 as 2^-80.  With the V scales of a sequence's
+                     pages within 2^90 of one another (appended ones of 16-bit
+                     values up to 2^34 are), no key of more than 2^-36 of its
+                     row's largest weight falls out of the normaliser. */
   int32_t* status; /* optional device word, see above */
   /* New tokens, rows *_stride elements apart (multiples of 16 bytes), heads
    * contiguous inside a row: q [num_tokens, Hq, d_qk], k_new [num_tokens, Hkv,
