@@ -31,9 +31,9 @@
 // walk's state stays out of the other roles' registers; loops that run once a
 // piece are rolled, since the roles share instruction caches.
 //
-// Values that are not finite in a tile that some rows mask in part are taken
-// out of the product (their zero weight would make NaN of them) and added in
-// the epilogue to the rows that keep them.
+// Values that are not finite in a tile that some rows mask in part, or of which
+// a page is masked for its id, are taken out of the product (their zero weight
+// would make NaN of them) and added in the epilogue to the rows that keep them.
 #pragma once
 #include <cuda.h>
 
@@ -925,11 +925,18 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
         for (int i = 0; i < 32; ++i)
           v[i] = n > 0 && !none ? __uint_as_float(o[i]) * inv : 0.f;
         if (bad && real) {
-          // values that are not finite, in tiles the block of rows masks in part
+          // values that are not finite, in the tiles they were taken out of:
+          // those the block of rows masks in part, or of which a page is none
           const int2 blk = p->all;
+          auto every_page = [&](int key) -> bool {
+#pragma unroll 1
+            for (int i = 0; i < kHalf; i += 16)
+              if (page_of(a, p->seq, key + i) < 0) return false;
+            return true;
+          };
           for (int j = 0; j < n; ++j) {
             const int key = key0 + j * kHalf;
-            if (key >= blk.x && key + kHalf <= blk.y) continue;
+            if (key >= blk.x && key + kHalf <= blk.y && every_page(key)) continue;
             for (int kk = max(key, lo); kk < min(key + kHalf, hi); ++kk) {
               const int page = page_of(a, p->seq, kk);
               if (page < 0) continue;

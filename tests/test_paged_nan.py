@@ -125,3 +125,26 @@ def test_nan_in_the_only_key(new, cache):
             k[int(c.table[s, j // 16]), 0, j % 16, 64] = 0x7F if cache == "fp8_e4m3" else 0x7FFF
             hit[s * new + i, :2] = True
     only_hit_rows_are_nan(c, p, hit, before)
+
+
+@pytest.mark.parametrize("cache", ["fp8_e4m3", "bf16"])
+@pytest.mark.parametrize("new", [1, 4, 80])
+def test_nan_value_beside_a_page_that_is_none(new, cache):
+    """A value that is NaN reaches the rows that keep it also where another page
+    of its 128 tokens is masked for its id."""
+    from bwd_tcgen05_tma_gb300 import attn as A
+
+    c = Paged([new], [300], seed=55, cache=cache)
+    A.attn_paged_append(c.params())
+    c.t["table"][0, 2] = -1
+    p = c.params(q_rot=None)
+    ref, ref_lse = c.attend(p)
+    assert c.status() == 7
+    v = c.t["v_cache"].view(torch.uint8 if cache == "fp8_e4m3" else torch.int16)
+    v[int(c.table[0, 0]), 1, 5, 9] = 0x7F if cache == "fp8_e4m3" else 0x7FC0
+    o, lse = c.attend(p)
+    assert torch.equal(bits(lse), bits(ref_lse))
+    got, want = o.float().cpu(), ref.float().cpu()
+    assert torch.isnan(got[:, 2:, 9]).all()
+    want[:, 2:, 9] = got[:, 2:, 9]
+    assert torch.equal(bits(got), bits(want))
