@@ -97,6 +97,12 @@ __device__ __forceinline__ Seq load_seq(const Args& a, int s) {
   return q;
 }
 
+// Has a sequence positions outside a table of `cap` slots, or new rows below
+// position 0?  (One of length 0 has padding for rows.)
+__device__ __forceinline__ bool outside(const Seq& q, int cap) {
+  return q.len > cap || (q.len > 0 && q.len < q.n);
+}
+
 // Page of position j of sequence s, or -1 (reported) when the table cannot
 // give one.
 __device__ __forceinline__ int page_of(const Args& a, int s, int j) {

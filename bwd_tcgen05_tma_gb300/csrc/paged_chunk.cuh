@@ -131,7 +131,7 @@ __device__ __forceinline__ SeqView view_of(const Args& a, int s) {
   SeqView v;
   v.q = load_seq(a, s);
   const int cap = a.max_pages << a.page_shift;
-  if (v.q.len > cap) flag_bounds(a);
+  if (outside(v.q, cap)) flag_bounds(a);
   v.hi = min(v.q.len, cap);
   return v;
 }

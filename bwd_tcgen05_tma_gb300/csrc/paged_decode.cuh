@@ -149,7 +149,7 @@ __device__ __forceinline__ Need need_of(const Args& a, int s, int rows_per) {
   Need d;
   d.q = load_seq(a, s);
   const int cap = a.max_pages << a.page_shift;
-  if (d.q.len > cap) flag_bounds(a);
+  if (outside(d.q, cap)) flag_bounds(a);
   d.hi = min(d.q.len, cap);
   int lo = 0;
   if (a.window >= 0) lo = max(0, d.q.len - d.q.n - a.window);
