@@ -79,6 +79,9 @@ attn_status_t validate_append(const attn_paged_params_t* p) {
   if (!p->k_new != !p->v_new) return ATTN_ERR_INVALID_ARG;
   if (!p->k_new && p->num_tokens > 0) return ATTN_ERR_INVALID_ARG;
   if (p->q && !p->q_rot) return ATTN_ERR_INVALID_ARG;
+  // in place a row is turned where it lies
+  if (p->q && p->q == p->q_rot && p->q_stride != p->q_rot_stride && p->num_tokens > 1)
+    return ATTN_ERR_INVALID_ARG;
   if (!row_stride_ok(p->k_new, p->k_new_stride, static_cast<int64_t>(p->Hkv) * p->d_qk) ||
       !row_stride_ok(p->v_new, p->v_new_stride, static_cast<int64_t>(p->Hkv) * p->d_v))
     return ATTN_ERR_INVALID_ARG;

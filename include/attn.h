@@ -474,8 +474,8 @@ typedef struct {
   /* New tokens, rows *_stride elements apart (multiples of 16 bytes), heads
    * contiguous inside a row: q [num_tokens, Hq, d_qk], k_new [num_tokens, Hkv,
    * d_qk], v_new [num_tokens, Hkv, d_v].  q_rot: rotated queries, written by
-   * attn_paged_append where q is given (q_rot == q rotates in place; both NULL:
-   * keys and values only) and read by attn_paged_fwd, which reads q when q_rot
+   * attn_paged_append where q is given (q_rot == q, with the same stride, rotates
+   * in place; they must not overlap otherwise; both NULL: keys and values only) and read by attn_paged_fwd, which reads q when q_rot
    * is NULL. */
   const void* q;
   const void* k_new;

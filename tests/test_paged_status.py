@@ -39,3 +39,16 @@ def test_attention_reports_positions_below_zero(new, mask):
     if mask == "CAUSAL":
         assert (o[:below] == 0).all() and (lse[:, :below] == -np.inf).all()
     assert torch.isfinite(o[below:]).all() and torch.isfinite(lse[:, below:]).all()
+
+
+def test_rotation_in_place_needs_one_layout():
+    """q_rot == q with rows at other distances would overwrite queries that are
+    still to be read: refused (on the host, nothing is launched)."""
+    from bwd_tcgen05_tma_gb300 import build
+    from test_paged_abi import INVALID, append, params, size
+
+    build.build()
+    lib = A.load_library()
+    assert append(lib, params(q_rot_stride=8 * 128 + 8)) == INVALID
+    assert append(lib, params(q_stride=8 * 128 + 64)) == INVALID
+    assert size(lib, params(q_rot_stride=8 * 128 + 8)) > 0  # the attention reads q_rot only
