@@ -219,6 +219,7 @@ __device__ __forceinline__ void turn_queries(const Args& a, int block) {
   const int u = threadIdx.x % units, i = threadIdx.x / units;
   const int t = (block / groups) * tokens + i, h0 = (block % groups) * kHeads;
   if (i >= tokens || t >= a.num_tokens) return;
+  if (a.cu && t >= a.cu[a.num_seqs]) return;  // padding: its row is not even read
   const int2 at = unit_at(u, a.rot, a.interleaved);
   const int heads = min(kHeads, a.Hq - h0);
   const uint16_t* src = a.q + t * a.q_stride + h0 * a.d_qk;
