@@ -13,6 +13,9 @@
 namespace attn {
 namespace paged {
 
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
 // Element kinds of a cache.
 enum CacheKind { kCacheBf16 = 0, kCacheF16 = 1, kCacheE4m3 = 2 };
 
@@ -125,9 +128,6 @@ __device__ __forceinline__ float elem(uint16_t x, int f16) {
 __device__ __forceinline__ uint32_t pack2(float lo, float hi, int f16) {
   return f16 ? sm103::pack_f16x2(lo, hi) : sm103::pack_bf16x2(lo, hi);
 }
-__device__ __forceinline__ uint16_t round16(float x, int f16) {
-  return static_cast<uint16_t>(pack2(x, 0.f, f16));
-}
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, uint64_t* bar, int x,
                                             int y, int z, int w) {
@@ -154,6 +154,19 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t c) {
 }
 __device__ __forceinline__ float e4m3_value(uint8_t c) {
   return __half2float(__ushort_as_half(static_cast<uint16_t>(e4m3x2_f16x2(c))));
+}
+// Top bits of a word's elements that are not finite.  (E4M3 has only NaN.)
+template <int KIND>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  if (KIND == kCacheE4m3) return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  if (KIND == kCacheF16) return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+  return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+// The word with zeros in their place.
+template <int KIND>
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+  const uint32_t f = not_finite<KIND>(w);
+  return w & ~(KIND == kCacheE4m3 ? (f >> 7) * 255u : (f >> 15) * 65535u);
 }
 // Two values of at most 448 in magnitude, or NaN, to E4M3 codes, nearest even.
 __device__ __forceinline__ uint16_t f32x2_e4m3x2(float lo, float hi) {

@@ -50,8 +50,6 @@ using namespace sm103;
 
 constexpr int kHalf = 128;             // rows per half, keys per tile
 constexpr int kChunkRows = 2 * kHalf;  // rows per block of rows
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 // the running maximum follows the true one within a factor of 2^8
 constexpr float kLazy = 8.f;
 
@@ -110,18 +108,6 @@ struct ChunkCfg {
     return kCodeOff + (kWide ? (e & 1) * (kK / 2) : (e & 3) * (kKV / 2));
   }
 };
-
-template <int KIND>
-__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
-  if (KIND == kCacheE4m3) return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-  if (KIND == kCacheF16) return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
-  return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-}
-template <int KIND>
-__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
-  const uint32_t f = not_finite<KIND>(w);
-  return w & ~(KIND == kCacheE4m3 ? (f >> 7) * 255u : (f >> 15) * 65535u);
-}
 
 struct SeqView {
   Seq q;

@@ -47,9 +47,6 @@ namespace {
 using sm103::ex2_approx;
 using sm103::smem_u32;
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
 template <int KIND, int DQK, int DV, int NT>
 struct Cfg {
   static constexpr int kCb = KIND == kCacheE4m3 ? 1 : 2;
@@ -113,14 +110,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Does a word hold an element that is not finite?  (E4M3 has only NaN.)
-template <int KIND>
-__device__ __forceinline__ uint32_t nonfinite(uint32_t w) {
-  if (KIND == kCacheE4m3) return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-  if (KIND == kCacheF16) return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
-  return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
 }
 
 // The four dims of slice ks that lane t holds, in the order of its 16-byte units
@@ -698,17 +687,12 @@ __global__ void __launch_bounds__(Cfg<KIND, DQK, DV, NT>::kThreads, Cfg<KIND, DQ
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int z = 0; z < kW; ++z) bad |= nonfinite<KIND>(v[j][z]);
+          for (int z = 0; z < kW; ++z) bad |= not_finite<KIND>(v[j][z]);
         if (__any_sync(0xffffffffu, bad != 0)) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int z = 0; z < kW; ++z) {
-              const uint32_t f = nonfinite<KIND>(v[j][z]);
-              // spread each element's flag (its top bit) over the element
-              const uint32_t mask = KIND == kCacheE4m3 ? (f >> 7) * 255u : (f >> 15) * 65535u;
-              v[j][z] &= ~mask;
-            }
+            for (int z = 0; z < kW; ++z) v[j][z] = finite_only<KIND>(v[j][z]);
           for (int r = 0; r < 16; ++r) {
             if (!okp[x] || key[x] + r < klo || key[x] + r >= khi) continue;
             const uint32_t row = at_stage[x] + C::kStageK + r * C::kVw;
