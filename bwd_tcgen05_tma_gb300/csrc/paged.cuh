@@ -100,10 +100,10 @@ __device__ __forceinline__ Seq load_seq(const Args& a, int s) {
   return q;
 }
 
-// Has a sequence positions outside a table of `cap` slots, or new rows below
-// position 0?  (One of length 0 has padding for rows.)
-__device__ __forceinline__ bool outside(const Seq& q, int cap) {
-  return q.len > cap || (q.len > 0 && q.len < q.n);
+// Has a sequence positions outside the table's row, or new rows below position
+// 0?  (One of length 0 has padding for rows.)
+__device__ __forceinline__ bool outside(const Args& a, const Seq& q) {
+  return q.len > a.max_pages << a.page_shift || (q.len > 0 && q.len < q.n);
 }
 
 // Page of position j of sequence s, or -1 (reported) when the table cannot

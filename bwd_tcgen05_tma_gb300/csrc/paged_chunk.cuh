@@ -117,7 +117,6 @@ __device__ __forceinline__ SeqView view_of(const Args& a, int s) {
   SeqView v;
   v.q = load_seq(a, s);
   const int cap = a.max_pages << a.page_shift;
-  if (outside(v.q, cap)) flag_bounds(a);
   v.hi = min(v.q.len, cap);
   return v;
 }
@@ -199,7 +198,11 @@ __device__ __forceinline__ void walk_init(const Args& a, ChunkAux* x, Walk& w) {
   const int per = (a.num_seqs + kN - 1) / kN;
   const int first = threadIdx.x * per, last = min(a.num_seqs, first + per);
   int64_t mine = 0;
-  for (int s = first; s < last; ++s) mine += a.Hkv * seq_units(a, view_of(a, s));
+  for (int s = first; s < last; ++s) {
+    const SeqView v = view_of(a, s);
+    if (outside(a, v.q)) flag_bounds(a);
+    mine += a.Hkv * seq_units(a, v);
+  }
   int64_t sum = mine;
 #pragma unroll
   for (int i = 1; i < 32; i <<= 1) {

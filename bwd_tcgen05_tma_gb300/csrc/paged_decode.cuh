@@ -138,7 +138,6 @@ __device__ __forceinline__ Need need_of(const Args& a, int s, int rows_per) {
   Need d;
   d.q = load_seq(a, s);
   const int cap = a.max_pages << a.page_shift;
-  if (outside(d.q, cap)) flag_bounds(a);
   d.hi = min(d.q.len, cap);
   int lo = 0;
   if (a.window >= 0) lo = max(0, d.q.len - d.q.n - a.window);
@@ -182,6 +181,7 @@ __device__ __forceinline__ Share find_share(const Args& a) {
   int most = 0;
   for (int s = first; s < last; ++s) {
     const Need d = need_of(a, s, C::kRows);
+    if (outside(a, d.q)) flag_bounds(a);
     const int64_t items = static_cast<int64_t>(d.nrb) * a.Hkv;
     const int steps = d.tiles(16);
     mine[0] += items * (kStart + d.tiles(C::kTileKeys));
