@@ -66,7 +66,8 @@ attn_status_t validate(const attn_paged_params_t* p) {
         p->v_cache_stride[i] % per16)
       return ATTN_ERR_INVALID_ARG;
   const bool scales = p->k_scale && p->v_scale, any = p->k_scale || p->v_scale;
-  if (p->cache_dtype == ATTN_DTYPE_FP8_E4M3 ? (!none && !scales) : any) return ATTN_ERR_INVALID_ARG;
+  if (p->cache_dtype == ATTN_DTYPE_FP8_E4M3 ? (!none && !scales && p->num_pages > 0) : any)
+    return ATTN_ERR_INVALID_ARG;
   const int64_t wq = static_cast<int64_t>(p->Hq) * p->d_qk;
   if (!row_stride_ok(p->q, p->q_stride, wq) || !row_stride_ok(p->q_rot, p->q_rot_stride, wq))
     return ATTN_ERR_INVALID_ARG;
