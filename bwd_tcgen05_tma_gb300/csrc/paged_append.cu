@@ -15,7 +15,7 @@
 // Work goes in units of 16 elements, two 16-byte loads: the eight pairs of a
 // rotation (halves rot/2 apart, or neighbours), or sixteen values that pass.
 // Bound by HBM: two bytes a query element each way, a key or value element
-// read as two bytes and written as one or two (17349 tokens of 64 query and 8
+// read as two bytes and written as one or two (17349 tokens of 32 query and 8
 // KV heads, d 128, into E4M3: 82 us, 4.9 TB/s).
 #include "paged.cuh"
 

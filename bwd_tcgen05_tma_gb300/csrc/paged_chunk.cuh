@@ -16,7 +16,7 @@
 // scaled after it is found.
 //
 // What bounds it (1024 tokens over 31744 cached ones, 64 query heads, E4M3:
-// 784 us, 1.38 PFLOP/s, tensor pipe 58 % busy): S, P and O of two halves fill
+// 790 us, 1.37 PFLOP/s, tensor pipe 58 % busy): S, P and O of two halves fill
 // tensor memory, so a half's MMAs and its softmax take turns, with only the
 // other half beside them; and shared memory, which the MMAs read at 192 KB a
 // tile of 2048 MMA clocks while the conversion reads 32 and writes 64.
@@ -765,8 +765,9 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
         // The row's scores are read twice, 32 at a time and the next 32 while
         // these are worked on: held whole they would cost 128 registers, and
         // spills meet an L1 that shared memory has left small.  (1024 tokens
-        // over 31744 cached ones, 64 query heads: 784 us; 16 at a time 818,
-        // 64 at a time without reading ahead 880, rolled loops 825-916.)
+        // over 31744 cached ones, 64 query heads: 784 us when this was chosen,
+        // 16 at a time 818, 64 at a time without reading ahead 880, rolled
+        // loops 825-916.)
         const bool whole = key >= all.x && key + kHalf <= all.y && okm == 0xff;
         if (!whole) {
           // masked scores to -inf where they lie, so that one copy of the

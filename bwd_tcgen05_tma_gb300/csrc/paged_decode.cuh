@@ -9,8 +9,9 @@
 //
 // What bounds it: every K and V byte is read once from HBM and used for 8
 // rows, 16 or 32 FLOP a byte, so the HBM rate (450 k keys of 8 heads in E4M3,
-// 922 MB: 149 us, 6.2 TB/s); mma.sync runs far below its peak here and no
-// tensor-memory round trip pays.
+// 922 MB: 150 us, 6.1 TB/s); mma.sync runs far below its peak here and no
+// tensor-memory round trip pays.  More rows are bound by the products and their
+// softmax (16 x 4096 keys, 32 rows, E4M3: 80 us where the bytes take 20).
 //
 // Layout.  One warp takes 16 keys a step, alone: no barrier between warps
 // until their states are joined.  A step's 16 slots of K and of V come by TMA
@@ -60,6 +61,8 @@ struct Cfg {
   // Steps a warp takes together: with one tile of rows a step is a chain of
   // dependent short operations, and two chains hide each other's latency (and
   // share the maximum's shuffles); more rows are independent work already.
+  // (One step at a time from the same ring: 4 contexts of 100-131 k keys 155 us
+  // against 150, 32 ragged ones 59 against 60, 256 short ones 32 against 32.6.)
   static constexpr int kTogether = NT == 1 ? 2 : 1;
   // blocks per SM: two where a stage is small, so that one streams while the
   // other joins its warps' states

@@ -68,10 +68,12 @@ typedef enum {
   ATTN_ERR_CUDA = 5,                /* a CUDA runtime call failed (launch, attribute) */
   ATTN_ERR_DEVICE_TIMEOUT = 6,      /* a kernel wait ran past its limit (read via
                                        attn_read_status) */
-  ATTN_ERR_DEVICE_BOUNDS = 7        /* checking build only (attn_build_flags):
-                                       a device-side bounds check failed and its
-                                       access was skipped (read via
-                                       attn_read_status) */
+  ATTN_ERR_DEVICE_BOUNDS = 7        /* a device-side bounds check failed and its
+                                       access was skipped: in the checking build
+                                       (attn_build_flags; read via
+                                       attn_read_status), and in every build for
+                                       what the paged calls read on the device
+                                       (their status word) */
 } attn_status_t;
 
 /* Q/K/V memory layouts (PR #2358, NVTE_3HD / NVTE_HD_2HD / NVTE_HD_HD_HD).
@@ -400,8 +402,8 @@ attn_status_t attn_fwd_noalloc(const attn_params_t* p, void* o, float* lse, void
  *   Infinities and NaN are stored as NaN and do not enter the scale.
  *   Slots other than the new tokens', and their pages, are left as they are.
  *   A page shared by several sequences may be read by all of them, but a call
- *   that appends to it through more than one sequence gives undefined
- *   contents (of that page only).
+ *   that appends to it through more than one sequence, or more than one entry
+ *   of a sequence's row, gives undefined contents (of that page only).
  *
  * attn_paged_fwd:
  *   S_ij = scale * Q_i . K_j,  P = softmax_j(S) over the keys j of the row's
@@ -418,8 +420,10 @@ attn_status_t attn_fwd_noalloc(const attn_params_t* p, void* o, float* lse, void
  *   scales applied in fp32); bf16 queries of an E4M3 cache are multiplied by a
  *   power of two for each row and enter as fp16, which is exact but for
  *   elements below 2^-28 of their row's largest; P is rounded to fp16 (to
- *   bf16 with a bf16 cache); sums and softmax statistics are fp32.  Results do
- *   not depend on the order in which blocks run.
+ *   bf16 with a bf16 cache) for the product with V, not for the normaliser;
+ *   sums and softmax statistics are fp32, exponentials (and the logarithm of a
+ *   V scale that is no power of two) the hardware's approximations.  Results
+ *   do not depend on the order in which blocks run.
  *
  * Streams, workspaces and errors as above; no call allocates or synchronises,
  * and all calls can be captured into graphs (lengths, tables and offsets are
@@ -445,8 +449,11 @@ typedef struct {
   int32_t mask;           /* ATTN_MASK_NONE or ATTN_MASK_CAUSAL */
   int32_t num_seqs;
   int32_t num_tokens; /* rows of q / k_new / v_new / q_rot / o, padding included */
-  int32_t max_q_len;  /* largest n_s (a hint that chooses the kernel; any value
-                         >= 1 gives right results) */
+  int32_t max_q_len;  /* largest n_s (a hint that chooses the kernel for the
+                         whole call; any value >= 1 gives right results).  A
+                         prompt's chunk and many single tokens are served
+                         faster by two calls, each on its sequences' parts of
+                         page_table, seq_lens and cu_seqlens_q */
   int32_t Hq, Hkv;    /* Hq a multiple of Hkv and at most 256 */
   int32_t d_qk, d_v;  /* as in attn_params_t */
   int32_t page_size;  /* 16, 32, 64, 128 or 256 tokens */
@@ -494,8 +501,8 @@ typedef struct {
   const float* sink;   /* fp32 [Hq] or NULL */
 } attn_paged_params_t;
 
-/* Workspace bytes attn_paged_fwd needs (0 on invalid parameters): 2.5 to 11 MB
- * for few query rows, 41 MB (d_v = 128) where max_q_len * Hq / Hkv > 64, or > 32
+/* Workspace bytes attn_paged_fwd needs (0 on invalid parameters): 1.3 to 10.2
+ * MB for few query rows, 41 MB (d_v = 128) or 21 (64) where max_q_len * Hq / Hkv > 64, or > 32
  * with more keys to see than some hundreds.  Depends on no device data; ask it
  * again when a field changes.  256-byte aligned. */
 size_t attn_paged_workspace_size(const attn_paged_params_t* p);
@@ -514,9 +521,11 @@ int32_t attn_abi_version(void);
  *  ATTN_BUILD_DEVICE_CHECKS  the checking build (libattn_sm103_debug.so,
  *    compiled with ATTN_DEBUG; the pages have no counterpart, it stands in for
  *    a memory checker): before every tensor-map copy and every global store a
- *    kernel checks the copy's coordinates (16-byte-aligned innermost
- *    coordinate, box inside the row, existing head, no store starting at a
- *    negative row) or the store's element range against the tensor's size.
+ *    kernel of attn_fwd and attn_bwd checks the copy's coordinates
+ *    (16-byte-aligned innermost coordinate, box inside the row, existing head,
+ *    no store starting at a negative row) or the store's element range against
+ *    the tensor's size.  (The paged calls' kernels check page ids, positions
+ *    and offsets in every build and have no further checks in this one.)
  *    A failed check records ATTN_ERR_DEVICE_BOUNDS and the check's site in
  *    the workspace status and skips the access (no trap); waits that then go
  *    unanswered run out and the kernel unwinds as for a timeout.  Same entry
