@@ -798,8 +798,8 @@ __global__ void __launch_bounds__(512, 1) chunk_kernel(const __grid_constant__ A
         };
         // A group's factor on the scores.  It may underflow (a query of zeros
         // over a page of zeros: 2^-117 * 2^-64) but not to 0, which would make
-        // NaN of the -inf of masked scores; the others are below 2^33, so that
-        // the bound moves them by less than 2^-93.
+        // NaN of the -inf of masked scores.  A score that is not masked is below
+        // 2^33, so that the bound moves its exponent by less than 2^-93.
         auto factor = [&](float ks) -> float { return max_nan(fac * ks, 0x1p-126f); };
         // the row's maximum: of each group, then scaled
         float mx = -INFINITY;

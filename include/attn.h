@@ -412,8 +412,8 @@ attn_status_t attn_fwd_noalloc(const attn_params_t* p, void* o, float* lse, void
  *   attn_fwd.  Kept: j < seq_lens[s]; with ATTN_MASK_CAUSAL also
  *   j <= position of i; with window_left >= 0 also j >= position - window_left.
  *   A row with no kept key, or with none whose score is above -inf, gets O = 0
- *   and LSE = -inf (its sink); a score that is NaN (a NaN in the query, or in a
- *   key that the row keeps) makes both NaN.  What lies in
+ *   and LSE = -inf (its sink); a score that is NaN or +inf (from a query, or a
+ *   key that the row keeps, that is not finite) makes both NaN.  What lies in
  *   slots at or behind seq_lens[s], and in unlisted pages, has no influence,
  *   NaN included, nor has the value of a key that no row of the sequence
  *   keeps.  K and V enter the MMAs exactly (E4M3 codes as fp16 values, their
@@ -482,8 +482,8 @@ typedef struct {
    * contiguous inside a row: q [num_tokens, Hq, d_qk], k_new [num_tokens, Hkv,
    * d_qk], v_new [num_tokens, Hkv, d_v].  q_rot: rotated queries, written by
    * attn_paged_append where q is given (q_rot == q, with the same stride, rotates
-   * in place; they must not overlap otherwise; both NULL: keys and values only) and read by attn_paged_fwd, which reads q when q_rot
-   * is NULL. */
+   * in place; they must not overlap otherwise; both NULL: keys and values only)
+   * and read by attn_paged_fwd, which reads q when q_rot is NULL. */
   const void* q;
   const void* k_new;
   const void* v_new;
@@ -502,9 +502,10 @@ typedef struct {
 } attn_paged_params_t;
 
 /* Workspace bytes attn_paged_fwd needs (0 on invalid parameters): 1.3 to 10.2
- * MB for few query rows, 41 MB (d_v = 128) or 21 (64) where max_q_len * Hq / Hkv > 64, or > 32
- * with more keys to see than some hundreds.  Depends on no device data; ask it
- * again when a field changes.  256-byte aligned. */
+ * MB for few query rows, 41 MB (d_v = 128) or 21 (64) where
+ * max_q_len * Hq / Hkv > 64, or > 32 with more keys to see than some hundreds.
+ * Depends on no device data; ask it again when a field changes.  256-byte
+ * aligned. */
 size_t attn_paged_workspace_size(const attn_paged_params_t* p);
 
 /* Rotates the new tokens and writes them into the cache. */
