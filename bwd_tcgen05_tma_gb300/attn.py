@@ -30,13 +30,20 @@ EXPORTED = ("attn_abi_version", "attn_status_string", "attn_fwd_workspace_size",
             "attn_read_status", "attn_set_trace_events", "attn_event_create",
             "attn_event_destroy", "attn_event_elapsed_ms", "attn_fwd_noalloc",
             "attn_build_flags", "attn_paged_workspace_size", "attn_paged_append",
-            "attn_paged_fwd")
+            "attn_paged_fwd", "attn_rope_table", "attn_rope", "attn_latent_expand",
+            "attn_latent_expand_bwd", "attn_latent_workspace_size", "attn_latent_append",
+            "attn_latent_fwd")
 ATTN_PAGED_PARAMS_VERSION = 1
+ATTN_ROPE_TABLE_PARAMS_VERSION = 1
+ATTN_ROPE_PARAMS_VERSION = 1
+ATTN_LATENT_EXPAND_PARAMS_VERSION = 1
+ATTN_LATENT_PARAMS_VERSION = 1
+ROPE_SCALINGS = {"NONE": 0, "LINEAR": 1, "BASE": 2, "TURNS": 3}
 FWD_NOALLOC_SCRATCH_BYTES = 4 << 20
 TRACE_SLOTS = ("meta", "fwd", "bwd_pre", "dkdv", "dq", "dbias")
 
-c_i32, c_i64, c_f32, c_vp, c_sz = (ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
-                                   ctypes.c_void_p, ctypes.c_size_t)
+c_i32, c_i64, c_f32, c_f64, c_vp, c_sz = (ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
+                                          ctypes.c_double, ctypes.c_void_p, ctypes.c_size_t)
 
 
 class attn_params_t(ctypes.Structure):
@@ -95,6 +102,52 @@ class attn_paged_params_t(ctypes.Structure):
     ]
 
 
+class attn_rope_table_params_t(ctypes.Structure):
+    _fields_ = [
+        ("struct_version", c_i32), ("scaling", c_i32), ("rope_len", c_i32), ("rot_dim", c_i32),
+        ("base", c_f64), ("factor", c_f64), ("turns_low", c_f64), ("turns_high", c_f64),
+        ("trained_len", c_i32), ("magnitude", c_f32), ("rope_cos", c_vp), ("rope_sin", c_vp),
+    ]
+
+
+class attn_rope_params_t(ctypes.Structure):
+    _fields_ = [
+        ("struct_version", c_i32), ("dtype", c_i32), ("num_tokens", c_i32), ("Hq", c_i32),
+        ("Hkv", c_i32), ("d", c_i32), ("rot_start", c_i32), ("rot_dim", c_i32),
+        ("rot_interleaved", c_i32), ("inverse", c_i32), ("rope_len", c_i32), ("seq_len", c_i32),
+        ("num_segments", c_i32), ("positions", c_vp), ("cu_seqlens", c_vp), ("rope_cos", c_vp),
+        ("rope_sin", c_vp), ("q", c_vp), ("k", c_vp), ("q_out", c_vp), ("k_out", c_vp),
+        ("q_stride", c_i64), ("k_stride", c_i64), ("q_out_stride", c_i64), ("k_out_stride", c_i64),
+        ("status", c_vp),
+    ]
+
+
+class attn_latent_expand_params_t(ctypes.Structure):
+    _fields_ = [
+        ("struct_version", c_i32), ("dtype", c_i32), ("num_tokens", c_i32), ("H", c_i32),
+        ("d_n", c_i32), ("d_v", c_i32), ("d_r", c_i32), ("rot_interleaved", c_i32),
+        ("rope_len", c_i32), ("seq_len", c_i32), ("num_segments", c_i32), ("positions", c_vp),
+        ("cu_seqlens", c_vp), ("rope_cos", c_vp), ("rope_sin", c_vp), ("kv", c_vp),
+        ("k_rope", c_vp), ("k", c_vp), ("v", c_vp), ("kv_stride", c_i64), ("k_rope_stride", c_i64),
+        ("k_stride", c_i64), ("v_stride", c_i64), ("status", c_vp),
+    ]
+
+
+class attn_latent_params_t(ctypes.Structure):
+    _fields_ = [
+        ("struct_version", c_i32), ("dtype", c_i32), ("mask", c_i32), ("num_seqs", c_i32),
+        ("num_tokens", c_i32), ("max_q_len", c_i32), ("H", c_i32), ("d_c", c_i32), ("d_r", c_i32),
+        ("page_size", c_i32), ("num_pages", c_i32), ("max_pages", c_i32), ("page_table", c_vp),
+        ("table_stride", c_i64), ("seq_lens", c_vp), ("cu_seqlens_q", c_vp), ("cache", c_vp),
+        ("cache_stride", c_i64 * 2), ("status", c_vp), ("c_new", c_vp), ("k_rope", c_vp),
+        ("q_rope", c_vp), ("q_lat", c_vp), ("q_rot", c_vp), ("c_new_stride", c_i64),
+        ("k_rope_stride", c_i64), ("q_rope_stride", c_i64 * 2), ("q_lat_stride", c_i64 * 2),
+        ("q_rot_stride", c_i64 * 2), ("rot_interleaved", c_i32), ("rope_len", c_i32),
+        ("rope_cos", c_vp), ("rope_sin", c_vp), ("rope_pos", c_vp), ("scale", c_f32),
+        ("window_left", c_i32), ("sink", c_vp),
+    ]
+
+
 _lib = None
 
 
@@ -141,6 +194,18 @@ def load_library(path: str = LIB_PATH):
     lib.attn_paged_append.argtypes = [PP, c_vp]
     lib.attn_paged_fwd.restype = c_i32
     lib.attn_paged_fwd.argtypes = [PP, c_vp, c_vp, c_vp, c_sz, c_vp]
+    for name, block in (("attn_rope_table", attn_rope_table_params_t),
+                        ("attn_rope", attn_rope_params_t),
+                        ("attn_latent_expand", attn_latent_expand_params_t),
+                        ("attn_latent_expand_bwd", attn_latent_expand_params_t),
+                        ("attn_latent_append", attn_latent_params_t)):
+        getattr(lib, name).restype = c_i32
+        getattr(lib, name).argtypes = [ctypes.POINTER(block), c_vp]
+    PL = ctypes.POINTER(attn_latent_params_t)
+    lib.attn_latent_workspace_size.restype = c_sz
+    lib.attn_latent_workspace_size.argtypes = [PL]
+    lib.attn_latent_fwd.restype = c_i32
+    lib.attn_latent_fwd.argtypes = [PL, c_vp, c_vp, c_vp, c_sz, c_vp]
     if lib.attn_abi_version() != ATTN_PARAMS_VERSION:
         raise RuntimeError("attention library ABI version mismatch")
     _lib = lib
@@ -291,6 +356,40 @@ def _rows(name, t, heads, dim):
     return t.stride(0) if t.shape[0] > 1 else heads * dim
 
 
+def _one_device(tensors):
+    """The device all of a block's tensors are on, which has to be current."""
+    import torch
+
+    devices = {t.device for t in tensors.values() if t is not None}
+    if len(devices) != 1:
+        raise ValueError(f"tensors on several devices: {sorted(map(str, devices))}")
+    device = devices.pop()
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return device
+
+
+def _check_types(tensors, dtypes):
+    for name, t in tensors.items():
+        if t is not None and t.dtype != dtypes[name]:
+            raise ValueError(f"{name}: {t.dtype}, expected {dtypes[name]}")
+
+
+def _check_contiguous(tensors, names):
+    for name in names:
+        if tensors[name] is not None and not tensors[name].is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+
+
+def _elem16(dtype):
+    import torch
+
+    if dtype not in ("bf16", "fp16"):
+        raise ValueError(f"dtype: {dtype}, expected bf16 or fp16")
+    return torch.bfloat16 if dtype == "bf16" else torch.float16
+
+
 def make_paged_params(*, dtype, cache_dtype, k_cache, v_cache, page_table, seq_lens, q=None,
                       k_new=None, v_new=None, q_rot=None, k_scale=None, v_scale=None,
                       cu_seqlens_q=None, max_q_len=1, rope_cos=None, rope_sin=None,
@@ -337,13 +436,7 @@ def make_paged_params(*, dtype, cache_dtype, k_cache, v_cache, page_table, seq_l
             raise ValueError(f"{name}: {t.dtype}, expected {dt}")
         want[name] = t
     given = dict(want, k_cache=k_cache, v_cache=v_cache)
-    devices = {t.device for t in given.values() if t is not None}
-    if len(devices) != 1:
-        raise ValueError(f"tensors on several devices: {sorted(map(str, devices))}")
-    device = devices.pop()
-    if device.type == "cuda" and device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    device = _one_device(given)
     for name in ("k_scale", "v_scale", "rope_cos", "rope_sin", "rope_pos", "sink", "seq_lens",
                  "cu_seqlens_q"):
         if given[name] is not None and not given[name].is_contiguous():
@@ -423,6 +516,19 @@ def attn_paged_append(p, stream=None):
         raise AttnError(s, "attn_paged_append")
 
 
+def _check_outputs(p, o, lse, ws, want, n_o, n_lse):
+    import torch
+
+    for name, t, n, dt in (("o", o, n_o, want), ("lse", lse, n_lse, torch.float32)):
+        if t is not None and (t.numel() != n or not t.is_contiguous() or t.dtype != dt or
+                              t.get_device() != p.device):
+            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected a "
+                             f"contiguous {dt} tensor of {n} elements on cuda:{p.device}")
+    if ws.get_device() != p.device or not ws.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{p.device}, got one "
+                         f"on {ws.device}")
+
+
 def attn_paged_fwd(p, o, lse, ws, stream=None):
     """Enqueue the attention over the cache on `stream` (default: torch's
     current stream).  o: [tokens, Hq, d_v]; lse: fp32 [Hq, tokens] or None;
@@ -431,19 +537,290 @@ def attn_paged_fwd(p, o, lse, ws, stream=None):
 
     _on_device(p)
     want = torch.bfloat16 if p.dtype == DTYPES["bf16"] else torch.float16
-    for name, t, n, dt in (("o", o, p.num_tokens * p.Hq * p.d_v, want),
-                           ("lse", lse, p.num_tokens * p.Hq, torch.float32)):
-        if t is not None and (t.numel() != n or not t.is_contiguous() or t.dtype != dt or
-                              t.get_device() != p.device):
-            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, expected a "
-                             f"contiguous {dt} tensor of {n} elements on cuda:{p.device}")
-    if ws.get_device() != p.device or not ws.is_contiguous():
-        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{p.device}, got one "
-                         f"on {ws.device}")
+    _check_outputs(p, o, lse, ws, want, p.num_tokens * p.Hq * p.d_v, p.num_tokens * p.Hq)
     s = load_library().attn_paged_fwd(ctypes.byref(p), _ptr(o), _ptr(lse), _ptr(ws),
                                       ws.numel() * ws.element_size(), _stream(stream))
     if s != 0:
         raise AttnError(s, "attn_paged_fwd")
+
+
+def _check_tables(rope_cos, rope_sin):
+    if rope_cos.dim() != 2 or rope_cos.shape != rope_sin.shape:
+        raise ValueError("rope_cos, rope_sin: [rope_len, rot_dim / 2]")
+
+
+def make_rope_table_params(*, cos, sin, base=10000.0, scaling="NONE", factor=1.0, trained_len=1,
+                           turns=(1.0, 32.0), magnitude=1.0):
+    """Fill an ``attn_rope_table_params_t`` (see attn.h).  cos, sin: fp32
+    [rope_len, rot_dim / 2], which ``attn_rope_table`` fills; scaling: "NONE",
+    "LINEAR", "BASE" or "TURNS", with its factor (and, for "TURNS", the trained
+    length and the turns between which frequencies go from stretched to kept)."""
+    import torch
+
+    given = dict(rope_cos=cos, rope_sin=sin)
+    _check_types(given, dict.fromkeys(given, torch.float32))
+    _check_tables(cos, sin)
+    _check_contiguous(given, given)
+    p = attn_rope_table_params_t()
+    p.tensors, p.device = given, _one_device(given).index
+    p.struct_version = ATTN_ROPE_TABLE_PARAMS_VERSION
+    p.scaling = ROPE_SCALINGS[scaling]
+    p.rope_len, p.rot_dim = int(cos.shape[0]), 2 * int(cos.shape[1])
+    p.base, p.factor, p.magnitude = float(base), float(factor), float(magnitude)
+    p.trained_len = int(trained_len)
+    p.turns_low, p.turns_high = (float(x) for x in turns)
+    p.rope_cos, p.rope_sin = _ptr(cos), _ptr(sin)
+    return p
+
+
+def _fill_places(p, given, tokens, seq_len):
+    """Positions, tables and status of a block that turns packed tokens."""
+    import torch
+
+    pos, cu = given["positions"], given["cu_seqlens"]
+    if pos is not None and cu is not None:
+        raise ValueError("positions and cu_seqlens: one of the two")
+    if pos is not None and tuple(pos.shape) != (tokens,):
+        raise ValueError("positions: [tokens]")
+    if cu is not None and (cu.dim() != 1 or cu.shape[0] < 1):
+        raise ValueError("cu_seqlens: [num_segments + 1]")
+    _check_contiguous(given, ("positions", "cu_seqlens", "rope_cos", "rope_sin"))
+    _check_tables(given["rope_cos"], given["rope_sin"])
+    p.num_tokens = tokens
+    p.seq_len = max(1, tokens) if seq_len is None else int(seq_len)
+    p.num_segments = 0 if cu is None else int(cu.shape[0]) - 1
+    p.rope_len = int(given["rope_cos"].shape[0])
+    for name in ("positions", "cu_seqlens", "rope_cos", "rope_sin", "status"):
+        setattr(p, name, _ptr(given[name]))
+
+
+def make_rope_params(*, dtype, rope_cos, rope_sin, q=None, k=None, q_out=None, k_out=None,
+                     positions=None, cu_seqlens=None, seq_len=None, rot_start=0,
+                     interleaved=False, inverse=False, status=None):
+    """Fill an ``attn_rope_params_t`` from tensors (see attn.h).  q [tokens, Hq,
+    d] and k [tokens, Hkv, d]: rows may lie apart (slices of a packed layout); one
+    of them may be None; q_out, k_out: None turns in place; rope_cos, rope_sin: fp32 [rope_len,
+    rot_dim / 2]; positions int32 [tokens], or cu_seqlens int32 [segments + 1], or
+    rows of seq_len tokens (None: one row).  The block keeps the tensors alive."""
+    import torch
+
+    if q is None and k is None:
+        raise ValueError("neither q nor k is given")
+    if (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError("an output without its input")
+    q_out = q if q_out is None else q_out
+    k_out = k if k_out is None else k_out
+    given = dict(q=q, k=k, q_out=q_out, k_out=k_out, rope_cos=rope_cos, rope_sin=rope_sin,
+                 positions=positions, cu_seqlens=cu_seqlens, status=status)
+    e16, f32, i32 = _elem16(dtype), torch.float32, torch.int32
+    _check_types(given, dict(q=e16, k=e16, q_out=e16, k_out=e16, rope_cos=f32, rope_sin=f32,
+                             positions=i32, cu_seqlens=i32, status=i32))
+    p = attn_rope_params_t()
+    p.tensors, p.device = given, _one_device(given).index
+    p.struct_version, p.dtype = ATTN_ROPE_PARAMS_VERSION, DTYPES[dtype]
+    rows = q if q is not None else k
+    if rows.dim() != 3:
+        raise ValueError("q, k: [tokens, heads, d]")
+    tokens, d = int(rows.shape[0]), int(rows.shape[2])
+    _fill_places(p, given, tokens, seq_len)
+    p.d, p.rot_start, p.rot_dim = d, int(rot_start), 2 * int(rope_cos.shape[1])
+    p.rot_interleaved, p.inverse = int(bool(interleaved)), int(bool(inverse))
+    for heads, names in (("Hq", ("q", "q_out")), ("Hkv", ("k", "k_out"))):
+        t = given[names[0]]
+        if t is None:
+            continue
+        h = int(t.shape[1])
+        setattr(p, heads, h)
+        for name in names:
+            if given[name].shape[0] != tokens:
+                raise ValueError(f"{name}: {given[name].shape[0]} rows, expected {tokens}")
+            setattr(p, name + "_stride", _rows(name, given[name], h, d))
+            setattr(p, name, _ptr(given[name]))
+    return p
+
+
+def make_latent_expand_params(*, dtype, kv, k_rope, k, v, rope_cos, rope_sin, positions=None,
+                              cu_seqlens=None, seq_len=None, interleaved=False, status=None):
+    """Fill an ``attn_latent_expand_params_t`` from tensors (see attn.h): kv
+    [tokens, H, d_n + d_v], k_rope [tokens, d_r], k [tokens, H, d_n + d_r], v
+    [tokens, H, d_v]; ``attn_latent_expand`` reads the first two and writes the
+    others, ``attn_latent_expand_bwd`` takes gradients the other way.  Positions
+    as in ``make_rope_params``.  The block keeps the tensors alive."""
+    import torch
+
+    given = dict(kv=kv, k_rope=k_rope, k=k, v=v, rope_cos=rope_cos, rope_sin=rope_sin,
+                 positions=positions, cu_seqlens=cu_seqlens, status=status)
+    e16, f32, i32 = _elem16(dtype), torch.float32, torch.int32
+    _check_types(given, dict(kv=e16, k_rope=e16, k=e16, v=e16, rope_cos=f32, rope_sin=f32,
+                             positions=i32, cu_seqlens=i32, status=i32))
+    p = attn_latent_expand_params_t()
+    p.tensors, p.device = given, _one_device(given).index
+    p.struct_version, p.dtype = ATTN_LATENT_EXPAND_PARAMS_VERSION, DTYPES[dtype]
+    if kv.dim() != 3 or k.dim() != 3 or v.dim() != 3 or k_rope.dim() != 2:
+        raise ValueError("kv, k, v: [tokens, H, dim]; k_rope: [tokens, d_r]")
+    tokens, H = int(kv.shape[0]), int(kv.shape[1])
+    d_r, d_v = int(k_rope.shape[1]), int(v.shape[2])
+    d_n = int(k.shape[2]) - d_r
+    _fill_places(p, given, tokens, seq_len)
+    if 2 * rope_cos.shape[1] != d_r:
+        raise ValueError("rope_cos, rope_sin: [rope_len, d_r / 2]")
+    p.H, p.d_n, p.d_r, p.d_v = H, d_n, d_r, d_v
+    p.rot_interleaved = int(bool(interleaved))
+    for name, t, h, d in (("kv", kv, H, d_n + d_v), ("k_rope", k_rope.unsqueeze(1), 1, d_r),
+                          ("k", k, H, d_n + d_r), ("v", v, H, d_v)):
+        if t.shape[0] != tokens:
+            raise ValueError(f"{name}: {t.shape[0]} rows, expected {tokens}")
+        setattr(p, name + "_stride", _rows(name, t, h, d))
+        setattr(p, name, _ptr(t))
+    return p
+
+
+def _heads(name, t, tokens, heads, dim):
+    """Strides of tokens and heads of a [tokens, heads, dim] tensor in any order
+    of memory with contiguous dims."""
+    if tuple(t.shape) != (tokens, heads, dim):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{tokens}, {heads}, {dim}]")
+    if t.numel() and t.stride(2) != 1:
+        raise ValueError(f"{name}: dims must be contiguous")
+    # the stride of an axis of one is never used
+    return (t.stride(0) if tokens > 1 else heads * dim), (t.stride(1) if heads > 1 else dim)
+
+
+def make_latent_params(*, dtype, cache, d_c, page_table, seq_lens, c_new=None, k_rope=None,
+                       q_rope=None, q_lat=None, q_rot=None, cu_seqlens_q=None, max_q_len=1,
+                       rope_cos=None, rope_sin=None, rope_pos=None, rope_interleaved=False,
+                       scale=None, mask="CAUSAL", window_left=None, sink=None, status=None):
+    """Fill an ``attn_latent_params_t`` from tensors (see attn.h).
+
+    cache: [num_pages, page_size, d_c + d_r] with contiguous dims; page_table,
+    seq_lens, cu_seqlens_q, max_q_len: as in ``make_paged_params``; c_new
+    [tokens, d_c], k_rope [tokens, d_r], q_rope [tokens, H, d_r] and the tables
+    fp32 [rope_len, d_r / 2] are what ``attn_latent_append`` reads, q_rot [tokens,
+    H, d_r] what it writes; q_lat [tokens, H, d_c] and q_rot are what
+    ``attn_latent_fwd`` reads, with the softmax scale, which it needs.  The block
+    keeps the tensors alive; their contents may change between calls."""
+    import torch
+
+    given = dict(cache=cache, page_table=page_table, seq_lens=seq_lens, c_new=c_new,
+                 k_rope=k_rope, q_rope=q_rope, q_lat=q_lat, q_rot=q_rot,
+                 cu_seqlens_q=cu_seqlens_q, rope_cos=rope_cos, rope_sin=rope_sin,
+                 rope_pos=rope_pos, sink=sink, status=status)
+    e16, f32, i32 = _elem16(dtype), torch.float32, torch.int32
+    _check_types(given, dict(cache=e16, page_table=i32, seq_lens=i32, c_new=e16, k_rope=e16,
+                             q_rope=e16, q_lat=e16, q_rot=e16, cu_seqlens_q=i32, rope_cos=f32,
+                             rope_sin=f32, rope_pos=i32, sink=f32, status=i32))
+    if cache.dim() != 3 or (cache.numel() and cache.stride(2) != 1):
+        raise ValueError("cache: [num_pages, page_size, d_c + d_r] with contiguous dims")
+    num_pages, page, width = (int(x) for x in cache.shape)
+    d_c, d_r = int(d_c), width - int(d_c)
+    rows = next((t for t in (q_lat, q_rope, q_rot, c_new) if t is not None), None)
+    if rows is None:
+        raise ValueError("neither queries nor new tokens are given")
+    heads = next((t for t in (q_lat, q_rope, q_rot) if t is not None), None)
+    if heads is not None and heads.dim() != 3:
+        raise ValueError("q_lat, q_rope, q_rot: [tokens, H, dim]")
+    tokens, H = int(rows.shape[0]), 1 if heads is None else int(heads.shape[1])
+    num_seqs = int(seq_lens.shape[0])
+    if page_table.dim() != 2 or page_table.shape[0] != num_seqs or (
+            page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table: [num_seqs, max_pages] with contiguous rows")
+    if cu_seqlens_q is not None and tuple(cu_seqlens_q.shape) != (num_seqs + 1,):
+        raise ValueError("cu_seqlens_q: [num_seqs + 1]")
+    _check_contiguous(given, ("seq_lens", "cu_seqlens_q", "rope_cos", "rope_sin", "rope_pos",
+                              "sink"))
+    if (rope_cos is None) != (rope_sin is None):
+        raise ValueError("rope_cos and rope_sin go together")
+    p = attn_latent_params_t()
+    p.tensors, p.device = given, _one_device(given).index
+    p.struct_version, p.dtype, p.mask = ATTN_LATENT_PARAMS_VERSION, DTYPES[dtype], MASKS[mask]
+    p.num_seqs, p.num_tokens, p.max_q_len = num_seqs, tokens, int(max_q_len)
+    p.H, p.d_c, p.d_r = H, d_c, d_r
+    p.page_size, p.num_pages, p.max_pages = page, num_pages, int(page_table.shape[1])
+    p.page_table, p.seq_lens, p.cu_seqlens_q = (_ptr(page_table), _ptr(seq_lens),
+                                                _ptr(cu_seqlens_q))
+    p.table_stride = page_table.stride(0) if num_seqs > 1 else p.max_pages
+    p.cache, p.status = _ptr(cache), _ptr(status)
+    for i in range(2):  # the stride of an axis of one is never used
+        p.cache_stride[i] = cache.stride(i) if cache.shape[i] > 1 else page * width
+    for name, t, d in (("c_new", c_new, d_c), ("k_rope", k_rope, d_r)):
+        if t is not None:
+            if tuple(t.shape) != (tokens, d):
+                raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{tokens}, {d}]")
+            setattr(p, name + "_stride", _rows(name, t.unsqueeze(1), 1, d))
+            setattr(p, name, _ptr(t))
+    for name, t, d in (("q_rope", q_rope, d_r), ("q_lat", q_lat, d_c), ("q_rot", q_rot, d_r)):
+        if t is not None:
+            field = getattr(p, name + "_stride")
+            field[0], field[1] = _heads(name, t, tokens, H, d)
+            setattr(p, name, _ptr(t))
+    if rope_cos is not None:
+        _check_tables(rope_cos, rope_sin)
+        if 2 * rope_cos.shape[1] != d_r:
+            raise ValueError("rope_cos, rope_sin: [rope_len, d_r / 2]")
+        p.rope_len = int(rope_cos.shape[0])
+        p.rope_cos, p.rope_sin = _ptr(rope_cos), _ptr(rope_sin)
+    if rope_pos is not None and tuple(rope_pos.shape) != (tokens,):
+        raise ValueError("rope_pos: [tokens]")
+    p.rope_pos = _ptr(rope_pos)
+    p.rot_interleaved = int(bool(rope_interleaved))
+    p.scale = 0.0 if scale is None else float(scale)
+    p.window_left = -1 if window_left is None else int(window_left)
+    if sink is not None and tuple(sink.shape) != (H,):
+        raise ValueError("sink: [H]")
+    p.sink = _ptr(sink)
+    return p
+
+
+def _enqueue(name, p, stream):
+    _on_device(p)
+    s = getattr(load_library(), name)(ctypes.byref(p), _stream(stream))
+    if s != 0:
+        raise AttnError(s, name)
+
+
+def attn_rope_table(p, stream=None):
+    """Enqueue the filling of the tables on `stream` (default: torch's current
+    stream), as the other calls of this module do."""
+    _enqueue("attn_rope_table", p, stream)
+
+
+def attn_rope(p, stream=None):
+    """Enqueue the rotation of q and k."""
+    _enqueue("attn_rope", p, stream)
+
+
+def attn_latent_expand(p, stream=None):
+    """Enqueue the making of K and V from kv and k_rope."""
+    _enqueue("attn_latent_expand", p, stream)
+
+
+def attn_latent_expand_bwd(p, stream=None):
+    """Enqueue the gradients of kv and k_rope from those of K and V."""
+    _enqueue("attn_latent_expand_bwd", p, stream)
+
+
+def attn_latent_workspace_size(p):
+    return int(load_library().attn_latent_workspace_size(ctypes.byref(p)))
+
+
+def attn_latent_append(p, stream=None):
+    """Enqueue the append to the latent cache."""
+    _enqueue("attn_latent_append", p, stream)
+
+
+def attn_latent_fwd(p, o, lse, ws, stream=None):
+    """Enqueue the attention over the latent cache.  o: [tokens, H, d_c]; lse:
+    fp32 [H, tokens] or None; both contiguous, as is ws, and all on the block's
+    device."""
+    import torch
+
+    _on_device(p)
+    want = torch.bfloat16 if p.dtype == DTYPES["bf16"] else torch.float16
+    _check_outputs(p, o, lse, ws, want, p.num_tokens * p.H * p.d_c, p.num_tokens * p.H)
+    s = load_library().attn_latent_fwd(ctypes.byref(p), _ptr(o), _ptr(lse), _ptr(ws),
+                                       ws.numel() * ws.element_size(), _stream(stream))
+    if s != 0:
+        raise AttnError(s, "attn_latent_fwd")
 
 
 def attn_read_status(ws, stream=None):

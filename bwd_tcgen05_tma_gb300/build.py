@@ -25,9 +25,12 @@ LIB_DEBUG = os.path.join(HERE, "libattn_sm103_debug.so")
 SOURCES = ["api.cu", "meta.cu", "fwd.cu", "bwd.cu", "bwd_bf16.cu", "bwd_f16.cu", "dkdv128.cu",
            "dq128.cu", "fwd2t.cu", "fwd_fp8.cu", "paged_api.cu", "paged_append.cu",
            "paged_decode_e4m3.cu", "paged_decode_f16.cu", "paged_decode_bf16.cu",
-           "paged_chunk_e4m3.cu", "paged_chunk_f16.cu", "paged_chunk_bf16.cu"]
+           "paged_chunk_e4m3.cu", "paged_chunk_f16.cu", "paged_chunk_bf16.cu",
+           "rope.cu", "latent_expand.cu", "latent_api.cu", "latent_append.cu", "latent_bf16.cu",
+           "latent_f16.cu"]
 HEADERS = ["attn_internal.cuh", "chunk_mask.h", "sm103_ptx.cuh", "bwd_passes.cuh", "debug_checks.h",
-           "paged.cuh", "paged_decode.cuh", "paged_chunk.cuh", os.path.join("..", "..", "include", "attn.h")]
+           "paged.cuh", "paged_decode.cuh", "paged_chunk.cuh", "rotate.cuh", "latent.cuh",
+           "latent_attend.cuh", os.path.join("..", "..", "include", "attn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,12 @@
+// Attention over a paged latent cache of bf16 rows.
+#include "latent_attend.cuh"
+
+namespace attn {
+namespace paged {
+
+cudaError_t launch_latent_bf16(const LatentArgs& l, int, int, cudaStream_t st) {
+  return launch_latent<false>(l, st);
+}
+
+}  // namespace paged
+}  // namespace attn

@@ -18,6 +18,7 @@
 // read as two bytes and written as one or two (17349 tokens of 32 query and 8
 // KV heads, d 128, into E4M3: 82 us, 4.9 TB/s).
 #include "paged.cuh"
+#include "rotate.cuh"
 
 namespace attn {
 namespace paged {
@@ -25,85 +26,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kHold = 4;
-
-struct Unit {
-  float x[16];  // first eight, second eight
-};
-
-// Element offsets of a unit's two halves inside a head of width d.
-__device__ __forceinline__ int2 unit_at(int u, int rot, int interleaved) {
-  if (!interleaved && u < rot / 16) return make_int2(8 * u, rot / 2 + 8 * u);
-  return make_int2(16 * u, 16 * u + 8);
-}
-
-__device__ __forceinline__ void unpack8(uint4 v, float* x, int f16) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (f16) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    } else {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-}
-
-// The two 16-byte halves of a unit as they lie in memory.
-struct Raw {
-  uint4 lo, hi;
-};
-__device__ __forceinline__ Raw load_raw(const uint16_t* src, int2 at) {
-  return {*reinterpret_cast<const uint4*>(src + at.x), *reinterpret_cast<const uint4*>(src + at.y)};
-}
-__device__ __forceinline__ void unpack(const Raw& v, Unit& r, int f16) {
-  unpack8(v.lo, r.x, f16);
-  unpack8(v.hi, r.x + 8, f16);
-}
-
-// A unit's cosines and sines: row `cs` of the tables, columns 8 u .. 8 u + 7.
-struct Turn {
-  float c[8], s[8];
-};
-__device__ __forceinline__ void load_turn(const Args& a, int u, int64_t cs, Turn& t) {
-  const float4* cp = reinterpret_cast<const float4*>(a.cos + cs * (a.rot / 2) + 8 * u);
-  const float4* sp = reinterpret_cast<const float4*>(a.sin + cs * (a.rot / 2) + 8 * u);
-  *reinterpret_cast<float4*>(t.c) = __ldg(cp);
-  *reinterpret_cast<float4*>(t.c + 4) = __ldg(cp + 1);
-  *reinterpret_cast<float4*>(t.s) = __ldg(sp);
-  *reinterpret_cast<float4*>(t.s + 4) = __ldg(sp + 1);
-}
-// a' = a c - b s and b' = b c + a s, each product and the sum rounded in fp32.
-__device__ __forceinline__ void turn_pair(float& x, float& y, float c, float s) {
-  const float a = x, b = y;
-  x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-  y = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
-}
-__device__ __forceinline__ void turn(Unit& r, const Turn& t, int interleaved) {
-  if (interleaved) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) turn_pair(r.x[2 * i], r.x[2 * i + 1], t.c[i], t.s[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) turn_pair(r.x[i], r.x[i + 8], t.c[i], t.s[i]);
-  }
-}
-
-__device__ __forceinline__ void store16(uint16_t* dst, int2 at, const Unit& r, int f16) {
-  uint4 lo, hi;
-  lo.x = pack2(r.x[0], r.x[1], f16);
-  lo.y = pack2(r.x[2], r.x[3], f16);
-  lo.z = pack2(r.x[4], r.x[5], f16);
-  lo.w = pack2(r.x[6], r.x[7], f16);
-  hi.x = pack2(r.x[8], r.x[9], f16);
-  hi.y = pack2(r.x[10], r.x[11], f16);
-  hi.z = pack2(r.x[12], r.x[13], f16);
-  hi.w = pack2(r.x[14], r.x[15], f16);
-  *reinterpret_cast<uint4*>(dst + at.x) = lo;
-  *reinterpret_cast<uint4*>(dst + at.y) = hi;
-}
 
 __device__ __forceinline__ void store8(uint8_t* dst, int2 at, Unit r, float inv) {
   float m = 0.f;
@@ -246,7 +168,7 @@ __device__ __forceinline__ void turn_queries(const Args& a, int block) {
   if (a.rot > 0) {
     const int row = table_row(a, t, q.len - q.n + t - q.row0);
     if (row < 0) return;
-    if (turns) load_turn(a, u, row, cs);
+    if (turns) load_turn(a.cos, a.sin, a.rot, u, row, cs);
   }
 #pragma unroll
   for (int b = 0; b < kHeads; b += 4) {
@@ -318,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     unpack(raw, r, a.f16);
     if (p.key && p.u < a.rot / 16) {
       Turn cs;
-      load_turn(a, p.u, row, cs);
+      load_turn(a.cos, a.sin, a.rot, p.u, row, cs);
       turn(r, cs, a.interleaved);
     }
     return true;

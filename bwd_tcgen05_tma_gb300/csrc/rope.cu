@@ -1,0 +1,282 @@
+// Rotary positions: the tables, and turning queries and keys (or their
+// gradients) in the layouts the attention reads.
+#include <cmath>
+
+#include "rotate.cuh"
+
+namespace attn {
+namespace paged {
+namespace {
+
+// ---------------------------------------------------------------- tables
+// Angles in turns, modulo 1, as 64-bit fixed-point fractions: position times
+// frequency is one integer product whose overflow is the modulo, exact whatever
+// the position (an error of half a unit of a frequency, 2^-65 turns, grows to
+// 2^-35 at position 2^30).  The nearest quarter is taken off before the rest
+// becomes a float, whose relative rounding is then that of an angle below pi/4.
+// (In fp64 the same products and reductions would run at a sixty-fourth of the
+// fp32 rate here.)
+constexpr int kTableThreads = 256;
+constexpr int kTableRows = 4;  // positions a thread takes
+
+struct TableArgs {
+  int rope_len, half;
+  float magnitude;
+  float* cos;
+  float* sin;
+  uint64_t freq[128];  // turns a position, times 2^64
+};
+
+__global__ void __launch_bounds__(kTableThreads) table_kernel(const __grid_constant__ TableArgs a) {
+  const int groups = a.half / 4, per = kTableThreads / groups;  // positions of a block at once
+  const int g = threadIdx.x % groups, i = threadIdx.x / groups;
+  if (i >= per) return;
+  uint64_t f[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f[k] = a.freq[4 * g + k];
+  sm103::grid_dep_wait();
+  const int j0 = blockIdx.x * per * kTableRows + i;
+#pragma unroll
+  for (int r = 0; r < kTableRows; ++r) {
+    const int j = j0 + r * per;
+    if (j >= a.rope_len) return;
+    float c[4], s[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint64_t turn = f[k] * static_cast<uint64_t>(j);
+      const uint32_t q = static_cast<uint32_t>((turn + (1ull << 61)) >> 62);
+      const int64_t rest = static_cast<int64_t>(turn - (static_cast<uint64_t>(q) << 62));
+      float cc, ss;
+      sincospif(__ll2float_rn(rest) * 0x1p-63f, &ss, &cc);  // half turns
+      const float x = (q & 1) ? ss : cc, y = (q & 1) ? cc : ss;
+      // quarters: (c, s), (-s, c), (-c, -s), (s, -c)
+      c[k] = (((q + 1) & 2) ? -x : x) * a.magnitude;
+      s[k] = ((q & 2) ? -y : y) * a.magnitude;
+    }
+    const int64_t at = static_cast<int64_t>(j) * a.half + 4 * g;
+    *reinterpret_cast<float4*>(a.cos + at) = make_float4(c[0], c[1], c[2], c[3]);
+    *reinterpret_cast<float4*>(a.sin + at) = make_float4(s[0], s[1], s[2], s[3]);
+  }
+}
+
+// ---------------------------------------------------------------- turning
+// One warp a token: its lanes take the units of several heads side by side, so
+// that a warp's accesses are whole lines, and each lane keeps its unit's cosines
+// and sines for all heads.  Bound by HBM, two bytes an element each way.
+constexpr int kWarps = 8;
+constexpr int kAtOnce = 4;  // loads in flight a lane
+
+struct RopeArgs {
+  Places w;
+  int Hq, heads, d, start, rot, interleaved, inverse, f16, copy;
+  const float* cos;
+  const float* sin;
+  const uint16_t* q;
+  const uint16_t* k;
+  uint16_t* q_out;
+  uint16_t* k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+};
+
+__global__ void __launch_bounds__(kWarps * 32) rope_kernel(const __grid_constant__ RopeArgs a) {
+  sm103::grid_dep_wait();
+  const int lane = threadIdx.x & 31;
+  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (t >= a.w.num_tokens) return;
+  const int row = place_of(a.w, t);
+  if (row < 0) return;
+  const uint16_t *q = a.q + t * a.q_stride, *k = a.k + t * a.k_stride;
+  uint16_t *qo = a.q_out + t * a.q_out_stride, *ko = a.k_out + t * a.k_out_stride;
+  auto src = [&](int h) { return h < a.Hq ? q + h * a.d : k + (h - a.Hq) * a.d; };
+  auto dst = [&](int h) { return h < a.Hq ? qo + h * a.d : ko + (h - a.Hq) * a.d; };
+
+  const int units = a.rot / 16, per = 32 / units;
+  const int u = lane % units, first = lane / units;
+  if (first < per) {
+    int2 at = unit_at(u, a.rot, a.interleaved);
+    at.x += a.start;
+    at.y += a.start;
+    Turn cs;
+    load_turn(a.cos, a.sin, a.rot, u, row, cs);
+    if (a.inverse) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cs.s[i] = -cs.s[i];
+    }
+    for (int h0 = first; h0 < a.heads; h0 += per * kAtOnce) {
+      Raw raw[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if (h0 + j * per < a.heads) raw[j] = load_raw(src(h0 + j * per), at);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        if (h0 + j * per >= a.heads) break;
+        Unit r;
+        unpack(raw[j], r, a.f16);
+        turn(r, cs, a.interleaved);
+        store16(dst(h0 + j * per), at, r, a.f16);
+      }
+    }
+  }
+  const int rest = (a.d - a.rot) / 8;  // 16-byte units of a head that pass
+  if (!a.copy || rest == 0) return;
+  const int before = a.start / 8, skip = a.rot / 8, step = 32 / rest, odd = 32 % rest;
+  int h = lane / rest, x = lane % rest;
+  while (h < a.heads) {
+    uint4 v[kAtOnce];
+    int hh = h, xx = x;
+    auto next = [&]() {
+      hh += step;
+      xx += odd;
+      if (xx >= rest) {
+        xx -= rest;
+        ++hh;
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int e = (xx < before ? xx : xx + skip) * 8;
+      if (hh < a.heads) v[j] = *reinterpret_cast<const uint4*>(src(hh) + e);
+      next();
+    }
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int e = (x < before ? x : x + skip) * 8;
+      if (h < a.heads) *reinterpret_cast<uint4*>(dst(h) + e) = v[j];
+      h += step;
+      x += odd;
+      if (x >= rest) {
+        x -= rest;
+        ++h;
+      }
+    }
+  }
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+attn_status_t check_table(const attn_rope_table_params_t* p) {
+  if (!p || p->struct_version != ATTN_ROPE_TABLE_PARAMS_VERSION) return ATTN_ERR_INVALID_ARG;
+  if (p->scaling < ATTN_ROPE_NONE || p->scaling > ATTN_ROPE_TURNS) return ATTN_ERR_INVALID_ARG;
+  if (p->rope_len < 0 || p->rot_dim <= 0) return ATTN_ERR_INVALID_ARG;
+  if (p->rope_len > (1 << 30) || p->rot_dim % 16 || p->rot_dim > 256) return ATTN_ERR_UNSUPPORTED;
+  if (!std::isfinite(p->base) || p->base < 1 || !std::isfinite(p->magnitude))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->scaling != ATTN_ROPE_NONE && (!std::isfinite(p->factor) || p->factor < 1))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->scaling == ATTN_ROPE_TURNS &&
+      (!std::isfinite(p->turns_low) || !std::isfinite(p->turns_high) ||
+       !(p->turns_low < p->turns_high) || p->trained_len < 1))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->rope_len > 0 && (!p->rope_cos || !p->rope_sin)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(p->rope_cos, 16) || !aligned(p->rope_sin, 16)) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+attn_status_t check_rope(const attn_rope_params_t* p) {
+  if (!p || p->struct_version != ATTN_ROPE_PARAMS_VERSION) return ATTN_ERR_INVALID_ARG;
+  if (p->dtype != ATTN_DTYPE_BF16 && p->dtype != ATTN_DTYPE_FP16) return ATTN_ERR_INVALID_ARG;
+  if (p->Hq < 0 || p->Hkv < 0 || p->Hq + int64_t{p->Hkv} == 0 || p->d <= 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (p->Hq > 1024 || p->Hkv > 1024 || p->d > 256 || p->d % 16) return ATTN_ERR_UNSUPPORTED;
+  if (p->rot_start < 0 || p->rot_dim <= 0 || int64_t{p->rot_start} + p->rot_dim > p->d)
+    return ATTN_ERR_INVALID_ARG;
+  if (p->rot_start % 8 || p->rot_dim % 16) return ATTN_ERR_UNSUPPORTED;
+  const attn_status_t s = check_places(p);
+  if (s != ATTN_OK) return s;
+  struct {
+    const void* in;
+    const void* out;
+    int64_t in_stride, out_stride;
+    int heads;
+  } const both[2] = {{p->q, p->q_out, p->q_stride, p->q_out_stride, p->Hq},
+                     {p->k, p->k_out, p->k_stride, p->k_out_stride, p->Hkv}};
+  for (const auto& x : both) {
+    if (x.heads == 0) continue;
+    const int64_t width = static_cast<int64_t>(x.heads) * p->d;
+    if (p->num_tokens > 0 && (!x.in || !x.out)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(x.in, 16) || !aligned(x.out, 16) || x.in_stride < width || x.out_stride < width ||
+        x.in_stride % 8 || x.out_stride % 8)
+      return ATTN_ERR_INVALID_ARG;
+    // in place a row is turned where it lies
+    if (x.in && x.in == x.out && x.in_stride != x.out_stride && p->num_tokens > 1)
+      return ATTN_ERR_INVALID_ARG;
+  }
+  return ATTN_OK;
+}
+
+}  // namespace
+}  // namespace paged
+}  // namespace attn
+
+using namespace attn::paged;
+
+extern "C" {
+
+attn_status_t attn_rope_table(const attn_rope_table_params_t* p, void* stream) {
+  const attn_status_t s = check_table(p);
+  if (s != ATTN_OK) return s;
+  TableArgs a = {};
+  a.rope_len = p->rope_len;
+  a.half = p->rot_dim / 2;
+  a.magnitude = p->magnitude;
+  a.cos = p->rope_cos;
+  a.sin = p->rope_sin;
+  const double pi2 = 6.283185307179586476925286766559;
+  double base = p->base;
+  if (p->scaling == ATTN_ROPE_BASE) {
+    base *= std::pow(p->factor, p->rot_dim / (p->rot_dim - 2.0));
+    if (!std::isfinite(base)) return ATTN_ERR_INVALID_ARG;
+  }
+  for (int i = 0; i < a.half; ++i) {
+    double f = std::pow(base, -2.0 * i / p->rot_dim);
+    if (p->scaling == ATTN_ROPE_LINEAR) f /= p->factor;
+    if (p->scaling == ATTN_ROPE_TURNS) {
+      const double turns = p->trained_len * f / pi2;
+      double w = (turns - p->turns_low) / (p->turns_high - p->turns_low);
+      w = w < 0 ? 0 : w > 1 ? 1 : w;
+      f *= w + (1 - w) / p->factor;
+    }
+    a.freq[i] = static_cast<uint64_t>(std::ldexp(f / pi2, 64) + 0.5);
+  }
+  if (p->rope_len == 0) return ATTN_OK;
+  const int rows = kTableThreads / (a.half / 4) * kTableRows;
+  const unsigned blocks = static_cast<unsigned>((int64_t{p->rope_len} + rows - 1) / rows);
+  return launch_early(table_kernel, dim3(blocks), dim3(kTableThreads), 0,
+                      static_cast<cudaStream_t>(stream), a) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
+}
+
+attn_status_t attn_rope(const attn_rope_params_t* p, void* stream) {
+  const attn_status_t s = check_rope(p);
+  if (s != ATTN_OK) return s;
+  if (p->num_tokens == 0) return ATTN_OK;
+  RopeArgs a = {};
+  a.w = places(p);
+  a.Hq = p->Hq;
+  a.heads = p->Hq + p->Hkv;
+  a.d = p->d;
+  a.start = p->rot_start;
+  a.rot = p->rot_dim;
+  a.interleaved = p->rot_interleaved != 0;
+  a.inverse = p->inverse != 0;
+  a.f16 = p->dtype == ATTN_DTYPE_FP16;
+  a.copy = (p->Hq && p->q != p->q_out) || (p->Hkv && p->k != p->k_out);
+  a.cos = p->rope_cos;
+  a.sin = p->rope_sin;
+  a.q = static_cast<const uint16_t*>(p->q);
+  a.k = static_cast<const uint16_t*>(p->k);
+  a.q_out = static_cast<uint16_t*>(p->q_out);
+  a.k_out = static_cast<uint16_t*>(p->k_out);
+  a.q_stride = p->q_stride;
+  a.k_stride = p->k_stride;
+  a.q_out_stride = p->q_out_stride;
+  a.k_out_stride = p->k_out_stride;
+  const unsigned blocks = (p->num_tokens + kWarps - 1) / kWarps;
+  return launch_early(rope_kernel, dim3(blocks), dim3(kWarps * 32), 0,
+                      static_cast<cudaStream_t>(stream), a) == cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -516,6 +516,248 @@ attn_status_t attn_paged_append(const attn_paged_params_t* p, void* stream);
 attn_status_t attn_paged_fwd(const attn_paged_params_t* p, void* o, float* lse, void* ws,
                              size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions.
+ *
+ * The pages have no counterpart (their attention takes Q and K as they are);
+ * these calls turn queries and keys by their tokens' positions before
+ * attn_fwd, and the gradients back behind attn_bwd.
+ *
+ * attn_rope_table fills the tables that every rotation of this library reads:
+ *   cos[j][p] = magnitude * cos(j f_p),  sin[j][p] = magnitude * sin(j f_p)
+ * for positions j < rope_len and pairs p < rot_dim / 2, with
+ *   g_p = base^(-2p / rot_dim) and
+ *   NONE:    f_p = g_p
+ *   LINEAR:  f_p = g_p / factor
+ *   BASE:    f_p = base'^(-2p / rot_dim), base' = base * factor^(rot_dim / (rot_dim - 2))
+ *            (the fastest pair keeps its frequency, the slowest is divided by factor)
+ *   TURNS:   f_p = g_p (w + (1 - w) / factor) with w going from 0 to 1 as the
+ *            turns trained_len * g_p / (2 pi) go from turns_low to turns_high
+ *            (linearly; frequencies that turn often in the trained context are
+ *            kept, those that hardly turn are divided by factor).
+ * Frequencies are computed in 64 bits and angles in fixed point, as turns modulo
+ * 1 with 64 bits, so that far positions lose nothing: each value is off by at
+ * most 2^-22 * |magnitude|.
+ *
+ * attn_rope:
+ *   the rot_dim coordinates from rot_start on of every head of q and k are
+ *   turned, with pair p = (p, p + rot_dim/2), or (2p, 2p+1) when
+ *   rot_interleaved:
+ *     a' = a cos - b sin,  b' = b cos + a sin
+ *   with row `position` of the tables; with inverse != 0 the sine's sign is
+ *   turned around, which is the transposed map and so the gradient.  Each
+ *   product and sum is rounded in fp32, the result once to dtype.  Other
+ *   coordinates are copied.
+ *
+ * Positions: positions[t]; or with cu_seqlens (int32[num_segments + 1]) the
+ * offset of t inside its segment; or with neither t % seq_len (dense rows).
+ * Tokens outside [cu_seqlens[0], cu_seqlens[num_segments]) are padding: their
+ * rows are neither read nor written.
+ *
+ * In place: q_out == q with q_out_stride == q_stride (and k alike).  Otherwise
+ * inputs and outputs must not overlap.  q may be NULL with Hq = 0, k with Hkv = 0.
+ *
+ * Streams and errors as above; neither call allocates or synchronises, both can
+ * be captured.  Checks on the device: a position outside [0, rope_len), and
+ * offsets outside [0, num_tokens] or decreasing, are never used: rows concerned
+ * are not written, and ATTN_ERR_DEVICE_BOUNDS is stored in *status, if given;
+ * the library never clears it. */
+typedef enum {
+  ATTN_ROPE_NONE = 0,
+  ATTN_ROPE_LINEAR = 1,
+  ATTN_ROPE_BASE = 2,
+  ATTN_ROPE_TURNS = 3
+} attn_rope_scaling_t;
+
+#define ATTN_ROPE_TABLE_PARAMS_VERSION 1
+typedef struct {
+  int32_t struct_version; /* = ATTN_ROPE_TABLE_PARAMS_VERSION */
+  int32_t scaling;        /* attn_rope_scaling_t */
+  int32_t rope_len;       /* positions, 0 to 2^30 */
+  int32_t rot_dim;        /* a multiple of 16, 16 to 256 */
+  double base;            /* finite, at least 1 */
+  double factor;          /* finite, at least 1; not read with NONE */
+  double turns_low, turns_high; /* TURNS: finite, low < high */
+  int32_t trained_len;    /* TURNS: at least 1 */
+  float magnitude;        /* finite */
+  float* rope_cos;        /* fp32 [rope_len, rot_dim / 2], 16-byte aligned */
+  float* rope_sin;
+} attn_rope_table_params_t;
+
+attn_status_t attn_rope_table(const attn_rope_table_params_t* p, void* stream);
+
+#define ATTN_ROPE_PARAMS_VERSION 1
+typedef struct {
+  int32_t struct_version; /* = ATTN_ROPE_PARAMS_VERSION */
+  int32_t dtype;          /* of q, k and the outputs: BF16 or FP16 */
+  int32_t num_tokens;     /* rows, padding included; at most 2^30 */
+  int32_t Hq, Hkv;        /* heads of q and of k; each at most 1024, not both 0 */
+  int32_t d;              /* width of a head: a multiple of 16, at most 256 */
+  int32_t rot_start;      /* a multiple of 8 */
+  int32_t rot_dim;        /* a multiple of 16, at least 16; rot_start + rot_dim <= d */
+  int32_t rot_interleaved;
+  int32_t inverse;
+  int32_t rope_len;       /* rows of the tables */
+  int32_t seq_len;        /* at least 1 where positions and cu_seqlens are NULL */
+  int32_t num_segments;   /* with cu_seqlens: at least 0 */
+  const int32_t* positions;  /* int32 [num_tokens] or NULL */
+  const int32_t* cu_seqlens; /* int32 [num_segments + 1] or NULL; not both */
+  const float* rope_cos;     /* fp32 [rope_len, rot_dim / 2], 16-byte aligned */
+  const float* rope_sin;
+  /* [num_tokens, heads, d]: rows *_stride elements apart (a multiple of 8, at
+   * least heads * d), heads contiguous inside a row, 16-byte aligned: slices of
+   * the 3HD and HD_2HD layouts as well as tensors of their own. */
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+  int32_t* status; /* optional device word */
+} attn_rope_params_t;
+
+attn_status_t attn_rope(const attn_rope_params_t* p, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Latent attention, expanded form: keys and values for attn_fwd from the
+ * up-projection of a latent vector a token.
+ *
+ * A token's latent vector c is projected to kv = c W, for every head d_n
+ * coordinates of its key and d_v of its value; the key's other d_r coordinates
+ * are one rotated vector that all heads share.  (The projections are the
+ * caller's matrix products, as Q, K and V of attn_fwd are.)
+ *
+ * attn_latent_expand reads kv and k_rope, writes k and v:
+ *   K[t,h] = [kv[t,h,:d_n] | rotate(k_rope[t])],  V[t,h] = kv[t,h,d_n:]
+ *   which attn_fwd takes as HD_HD_HD with Hkv = H and d_qk = d_n + d_r.
+ * attn_latent_expand_bwd takes gradients in the same block: reads k (dK) and v
+ *   (dV), writes kv and k_rope:
+ *   dkv[t,h] = [dK[t,h,:d_n] | dV[t,h]],
+ *   dk_rope[t] = rotate^T(sum_h dK[t,h,d_n:])
+ *   The sum and the rotation are fp32, rounded once; the order of the sum is
+ *   fixed.
+ * (Queries: attn_rope with rot_start = d_n.)
+ *
+ * Rotation, positions, padding, streams, errors and status are attn_rope's. */
+#define ATTN_LATENT_EXPAND_PARAMS_VERSION 1
+typedef struct {
+  int32_t struct_version; /* = ATTN_LATENT_EXPAND_PARAMS_VERSION */
+  int32_t dtype;          /* BF16 or FP16 */
+  int32_t num_tokens;     /* at most 2^30 */
+  int32_t H;              /* 1 to 1024 */
+  int32_t d_n, d_v;       /* multiples of 8, 8 to 256 */
+  int32_t d_r;            /* 32, 64 or 128 */
+  int32_t rot_interleaved;
+  int32_t rope_len, seq_len, num_segments; /* as in attn_rope_params_t */
+  const int32_t* positions;
+  const int32_t* cu_seqlens;
+  const float* rope_cos; /* fp32 [rope_len, d_r / 2] */
+  const float* rope_sin;
+  /* Rows *_stride elements apart (multiples of 8), contiguous inside, 16-byte
+   * aligned: kv [num_tokens, H, d_n + d_v], k_rope [num_tokens, d_r],
+   * k [num_tokens, H, d_n + d_r], v [num_tokens, H, d_v].  No two overlap. */
+  void* kv;
+  void* k_rope;
+  void* k;
+  void* v;
+  int64_t kv_stride, k_rope_stride, k_stride, v_stride;
+  int32_t* status;
+} attn_latent_expand_params_t;
+
+attn_status_t attn_latent_expand(const attn_latent_expand_params_t* p, void* stream);
+attn_status_t attn_latent_expand_bwd(const attn_latent_expand_params_t* p, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Latent attention, absorbed form: serving from a paged cache of one row a
+ * token.
+ *
+ * A row is [c | k_r]: the latent vector of d_c coordinates and the rotated
+ * shared part of d_r.  With the keys' up-projection taken into the queries
+ * (q_lat = q_n W_k, the caller's product by heads) all heads attend to the same
+ * row, whose c is also the value; the values' up-projection is applied to O.
+ *
+ * Pages, tables, lengths, offsets and padding are those of the paged cache
+ * above, with slots of one row: sequence s has seq_lens[s] tokens including
+ * its n_s new ones, and so on.
+ *
+ * attn_latent_append:  row_j = [c_new_j | rotate(k_rope_j)],
+ *                      q_rot_i,h = rotate(q_rope_i,h)
+ *   Rotation as attn_rope's over the whole of d_r, by the token's position (or
+ *   rope_pos).  c_new is copied, bit for bit.  Slots other than the new tokens'
+ *   are left as they are.
+ *
+ * attn_latent_fwd:
+ *   S_ihj = scale (q_lat_ih . c_j + q_rot_ih . k_r_j),  P = softmax_j(S) over the
+ *   keys that the mask keeps,  O_ih = sum_j P_ihj c_j,  LSE_ih = ln sum_j exp(S_ihj)
+ *   with masks, window, sink logits, rows without a key, scores and values that
+ *   are not finite as in attn_paged_fwd.  P is rounded to dtype for the product
+ *   with c, not for the normaliser; sums and softmax statistics are fp32,
+ *   exponentials the hardware's approximation.  Results do not depend on the
+ *   order in which blocks run.
+ *
+ * Streams, workspaces, errors, device checks and the status word are those of
+ * the paged calls.  An E4M3 cache is not offered (cache and queries share
+ * dtype). */
+#define ATTN_LATENT_PARAMS_VERSION 1
+typedef struct {
+  int32_t struct_version; /* = ATTN_LATENT_PARAMS_VERSION */
+  int32_t dtype;          /* of the cache and of every 16-bit tensor: BF16 or FP16 */
+  int32_t mask;           /* ATTN_MASK_NONE or ATTN_MASK_CAUSAL */
+  int32_t num_seqs;
+  int32_t num_tokens; /* rows of the new tokens' tensors, padding included */
+  int32_t max_q_len;  /* largest n_s (a hint that chooses the kernel; any value
+                         >= 1 gives right results) */
+  int32_t H;          /* query heads, 1 to 256 */
+  int32_t d_c;        /* 256 or 512 */
+  int32_t d_r;        /* 64 */
+  int32_t page_size;  /* 16, 32, 64, 128 or 256 tokens */
+  int32_t num_pages;
+  int32_t max_pages;  /* columns of the page table; max_pages * page_size and
+                         num_tokens * H are at most 2^30 */
+  const int32_t* page_table; /* [num_seqs, max_pages], rows table_stride apart */
+  int64_t table_stride;
+  const int32_t* seq_lens;     /* [num_seqs] */
+  const int32_t* cu_seqlens_q; /* [num_seqs + 1] or NULL (num_tokens == num_seqs) */
+  /* Cache [page][slot][d_c + d_r]: strides in elements of the first two,
+   * positive multiples of 8, dims contiguous, 16-byte aligned. */
+  void* cache;
+  int64_t cache_stride[2];
+  int32_t* status;
+  /* New tokens.  c_new [num_tokens, d_c] and k_rope [num_tokens, d_r]: rows
+   * *_stride elements apart; q_lat [num_tokens, H, d_c], q_rope and q_rot
+   * [num_tokens, H, d_r]: strides of tokens and of heads (any order of memory).
+   * Strides are positive multiples of 8, dims contiguous, 16-byte aligned.
+   * The append reads c_new, k_rope and, where given, q_rope, and writes q_rot
+   * (in place where q_rot == q_rope with the same strides; otherwise the two
+   * must not overlap); the attention reads q_lat and q_rot. */
+  const void* c_new;
+  const void* k_rope;
+  const void* q_rope;
+  const void* q_lat;
+  void* q_rot;
+  int64_t c_new_stride, k_rope_stride;
+  int64_t q_rope_stride[2], q_lat_stride[2], q_rot_stride[2];
+  int32_t rot_interleaved;
+  int32_t rope_len;        /* rows of the tables */
+  const float* rope_cos;   /* fp32 [rope_len, d_r / 2], 16-byte aligned */
+  const float* rope_sin;
+  const int32_t* rope_pos; /* int32 [num_tokens], or NULL: the token's position */
+  /* Attention. */
+  float scale;         /* of the scores (not d_c + d_r but the expanded heads' width counts) */
+  int32_t window_left; /* negative: no window */
+  const float* sink;   /* fp32 [H] or NULL */
+} attn_latent_params_t;
+
+/* Workspace bytes attn_latent_fwd needs (0 on invalid parameters).  Depends on no
+ * device data; ask it again when a field changes.  256-byte aligned. */
+size_t attn_latent_workspace_size(const attn_latent_params_t* p);
+
+/* Writes the new tokens' rows into the cache and turns the queries' parts. */
+attn_status_t attn_latent_append(const attn_latent_params_t* p, void* stream);
+
+/* o: [num_tokens, H, d_c] of `dtype`; lse: fp32 [H, num_tokens] or NULL. */
+attn_status_t attn_latent_fwd(const attn_latent_params_t* p, void* o, float* lse, void* ws,
+                              size_t ws_bytes, void* stream);
+
 int32_t attn_abi_version(void);
 
 /* Properties of this build of the library, as bit flags:
