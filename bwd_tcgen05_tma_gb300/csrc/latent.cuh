@@ -22,6 +22,13 @@ struct LatentArgs {
 
 constexpr int kLatentRope = 64;  // width of the rotated part
 
+// Rows (tokens x heads) the attention's kernel takes at once, and its blocks.
+constexpr int kLatentMaxCtas = 152;
+inline int latent_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// Tensor map over the cache, [page][64 coordinates][slot][coordinate]: boxes of
+// `slots` slots and `chunks` times 64 coordinates, 128-byte swizzle.
+bool latent_map(CUtensorMap* m, const LatentArgs& l, int slots, int chunks);
+
 cudaError_t launch_latent_append(const LatentArgs& a, cudaStream_t st);
 cudaError_t launch_latent_bf16(const LatentArgs& a, int rows, int sms, cudaStream_t st);
 cudaError_t launch_latent_f16(const LatentArgs& a, int rows, int sms, cudaStream_t st);

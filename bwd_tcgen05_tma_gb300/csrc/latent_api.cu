@@ -1,7 +1,10 @@
 // Host side of the paged latent cache's calls: argument validation, workspace
 // layout and launches.
+#include <cudaTypedefs.h>
+
 #include <cmath>
 #include <cstring>
+#include <mutex>
 
 #include "latent.cuh"
 
@@ -133,6 +136,39 @@ void fill(LatentArgs& l, const attn_latent_params_t* p) {
   l.q_rot_head = p->q_rot_stride[1];
 }
 
+// Workspace: descriptors of split row blocks, then their partial states, two a
+// block of all its rows.
+struct Plan {
+  size_t desc, ml, part, total;
+};
+int rows_of(const attn_latent_params_t* p) {
+  return latent_rows(static_cast<int64_t>(p->max_q_len) * p->H);
+}
+Plan make_plan(const attn_latent_params_t* p) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t rows = size_t{2} * kLatentMaxCtas * rows_of(p);
+  Plan pl;
+  pl.desc = 0;
+  pl.ml = up(kLatentMaxCtas * sizeof(int4));
+  pl.part = pl.ml + up(rows * sizeof(float2));
+  pl.total = pl.part + rows * p->d_c * sizeof(float);
+  return pl;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
 int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -142,6 +178,27 @@ int sm_count() {
 }
 
 }  // namespace
+
+bool latent_map(CUtensorMap* m, const LatentArgs& l, int slots, int chunks) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const Args& a = l.a;
+  // a pool without pages has no memory; no box of it is ever asked for
+  const void* mem = a.num_pages > 0 ? static_cast<const void*>(a.kc) : l.q_lat;
+  const cuuint64_t dims[4] = {64, cuuint64_t{1} << a.page_shift,
+                              static_cast<cuuint64_t>(a.d_qk / 64),
+                              static_cast<cuuint64_t>(a.num_pages > 0 ? a.num_pages : 1)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(a.k_tok), 128,
+                                 static_cast<cuuint64_t>(a.k_page)};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(slots), static_cast<cuuint32_t>(chunks),
+                             1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, a.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+            const_cast<void*>(mem), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace paged
 }  // namespace attn
 
@@ -151,7 +208,7 @@ extern "C" {
 
 size_t attn_latent_workspace_size(const attn_latent_params_t* p) {
   if (validate_fwd(p) != ATTN_OK) return 0;
-  return 256;
+  return make_plan(p).total;
 }
 
 attn_status_t attn_latent_append(const attn_latent_params_t* p, void* stream) {
@@ -172,16 +229,22 @@ attn_status_t attn_latent_fwd(const attn_latent_params_t* p, void* o, float* lse
   if (p->num_seqs == 0 || p->num_tokens == 0) return ATTN_OK;
   if (!o || !aligned(o, 16) || !aligned(lse, 4) || !ws || !aligned(ws, 256))
     return ATTN_ERR_INVALID_ARG;
-  if (ws_bytes < attn_latent_workspace_size(p)) return ATTN_ERR_WORKSPACE_TOO_SMALL;
+  const Plan pl = make_plan(p);
+  if (ws_bytes < pl.total) return ATTN_ERR_WORKSPACE_TOO_SMALL;
   LatentArgs l;
   fill(l, p);
   l.a.o = static_cast<uint16_t*>(o);
   l.a.lse = lse;
+  char* w = static_cast<char*>(ws);
+  l.a.split_desc = reinterpret_cast<int4*>(w + pl.desc);
+  l.a.part_ml = reinterpret_cast<float2*>(w + pl.ml);
+  l.a.part = reinterpret_cast<float*>(w + pl.part);
   const int sms = sm_count();
   if (sms <= 0) return ATTN_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int rows = rows_of(p);
   const cudaError_t e =
-      l.a.f16 ? launch_latent_f16(l, 0, sms, st) : launch_latent_bf16(l, 0, sms, st);
+      l.a.f16 ? launch_latent_f16(l, rows, sms, st) : launch_latent_bf16(l, rows, sms, st);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

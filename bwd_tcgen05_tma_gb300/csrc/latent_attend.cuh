@@ -1,92 +1,926 @@
-// Attention over the paged latent cache: one block a (token, head), a plain
-// kernel.  Four warps take a sequence's keys in turn, a lane a slice of the
-// coordinates, with a running maximum and sum each, and join their states.
+// Attention over the paged latent cache (tcgen05).
+//
+// Mathematics and tiling.  All heads of a token, and all new tokens of a sequence,
+// attend to the same rows [c | k_r], and c is also the value.  The (token, head)
+// rows are the columns of transposed products, so that 16 of them fill an MMA as
+// well as 64 do:
+//   S^T [64 keys x N] = [c | k_r] [q_lat | q_rot]^T,
+//   O^T [d_c x N] += c^T P^T, in blocks of 128 coordinates,
+// with the rows of a tile in shared memory once: the first product reads them as
+// they lie (K-major), the second turned (MN-major).  N is 16, 32 or 64; O^T takes
+// d_c / 128 * N columns of tensor memory and two tiles of scores 2 N.
+//
+// The softmax runs down the columns.  A thread holds two keys of N / 4 rows (the
+// 16x256b shape).  The running maximum follows the true one within 2^8, so whether
+// any row's has to move is one barrier's vote; only then (the first tile, and
+// rarely after it) is the maximum joined across threads and O rescaled.  Sums stay
+// in each thread's registers until the end.
+//
+// Work split.  As in the kernels of the paged cache: all tiles in order (sequence,
+// row block, tile) cut into equal shares, one a block, one block an SM; pieces of
+// a row block meet in a second kernel in a fixed order.
+//
+// Roles: MMA issuer, TMA producer, scheduler (a warp each), four softmax warps, four
+// warps that copy queries.
+//
+// Values that are not finite in a tile that some rows mask in part are taken out of
+// the product (their zero weight would make NaN of them); a row that keeps such a
+// key gets NaN in that coordinate in the epilogue, which is what its score makes of
+// it (0 * inf where the score is -inf, NaN throughout otherwise).
 #pragma once
+#include <cfloat>
+#include <climits>
+
 #include "latent.cuh"
 
 namespace attn {
 namespace paged {
 namespace {
 
-using sm103::ex2_approx;
+using namespace sm103;
 
-template <bool F16, int DC>
-__global__ void __launch_bounds__(128) latent_plain_kernel(const __grid_constant__ LatentArgs l) {
-  constexpr int kV = DC / 32;
-  __shared__ float s_o[4][DC];
-  __shared__ float s_m[4], s_l[4];
-  sm103::grid_dep_wait();
-  const Args& a = l.a;
-  const int t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int s = t;
-  if (a.cu) {
-    if (t >= a.cu[a.num_seqs]) return;
-    int lo = 0, hi = a.num_seqs;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (a.cu[mid] <= t) lo = mid;
-      else hi = mid;
+constexpr int kKeys = 64;      // keys a tile
+constexpr int kThreads = 384;  // warps: MMA, TMA, scheduler, -, 4 softmax, 4 queries
+constexpr float kLazy = 8.f;
+
+struct LatentMaps {
+  CUtensorMap lat, rope;
+};
+
+// A piece of a block of rows, as the scheduler warp hands it to the others.
+struct Piece {
+  int n, key;   // key tiles (0: no row keeps a key, < 0: the end), first key
+  int seq, rb;  // sequence, block of rows
+  int first, whole;  // begins with the block's first tile; holds all its tiles
+  int pieces;        // of a split block, in its first piece: how many there are
+  int row0, new_rows, pos0, hi;  // of the sequence: first row, tokens, first position, keys
+  int2 any, all;     // keys some row, and every row, of the block keeps
+};
+
+template <int N, int SLOTS, int RSLOTS>
+struct LatentAux {
+  uint64_t lat_full[SLOTS], lat_empty[SLOTS], rope_full[RSLOTS], rope_empty[RSLOTS];
+  uint64_t q_full, q_empty, s_full[2], p_full, o_done, o_empty;
+  uint64_t piece_full[4], piece_empty[4];
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+  uint32_t bad;     // number + 1 of the last piece a value was taken out of
+  int ok_mask[8];   // by tile: 16-key groups whose page exists
+  int64_t part[kThreads / 32];
+  int64_t begin, total;  // the block's first unit, all units
+  int ctas, unit0, seq, rb;
+  Piece piece[4];
+  int row_lo[N], row_hi[N];
+  float col[4][N];  // by softmax warp: maxima, or sums
+  float fac[N];
+};
+
+template <int DC, int N>
+struct LatentCfg {
+  static constexpr int kNB = DC / 128;       // value blocks of a tile
+  static constexpr int kSlot = kKeys * 256;  // one block: 128 coordinates of 64 keys
+  static constexpr int kRope = kKeys * 128;
+  static constexpr int kP = kKeys * 128;     // P^T [64 keys][64 rows], N of them used
+  static constexpr int kQ = N * (DC + kLatentRope) * 2;
+  static constexpr int kRSlots = DC == 512 ? 2 : 4;
+  static constexpr int kAuxRoom = 3072;
+  static constexpr int kFit = (227 * 1024 - kQ - kP - kRSlots * kRope - kAuxRoom) / kSlot;
+  static constexpr int kSlots = kFit > 4 * kNB ? 4 * kNB : kFit;
+  static_assert(kSlots >= 2 * kNB, "two tiles");
+  static constexpr int kLatOff = kQ;
+  static constexpr int kRopeOff = kLatOff + kSlots * kSlot;
+  static constexpr int kPOff = kRopeOff + kRSlots * kRope;
+  static constexpr int kAuxOff = kPOff + kP;
+  using Aux = LatentAux<N, kSlots, kRSlots>;
+  static constexpr int kSmem = kAuxOff + (static_cast<int>(sizeof(Aux)) + 127) / 128 * 128;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static constexpr uint32_t kColO = 2 * N;
+};
+
+// One sequence and the keys it has in the cache.
+struct SeqView {
+  Seq q;
+  int hi;
+};
+__device__ __forceinline__ SeqView view_of(const Args& a, int s) {
+  SeqView v;
+  v.q = load_seq(a, s);
+  v.hi = min(v.q.len, a.max_pages << a.page_shift);
+  return v;
+}
+template <int N>
+__device__ __forceinline__ int blocks_of(const Args& a, const SeqView& v) {
+  return (v.q.n * a.group + N - 1) / N;
+}
+// Keys [x, y) that some (any) or every row of rows [r0, r1) keeps.
+__device__ __forceinline__ int2 keys_any(const Args& a, const SeqView& v, int r0, int r1) {
+  const int pos0 = v.q.len - v.q.n;
+  const int lo = div_group(a, r0), hi = div_group(a, min(r1, v.q.n * a.group) - 1);
+  return make_int2(a.window >= 0 ? max(0, pos0 + lo - a.window) : 0,
+                   a.causal ? min(v.hi, pos0 + hi + 1) : v.hi);
+}
+__device__ __forceinline__ int2 keys_all(const Args& a, const SeqView& v, int r0, int r1) {
+  const int pos0 = v.q.len - v.q.n;
+  const int lo = div_group(a, r0), hi = div_group(a, min(r1, v.q.n * a.group) - 1);
+  return make_int2(a.window >= 0 ? max(0, pos0 + hi - a.window) : 0,
+                   a.causal ? min(v.hi, pos0 + lo + 1) : v.hi);
+}
+// A block of rows costs its tiles and about as much as this many more: queries to
+// load, a pipeline to fill, O to write.  Shares are cut by that sum.
+constexpr int kStart = 3;
+template <int N>
+__device__ __forceinline__ int tiles_of(const Args& a, const SeqView& v, int rb) {
+  const int2 k = keys_any(a, v, rb * N, (rb + 1) * N);
+  return max(1, (k.y - (k.x & ~(kKeys - 1)) + kKeys - 1) / kKeys);
+}
+template <int N>
+__device__ __forceinline__ int64_t seq_units(const Args& a, const SeqView& v) {
+  int64_t n = 0;
+  const int nrb = blocks_of<N>(a, v);
+  for (int rb = 0; rb < nrb; ++rb) n += kStart + tiles_of<N>(a, v, rb);
+  return n;
+}
+
+// Walks the block's pieces (the scheduler warp does).  Units [0, kStart) of a block
+// of rows are its start, the others its tiles.
+struct Walk {
+  int done, share;  // units behind the current piece's first, and in all
+  int seq, rb, u0;
+  SeqView v;
+  // the current piece: tiles [t0, t1) of nt
+  int u1, t0, t1, nt;
+  int2 any;    // keys some row of the block of rows keeps
+  int n, key;  // key tiles (0: no row keeps a key), first key of the first
+};
+template <int N>
+__device__ __forceinline__ bool walk_piece(const Args& a, Walk& w) {
+  w.nt = tiles_of<N>(a, w.v, w.rb);
+  w.u1 = min(w.nt + kStart, w.u0 + (w.share - w.done));
+  w.t0 = max(0, w.u0 - kStart);
+  w.t1 = max(0, w.u1 - kStart);
+  w.any = keys_any(a, w.v, w.rb * N, (w.rb + 1) * N);
+  w.key = (w.any.x & ~(kKeys - 1)) + w.t0 * kKeys;
+  w.n = w.any.y > w.any.x ? w.t1 - w.t0 : 0;
+  return w.t1 > w.t0;
+}
+// The next piece with tiles.
+template <int N>
+__device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
+  do {
+    w.done += w.u1 - w.u0;
+    if (w.done >= w.share) return false;
+    w.u0 = 0;
+    if (++w.rb >= blocks_of<N>(a, w.v)) {
+      w.rb = 0;
+      do w.v = view_of(a, ++w.seq);
+      while (w.v.q.n == 0);
     }
-    s = lo;
+  } while (!walk_piece<N>(a, w));
+  return true;
+}
+
+// This block's share, found by all threads.
+template <int N, class Aux>
+__device__ __forceinline__ void walk_init(const Args& a, Aux* x, Walk& w) {
+  const int per = (a.num_seqs + kThreads - 1) / kThreads;
+  const int first = min(a.num_seqs, static_cast<int>(threadIdx.x) * per);
+  const int last = min(a.num_seqs, first + per);
+  int64_t mine = 0;
+  for (int s = first; s < last; ++s) {
+    const SeqView v = view_of(a, s);
+    if (outside(a, v.q)) flag_bounds(a);
+    mine += seq_units<N>(a, v);
   }
-  const Seq q = load_seq(a, s);
-  if (t < q.row0 || t >= q.row0 + q.n) return;
-  if (outside(a, q)) flag_bounds(a);
-  const int pos = q.len - q.n + t - q.row0, cap = a.max_pages << a.page_shift;
-  const int lo = a.window >= 0 ? max(0, pos - a.window) : 0;
-  const int hi = min(a.causal ? min(q.len, pos + 1) : q.len, cap);
-  float ql[kV], qr[2];
-  for (int i = 0; i < kV; ++i)
-    ql[i] = elem(l.q_lat[t * l.q_lat_tok + h * l.q_lat_head + lane + 32 * i], F16);
-  for (int i = 0; i < 2; ++i)
-    qr[i] = elem(l.q_rot[t * l.q_rot_tok + h * l.q_rot_head + lane + 32 * i], F16);
-  float o[kV], m = -INFINITY, sum = 0.f;
-  for (int i = 0; i < kV; ++i) o[i] = 0.f;
-  for (int j = lo + w; j < hi; j += 4) {
-    const int page = page_of(a, s, j);
-    if (page < 0) continue;
-    const uint16_t* c = reinterpret_cast<const uint16_t*>(
-        a.kc + page * a.k_page + (j & ((1 << a.page_shift) - 1)) * a.k_tok);
-    float v[kV], d = 0.f;
-    for (int i = 0; i < kV; ++i) {
-      v[i] = elem(c[lane + 32 * i], F16);
-      d += v[i] * ql[i];
-    }
-    for (int i = 0; i < 2; ++i) d += elem(c[DC + lane + 32 * i], F16) * qr[i];
-    for (int x = 16; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
-    d *= a.scale * kLog2e;
-    const float mn = fmaxf(m, d), mu = mn == -INFINITY ? 0.f : mn;
-    const float f = ex2_approx(m - mu), p = ex2_approx(d - mu);
-    sum = sum * f + p;
-    for (int i = 0; i < kV; ++i) o[i] = o[i] * f + (p == 0.f ? 0.f : p * v[i]);
-    m = mn;
+  int64_t sum = mine;
+#pragma unroll
+  for (int i = 1; i < 32; i <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, sum, i);
+    if ((threadIdx.x & 31) >= i) sum += y;
   }
-  for (int i = 0; i < kV; ++i) s_o[w][lane + 32 * i] = o[i];
-  if (lane == 0) s_m[w] = m, s_l[w] = sum;
+  if ((threadIdx.x & 31) == 31) x->part[threadIdx.x / 32] = sum;
   __syncthreads();
-  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  const float s2 = a.sink ? a.sink[h] * kLog2e : -INFINITY, mt = fmaxf(m, s2);
-  const float mu = mt == -INFINITY ? 0.f : mt;
-  float keys = 0.f;
-  for (int i = 0; i < 4; ++i) keys += s_l[i] * ex2_approx(s_m[i] - mu);
-  const float lt = keys + ex2_approx(s2 - mu);
-  const bool none = no_key(m, keys);
-  uint16_t* out = a.o + (static_cast<int64_t>(t) * a.Hq + h) * DC;
-  for (int d = threadIdx.x; d < DC; d += 128) {
-    float x = 0.f;
-    for (int i = 0; i < 4; ++i) x += s_o[i][d] * ex2_approx(s_m[i] - mu);
-    out[d] = static_cast<uint16_t>(pack2(none ? 0.f : x / lt, 0.f, F16));
+  int64_t total = 0, before = sum - mine;
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < static_cast<int>(threadIdx.x) / 32) before += x->part[i];
+    total += x->part[i];
   }
-  if (a.lse && threadIdx.x == 0)
-    a.lse[static_cast<int64_t>(h) * a.num_tokens + t] =
-        none ? (a.sink ? a.sink[h] : -INFINITY) : mt * kLn2 + logf(lt);
+  const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+  w.done = w.share = 0;
+  if (static_cast<int>(blockIdx.x) < ctas) {
+    const int64_t begin = blockIdx.x * total / ctas;
+    w.share = static_cast<int>((blockIdx.x + 1) * total / ctas - begin);
+    if (begin >= before && begin < before + mine) {
+      int64_t off = begin - before;
+      int s = first;
+      for (;; ++s) {
+        const SeqView v = view_of(a, s);
+        const int64_t units = seq_units<N>(a, v);
+        if (off >= units) {
+          off -= units;
+          continue;
+        }
+        x->seq = s;
+        int rb = 0;
+        for (int n; off >= (n = kStart + tiles_of<N>(a, v, rb)); ++rb) off -= n;
+        x->rb = rb;
+        x->unit0 = static_cast<int>(off);
+        x->begin = begin;
+        x->total = total;
+        x->ctas = ctas;
+        break;
+      }
+    }
+  }
+  __syncthreads();
+  if (w.share > 0) {
+    w.seq = x->seq;
+    w.rb = x->rb;
+    w.u0 = x->unit0;
+    w.v = view_of(a, w.seq);
+    // a share that ends inside its only start has no piece
+    if (!walk_piece<N>(a, w) && !walk_next<N>(a, w)) w.share = 0;
+  }
+}
+
+// A barrier of the softmax warps that also tells whether any thread's p holds.
+__device__ __forceinline__ bool softmax_any(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(p))
+      : "memory");
+  return r != 0;
+}
+
+template <bool F16, int DC, int N>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_kernel(const __grid_constant__ LatentArgs l, const __grid_constant__ LatentMaps maps) {
+  using L = LatentCfg<DC, N>;
+  constexpr int NB = L::kNB, NS = L::kSlots, NR = L::kRSlots;
+  constexpr int kC = N / 4;                       // columns a softmax thread holds
+  constexpr float kShift = F16 ? 7.f : 0.f;       // P <= 2^(7 + 8) in fp16
+  constexpr int kKind = F16 ? kCacheF16 : kCacheBf16;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  typename L::Aux* const x = reinterpret_cast<typename L::Aux*>(sm + L::kAuxOff);
+  const Args& a = l.a;
+  volatile int* const abort = &x->abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (smem_u32(sm) & 1023u) return;  // the swizzle needs it; the window starts aligned
+
+  auto timeout = [&]() {
+    if (a.status) *a.status = ATTN_ERR_DEVICE_TIMEOUT;
+    *abort = 1;
+  };
+  if (tid == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&x->lat_full[s], 1);
+      mbar_init(&x->lat_empty[s], 1);
+    }
+    for (int s = 0; s < NR; ++s) {
+      mbar_init(&x->rope_full[s], 1);
+      mbar_init(&x->rope_empty[s], 1);
+    }
+    mbar_init(&x->q_full, 128);
+    mbar_init(&x->q_empty, 1);
+    mbar_init(&x->s_full[0], 1);
+    mbar_init(&x->s_full[1], 1);
+    mbar_init(&x->p_full, 128);
+    mbar_init(&x->o_done, 1);
+    mbar_init(&x->o_empty, 128);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&x->piece_full[s], 1);
+      mbar_init(&x->piece_empty[s], 1 + 1 + 4 + 4);  // MMA, producer, query, softmax warps
+    }
+    mbar_init(&x->drain, 1);
+    x->abort = 0;
+    x->bad = 0;
+    mbar_fence_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&x->tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  grid_dep_wait();
+  if (tid == 0) a.split_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  Walk w;
+  walk_init<N>(a, x, w);  // two block barriers
+  tc_fence_after();
+  grid_dep_launch();
+  const uint32_t tmem = x->tmem;
+
+  // The i-th piece (in shared memory), and this warp's release of it.
+  auto take = [&](uint32_t i, bool* ok) -> const Piece* {
+    *ok = mbar_wait_warp(&x->piece_full[i & 3], (i >> 2) & 1);
+    return &x->piece[i & 3];
+  };
+  auto release = [&](uint32_t i) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&x->piece_empty[i & 3]);
+  };
+
+  if (warp == 2) {
+    // -------------------------------------------------------------- scheduler
+    bool ok = true, live = w.share > 0;
+    for (uint32_t i = 0; ok; ++i) {
+      if (i >= 4 && !(ok = mbar_wait_warp(&x->piece_empty[i & 3], ((i >> 2) - 1) & 1))) break;
+      if (lane == 0) {
+        Piece& p = x->piece[i & 3];
+        if (live) {
+          p.n = w.n;
+          p.key = w.key;
+          p.seq = w.seq;
+          p.rb = w.rb;
+          p.first = w.t0 == 0;
+          p.whole = w.t0 == 0 && w.t1 == w.nt;
+          const int64_t end = x->begin + w.done + (w.nt + kStart - w.u0);  // of the block's units
+          p.pieces = static_cast<int>((end * x->ctas + x->total - 1) / x->total) -
+                     static_cast<int>(blockIdx.x);
+          p.row0 = w.v.q.row0;
+          p.new_rows = w.v.q.n;
+          p.pos0 = w.v.q.len - w.v.q.n;
+          p.hi = w.v.hi;
+          p.any = w.any;
+          p.all = keys_all(a, w.v, w.rb * N, (w.rb + 1) * N);
+        } else {
+          p.n = -1;
+        }
+        mbar_arrive(&x->piece_full[i & 3]);
+      }
+      if (__any_sync(0xffffffffu, !live || *abort != 0)) break;
+      live = walk_next<N>(a, w);
+    }
+    if (!ok && lane == 0) timeout();
+  } else if (warp == 0) {
+    // -------------------------------------------------------------- MMA issuer
+    // Scores may run a tile ahead of P c.  Whichever is ready goes first: P c
+    // frees its tile's slots, and the next tile's blocks join the scores as they
+    // land.
+    constexpr uint32_t id_s = idesc_f32acc(F16 ? 0 : 1, kKeys, N, false, false);
+    constexpr uint32_t id_o = idesc_f32acc(F16 ? 0 : 1, 128, N, true, true);
+    const uint32_t tm = warp_uniform(tmem);
+    const uint64_t q_km = sdesc_sw128(smem_u32(sm), 16, 1024);
+    const uint64_t lat_km = sdesc_sw128(smem_u32(sm + L::kLatOff), 16, 1024);
+    const uint64_t lat_mn = sdesc_sw128(smem_u32(sm + L::kLatOff), kKeys * 128, 1024);
+    const uint64_t rope_km = sdesc_sw128(smem_u32(sm + L::kRopeOff), 16, 1024);
+    const uint64_t p_mn = sdesc_sw128(smem_u32(sm + L::kPOff), kKeys * 128, 1024);
+    uint32_t ks = 0, kp = 0;     // tiles whose scores, and whose P c, have been issued
+    uint32_t first = 0;          // by tile mod 4: begins its piece
+    uint32_t pi = 0, it = 0;     // pieces taken; pieces with tiles begun
+    uint32_t io = 0;             // pieces whose O was begun
+    int left = 0, slot = 0;      // tiles of the scores' piece to come; blocks of the next tile done
+    bool begun = false, end = false, ok = true;
+    auto ready = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
+    };
+    uint64_t t0 = globaltimer_ns();
+    for (uint32_t spin = 0; ok;) {
+      bool moved = false;
+      // P c of the oldest tile
+      if (kp < ks && ready(&x->p_full, kp & 1) &&
+          (!(first >> (kp & 3) & 1) || io == 0 || ready(&x->o_empty, (io - 1) & 1))) {
+        const bool begins = first >> (kp & 3) & 1;
+        tc_fence_after();
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const uint32_t s = (kp * NB + b) % NS;
+          mma_ss_warp<4, 4, 128, 128, 128, 128>(tm + L::kColO + b * N,
+                                                lat_mn + ((s * L::kSlot) >> 4), p_mn, id_o,
+                                                begins ? 0u : 1u);
+          mma_commit_warp(&x->lat_empty[s]);
+        }
+        mma_commit_warp(&x->o_done);
+        if (begins) ++io;
+        ++kp;
+        moved = true;
+      }
+      // a block of the next tile's scores
+      if (!moved && !end && left == 0) {
+        // the next piece with tiles
+        if (ready(&x->piece_full[pi & 3], (pi >> 2) & 1)) {
+          const int n = x->piece[pi & 3].n;
+          release(pi++);
+          if (n < 0) end = true;
+          left = n > 0 ? n : 0;
+          begun = false;
+          moved = true;
+        }
+      } else if (!moved && !end && ks - kp < 2) {
+        if (!begun && ready(&x->q_full, it & 1)) {
+          begun = true;
+          first |= 1u << (ks & 3);
+        }
+        if (begun) {
+          const uint32_t sb = tm + (ks & 1) * N;
+          if (slot < NB) {
+            const uint32_t e = ks * NB + slot, s = e % NS;
+            if (ready(&x->lat_full[s], (e / NS) & 1)) {
+              tc_fence_after();
+              mma_ss_warp<8, 4, 2, 506, 2, 8 * N - 6>(
+                  sb, lat_km + ((s * L::kSlot) >> 4), q_km + ((slot * 2 * N * 128) >> 4), id_s,
+                  slot == 0 ? 0u : 1u);
+              ++slot;
+              moved = true;
+            }
+          } else {
+            const uint32_t s = ks % NR;
+            if (ready(&x->rope_full[s], (ks / NR) & 1)) {
+              tc_fence_after();
+              mma_ss_warp<4, 4, 2, 2, 2, 2>(sb, rope_km + ((s * L::kRope) >> 4),
+                                            q_km + ((NB * 2 * N * 128) >> 4), id_s, 1u);
+              mma_commit_warp(&x->s_full[ks & 1]);
+              mma_commit_warp(&x->rope_empty[s]);
+              slot = 0;
+              if (--left == 0) {
+                mma_commit_warp(&x->q_empty);
+                ++it;
+              }
+              ++ks;
+              first &= ~(1u << (ks & 3));
+              moved = true;
+            }
+          }
+        }
+      }
+      if (end && kp == ks) break;
+      if (moved) {
+        spin = 0;
+      } else if ((++spin & 255u) == 0u) {
+        if (spin == 256u) t0 = globaltimer_ns();
+        ok = __all_sync(0xffffffffu, globaltimer_ns() - t0 <= 2000000000ull);
+      }
+    }
+    if (!ok && lane == 0) timeout();
+    mma_commit_warp(&x->drain);
+    mbar_wait(&x->drain, 0, 200000000ull);
+  } else if (warp == 1) {
+    // -------------------------------------------------------------- TMA producer
+    // Lane i looks after box i of a tile: a page, or 64 tokens of one.  The table
+    // is read a tile ahead.
+    const int rows_log = min(a.page_shift, 6), boxes = kKeys >> rows_log;
+    const int page_mask = (1 << a.page_shift) - 1;
+    uint32_t k = 0;
+    bool ok = true;
+    for (uint32_t pi = 0;; ++pi) {
+      const Piece* const p = take(pi, &ok);
+      if (!ok || p->n < 0) break;
+      const int n = p->n, key0 = p->key, end = p->any.y;
+      const int32_t* const table = a.table + p->seq * a.table_stride;
+      release(pi);
+      // box of this lane's copies: chunks of 64 coordinates take turns over lanes
+      const int box = lane % boxes, chunk = lane / boxes;
+      auto key_of = [&](int j) -> int { return key0 + j * kKeys + (box << rows_log); };
+      auto load_entry = [&](int j) -> int {
+        if (j >= n || key_of(j) >= end) return INT_MIN;
+        const int col = key_of(j) >> a.page_shift;
+        return col < a.max_pages ? table[col] : -1;
+      };
+      int ahead = load_entry(0);
+      for (int j = 0; j < n && ok; ++j, ++k) {
+        int id = ahead;
+        ahead = load_entry(j + 1);
+        if (id < 0 || id >= a.num_pages) {
+          if (id != INT_MIN) flag_bounds(a);
+          id = -1;
+        }
+        const unsigned okm = __ballot_sync(0xffffffffu, id >= 0);
+        const uint32_t count = __popc(okm & ((1u << boxes) - 1));
+        const int slot = key_of(j) & page_mask;
+        const uint32_t rows = count << rows_log;
+        const uint32_t at = static_cast<uint32_t>(box << rows_log) * 128;
+#pragma unroll 1
+        for (int b = 0; b < NB; ++b) {
+          const uint32_t e = k * NB + b, s = e % NS;
+          if (e >= NS && !(ok = mbar_wait_warp(&x->lat_empty[s], (e / NS - 1) & 1))) break;
+          if (b == 0) {
+            const int g = (16 * (lane & 3)) >> rows_log;
+            const unsigned m = __ballot_sync(0xffffffffu, okm >> g & 1) & 0xfu;
+            if (lane == 0) x->ok_mask[k & 7] = m;
+          }
+          // the arrival (release) publishes the mask; the copies follow it
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&x->lat_full[s], rows * 256);
+          __syncwarp();
+          const uint32_t dst = smem_u32(sm + L::kLatOff) + s * L::kSlot + at;
+          if (boxes == 1) {
+            if (lane == 0 && id >= 0)
+              tma_load_4d(dst, &maps.lat, &x->lat_full[s], 0, slot, 2 * b, id);
+          } else if (chunk < 2 && id >= 0) {
+            tma_load_4d(dst + chunk * (kKeys * 128), &maps.lat, &x->lat_full[s], 0, slot,
+                        2 * b + chunk, id);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        const uint32_t s = k % NR;
+        if (k >= NR && !(ok = mbar_wait_warp(&x->rope_empty[s], (k / NR - 1) & 1))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&x->rope_full[s], rows * 128);
+        __syncwarp();
+        if (chunk == 0 && id >= 0)
+          tma_load_4d(smem_u32(sm + L::kRopeOff) + s * L::kRope + at, &maps.rope,
+                      &x->rope_full[s], 0, slot, 2 * NB, id);
+        __syncwarp();
+      }
+      if (!ok) break;
+    }
+    if (!ok && lane == 0) timeout();
+    // copies in flight land before the block may leave
+    for (uint32_t e = k * NB > NS ? k * NB - NS : 0; e < k * NB; ++e)
+      mbar_wait(&x->lat_full[e % NS], (e / NS) & 1, 100000000ull);
+    for (uint32_t e = k > NR ? k - NR : 0; e < k; ++e)
+      mbar_wait(&x->rope_full[e % NR], (e / NR) & 1, 100000000ull);
+  } else if (warp >= 8) {
+    // -------------------------------------------------------------- queries
+    // A warp a row: 16 bytes a lane to where the MMA reads them.
+    uint32_t it = 0;
+    bool ok = true;
+    for (uint32_t pi = 0;; ++pi) {
+      const Piece* const p = take(pi, &ok);
+      if (!ok || p->n < 0) break;
+      const int n = p->n, r0 = p->rb * N, row0 = p->row0, new_rows = p->new_rows;
+      release(pi);
+      if (n == 0) continue;
+      if (it > 0 && !(ok = mbar_wait_warp(&x->q_empty, (it - 1) & 1))) break;
+      auto copy = [&](int r, int unit, const uint16_t* src, bool real) {
+        const uint32_t dst = smem_u32(sm) + (unit >> 3) * (N * 128) + r * 128 +
+                             (((unit & 7) ^ (r & 7)) << 4);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                     "r"(real ? 16 : 0)
+                     : "memory");
+      };
+#pragma unroll 2
+      for (int r = warp - 8; r < N; r += 4) {
+        const int rr = r0 + r, tok = div_group(a, rr), head = rr - tok * a.group;
+        const bool real = tok < new_rows;
+        const int64_t t = real ? row0 + tok : 0;
+        const uint16_t* src = l.q_lat + (real ? t * l.q_lat_tok + head * l.q_lat_head : 0);
+#pragma unroll
+        for (int u = 0; u < DC / 256; ++u)
+          copy(r, lane + 32 * u, src + (real ? (lane + 32 * u) * 8 : 0), real);
+        const uint16_t* rot = l.q_rot + (real ? t * l.q_rot_tok + head * l.q_rot_head : 0);
+        if (lane < 8) copy(r, DC / 8 + lane, rot + (real ? lane * 8 : 0), real);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      mbar_arrive(&x->q_full);
+      ++it;
+    }
+    if (!ok && lane == 0) timeout();
+  } else if (warp >= 4) {
+    // -------------------------------------------------------------- softmax
+    const int sw = warp - 4, st = tid - 128, g = lane >> 2, c2 = 2 * (lane & 3);
+    const uint32_t lanes = static_cast<uint32_t>(sw * 32) << 16;
+    const uint32_t o_tm = tmem + lanes + L::kColO;
+    const float fac = a.scale * kLog2e;
+    uint32_t k = 0, it = 0;
+    // A wait that ran out here is told to the other softmax warps at their next
+    // vote, so that all four leave together and none stays at their barrier.
+    bool failed = false;
+    for (uint32_t pi = 0;; ++pi) {
+      bool ok;
+      const Piece* const p = take(pi, &ok);
+      failed |= !ok;
+      const int n = ok ? p->n : -1, key0 = p->key;
+      if (n >= 0 && st < N) {  // keys that row st keeps
+        const int tok = div_group(a, p->rb * N + st), pos = p->pos0 + tok;
+        x->row_lo[st] = a.window >= 0 ? max(0, pos - a.window) : 0;
+        x->row_hi[st] = tok < p->new_rows ? (a.causal ? min(p->hi, pos + 1) : p->hi) : 0;
+      }
+      if (softmax_any(failed) || n < 0) break;
+      // column 8 b + c2 + e is index 2 b + e
+      float m[kC], sum[kC];
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+        m[i] = -FLT_MAX;
+        sum[i] = 0.f;
+      }
+      for (int j = 0; j < n; ++j, ++k) {
+        const int key = key0 + j * kKeys;
+        failed |= !mbar_wait_warp(&x->s_full[k & 1], (k >> 1) & 1);
+        // (the tile has landed; this orders what the producer wrote for it)
+        failed |= !mbar_wait_warp(&x->lat_full[(k * NB) % NS], (k * NB / NS) & 1);
+        tc_fence_after();
+        uint32_t u[2 * kC];
+        tmem_ld16x256b(tmem + lanes + (k & 1) * N, u);
+        const int okm = x->ok_mask[k & 7];
+        const bool whole = key >= p->all.x && key + kKeys <= p->all.y && okm == 0xf;
+        tmem_ld_wait(u);
+        float s[2 * kC];
+#pragma unroll
+        for (int i = 0; i < 2 * kC; ++i) s[i] = __uint_as_float(u[i]);
+        if (!whole) {
+          const int k0 = key + 16 * sw + g;
+          const bool page = okm >> sw & 1;
+#pragma unroll
+          for (int b = 0; b < N / 8; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int lo = x->row_lo[8 * b + c2 + e], hi = x->row_hi[8 * b + c2 + e];
+              if (!(page && k0 >= lo && k0 < hi)) s[4 * b + e] = -INFINITY;
+              if (!(page && k0 + 8 >= lo && k0 + 8 < hi)) s[4 * b + 2 + e] = -INFINITY;
+            }
+        }
+        // exponents against the maximum so far
+        bool grow = failed;
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+          const float mx = fmaxf(s[4 * (i >> 1) + (i & 1)], s[4 * (i >> 1) + 2 + (i & 1)]);
+          grow |= fmaf(mx, fac, -m[i]) > kLazy;
+        }
+        bool again = false;
+        if (softmax_any(grow)) {
+#pragma unroll
+          for (int i = 0; i < kC; ++i) {
+            float mx = fmaxf(s[4 * (i >> 1) + (i & 1)], s[4 * (i >> 1) + 2 + (i & 1)]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            if (g == 0) x->col[sw][8 * (i >> 1) + c2 + (i & 1)] = mx;
+          }
+          if (softmax_any(failed)) {
+            failed = true;
+            break;
+          }
+#pragma unroll
+          for (int i = 0; i < kC; ++i) {
+            const int c = 8 * (i >> 1) + c2 + (i & 1);
+            const float mx = fmax3(x->col[0][c], x->col[1][c], fmaxf(x->col[2][c], x->col[3][c])) * fac;
+            const bool up = mx - m[i] > kLazy;
+            const float f = up ? ex2_approx(m[i] - mx) : 1.f;
+            if (up) m[i] = mx;
+            sum[i] *= f;
+            if (sw == 0 && g == 0) x->fac[c] = f;
+          }
+          again = softmax_any(j > 0);
+        }
+        // P, over its rounded pairs of columns
+        uint32_t pk[kC];
+#pragma unroll
+        for (int b = 0; b < N / 8; ++b)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float p0 = ex2_approx(fmaf(s[4 * b + 2 * h], fac, kShift - m[2 * b]));
+            const float p1 = ex2_approx(fmaf(s[4 * b + 2 * h + 1], fac, kShift - m[2 * b + 1]));
+            sum[2 * b] += p0;
+            sum[2 * b + 1] += p1;
+            pk[2 * b + h] = F16 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          }
+        // the tile before this one is done with P and O
+        if (k > 0) failed |= !mbar_wait_warp(&x->o_done, (k - 1) & 1);
+        tc_fence_after();
+        if (again) {
+#pragma unroll 1
+          for (int q = 0; q < NB * N / 16; ++q) {
+            uint32_t o[16];
+            tmem_ld32x32b_x16(o_tm + q * 16, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * x->fac[(q * 16 + e) % N]);
+            tmem_st32x32b_x16(o_tm + q * 16, o);
+          }
+          tmem_st_wait();
+        }
+        {
+          const uint32_t row = smem_u32(sm + L::kPOff) + (16 * sw + g) * 128;
+#pragma unroll
+          for (int b = 0; b < N / 8; ++b)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + h * 1024 + ((b ^ g) << 4) + c2 * 2),
+                           "r"(pk[2 * b + h])
+                           : "memory");
+        }
+        if (!whole) {
+          // rows no one keeps become zeros; of the others what is not finite
+          const int r = st >> 1;
+          const bool in = (okm >> (r >> 4) & 1) && key + r >= p->any.x && key + r < p->any.y;
+#pragma unroll 1
+          for (int b = 0; b < NB; ++b) {
+            const uint32_t e = k * NB + b;
+            failed |= !mbar_wait_warp(&x->lat_full[e % NS], (e / NS) & 1);
+            const uint32_t at = smem_u32(sm + L::kLatOff) + (e % NS) * L::kSlot +
+                                (st & 1) * (kKeys * 128) + r * 128;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t q = at + ((i ^ (r & 7)) << 4);
+              if (!in) {
+                st_shared_v4(q, 0, 0, 0, 0);
+                continue;
+              }
+              const uint4 v = lds128(q);
+              if (not_finite<kKind>(v.x) | not_finite<kKind>(v.y) | not_finite<kKind>(v.z) |
+                  not_finite<kKind>(v.w)) {
+                x->bad = it + 1;
+                st_shared_v4(q, finite_only<kKind>(v.x), finite_only<kKind>(v.y),
+                             finite_only<kKind>(v.z), finite_only<kKind>(v.w));
+              }
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(&x->p_full);
+      }
+      // ---- epilogue: O or the piece's partial state
+      const bool complete = p->whole;
+      const int slot = 2 * blockIdx.x + p->first;
+      const int rows = min(N, p->new_rows * a.group - p->rb * N);
+      const int64_t out0 = static_cast<int64_t>(p->row0) * a.group + p->rb * N;  // of [T * H]
+      if (softmax_any(failed)) break;  // (`col` and `fac` have been read)
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], d);
+        if (g == 0) {
+          const int c = 8 * (i >> 1) + c2 + (i & 1);
+          x->col[sw][c] = sum[i];
+          if (sw == 0) x->fac[c] = m[i];
+        }
+      }
+      softmax_any(false);
+      float norm = 0.f;
+      if (st < N) {
+        const float lsum = x->col[0][st] + x->col[1][st] + (x->col[2][st] + x->col[3][st]);
+        const float mx = x->fac[st];
+        const bool none = mx == -FLT_MAX && lsum == 0.f;
+        if (!complete) {
+          norm = none ? 0.f : 1.f;
+          if (st < rows)
+            a.part_ml[static_cast<int64_t>(slot) * N + st] =
+                make_float2(none ? -INFINITY : mx, none ? 0.f : lsum);
+        } else {
+          const int rr = p->rb * N + st, tok = div_group(a, rr), head = rr - tok * a.group;
+          float lt = lsum, mt = mx, keep = 1.f;
+          if (a.sink && st < rows) {
+            const float s2 = a.sink[head] * kLog2e;
+            mt = none ? s2 : fmaxf(mx, s2);
+            const float mu = mt == -INFINITY ? 0.f : mt;
+            keep = ex2_approx(mx - mu);
+            lt = lsum * keep + ex2_approx(s2 - mu + kShift);
+          }
+          norm = none ? 0.f : keep / lt;
+          if (a.lse && st < rows)
+            a.lse[static_cast<int64_t>(head) * a.num_tokens + p->row0 + tok] =
+                none ? (a.sink ? a.sink[head] : -INFINITY) : (mt - kShift) * kLn2 + logf(lt);
+        }
+      }
+      softmax_any(false);
+      if (st < N) x->fac[st] = norm;
+      softmax_any(false);
+      const bool bad = n > 0 && x->bad == it + 1;
+      if (n > 0) {
+        failed |= !mbar_wait_warp(&x->o_done, (k - 1) & 1);
+        tc_fence_after();
+      }
+#pragma unroll 1
+      for (int b = 0; b < NB; ++b) {
+        const int d = b * 128 + st;  // this lane's coordinate
+#pragma unroll 1
+        for (int c0 = 0; c0 < N; c0 += 16) {
+          if (c0 >= rows) break;
+          uint32_t o[16];
+          if (n > 0) {
+            tmem_ld32x32b_x16(o_tm + b * N + c0, o);
+            tmem_ld_wait(o);
+          }
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float f = x->fac[c0 + i];
+            v[i] = n > 0 && f != 0.f ? __uint_as_float(o[i]) * f : 0.f;
+          }
+          if (bad) {
+            for (int j = 0; j < n; ++j) {
+              const int key = key0 + j * kKeys;
+              for (int kk = max(key, p->any.x); kk < min(key + kKeys, p->any.y); ++kk) {
+                const int page = page_of(a, p->seq, kk);
+                if (page < 0) continue;
+                const float e = elem(
+                    reinterpret_cast<const uint16_t*>(
+                        a.kc + page * a.k_page +
+                        static_cast<int64_t>(kk & ((1 << a.page_shift) - 1)) * a.k_tok)[d],
+                    F16);
+                if (fabsf(e) < INFINITY) continue;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  if (kk >= x->row_lo[c0 + i] && kk < x->row_hi[c0 + i]) v[i] = NAN;
+              }
+            }
+          }
+          if (complete) {
+            // neighbours swap, so that a lane has two coordinates of one row
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const bool odd = lane & 1;
+              const float y = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+              const uint32_t w2 = odd ? pack2(y, v[i + 1], F16) : pack2(v[i], y, F16);
+              const int r = c0 + i + odd;
+              if (r < rows)
+                *reinterpret_cast<uint32_t*>(a.o + (out0 + r) * DC + (d & ~1)) = w2;
+            }
+          } else {
+            float* dst = a.part + (static_cast<int64_t>(slot) * N + c0) * DC + d;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (c0 + i < rows) dst[i * DC] = v[i];
+          }
+        }
+      }
+      if (n > 0) {
+        tc_fence_before();
+        mbar_arrive(&x->o_empty);
+      }
+      if (!complete && p->first && st == 0)
+        a.split_desc[blockIdx.x] = make_int4(p->pieces, p->seq, p->rb, 0);
+      if (softmax_any(failed)) break;  // (row bounds, `fac` and the piece have been read)
+      release(pi);
+      if (n > 0) ++it;
+    }
+    if (failed && lane == 0) timeout();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the pieces of split blocks of rows: block (i, y) rows y, y + gridDim.y, ...
+// of the block of rows whose first piece is block i's, four coordinates a thread.
+template <bool F16, int DC, int N>
+__global__ void __launch_bounds__(DC / 4) latent_join_kernel(const __grid_constant__ Args a) {
+  constexpr float kShift = F16 ? 7.f : 0.f;
+  grid_dep_wait();
+  const int4 d = a.split_desc[blockIdx.x];
+  if (d.x == 0) return;
+  const Seq q = load_seq(a, d.y);
+  const int rows = min(N, q.n * a.group - d.z * N);
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    const int rr = d.z * N + r, tok = div_group(a, rr), head = rr - tok * a.group;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = -INFINITY, sum = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < d.x; ++p) {
+      const int64_t at = (2 * (static_cast<int64_t>(blockIdx.x) + p) + (p == 0 ? 1 : 0)) * N + r;
+      const float2 ml = a.part_ml[at];
+      const float4 v = reinterpret_cast<const float4*>(a.part + at * DC)[threadIdx.x];
+      const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
+      const float f0 = ex2_approx(m - mu), f1 = ex2_approx(ml.x - mu);
+      acc = make_float4(acc.x * f0 + v.x * f1, acc.y * f0 + v.y * f1, acc.z * f0 + v.z * f1,
+                        acc.w * f0 + v.w * f1);
+      sum = sum * f0 + ml.y * f1;
+      m = mn;
+    }
+    const bool none = no_key(m, sum);
+    float mt = m, lt = sum, keep = 1.f;
+    if (a.sink) {
+      const float s2 = a.sink[head] * kLog2e;
+      mt = fmaxf(m, s2);
+      const float mu = mt == -INFINITY ? 0.f : mt;
+      keep = ex2_approx(m - mu);
+      lt = sum * keep + ex2_approx(s2 - mu + kShift);
+    }
+    const float inv = none ? 0.f : keep / lt;
+    const int64_t t = q.row0 + tok;
+    *reinterpret_cast<uint2*>(a.o + (t * a.group + head) * DC + 4 * threadIdx.x) =
+        make_uint2(pack2(acc.x * inv, acc.y * inv, F16), pack2(acc.z * inv, acc.w * inv, F16));
+    if (a.lse && threadIdx.x == 0)
+      a.lse[static_cast<int64_t>(head) * a.num_tokens + t] =
+          none ? (a.sink ? a.sink[head] : -INFINITY) : (mt - kShift) * kLn2 + logf(lt);
+  }
+}
+
+template <bool F16, int DC, int N>
+cudaError_t latent_one(const LatentArgs& l, int sms, cudaStream_t st) {
+  using L = LatentCfg<DC, N>;
+  auto kern = latent_kernel<F16, DC, N>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  if (e != cudaSuccess) return e;
+  LatentMaps maps;
+  const int slots = l.a.page_shift < 6 ? 1 << l.a.page_shift : kKeys;
+  if (!latent_map(&maps.lat, l, slots, slots == kKeys ? 2 : 1) ||
+      !latent_map(&maps.rope, l, slots, 1))
+    return cudaErrorInvalidValue;
+  const unsigned ctas = sms < kLatentMaxCtas ? sms : kLatentMaxCtas;
+  e = launch_early(kern, dim3(ctas), dim3(kThreads), L::kSmem, st, l, maps);
+  if (e != cudaSuccess) return e;
+  return launch_early(latent_join_kernel<F16, DC, N>, dim3(ctas, N < 32 ? N : 32), dim3(DC / 4), 0,
+                      st, l.a);
 }
 
 template <bool F16>
-cudaError_t launch_latent(const LatentArgs& l, cudaStream_t st) {
-  const dim3 grid(l.a.num_tokens, l.a.Hq);
-  return l.d_c == 512 ? launch_early(latent_plain_kernel<F16, 512>, grid, dim3(128), 0, st, l)
-                      : launch_early(latent_plain_kernel<F16, 256>, grid, dim3(128), 0, st, l);
+cudaError_t launch_latent(const LatentArgs& l, int rows, int sms, cudaStream_t st) {
+  if (l.d_c == 512)
+    return rows == 16   ? latent_one<F16, 512, 16>(l, sms, st)
+           : rows == 32 ? latent_one<F16, 512, 32>(l, sms, st)
+                        : latent_one<F16, 512, 64>(l, sms, st);
+  return rows == 16   ? latent_one<F16, 256, 16>(l, sms, st)
+         : rows == 32 ? latent_one<F16, 256, 32>(l, sms, st)
+                      : latent_one<F16, 256, 64>(l, sms, st);
 }
 
 }  // namespace

@@ -4,8 +4,8 @@
 namespace attn {
 namespace paged {
 
-cudaError_t launch_latent_bf16(const LatentArgs& l, int, int, cudaStream_t st) {
-  return launch_latent<false>(l, st);
+cudaError_t launch_latent_bf16(const LatentArgs& l, int rows, int sms, cudaStream_t st) {
+  return launch_latent<false>(l, rows, sms, st);
 }
 
 }  // namespace paged
