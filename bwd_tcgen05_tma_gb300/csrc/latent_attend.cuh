@@ -20,8 +20,8 @@
 // row block, tile) cut into equal shares, one a block, one block an SM; pieces of
 // a row block meet in a second kernel in a fixed order.
 //
-// Roles: MMA issuer, TMA producer, scheduler (a warp each), four softmax warps, four
-// warps that copy queries.
+// Roles: an MMA issuer for each product, TMA producer, scheduler (a warp each), four
+// softmax warps, four warps that copy queries.
 //
 // Values that are not finite in a tile that some rows mask in part are taken out of
 // the product (their zero weight would make NaN of them); a row that keeps such a
@@ -40,7 +40,7 @@ namespace {
 using namespace sm103;
 
 constexpr int kKeys = 64;      // keys a tile
-constexpr int kThreads = 384;  // warps: MMA, TMA, scheduler, -, 4 softmax, 4 queries
+constexpr int kThreads = 384;  // warps: S, TMA, scheduler, P c, 4 softmax, 4 queries
 constexpr float kLazy = 8.f;
 
 struct LatentMaps {
@@ -60,9 +60,9 @@ struct Piece {
 template <int N, int SLOTS, int RSLOTS>
 struct LatentAux {
   uint64_t lat_full[SLOTS], lat_empty[SLOTS], rope_full[RSLOTS], rope_empty[RSLOTS];
-  uint64_t q_full, q_empty, s_full[2], p_full, o_done, o_empty;
+  uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full, o_done, o_empty;
   uint64_t piece_full[4], piece_empty[4];
-  uint64_t drain;
+  uint64_t drain[2];
   uint32_t tmem;
   int abort;
   uint32_t bad;     // number + 1 of the last piece a value was taken out of
@@ -287,14 +287,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&x->q_empty, 1);
     mbar_init(&x->s_full[0], 1);
     mbar_init(&x->s_full[1], 1);
+    mbar_init(&x->s_empty[0], 4);
+    mbar_init(&x->s_empty[1], 4);
     mbar_init(&x->p_full, 128);
     mbar_init(&x->o_done, 1);
     mbar_init(&x->o_empty, 128);
     for (int s = 0; s < 4; ++s) {
       mbar_init(&x->piece_full[s], 1);
-      mbar_init(&x->piece_empty[s], 1 + 1 + 4 + 4);  // MMA, producer, query, softmax warps
+      mbar_init(&x->piece_empty[s], 2 + 1 + 4 + 4);  // MMA, producer, query, softmax warps
     }
-    mbar_init(&x->drain, 1);
+    mbar_init(&x->drain[0], 1);
+    mbar_init(&x->drain[1], 1);
     x->abort = 0;
     x->bad = 0;
     mbar_fence_init();
@@ -355,107 +358,85 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && lane == 0) timeout();
   } else if (warp == 0) {
-    // -------------------------------------------------------------- MMA issuer
-    // Scores may run a tile ahead of P c.  Whichever is ready goes first: P c
-    // frees its tile's slots, and the next tile's blocks join the scores as they
-    // land.
+    // -------------------------------------------------------------- scores' issuer
+    // Up to two tiles ahead of the softmax; a tile's blocks join as they land.
     constexpr uint32_t id_s = idesc_f32acc(F16 ? 0 : 1, kKeys, N, false, false);
-    constexpr uint32_t id_o = idesc_f32acc(F16 ? 0 : 1, 128, N, true, true);
     const uint32_t tm = warp_uniform(tmem);
     const uint64_t q_km = sdesc_sw128(smem_u32(sm), 16, 1024);
     const uint64_t lat_km = sdesc_sw128(smem_u32(sm + L::kLatOff), 16, 1024);
-    const uint64_t lat_mn = sdesc_sw128(smem_u32(sm + L::kLatOff), kKeys * 128, 1024);
     const uint64_t rope_km = sdesc_sw128(smem_u32(sm + L::kRopeOff), 16, 1024);
+    uint32_t k = 0, it = 0;
+    bool ok = true;
+    for (uint32_t pi = 0;; ++pi) {
+      const Piece* const p = take(pi, &ok);
+      const int n = ok ? p->n : -1;
+      release(pi);
+      if (n < 0) break;
+      if (n == 0) continue;
+      if (!(ok = mbar_wait_warp(&x->q_full, it & 1))) break;
+      for (int j = 0; j < n && ok; ++j, ++k) {
+        // the softmax has read the scores these replace
+        if (k >= 2 && !(ok = mbar_wait_warp(&x->s_empty[k & 1], ((k >> 1) - 1) & 1))) break;
+        const uint32_t d = tm + (k & 1) * N;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const uint32_t e = k * NB + b, s = e % NS;
+          if (!(ok = mbar_wait_warp(&x->lat_full[s], (e / NS) & 1))) break;
+          tc_fence_after();
+          mma_ss_warp<8, 4, 2, 506, 2, 8 * N - 6>(d, lat_km + ((s * L::kSlot) >> 4),
+                                                  q_km + ((b * 2 * N * 128) >> 4), id_s,
+                                                  b == 0 ? 0u : 1u);
+        }
+        const uint32_t s = k % NR;
+        if (!ok || !(ok = mbar_wait_warp(&x->rope_full[s], (k / NR) & 1))) break;
+        tc_fence_after();
+        mma_ss_warp<4, 4, 2, 2, 2, 2>(d, rope_km + ((s * L::kRope) >> 4),
+                                      q_km + ((NB * 2 * N * 128) >> 4), id_s, 1u);
+        mma_commit_warp(&x->s_full[k & 1]);
+        mma_commit_warp(&x->rope_empty[s]);
+      }
+      if (!ok) break;
+      mma_commit_warp(&x->q_empty);
+      ++it;
+    }
+    if (!ok && lane == 0) timeout();
+    mma_commit_warp(&x->drain[0]);
+    mbar_wait(&x->drain[0], 0, 200000000ull);
+  } else if (warp == 3) {
+    // -------------------------------------------------------------- P c's issuer
+    // A warp of its own: neither product waits for what the other waits for.
+    constexpr uint32_t id_o = idesc_f32acc(F16 ? 0 : 1, 128, N, true, true);
+    const uint32_t tm = warp_uniform(tmem);
+    const uint64_t lat_mn = sdesc_sw128(smem_u32(sm + L::kLatOff), kKeys * 128, 1024);
     const uint64_t p_mn = sdesc_sw128(smem_u32(sm + L::kPOff), kKeys * 128, 1024);
-    uint32_t ks = 0, kp = 0;     // tiles whose scores, and whose P c, have been issued
-    uint32_t first = 0;          // by tile mod 4: begins its piece
-    uint32_t pi = 0, it = 0;     // pieces taken; pieces with tiles begun
-    uint32_t io = 0;             // pieces whose O was begun
-    int left = 0, slot = 0;      // tiles of the scores' piece to come; blocks of the next tile done
-    bool begun = false, end = false, ok = true;
-    auto ready = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
-    };
-    uint64_t t0 = globaltimer_ns();
-    for (uint32_t spin = 0; ok;) {
-      bool moved = false;
-      // P c of the oldest tile
-      if (kp < ks && ready(&x->p_full, kp & 1) &&
-          (!(first >> (kp & 3) & 1) || io == 0 || ready(&x->o_empty, (io - 1) & 1))) {
-        const bool begins = first >> (kp & 3) & 1;
+    uint32_t k = 0, it = 0;
+    bool ok = true;
+    for (uint32_t pi = 0;; ++pi) {
+      const Piece* const p = take(pi, &ok);
+      const int n = ok ? p->n : -1;
+      release(pi);
+      if (n < 0) break;
+      if (n == 0) continue;
+      if (it > 0 && !(ok = mbar_wait_warp(&x->o_empty, (it - 1) & 1))) break;
+      for (int j = 0; j < n; ++j, ++k) {
+        if (!(ok = mbar_wait_warp(&x->p_full, k & 1))) break;
         tc_fence_after();
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const uint32_t s = (kp * NB + b) % NS;
+          const uint32_t s = (k * NB + b) % NS;
           mma_ss_warp<4, 4, 128, 128, 128, 128>(tm + L::kColO + b * N,
                                                 lat_mn + ((s * L::kSlot) >> 4), p_mn, id_o,
-                                                begins ? 0u : 1u);
+                                                j == 0 ? 0u : 1u);
           mma_commit_warp(&x->lat_empty[s]);
         }
         mma_commit_warp(&x->o_done);
-        if (begins) ++io;
-        ++kp;
-        moved = true;
       }
-      // a block of the next tile's scores
-      if (!moved && !end && left == 0) {
-        // the next piece with tiles
-        if (ready(&x->piece_full[pi & 3], (pi >> 2) & 1)) {
-          const int n = x->piece[pi & 3].n;
-          release(pi++);
-          if (n < 0) end = true;
-          left = n > 0 ? n : 0;
-          begun = false;
-          moved = true;
-        }
-      } else if (!moved && !end && ks - kp < 2) {
-        if (!begun && ready(&x->q_full, it & 1)) {
-          begun = true;
-          first |= 1u << (ks & 3);
-        }
-        if (begun) {
-          const uint32_t sb = tm + (ks & 1) * N;
-          if (slot < NB) {
-            const uint32_t e = ks * NB + slot, s = e % NS;
-            if (ready(&x->lat_full[s], (e / NS) & 1)) {
-              tc_fence_after();
-              mma_ss_warp<8, 4, 2, 506, 2, 8 * N - 6>(
-                  sb, lat_km + ((s * L::kSlot) >> 4), q_km + ((slot * 2 * N * 128) >> 4), id_s,
-                  slot == 0 ? 0u : 1u);
-              ++slot;
-              moved = true;
-            }
-          } else {
-            const uint32_t s = ks % NR;
-            if (ready(&x->rope_full[s], (ks / NR) & 1)) {
-              tc_fence_after();
-              mma_ss_warp<4, 4, 2, 2, 2, 2>(sb, rope_km + ((s * L::kRope) >> 4),
-                                            q_km + ((NB * 2 * N * 128) >> 4), id_s, 1u);
-              mma_commit_warp(&x->s_full[ks & 1]);
-              mma_commit_warp(&x->rope_empty[s]);
-              slot = 0;
-              if (--left == 0) {
-                mma_commit_warp(&x->q_empty);
-                ++it;
-              }
-              ++ks;
-              first &= ~(1u << (ks & 3));
-              moved = true;
-            }
-          }
-        }
-      }
-      if (end && kp == ks) break;
-      if (moved) {
-        spin = 0;
-      } else if ((++spin & 255u) == 0u) {
-        if (spin == 256u) t0 = globaltimer_ns();
-        ok = __all_sync(0xffffffffu, globaltimer_ns() - t0 <= 2000000000ull);
-      }
+      if (!ok) break;
+      ++it;
     }
     if (!ok && lane == 0) timeout();
-    mma_commit_warp(&x->drain);
-    mbar_wait(&x->drain, 0, 200000000ull);
+    mma_commit_warp(&x->drain[1]);
+    mbar_wait(&x->drain[1], 0, 200000000ull);
   } else if (warp == 1) {
     // -------------------------------------------------------------- TMA producer
     // Lane i looks after box i of a tile: a page, or 64 tokens of one.  The table
@@ -608,6 +589,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int okm = x->ok_mask[k & 7];
         const bool whole = key >= p->all.x && key + kKeys <= p->all.y && okm == 0xf;
         tmem_ld_wait(u);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x->s_empty[k & 1]);
         float s[2 * kC];
 #pragma unroll
         for (int i = 0; i < 2 * kC; ++i) s[i] = __uint_as_float(u[i]);
