@@ -57,6 +57,23 @@ struct Piece {
   int2 any, all;     // keys some row, and every row, of the block keeps
 };
 
+// Units in equal shares, block i from floor(i total / ctas) on: one division of
+// 64 bits a call (they take as long as a read from memory here).
+struct Shares {
+  int64_t each;
+  int rest, ctas;
+  __device__ __forceinline__ int64_t begin(int i) const { return i * each + i * rest / ctas; }
+};
+__device__ __forceinline__ Shares shares_of(int64_t total, int ctas) {
+  Shares s;
+  s.ctas = max(ctas, 1);
+  s.each = total >> 31 ? total / s.ctas
+                       : static_cast<int64_t>(static_cast<uint32_t>(total) /
+                                              static_cast<uint32_t>(s.ctas));
+  s.rest = static_cast<int>(total - s.each * s.ctas);
+  return s;
+}
+
 template <int N, int SLOTS, int RSLOTS>
 struct LatentAux {
   uint64_t lat_full[SLOTS], lat_empty[SLOTS], rope_full[RSLOTS], rope_empty[RSLOTS];
@@ -68,8 +85,9 @@ struct LatentAux {
   uint32_t bad;     // number + 1 of the last piece a value was taken out of
   int ok_mask[8];   // by tile: 16-key groups whose page exists
   int64_t part[kThreads / 32];
-  int64_t begin, total;  // the block's first unit, all units
-  int ctas, unit0, seq, rb;
+  int64_t begin;  // the block's first unit
+  Shares shares;
+  int unit0, seq, rb;
   Piece piece[4];
   int row_lo[N], row_hi[N];
   float col[4][N];  // by softmax warp: maxima, or sums
@@ -206,10 +224,11 @@ __device__ __forceinline__ void walk_init(const Args& a, Aux* x, Walk& w) {
     total += x->part[i];
   }
   const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+  const Shares sh = shares_of(total, ctas);
   w.done = w.share = 0;
   if (static_cast<int>(blockIdx.x) < ctas) {
-    const int64_t begin = blockIdx.x * total / ctas;
-    w.share = static_cast<int>((blockIdx.x + 1) * total / ctas - begin);
+    const int64_t begin = sh.begin(blockIdx.x);
+    w.share = static_cast<int>(sh.begin(blockIdx.x + 1) - begin);
     if (begin >= before && begin < before + mine) {
       int64_t off = begin - before;
       int s = first;
@@ -226,8 +245,7 @@ __device__ __forceinline__ void walk_init(const Args& a, Aux* x, Walk& w) {
         x->rb = rb;
         x->unit0 = static_cast<int>(off);
         x->begin = begin;
-        x->total = total;
-        x->ctas = ctas;
+        x->shares = sh;
         break;
       }
     }
@@ -339,9 +357,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.rb = w.rb;
           p.first = w.t0 == 0;
           p.whole = w.t0 == 0 && w.t1 == w.nt;
-          const int64_t end = x->begin + w.done + (w.nt + kStart - w.u0);  // of the block's units
-          p.pieces = static_cast<int>((end * x->ctas + x->total - 1) / x->total) -
-                     static_cast<int>(blockIdx.x);
+          p.pieces = 0;
+          if (p.first && !p.whole) {  // blocks that begin before the row block ends
+            const int64_t end = x->begin + w.done + (w.nt + kStart - w.u0);
+            int c = blockIdx.x + 1;
+            while (c < x->shares.ctas && x->shares.begin(c) < end) ++c;
+            p.pieces = c - static_cast<int>(blockIdx.x);
+          }
           p.row0 = w.v.q.row0;
           p.new_rows = w.v.q.n;
           p.pos0 = w.v.q.len - w.v.q.n;
@@ -525,24 +547,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       release(pi);
       if (n == 0) continue;
       if (it > 0 && !(ok = mbar_wait_warp(&x->q_empty, (it - 1) & 1))) break;
-      auto copy = [&](int r, int unit, const uint16_t* src, bool real) {
-        const uint32_t dst = smem_u32(sm) + (unit >> 3) * (N * 128) + r * 128 +
-                             (((unit & 7) ^ (r & 7)) << 4);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                     "r"(real ? 16 : 0)
-                     : "memory");
-      };
-#pragma unroll 2
-      for (int r = warp - 8; r < N; r += 4) {
-        const int rr = r0 + r, tok = div_group(a, rr), head = rr - tok * a.group;
-        const bool real = tok < new_rows;
-        const int64_t t = real ? row0 + tok : 0;
-        const uint16_t* src = l.q_lat + (real ? t * l.q_lat_tok + head * l.q_lat_head : 0);
+      // a lane finds a row's addresses (offsets in 16-byte units, < 0: no such row)
+      constexpr int kRowsWarp = N / 4;
+      int64_t lat_at = -1, rot_at = 0;
+      if (lane < kRowsWarp) {
+        const int rr = r0 + (warp - 8) * kRowsWarp + lane, tok = div_group(a, rr);
+        if (tok < new_rows) {
+          const int64_t t = row0 + tok, head = rr - tok * a.group;
+          lat_at = (t * l.q_lat_tok + head * l.q_lat_head) >> 3;
+          rot_at = (t * l.q_rot_tok + head * l.q_rot_head) >> 3;
+        }
+      }
+      const uint4* const lat = reinterpret_cast<const uint4*>(l.q_lat);
+      const uint4* const rot = reinterpret_cast<const uint4*>(l.q_rot);
+#pragma unroll 4
+      for (int i = 0; i < kRowsWarp; ++i) {
+        const int r = (warp - 8) * kRowsWarp + i;
+        const int64_t la = __shfl_sync(0xffffffffu, lat_at, i);
+        const int64_t ra = __shfl_sync(0xffffffffu, rot_at, i);
+        const int bytes = la >= 0 ? 16 : 0;
+        const uint4* const src = lat + (la >= 0 ? la + lane : 0);
+        const uint32_t dst = smem_u32(sm) + (lane >> 3) * (N * 128) + r * 128 +
+                             (((lane & 7) ^ (r & 7)) << 4);
+        auto copy = [&](uint32_t to, const uint4* from) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
+                       "r"(bytes)
+                       : "memory");
+        };
 #pragma unroll
         for (int u = 0; u < DC / 256; ++u)
-          copy(r, lane + 32 * u, src + (real ? (lane + 32 * u) * 8 : 0), real);
-        const uint16_t* rot = l.q_rot + (real ? t * l.q_rot_tok + head * l.q_rot_head : 0);
-        if (lane < 8) copy(r, DC / 8 + lane, rot + (real ? lane * 8 : 0), real);
+          copy(dst + u * 4 * (N * 128), src + (la >= 0 ? 32 * u : 0));
+        if (lane < 8) copy(dst + (DC / 64) * (N * 128), rot + (la >= 0 ? ra + lane : 0));
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_smem();
@@ -732,9 +767,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool none = mx == -FLT_MAX && lsum == 0.f;
         if (!complete) {
           norm = none ? 0.f : 1.f;
-          if (st < rows)
-            a.part_ml[static_cast<int64_t>(slot) * N + st] =
-                make_float2(none ? -INFINITY : mx, none ? 0.f : lsum);
+          float* const ml = reinterpret_cast<float*>(a.part_ml + static_cast<int64_t>(slot) * N);
+          ml[st] = none ? -INFINITY : mx;
+          ml[N + st] = none ? 0.f : lsum;
         } else {
           const int rr = p->rb * N + st, tok = div_group(a, rr), head = rr - tok * a.group;
           float lt = lsum, mt = mx, keep = 1.f;
@@ -806,10 +841,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint32_t*>(a.o + (out0 + r) * DC + (d & ~1)) = w2;
             }
           } else {
-            float* dst = a.part + (static_cast<int64_t>(slot) * N + c0) * DC + d;
+            // [slot][coordinate][row]: a lane's rows are contiguous
+            float* dst = a.part + (static_cast<int64_t>(slot) * DC + d) * N + c0;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (c0 + i < rows) dst[i * DC] = v[i];
+            for (int i = 0; i < 16; i += 8)
+              st_global_v8(dst + i, __float_as_uint(v[i]), __float_as_uint(v[i + 1]),
+                           __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]),
+                           __float_as_uint(v[i + 4]), __float_as_uint(v[i + 5]),
+                           __float_as_uint(v[i + 6]), __float_as_uint(v[i + 7]));
           }
         }
       }
@@ -833,48 +872,123 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the pieces of split blocks of rows: block (i, y) rows y, y + gridDim.y, ...
-// of the block of rows whose first piece is block i's, four coordinates a thread.
+// Joins the pieces of split blocks of rows.  A unit is 1024 values of one block of
+// rows, all its rows and 1024 / N coordinates, four rows a thread; the two halves
+// of a thread block take the pieces in turn.  Units are shared out over the grid,
+// whose blocks read all descriptors at once.
+constexpr int kJoinThreads = 512;
 template <bool F16, int DC, int N>
-__global__ void __launch_bounds__(DC / 4) latent_join_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kJoinThreads)
+    latent_join_kernel(const __grid_constant__ Args a, int blocks) {
   constexpr float kShift = F16 ? 7.f : 0.f;
+  constexpr int kDims = 1024 / N, kUnits = DC / kDims, kGroups = kJoinThreads / N;
+  __shared__ int s_first[kLatentMaxCtas], s_warp[kJoinThreads / 32];
+  __shared__ int4 s_desc[kLatentMaxCtas];
+  __shared__ float s_red[kGroups][N];
+  __shared__ __align__(16) float s_mu[N], s_scale[N];
+  __shared__ float4 s_acc[256];
+  __shared__ __align__(16) uint16_t s_o[N][kDims + 8];
+  const int tid = threadIdx.x;
   grid_dep_wait();
-  const int4 d = a.split_desc[blockIdx.x];
-  if (d.x == 0) return;
-  const Seq q = load_seq(a, d.y);
-  const int rows = min(N, q.n * a.group - d.z * N);
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    const int rr = d.z * N + r, tok = div_group(a, rr), head = rr - tok * a.group;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float m = -INFINITY, sum = 0.f;
+  // the blocks that hold a first piece, in order
+  int4 desc = make_int4(0, 0, 0, 0);
+  if (tid < blocks) s_desc[tid] = desc = a.split_desc[tid];
+  const unsigned has = __ballot_sync(0xffffffffu, desc.x != 0);
+  if ((tid & 31) == 0) s_warp[tid >> 5] = __popc(has);
+  __syncthreads();
+  int count = 0, before = 0;
+#pragma unroll
+  for (int i = 0; i < kJoinThreads / 32; ++i) {
+    before += i < (tid >> 5) ? s_warp[i] : 0;
+    count += s_warp[i];
+  }
+  if (desc.x) s_first[before + __popc(has & ((1u << (tid & 31)) - 1))] = tid;
+  __syncthreads();
+  const int units = count * kUnits;
+  for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int first = s_first[unit / kUnits], dim0 = unit % kUnits * kDims;
+    const int4 d = s_desc[first];
+    const int pieces = d.x;
+    auto slot_of = [&](int p) -> int64_t { return 2 * (first + p) + (p == 0 ? 1 : 0); };
+    const Seq q = load_seq(a, d.y);
+    // this thread's values: coordinate dim0 + 4 (tid % 256) / N, rows r4 .. r4 + 3
+    const int v4 = tid & 255, half = tid >> 8, r4 = 4 * v4 % N;
+    const float4* const part = reinterpret_cast<const float4*>(a.part) + dim0 * (N / 4) + v4;
+    // a row's maximum and sum over the pieces
+    const float* const ml = reinterpret_cast<const float*>(a.part_ml);
+    const int row = tid % N, grp = tid / N;
+    float m = -INFINITY;
 #pragma unroll 4
-    for (int p = 0; p < d.x; ++p) {
-      const int64_t at = (2 * (static_cast<int64_t>(blockIdx.x) + p) + (p == 0 ? 1 : 0)) * N + r;
-      const float2 ml = a.part_ml[at];
-      const float4 v = reinterpret_cast<const float4*>(a.part + at * DC)[threadIdx.x];
-      const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
-      const float f0 = ex2_approx(m - mu), f1 = ex2_approx(ml.x - mu);
-      acc = make_float4(acc.x * f0 + v.x * f1, acc.y * f0 + v.y * f1, acc.z * f0 + v.z * f1,
-                        acc.w * f0 + v.w * f1);
-      sum = sum * f0 + ml.y * f1;
-      m = mn;
+    for (int p = grp; p < pieces; p += kGroups) m = fmaxf(m, ml[slot_of(p) * 2 * N + row]);
+    s_red[grp][row] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) m = fmaxf(m, s_red[i][row]);
+    const float mu = m == -INFINITY ? 0.f : m;
+    float sum = 0.f;
+#pragma unroll 4
+    for (int p = grp; p < pieces; p += kGroups) {
+      const float* const at = ml + slot_of(p) * 2 * N + row;
+      sum += at[N] * ex2_approx(at[0] - mu);
     }
-    const bool none = no_key(m, sum);
-    float mt = m, lt = sum, keep = 1.f;
-    if (a.sink) {
-      const float s2 = a.sink[head] * kLog2e;
-      mt = fmaxf(m, s2);
-      const float mu = mt == -INFINITY ? 0.f : mt;
-      keep = ex2_approx(m - mu);
-      lt = sum * keep + ex2_approx(s2 - mu + kShift);
+    __syncthreads();
+    s_red[grp][row] = sum;
+    if (grp == 0) s_mu[row] = mu;
+    __syncthreads();
+    if (grp == 0) {
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) sum += s_red[i][row];
+      const bool none = no_key(m, sum);
+      float mt = m, lt = sum, keep = 1.f;
+      const int rr = d.z * N + row, tok = div_group(a, rr), head = rr - tok * a.group;
+      const bool real = tok < q.n;
+      if (a.sink && real) {
+        const float s2 = a.sink[head] * kLog2e;
+        mt = fmaxf(m, s2);
+        const float mx = mt == -INFINITY ? 0.f : mt;
+        keep = ex2_approx(m - mx);
+        lt = sum * keep + ex2_approx(s2 - mx + kShift);
+      }
+      s_scale[row] = none ? 0.f : keep / lt;
+      if (a.lse && real && dim0 == 0)
+        a.lse[static_cast<int64_t>(head) * a.num_tokens + q.row0 + tok] =
+            none ? (a.sink ? a.sink[head] : -INFINITY) : (mt - kShift) * kLn2 + logf(lt);
     }
-    const float inv = none ? 0.f : keep / lt;
-    const int64_t t = q.row0 + tok;
-    *reinterpret_cast<uint2*>(a.o + (t * a.group + head) * DC + 4 * threadIdx.x) =
-        make_uint2(pack2(acc.x * inv, acc.y * inv, F16), pack2(acc.z * inv, acc.w * inv, F16));
-    if (a.lse && threadIdx.x == 0)
-      a.lse[static_cast<int64_t>(head) * a.num_tokens + t] =
-          none ? (a.sink ? a.sink[head] : -INFINITY) : (mt - kShift) * kLn2 + logf(lt);
+    // O
+    const float4 mu4 = *reinterpret_cast<const float4*>(&s_mu[r4]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = half; p < pieces; p += 2) {
+      const int64_t slot = slot_of(p);
+      const float4 v = part[slot * (DC * N / 4)];
+      const float4 x = *reinterpret_cast<const float4*>(ml + slot * 2 * N + r4);
+      acc.x = fmaf(v.x, ex2_approx(x.x - mu4.x), acc.x);
+      acc.y = fmaf(v.y, ex2_approx(x.y - mu4.y), acc.y);
+      acc.z = fmaf(v.z, ex2_approx(x.z - mu4.z), acc.z);
+      acc.w = fmaf(v.w, ex2_approx(x.w - mu4.w), acc.w);
+    }
+    if (half) s_acc[v4] = acc;
+    __syncthreads();
+    if (!half) {
+      const float4 o = s_acc[v4], f = *reinterpret_cast<const float4*>(&s_scale[r4]);
+      const float y[4] = {(acc.x + o.x) * f.x, (acc.y + o.y) * f.y, (acc.z + o.z) * f.z,
+                          (acc.w + o.w) * f.w};
+      const float g[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        s_o[r4 + i][4 * v4 / N] =
+            static_cast<uint16_t>(pack2(g[i] == 0.f ? 0.f : y[i], 0.f, F16));
+    }
+    __syncthreads();
+    constexpr int kPer = kDims / 8;  // 16-byte units of a row
+    if (tid < N * kPer) {
+      const int r = tid / kPer, u = tid % kPer;
+      if (d.z * N + r < q.n * a.group)
+        *reinterpret_cast<uint4*>(a.o + (static_cast<int64_t>(q.row0) * a.group + d.z * N + r) * DC +
+                                  dim0 + 8 * u) = *reinterpret_cast<const uint4*>(&s_o[r][8 * u]);
+    }
+    __syncthreads();
   }
 }
 
@@ -892,8 +1006,8 @@ cudaError_t latent_one(const LatentArgs& l, int sms, cudaStream_t st) {
   const unsigned ctas = sms < kLatentMaxCtas ? sms : kLatentMaxCtas;
   e = launch_early(kern, dim3(ctas), dim3(kThreads), L::kSmem, st, l, maps);
   if (e != cudaSuccess) return e;
-  return launch_early(latent_join_kernel<F16, DC, N>, dim3(ctas, N < 32 ? N : 32), dim3(DC / 4), 0,
-                      st, l.a);
+  return launch_early(latent_join_kernel<F16, DC, N>, dim3(2 * ctas), dim3(kJoinThreads), 0, st, l.a,
+                      static_cast<int>(ctas));
 }
 
 template <bool F16>

@@ -145,6 +145,9 @@ ATTEND = {
     "chunk": dict(new=[70, 0, 33], ctx=[130, 7, 0], H=5, pad=3),
     "chunk_fp16": dict(new=[65], ctx=[100], H=4, dtype="fp16", page=16),
     "prompt": dict(new=[130], ctx=[0], H=2, page=32),
+    "batch": dict(new=[1] * 64, ctx=[(i * i * 37) % 900 for i in range(64)], one=True),
+    "batch_verify": dict(new=[2] * 40, ctx=[(i * i * 37) % 500 for i in range(40)]),
+    "chunks": dict(new=[90, 100, 40], ctx=[500, 100, 900]),
     "wide": dict(new=[1, 5], ctx=[100, 200], layout="wide", H=12),
     "slots_by_head": dict(new=[1, 5], ctx=[100, 200], layout="slots", by_head=True, H=12),
     "fused": dict(new=[2, 5], ctx=[100, 200], fused=True, H=12),
