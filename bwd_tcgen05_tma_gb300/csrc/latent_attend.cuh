@@ -10,7 +10,7 @@
 // they lie (K-major), the second turned (MN-major).  N is 16, 32 or 64; O^T takes
 // d_c / 128 * N columns of tensor memory and two tiles of scores 2 N.
 //
-// The softmax runs down the columns.  A thread holds two keys of N / 4 rows (the
+// The softmax runs down the columns.  A thread holds two keys of N / 8 rows (the
 // 16x256b shape).  The running maximum follows the true one within 2^8, so whether
 // any row's has to move is one barrier's vote; only then (the first tile, and
 // rarely after it) is the maximum joined across threads and O rescaled.  Sums stay
@@ -20,8 +20,9 @@
 // row block, tile) cut into equal shares, one a block, one block an SM; pieces of
 // a row block meet in a second kernel in a fixed order.
 //
-// Roles: an MMA issuer for each product, TMA producer, scheduler (a warp each), four
-// softmax warps, four warps that copy queries.
+// Roles: an MMA issuer for each product, TMA producer, scheduler (a warp each), eight
+// softmax warps (four read a tile's 64 lanes, for one half of the columns), four
+// warps that copy queries.
 //
 // Values that are not finite in a tile that some rows mask in part are taken out of
 // the product (their zero weight would make NaN of them); a row that keeps such a
@@ -40,7 +41,7 @@ namespace {
 using namespace sm103;
 
 constexpr int kKeys = 64;      // keys a tile
-constexpr int kThreads = 384;  // warps: S, TMA, scheduler, P c, 4 softmax, 4 queries
+constexpr int kThreads = 512;  // warps: S, TMA, scheduler, P c, 8 softmax, 4 queries
 constexpr float kLazy = 8.f;
 
 struct LatentMaps {
@@ -84,14 +85,13 @@ struct LatentAux {
   int abort;
   uint32_t bad;     // number + 1 of the last piece a value was taken out of
   int ok_mask[8];   // by tile: 16-key groups whose page exists
-  int64_t part[kThreads / 32];
   int64_t begin;  // the block's first unit
   Shares shares;
-  int unit0, seq, rb;
   Piece piece[4];
   int row_lo[N], row_hi[N];
   float col[4][N];  // by softmax warp: maxima, or sums
-  float fac[N];
+  alignas(16) float fac[N];  // factors of the rows' O
+  float top[N];              // the rows' maxima
 };
 
 template <int DC, int N>
@@ -152,12 +152,40 @@ __device__ __forceinline__ int tiles_of(const Args& a, const SeqView& v, int rb)
   const int2 k = keys_any(a, v, rb * N, (rb + 1) * N);
   return max(1, (k.y - (k.x & ~(kKeys - 1)) + kKeys - 1) / kKeys);
 }
+// Units of a warp's sequences: `per` a lane, from `first` on.  The row blocks of a
+// sequence that has many (a prompt's chunk) are summed by all lanes together.
 template <int N>
-__device__ __forceinline__ int64_t seq_units(const Args& a, const SeqView& v) {
-  int64_t n = 0;
-  const int nrb = blocks_of<N>(a, v);
-  for (int rb = 0; rb < nrb; ++rb) n += kStart + tiles_of<N>(a, v, rb);
-  return n;
+__device__ __forceinline__ int64_t units_of(const Args& a, int first, int per) {
+  const int lane = threadIdx.x & 31;
+  int64_t mine = 0;
+  for (int i = 0; i < per; ++i) {
+    SeqView v = {{0, 0, 0}, 0};
+    int nrb = 0;
+    if (first + i < a.num_seqs) {
+      v = view_of(a, first + i);
+      if (outside(a, v.q)) flag_bounds(a);
+      nrb = blocks_of<N>(a, v);
+    }
+    const bool many = nrb > 2;
+    if (!many)
+      for (int rb = 0; rb < nrb; ++rb) mine += kStart + tiles_of<N>(a, v, rb);
+    unsigned todo = __ballot_sync(0xffffffffu, many);
+    while (todo) {
+      const int o = __ffs(todo) - 1;
+      todo &= todo - 1;
+      SeqView u;
+      u.q.len = __shfl_sync(0xffffffffu, v.q.len, o);
+      u.q.n = __shfl_sync(0xffffffffu, v.q.n, o);
+      u.hi = __shfl_sync(0xffffffffu, v.hi, o);
+      const int n = __shfl_sync(0xffffffffu, nrb, o);
+      int64_t sum = 0;
+      for (int rb = lane; rb < n; rb += 32) sum += kStart + tiles_of<N>(a, u, rb);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (lane == o) mine += sum;
+    }
+  }
+  return mine;
 }
 
 // Walks the block's pieces (the scheduler warp does).  Units [0, kStart) of a block
@@ -198,67 +226,79 @@ __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
   return true;
 }
 
-// This block's share, found by all threads.
+// This block's share, found by the scheduler warp.  With few sequences the warp
+// reads them all; otherwise the block's threads have left their ranges' units in
+// `scratch`.  (The warp alone needs no barrier: the other roles start meanwhile.)
+constexpr int kFewSeqs = 256;
 template <int N, class Aux>
-__device__ __forceinline__ void walk_init(const Args& a, Aux* x, Walk& w) {
-  const int per = (a.num_seqs + kThreads - 1) / kThreads;
-  const int first = min(a.num_seqs, static_cast<int>(threadIdx.x) * per);
-  const int last = min(a.num_seqs, first + per);
+__device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* scratch, Walk& w) {
+  const int lane = threadIdx.x & 31;
+  const bool few = a.num_seqs <= kFewSeqs;
+  const int ranges = few ? 32 : kThreads, per = (a.num_seqs + ranges - 1) / ranges;
   int64_t mine = 0;
-  for (int s = first; s < last; ++s) {
-    const SeqView v = view_of(a, s);
-    if (outside(a, v.q)) flag_bounds(a);
-    mine += seq_units<N>(a, v);
+  if (few) {
+    mine = units_of<N>(a, lane * per, per);
+  } else {
+    for (int i = 0; i < kThreads / 32; ++i) mine += scratch[lane * (kThreads / 32) + i];
   }
   int64_t sum = mine;
 #pragma unroll
   for (int i = 1; i < 32; i <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, sum, i);
-    if ((threadIdx.x & 31) >= i) sum += y;
+    if (lane >= i) sum += y;
   }
-  if ((threadIdx.x & 31) == 31) x->part[threadIdx.x / 32] = sum;
-  __syncthreads();
-  int64_t total = 0, before = sum - mine;
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < static_cast<int>(threadIdx.x) / 32) before += x->part[i];
-    total += x->part[i];
-  }
+  const int64_t total = __shfl_sync(0xffffffffu, sum, 31);
   const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
-  const Shares sh = shares_of(total, ctas);
   w.done = w.share = 0;
-  if (static_cast<int>(blockIdx.x) < ctas) {
-    const int64_t begin = sh.begin(blockIdx.x);
-    w.share = static_cast<int>(sh.begin(blockIdx.x + 1) - begin);
-    if (begin >= before && begin < before + mine) {
-      int64_t off = begin - before;
-      int s = first;
-      for (;; ++s) {
-        const SeqView v = view_of(a, s);
-        const int64_t units = seq_units<N>(a, v);
-        if (off >= units) {
-          off -= units;
-          continue;
-        }
-        x->seq = s;
-        int rb = 0;
-        for (int n; off >= (n = kStart + tiles_of<N>(a, v, rb)); ++rb) off -= n;
-        x->rb = rb;
-        x->unit0 = static_cast<int>(off);
-        x->begin = begin;
-        x->shares = sh;
+  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  const Shares sh = shares_of(total, ctas);
+  const int64_t begin = sh.begin(blockIdx.x);
+  w.share = static_cast<int>(sh.begin(blockIdx.x + 1) - begin);
+  // the lane, the range and the sequence that hold the first unit
+  const unsigned at = __ballot_sync(0xffffffffu, sum > begin);
+  const int o = __ffs(at) - 1;
+  int64_t off = begin - __shfl_sync(0xffffffffu, sum - mine, o);
+  int s = o * per;
+  if (!few) {
+    int r = o * (kThreads / 32);
+    while (off >= scratch[r]) off -= scratch[r++];
+    s = r * per;
+  }
+  SeqView v;
+  int rb = 0;
+  for (;; ++s) {  // row blocks of 32 at a time, all lanes
+    v = view_of(a, s);
+    const int nrb = blocks_of<N>(a, v);
+    for (rb = 0; rb < nrb; rb += 32) {
+      const int n = rb + lane < nrb ? kStart + tiles_of<N>(a, v, rb + lane) : 0;
+      int64_t upto = n;
+#pragma unroll
+      for (int i = 1; i < 32; i <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, upto, i);
+        if (lane >= i) upto += y;
+      }
+      const unsigned in = __ballot_sync(0xffffffffu, upto > off);
+      if (in) {
+        const int f = __ffs(in) - 1;
+        off -= __shfl_sync(0xffffffffu, upto - n, f);
+        rb += f;
         break;
       }
+      off -= __shfl_sync(0xffffffffu, upto, 31);
     }
+    if (rb < nrb) break;
   }
-  __syncthreads();
-  if (w.share > 0) {
-    w.seq = x->seq;
-    w.rb = x->rb;
-    w.u0 = x->unit0;
-    w.v = view_of(a, w.seq);
-    // a share that ends inside its only start has no piece
-    if (!walk_piece<N>(a, w) && !walk_next<N>(a, w)) w.share = 0;
+  if (lane == 0) {
+    x->begin = begin;
+    x->shares = sh;
   }
+  __syncwarp();
+  w.seq = s;
+  w.rb = rb;
+  w.u0 = static_cast<int>(off);
+  w.v = v;
+  // a share that ends inside its only start has no piece
+  if (!walk_piece<N>(a, w) && !walk_next<N>(a, w)) w.share = 0;
 }
 
 // A barrier of the softmax warps that also tells whether any thread's p holds.
@@ -266,7 +306,7 @@ __device__ __forceinline__ bool softmax_any(bool p) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"(static_cast<uint32_t>(p))
       : "memory");
@@ -278,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     latent_kernel(const __grid_constant__ LatentArgs l, const __grid_constant__ LatentMaps maps) {
   using L = LatentCfg<DC, N>;
   constexpr int NB = L::kNB, NS = L::kSlots, NR = L::kRSlots;
-  constexpr int kC = N / 4;                       // columns a softmax thread holds
+  constexpr int kC = N / 8;                       // columns a softmax thread holds
   constexpr float kShift = F16 ? 7.f : 0.f;       // P <= 2^(7 + 8) in fp16
   constexpr int kKind = F16 ? kCacheF16 : kCacheBf16;
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -305,14 +345,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&x->q_empty, 1);
     mbar_init(&x->s_full[0], 1);
     mbar_init(&x->s_full[1], 1);
-    mbar_init(&x->s_empty[0], 4);
-    mbar_init(&x->s_empty[1], 4);
-    mbar_init(&x->p_full, 128);
+    mbar_init(&x->s_empty[0], 8);
+    mbar_init(&x->s_empty[1], 8);
+    mbar_init(&x->p_full, 256);
     mbar_init(&x->o_done, 1);
-    mbar_init(&x->o_empty, 128);
+    mbar_init(&x->o_empty, 256);
     for (int s = 0; s < 4; ++s) {
       mbar_init(&x->piece_full[s], 1);
-      mbar_init(&x->piece_empty[s], 2 + 1 + 4 + 4);  // MMA, producer, query, softmax warps
+      mbar_init(&x->piece_empty[s], 2 + 1 + 4 + 8);  // MMA, producer, query, softmax warps
     }
     mbar_init(&x->drain[0], 1);
     mbar_init(&x->drain[1], 1);
@@ -324,12 +364,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&x->tmem, 512);
     tmem_relinquish();
   }
+  if (tid == 32) {
+    prefetch_tensormap(&maps.lat);
+    prefetch_tensormap(&maps.rope);
+  }
   tc_fence_before();
-  grid_dep_wait();
-  if (tid == 0) a.split_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
-  Walk w;
-  walk_init<N>(a, x, w);  // two block barriers
+  __syncthreads();
   tc_fence_after();
+  grid_dep_wait();
+  int64_t* const scratch = reinterpret_cast<int64_t*>(sm);  // where queries will lie
+  if (a.num_seqs > kFewSeqs) {
+    const int per = (a.num_seqs + kThreads - 1) / kThreads;
+    scratch[tid] = units_of<N>(a, tid * per, per);
+    __syncthreads();
+  }
   grid_dep_launch();
   const uint32_t tmem = x->tmem;
 
@@ -345,6 +393,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 2) {
     // -------------------------------------------------------------- scheduler
+    if (lane == 0) a.split_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    Walk w;
+    walk_init<N>(a, x, scratch, w);
     bool ok = true, live = w.share > 0;
     for (uint32_t i = 0; ok; ++i) {
       if (i >= 4 && !(ok = mbar_wait_warp(&x->piece_empty[i & 3], ((i >> 2) - 1) & 1))) break;
@@ -535,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&x->lat_full[e % NS], (e / NS) & 1, 100000000ull);
     for (uint32_t e = k > NR ? k - NR : 0; e < k; ++e)
       mbar_wait(&x->rope_full[e % NR], (e / NR) & 1, 100000000ull);
-  } else if (warp >= 8) {
+  } else if (warp >= 12) {
     // -------------------------------------------------------------- queries
     // A warp a row: 16 bytes a lane to where the MMA reads them.
     uint32_t it = 0;
@@ -551,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kRowsWarp = N / 4;
       int64_t lat_at = -1, rot_at = 0;
       if (lane < kRowsWarp) {
-        const int rr = r0 + (warp - 8) * kRowsWarp + lane, tok = div_group(a, rr);
+        const int rr = r0 + (warp - 12) * kRowsWarp + lane, tok = div_group(a, rr);
         if (tok < new_rows) {
           const int64_t t = row0 + tok, head = rr - tok * a.group;
           lat_at = (t * l.q_lat_tok + head * l.q_lat_head) >> 3;
@@ -562,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint4* const rot = reinterpret_cast<const uint4*>(l.q_rot);
 #pragma unroll 4
       for (int i = 0; i < kRowsWarp; ++i) {
-        const int r = (warp - 8) * kRowsWarp + i;
+        const int r = (warp - 12) * kRowsWarp + i;
         const int64_t la = __shfl_sync(0xffffffffu, lat_at, i);
         const int64_t ra = __shfl_sync(0xffffffffu, rot_at, i);
         const int bytes = la >= 0 ? 16 : 0;
@@ -587,9 +638,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) timeout();
   } else if (warp >= 4) {
     // -------------------------------------------------------------- softmax
-    const int sw = warp - 4, st = tid - 128, g = lane >> 2, c2 = 2 * (lane & 3);
+    // warp: 16 keys of the tile, one half of the rows
+    const int sw = warp & 3, half = (warp - 4) >> 2, st = tid - 128;
+    const int g = lane >> 2, c0 = half * (N / 2) + 2 * (lane & 3);
     const uint32_t lanes = static_cast<uint32_t>(sw * 32) << 16;
-    const uint32_t o_tm = tmem + lanes + L::kColO;
+    const uint32_t o_half = tmem + lanes + L::kColO + half * (NB / 2) * N;
     const float fac = a.scale * kLog2e;
     uint32_t k = 0, it = 0;
     // A wait that ran out here is told to the other softmax warps at their next
@@ -606,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         x->row_hi[st] = tok < p->new_rows ? (a.causal ? min(p->hi, pos + 1) : p->hi) : 0;
       }
       if (softmax_any(failed) || n < 0) break;
-      // column 8 b + c2 + e is index 2 b + e
+      // column c0 + 8 b + e is index 2 b + e
       float m[kC], sum[kC];
 #pragma unroll
       for (int i = 0; i < kC; ++i) {
@@ -620,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         failed |= !mbar_wait_warp(&x->lat_full[(k * NB) % NS], (k * NB / NS) & 1);
         tc_fence_after();
         uint32_t u[2 * kC];
-        tmem_ld16x256b(tmem + lanes + (k & 1) * N, u);
+        tmem_ld16x256b(tmem + lanes + (k & 1) * N + half * (N / 2), u);
         const int okm = x->ok_mask[k & 7];
         const bool whole = key >= p->all.x && key + kKeys <= p->all.y && okm == 0xf;
         tmem_ld_wait(u);
@@ -634,10 +687,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int k0 = key + 16 * sw + g;
           const bool page = okm >> sw & 1;
 #pragma unroll
-          for (int b = 0; b < N / 8; ++b)
+          for (int b = 0; b < N / 16; ++b)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int lo = x->row_lo[8 * b + c2 + e], hi = x->row_hi[8 * b + c2 + e];
+              const int lo = x->row_lo[c0 + 8 * b + e], hi = x->row_hi[c0 + 8 * b + e];
               if (!(page && k0 >= lo && k0 < hi)) s[4 * b + e] = -INFINITY;
               if (!(page && k0 + 8 >= lo && k0 + 8 < hi)) s[4 * b + 2 + e] = -INFINITY;
             }
@@ -656,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float mx = fmaxf(s[4 * (i >> 1) + (i & 1)], s[4 * (i >> 1) + 2 + (i & 1)]);
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-            if (g == 0) x->col[sw][8 * (i >> 1) + c2 + (i & 1)] = mx;
+            if (g == 0) x->col[sw][c0 + 8 * (i >> 1) + (i & 1)] = mx;
           }
           if (softmax_any(failed)) {
             failed = true;
@@ -664,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int i = 0; i < kC; ++i) {
-            const int c = 8 * (i >> 1) + c2 + (i & 1);
+            const int c = c0 + 8 * (i >> 1) + (i & 1);
             const float mx = fmax3(x->col[0][c], x->col[1][c], fmaxf(x->col[2][c], x->col[3][c])) * fac;
             const bool up = mx - m[i] > kLazy;
             const float f = up ? ex2_approx(m[i] - mx) : 1.f;
@@ -677,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // P, over its rounded pairs of columns
         uint32_t pk[kC];
 #pragma unroll
-        for (int b = 0; b < N / 8; ++b)
+        for (int b = 0; b < N / 16; ++b)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float p0 = ex2_approx(fmaf(s[4 * b + 2 * h], fac, kShift - m[2 * b]));
@@ -691,40 +744,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (again) {
 #pragma unroll 1
-          for (int q = 0; q < NB * N / 16; ++q) {
+          for (int q = 0; q < NB * N / 32; ++q) {  // this half of the blocks
             uint32_t o[16];
-            tmem_ld32x32b_x16(o_tm + q * 16, o);
+            tmem_ld32x32b_x16(o_half + q * 16, o);
             tmem_ld_wait(o);
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              o[e] = __float_as_uint(__uint_as_float(o[e]) * x->fac[(q * 16 + e) % N]);
-            tmem_st32x32b_x16(o_tm + q * 16, o);
+            for (int e = 0; e < 16; e += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(&x->fac[(q * 16 + e) % N]);
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * f.x);
+              o[e + 1] = __float_as_uint(__uint_as_float(o[e + 1]) * f.y);
+              o[e + 2] = __float_as_uint(__uint_as_float(o[e + 2]) * f.z);
+              o[e + 3] = __float_as_uint(__uint_as_float(o[e + 3]) * f.w);
+            }
+            tmem_st32x32b_x16(o_half + q * 16, o);
           }
           tmem_st_wait();
         }
         {
           const uint32_t row = smem_u32(sm + L::kPOff) + (16 * sw + g) * 128;
 #pragma unroll
-          for (int b = 0; b < N / 8; ++b)
+          for (int b = 0; b < N / 16; ++b)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + h * 1024 + ((b ^ g) << 4) + c2 * 2),
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(row + h * 1024 +
+                                                                  (((half * (N / 16) + b) ^ g) << 4) +
+                                                                  4 * (lane & 3)),
                            "r"(pk[2 * b + h])
                            : "memory");
         }
         if (!whole) {
           // rows no one keeps become zeros; of the others what is not finite
-          const int r = st >> 1;
+          const int r = st >> 2;
           const bool in = (okm >> (r >> 4) & 1) && key + r >= p->any.x && key + r < p->any.y;
 #pragma unroll 1
           for (int b = 0; b < NB; ++b) {
             const uint32_t e = k * NB + b;
             failed |= !mbar_wait_warp(&x->lat_full[e % NS], (e / NS) & 1);
             const uint32_t at = smem_u32(sm + L::kLatOff) + (e % NS) * L::kSlot +
-                                (st & 1) * (kKeys * 128) + r * 128;
+                                (st >> 1 & 1) * (kKeys * 128) + r * 128;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t q = at + ((i ^ (r & 7)) << 4);
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t q = at + ((4 * (st & 1) + i) << 4);
               if (!in) {
                 st_shared_v4(q, 0, 0, 0, 0);
                 continue;
@@ -748,22 +808,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int slot = 2 * blockIdx.x + p->first;
       const int rows = min(N, p->new_rows * a.group - p->rb * N);
       const int64_t out0 = static_cast<int64_t>(p->row0) * a.group + p->rb * N;  // of [T * H]
-      if (softmax_any(failed)) break;  // (`col` and `fac` have been read)
 #pragma unroll
       for (int i = 0; i < kC; ++i) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], d);
         if (g == 0) {
-          const int c = 8 * (i >> 1) + c2 + (i & 1);
+          const int c = c0 + 8 * (i >> 1) + (i & 1);
           x->col[sw][c] = sum[i];
-          if (sw == 0) x->fac[c] = m[i];
+          if (sw == 0) x->top[c] = m[i];
         }
       }
-      softmax_any(false);
-      float norm = 0.f;
+      if (softmax_any(failed)) break;
       if (st < N) {
+        float norm;
         const float lsum = x->col[0][st] + x->col[1][st] + (x->col[2][st] + x->col[3][st]);
-        const float mx = x->fac[st];
+        const float mx = x->top[st];
         const bool none = mx == -FLT_MAX && lsum == 0.f;
         if (!complete) {
           norm = none ? 0.f : 1.f;
@@ -785,71 +844,69 @@ __global__ void __launch_bounds__(kThreads, 1)
             a.lse[static_cast<int64_t>(head) * a.num_tokens + p->row0 + tok] =
                 none ? (a.sink ? a.sink[head] : -INFINITY) : (mt - kShift) * kLn2 + logf(lt);
         }
+        x->fac[st] = norm;
       }
-      softmax_any(false);
-      if (st < N) x->fac[st] = norm;
       softmax_any(false);
       const bool bad = n > 0 && x->bad == it + 1;
       if (n > 0) {
         failed |= !mbar_wait_warp(&x->o_done, (k - 1) & 1);
         tc_fence_after();
       }
+      constexpr int kCols = N < 32 ? N : 32;  // columns at a time
 #pragma unroll 1
-      for (int b = 0; b < NB; ++b) {
-        const int d = b * 128 + st;  // this lane's coordinate
-#pragma unroll 1
-        for (int c0 = 0; c0 < N; c0 += 16) {
-          if (c0 >= rows) break;
-          uint32_t o[16];
-          if (n > 0) {
-            tmem_ld32x32b_x16(o_tm + b * N + c0, o);
-            tmem_ld_wait(o);
-          }
-          float v[16];
+      for (int q = 0; q < NB / 2 * N / kCols; ++q) {
+        const int cc = q * kCols % N;
+        const int d = (half * (NB / 2) + q * kCols / N) * 128 + sw * 32 + lane;  // coordinate
+        if (cc >= rows) continue;
+        uint32_t o[kCols];
+        if (n > 0) {
+          if constexpr (kCols == 32) tmem_ld32x32b_x32(o_half + q * kCols, o);
+          else tmem_ld32x32b_x16(o_half + q * kCols, o);
+          tmem_ld_wait(o);
+        }
+        float v[kCols];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float f = x->fac[c0 + i];
-            v[i] = n > 0 && f != 0.f ? __uint_as_float(o[i]) * f : 0.f;
-          }
-          if (bad) {
-            for (int j = 0; j < n; ++j) {
-              const int key = key0 + j * kKeys;
-              for (int kk = max(key, p->any.x); kk < min(key + kKeys, p->any.y); ++kk) {
-                const int page = page_of(a, p->seq, kk);
-                if (page < 0) continue;
-                const float e = elem(
-                    reinterpret_cast<const uint16_t*>(
-                        a.kc + page * a.k_page +
-                        static_cast<int64_t>(kk & ((1 << a.page_shift) - 1)) * a.k_tok)[d],
-                    F16);
-                if (fabsf(e) < INFINITY) continue;
+        for (int i = 0; i < kCols; i += 4) {
+          const float4 f4 = *reinterpret_cast<const float4*>(&x->fac[cc + i]);
+          const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  if (kk >= x->row_lo[c0 + i] && kk < x->row_hi[c0 + i]) v[i] = NAN;
-              }
-            }
-          }
-          if (complete) {
-            // neighbours swap, so that a lane has two coordinates of one row
+          for (int e = 0; e < 4; ++e)
+            v[i + e] = n > 0 && f[e] != 0.f ? __uint_as_float(o[i + e]) * f[e] : 0.f;
+        }
+        if (bad) {
+          for (int kk = max(key0, p->any.x); kk < min(key0 + n * kKeys, p->any.y); ++kk) {
+            const int page = page_of(a, p->seq, kk);
+            if (page < 0) continue;
+            const float e =
+                elem(reinterpret_cast<const uint16_t*>(
+                         a.kc + page * a.k_page +
+                         static_cast<int64_t>(kk & ((1 << a.page_shift) - 1)) * a.k_tok)[d],
+                     F16);
+            if (fabsf(e) < INFINITY) continue;
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const bool odd = lane & 1;
-              const float y = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
-              const uint32_t w2 = odd ? pack2(y, v[i + 1], F16) : pack2(v[i], y, F16);
-              const int r = c0 + i + odd;
-              if (r < rows)
-                *reinterpret_cast<uint32_t*>(a.o + (out0 + r) * DC + (d & ~1)) = w2;
-            }
-          } else {
-            // [slot][coordinate][row]: a lane's rows are contiguous
-            float* dst = a.part + (static_cast<int64_t>(slot) * DC + d) * N + c0;
-#pragma unroll
-            for (int i = 0; i < 16; i += 8)
-              st_global_v8(dst + i, __float_as_uint(v[i]), __float_as_uint(v[i + 1]),
-                           __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]),
-                           __float_as_uint(v[i + 4]), __float_as_uint(v[i + 5]),
-                           __float_as_uint(v[i + 6]), __float_as_uint(v[i + 7]));
+            for (int i = 0; i < kCols; ++i)
+              if (kk >= x->row_lo[cc + i] && kk < x->row_hi[cc + i]) v[i] = NAN;
           }
+        }
+        if (complete) {
+          // neighbours swap, so that a lane has two coordinates of one row
+          const bool odd = lane & 1;
+          uint16_t* dst = a.o + (out0 + cc + odd) * DC + (d & ~1);
+#pragma unroll
+          for (int i = 0; i < kCols; i += 2) {
+            const float y = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+            const uint32_t w2 = odd ? pack2(y, v[i + 1], F16) : pack2(v[i], y, F16);
+            if (cc + i + odd < rows) *reinterpret_cast<uint32_t*>(dst + i * DC) = w2;
+          }
+        } else {
+          // [slot][coordinate][row]: a lane's rows are contiguous
+          float* dst = a.part + (static_cast<int64_t>(slot) * DC + d) * N + cc;
+#pragma unroll
+          for (int i = 0; i < kCols; i += 8)
+            st_global_v8(dst + i, __float_as_uint(v[i]), __float_as_uint(v[i + 1]),
+                         __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]),
+                         __float_as_uint(v[i + 4]), __float_as_uint(v[i + 5]),
+                         __float_as_uint(v[i + 6]), __float_as_uint(v[i + 7]));
         }
       }
       if (n > 0) {

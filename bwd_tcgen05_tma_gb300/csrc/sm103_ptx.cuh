@@ -506,6 +506,12 @@ SM103_DEV void tmem_st32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
 // repeat.  Thread (g = t / 4, c = t % 4) gets, for repeat b, columns 8b + 2c and
 // 8b + 2c + 1 of lane g in registers 4b and 4b + 1, and of lane g + 8 in 4b + 2
 // and 4b + 3.
+SM103_DEV void tmem_ld16x256b(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr)
+               : "memory");
+}
 SM103_DEV void tmem_ld16x256b(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -521,14 +527,9 @@ SM103_DEV void tmem_ld16x256b(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
-SM103_DEV void tmem_ld16x256b(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : SM103_R8(r, 0), SM103_R8(r, 8), SM103_R8(r, 16), SM103_R8(r, 24)
-      : "r"(taddr)
-      : "memory");
+SM103_DEV void tmem_ld_wait(uint32_t (&r)[4]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3])::"memory");
 }
 SM103_DEV void tmem_ld_wait(uint32_t (&r)[8]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : SM103_RW8(r, 0)::"memory");
