@@ -899,14 +899,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (cc + i + odd < rows) *reinterpret_cast<uint32_t*>(dst + i * DC) = w2;
           }
         } else {
-          // [slot][coordinate][row]: a lane's rows are contiguous
-          float* dst = a.part + (static_cast<int64_t>(slot) * DC + d) * N + cc;
+          float* dst = a.part + (static_cast<int64_t>(slot) * N + cc) * DC + d;
 #pragma unroll
-          for (int i = 0; i < kCols; i += 8)
-            st_global_v8(dst + i, __float_as_uint(v[i]), __float_as_uint(v[i + 1]),
-                         __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]),
-                         __float_as_uint(v[i + 4]), __float_as_uint(v[i + 5]),
-                         __float_as_uint(v[i + 6]), __float_as_uint(v[i + 7]));
+          for (int i = 0; i < kCols; ++i)
+            if (cc + i < rows) dst[i * DC] = v[i];
         }
       }
       if (n > 0) {
@@ -929,123 +925,108 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the pieces of split blocks of rows.  A unit is 1024 values of one block of
-// rows, all its rows and 1024 / N coordinates, four rows a thread; the two halves
-// of a thread block take the pieces in turn.  Units are shared out over the grid,
-// whose blocks read all descriptors at once.
+// Joins the pieces of split blocks of rows.  A warp takes 128 coordinates of a row,
+// four a lane, and works alone: it finds the row's statistics itself, a piece a
+// lane, while its first values are on their way.  The grid fills the SMs; its
+// blocks read all descriptors at once.
 constexpr int kJoinThreads = 512;
 template <bool F16, int DC, int N>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, 2)
     latent_join_kernel(const __grid_constant__ Args a, int blocks) {
   constexpr float kShift = F16 ? 7.f : 0.f;
-  constexpr int kDims = 1024 / N, kUnits = DC / kDims, kGroups = kJoinThreads / N;
+  constexpr int kParts = DC / 128, kUnits = N * kParts;
+  constexpr int kMost = (kLatentMaxCtas + 31) / 32;  // pieces a lane
+  constexpr int kAhead = 4;
   __shared__ int s_first[kLatentMaxCtas], s_warp[kJoinThreads / 32];
   __shared__ int4 s_desc[kLatentMaxCtas];
-  __shared__ float s_red[kGroups][N];
-  __shared__ __align__(16) float s_mu[N], s_scale[N];
-  __shared__ float4 s_acc[256];
-  __shared__ __align__(16) uint16_t s_o[N][kDims + 8];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   grid_dep_wait();
   // the blocks that hold a first piece, in order
   int4 desc = make_int4(0, 0, 0, 0);
   if (tid < blocks) s_desc[tid] = desc = a.split_desc[tid];
   const unsigned has = __ballot_sync(0xffffffffu, desc.x != 0);
-  if ((tid & 31) == 0) s_warp[tid >> 5] = __popc(has);
+  if (lane == 0) s_warp[tid >> 5] = __popc(has);
   __syncthreads();
   int count = 0, before = 0;
 #pragma unroll
-  for (int i = 0; i < kJoinThreads / 32; ++i) {
+  for (int i = 0; i < (kLatentMaxCtas + 31) / 32; ++i) {
     before += i < (tid >> 5) ? s_warp[i] : 0;
     count += s_warp[i];
   }
-  if (desc.x) s_first[before + __popc(has & ((1u << (tid & 31)) - 1))] = tid;
+  if (desc.x) s_first[before + __popc(has & ((1u << lane) - 1))] = tid;
   __syncthreads();
   const int units = count * kUnits;
-  for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int first = s_first[unit / kUnits], dim0 = unit % kUnits * kDims;
+  for (int unit = (tid >> 5) * gridDim.x + blockIdx.x; unit < units;
+       unit += gridDim.x * (kJoinThreads / 32)) {
+    const int first = s_first[unit / kUnits];
+    const int row = unit % kUnits / kParts, col = unit % kParts * 32 + lane;  // (16-byte columns)
     const int4 d = s_desc[first];
     const int pieces = d.x;
-    auto slot_of = [&](int p) -> int64_t { return 2 * (first + p) + (p == 0 ? 1 : 0); };
     const Seq q = load_seq(a, d.y);
-    // this thread's values: coordinate dim0 + 4 (tid % 256) / N, rows r4 .. r4 + 3
-    const int v4 = tid & 255, half = tid >> 8, r4 = 4 * v4 % N;
-    const float4* const part = reinterpret_cast<const float4*>(a.part) + dim0 * (N / 4) + v4;
-    // a row's maximum and sum over the pieces
-    const float* const ml = reinterpret_cast<const float*>(a.part_ml);
-    const int row = tid % N, grp = tid / N;
-    float m = -INFINITY;
-#pragma unroll 4
-    for (int p = grp; p < pieces; p += kGroups) m = fmaxf(m, ml[slot_of(p) * 2 * N + row]);
-    s_red[grp][row] = m;
-    __syncthreads();
+    auto slot_of = [&](int p) -> int64_t { return 2 * (first + p) + (p == 0 ? 1 : 0); };
+    const float4* const part = reinterpret_cast<const float4*>(a.part) + row * (DC / 4) + col;
+    float4 v[kAhead];
+    auto fetch = [&](int p0) {
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) m = fmaxf(m, s_red[i][row]);
+      for (int j = 0; j < kAhead; ++j)
+        if (p0 + j < pieces) v[j] = part[slot_of(p0 + j) * (N * DC / 4)];
+    };
+    fetch(0);
+    // the row's maximum and sum over the pieces, and each piece's weight
+    const float* const ml = reinterpret_cast<const float*>(a.part_ml) + row;
+    float wt[kMost], m = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+      const int p = lane + 32 * i;
+      wt[i] = p < pieces ? ml[slot_of(p) * 2 * N] : -INFINITY;
+      m = fmaxf(m, wt[i]);
+    }
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
     const float mu = m == -INFINITY ? 0.f : m;
-    float sum = 0.f;
-#pragma unroll 4
-    for (int p = grp; p < pieces; p += kGroups) {
-      const float* const at = ml + slot_of(p) * 2 * N + row;
-      sum += at[N] * ex2_approx(at[0] - mu);
-    }
-    __syncthreads();
-    s_red[grp][row] = sum;
-    if (grp == 0) s_mu[row] = mu;
-    __syncthreads();
-    if (grp == 0) {
-      sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i) sum += s_red[i][row];
-      const bool none = no_key(m, sum);
-      float mt = m, lt = sum, keep = 1.f;
-      const int rr = d.z * N + row, tok = div_group(a, rr), head = rr - tok * a.group;
-      const bool real = tok < q.n;
-      if (a.sink && real) {
-        const float s2 = a.sink[head] * kLog2e;
-        mt = fmaxf(m, s2);
-        const float mx = mt == -INFINITY ? 0.f : mt;
-        keep = ex2_approx(m - mx);
-        lt = sum * keep + ex2_approx(s2 - mx + kShift);
-      }
-      s_scale[row] = none ? 0.f : keep / lt;
-      if (a.lse && real && dim0 == 0)
-        a.lse[static_cast<int64_t>(head) * a.num_tokens + q.row0 + tok] =
-            none ? (a.sink ? a.sink[head] : -INFINITY) : (mt - kShift) * kLn2 + logf(lt);
+    for (int i = 0; i < kMost; ++i) {
+      const int p = lane + 32 * i;
+      wt[i] = ex2_approx(wt[i] - mu);
+      if (p < pieces) sum = fmaf(ml[slot_of(p) * 2 * N + N], wt[i], sum);
     }
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
     // O
-    const float4 mu4 = *reinterpret_cast<const float4*>(&s_mu[r4]);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int p = half; p < pieces; p += 2) {
-      const int64_t slot = slot_of(p);
-      const float4 v = part[slot * (DC * N / 4)];
-      const float4 x = *reinterpret_cast<const float4*>(ml + slot * 2 * N + r4);
-      acc.x = fmaf(v.x, ex2_approx(x.x - mu4.x), acc.x);
-      acc.y = fmaf(v.y, ex2_approx(x.y - mu4.y), acc.y);
-      acc.z = fmaf(v.z, ex2_approx(x.z - mu4.z), acc.z);
-      acc.w = fmaf(v.w, ex2_approx(x.w - mu4.w), acc.w);
-    }
-    if (half) s_acc[v4] = acc;
-    __syncthreads();
-    if (!half) {
-      const float4 o = s_acc[v4], f = *reinterpret_cast<const float4*>(&s_scale[r4]);
-      const float y[4] = {(acc.x + o.x) * f.x, (acc.y + o.y) * f.y, (acc.z + o.z) * f.z,
-                          (acc.w + o.w) * f.w};
-      const float g[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        s_o[r4 + i][4 * v4 / N] =
-            static_cast<uint16_t>(pack2(g[i] == 0.f ? 0.f : y[i], 0.f, F16));
+    for (int i = 0; i < kMost; ++i) {
+#pragma unroll 1
+      for (int p0 = 32 * i; p0 < min(pieces, 32 * (i + 1)); p0 += kAhead) {
+        if (p0 > 0) fetch(p0);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const float w = __shfl_sync(0xffffffffu, wt[i], (p0 + j) & 31);
+          if (p0 + j < pieces)
+            acc = make_float4(fmaf(v[j].x, w, acc.x), fmaf(v[j].y, w, acc.y),
+                              fmaf(v[j].z, w, acc.z), fmaf(v[j].w, w, acc.w));
+        }
+      }
     }
-    __syncthreads();
-    constexpr int kPer = kDims / 8;  // 16-byte units of a row
-    if (tid < N * kPer) {
-      const int r = tid / kPer, u = tid % kPer;
-      if (d.z * N + r < q.n * a.group)
-        *reinterpret_cast<uint4*>(a.o + (static_cast<int64_t>(q.row0) * a.group + d.z * N + r) * DC +
-                                  dim0 + 8 * u) = *reinterpret_cast<const uint4*>(&s_o[r][8 * u]);
+    const int rr = d.z * N + row, tok = div_group(a, rr), head = rr - tok * a.group;
+    if (tok >= q.n) continue;
+    const bool none = no_key(m, sum);
+    float mt = m, lt = sum, keep = 1.f;
+    if (a.sink) {
+      const float s2 = a.sink[head] * kLog2e;
+      mt = fmaxf(m, s2);
+      const float mx = mt == -INFINITY ? 0.f : mt;
+      keep = ex2_approx(m - mx);
+      lt = sum * keep + ex2_approx(s2 - mx + kShift);
     }
-    __syncthreads();
+    const float f = keep / lt;
+    if (none) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    else acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+    reinterpret_cast<uint2*>(a.o + (static_cast<int64_t>(q.row0) * a.group + rr) * DC)[col] =
+        make_uint2(pack2(acc.x, acc.y, F16), pack2(acc.z, acc.w, F16));
+    if (a.lse && col == 0)
+      a.lse[static_cast<int64_t>(head) * a.num_tokens + q.row0 + tok] =
+          none ? (a.sink ? a.sink[head] : -INFINITY) : (mt - kShift) * kLn2 + logf(lt);
   }
 }
 
