@@ -145,8 +145,12 @@ __device__ __forceinline__ int2 keys_all(const Args& a, const SeqView& v, int r0
                    a.causal ? min(v.hi, pos0 + lo + 1) : v.hi);
 }
 // A block of rows costs its tiles and about as much as this many more: queries to
-// load, a pipeline to fill, O to write.  Shares are cut by that sum.
-constexpr int kStart = 3;
+// load, a pipeline to fill, O to write (131 KB of a partial state of 64 rows).  Shares
+// are cut by that sum.  (1, 2, 3, 5, 8: three chunks over long prefixes, 64 rows,
+// 276, 268, 260, 248, 250 us; 64 ragged contexts, 16 rows, 55.9, 55.1, 56.1, 56.1,
+// 56.6.)
+template <int N>
+constexpr int kStart = N == 64 ? 6 : 2;
 template <int N>
 __device__ __forceinline__ int tiles_of(const Args& a, const SeqView& v, int rb) {
   const int2 k = keys_any(a, v, rb * N, (rb + 1) * N);
@@ -168,7 +172,7 @@ __device__ __forceinline__ int64_t units_of(const Args& a, int first, int per) {
     }
     const bool many = nrb > 2;
     if (!many)
-      for (int rb = 0; rb < nrb; ++rb) mine += kStart + tiles_of<N>(a, v, rb);
+      for (int rb = 0; rb < nrb; ++rb) mine += kStart<N> + tiles_of<N>(a, v, rb);
     unsigned todo = __ballot_sync(0xffffffffu, many);
     while (todo) {
       const int o = __ffs(todo) - 1;
@@ -179,7 +183,7 @@ __device__ __forceinline__ int64_t units_of(const Args& a, int first, int per) {
       u.hi = __shfl_sync(0xffffffffu, v.hi, o);
       const int n = __shfl_sync(0xffffffffu, nrb, o);
       int64_t sum = 0;
-      for (int rb = lane; rb < n; rb += 32) sum += kStart + tiles_of<N>(a, u, rb);
+      for (int rb = lane; rb < n; rb += 32) sum += kStart<N> + tiles_of<N>(a, u, rb);
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (lane == o) mine += sum;
@@ -188,7 +192,7 @@ __device__ __forceinline__ int64_t units_of(const Args& a, int first, int per) {
   return mine;
 }
 
-// Walks the block's pieces (the scheduler warp does).  Units [0, kStart) of a block
+// Walks the block's pieces (the scheduler warp does).  Units [0, kStart<N>) of a block
 // of rows are its start, the others its tiles.
 struct Walk {
   int done, share;  // units behind the current piece's first, and in all
@@ -202,9 +206,9 @@ struct Walk {
 template <int N>
 __device__ __forceinline__ bool walk_piece(const Args& a, Walk& w) {
   w.nt = tiles_of<N>(a, w.v, w.rb);
-  w.u1 = min(w.nt + kStart, w.u0 + (w.share - w.done));
-  w.t0 = max(0, w.u0 - kStart);
-  w.t1 = max(0, w.u1 - kStart);
+  w.u1 = min(w.nt + kStart<N>, w.u0 + (w.share - w.done));
+  w.t0 = max(0, w.u0 - kStart<N>);
+  w.t1 = max(0, w.u1 - kStart<N>);
   w.any = keys_any(a, w.v, w.rb * N, (w.rb + 1) * N);
   w.key = (w.any.x & ~(kKeys - 1)) + w.t0 * kKeys;
   w.n = w.any.y > w.any.x ? w.t1 - w.t0 : 0;
@@ -270,7 +274,7 @@ __device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* 
     v = view_of(a, s);
     const int nrb = blocks_of<N>(a, v);
     for (rb = 0; rb < nrb; rb += 32) {
-      const int n = rb + lane < nrb ? kStart + tiles_of<N>(a, v, rb + lane) : 0;
+      const int n = rb + lane < nrb ? kStart<N> + tiles_of<N>(a, v, rb + lane) : 0;
       int64_t upto = n;
 #pragma unroll
       for (int i = 1; i < 32; i <<= 1) {
@@ -410,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.whole = w.t0 == 0 && w.t1 == w.nt;
           p.pieces = 0;
           if (p.first && !p.whole) {  // blocks that begin before the row block ends
-            const int64_t end = x->begin + w.done + (w.nt + kStart - w.u0);
+            const int64_t end = x->begin + w.done + (w.nt + kStart<N> - w.u0);
             int c = blockIdx.x + 1;
             while (c < x->shares.ctas && x->shares.begin(c) < end) ++c;
             p.pieces = c - static_cast<int>(blockIdx.x);

@@ -13,8 +13,8 @@ namespace attn {
 namespace paged {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kAtOnce = 4;  // loads in flight a lane
+constexpr int kWarps = 4;
+constexpr int kAtOnce = 6;  // loads in flight a lane
 
 struct ExpandArgs {
   Places w;
@@ -59,11 +59,6 @@ __device__ __forceinline__ void turn_shared(const ExpandArgs& a, int u, int row,
   }
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8], int f16) {
-  return make_uint4(pack2(x[0], x[1], f16), pack2(x[2], x[3], f16), pack2(x[4], x[5], f16),
-                    pack2(x[6], x[7], f16));
-}
-
 // kUnits: 16-byte units of the shared part.
 template <int kUnits, bool kBack>
 __global__ void __launch_bounds__(kWarps * 32) expand_kernel(const __grid_constant__ ExpandArgs a) {
@@ -100,12 +95,12 @@ __global__ void __launch_bounds__(kWarps * 32) expand_kernel(const __grid_consta
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
       if (hh < a.H)
-        r[j] = *reinterpret_cast<const uint4*>(kBack ? apart(hh, xx) : packed(hh, xx));
+        r[j] = ld16(kBack ? apart(hh, xx) : packed(hh, xx));
       next(hh, xx);
     }
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j) {
-      if (h < a.H) *reinterpret_cast<uint4*>(kBack ? packed(h, x) : apart(h, x)) = r[j];
+      if (h < a.H) st16(kBack ? packed(h, x) : apart(h, x), r[j]);
       next(h, x);
     }
   }
@@ -117,7 +112,7 @@ __global__ void __launch_bounds__(kWarps * 32) expand_kernel(const __grid_consta
     turn_shared<kUnits>(a, u, row, false, y);
     const uint4 o = pack8(y, a.f16);
     for (int hh = first; hh < a.H; hh += kPer)
-      *reinterpret_cast<uint4*>(k + hh * k_head + a.d_n + 8 * u) = o;
+      st16(k + hh * k_head + a.d_n + 8 * u, o);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = 0.f;
@@ -126,7 +121,7 @@ __global__ void __launch_bounds__(kWarps * 32) expand_kernel(const __grid_consta
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j)
         if (h0 + j * kPer < a.H)
-          r[j] = *reinterpret_cast<const uint4*>(k + (h0 + j * kPer) * k_head + a.d_n + 8 * u);
+          r[j] = ld16(k + (h0 + j * kPer) * k_head + a.d_n + 8 * u);
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
         if (h0 + j * kPer >= a.H) break;

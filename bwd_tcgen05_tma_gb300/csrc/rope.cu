@@ -27,6 +27,21 @@ struct TableArgs {
   uint64_t freq[128];  // turns a position, times 2^64
 };
 
+// Taylor's series of cos x and sin x for |x| <= pi/4, cut where the next term is
+// below 2e-9; with the roundings of x and of the sums off by less than 2^-23.
+__device__ __forceinline__ void sincos_eighth(float x, float& c, float& s) {
+  const float z = x * x;
+  float p = fmaf(z, -1.f / 3628800, 1.f / 40320);
+  p = fmaf(z, p, -1.f / 720);
+  p = fmaf(z, p, 1.f / 24);
+  p = fmaf(z, p, -0.5f);
+  c = fmaf(z, p, 1.f);
+  float q = fmaf(z, 1.f / 362880, -1.f / 5040);
+  q = fmaf(z, q, 1.f / 120);
+  q = fmaf(z, q, -1.f / 6);
+  s = fmaf(x * z, q, x);
+}
+
 __global__ void __launch_bounds__(kTableThreads) table_kernel(const __grid_constant__ TableArgs a) {
   const int groups = a.half / 4, per = kTableThreads / groups;  // positions of a block at once
   const int g = threadIdx.x % groups, i = threadIdx.x / groups;
@@ -47,7 +62,7 @@ __global__ void __launch_bounds__(kTableThreads) table_kernel(const __grid_const
       const uint32_t q = static_cast<uint32_t>((turn + (1ull << 61)) >> 62);
       const int64_t rest = static_cast<int64_t>(turn - (static_cast<uint64_t>(q) << 62));
       float cc, ss;
-      sincospif(__ll2float_rn(rest) * 0x1p-63f, &ss, &cc);  // half turns
+      sincos_eighth(__ll2float_rn(rest) * (6.2831853f * 0x1p-64f), cc, ss);
       const float x = (q & 1) ? ss : cc, y = (q & 1) ? cc : ss;
       // quarters: (c, s), (-s, c), (-c, -s), (s, -c)
       c[k] = (((q + 1) & 2) ? -x : x) * a.magnitude;
@@ -63,8 +78,9 @@ __global__ void __launch_bounds__(kTableThreads) table_kernel(const __grid_const
 // One warp a token: its lanes take the units of several heads side by side, so
 // that a warp's accesses are whole lines, and each lane keeps its unit's cosines
 // and sines for all heads.  Bound by HBM, two bytes an element each way.
-constexpr int kWarps = 8;
-constexpr int kAtOnce = 4;  // loads in flight a lane
+constexpr int kWarps = 4;
+constexpr int kAtOnce = 4;  // units in flight a lane
+constexpr int kCopies = 8;
 
 struct RopeArgs {
   Places w;
@@ -106,14 +122,17 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const __grid_constant
       Raw raw[kAtOnce];
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j)
-        if (h0 + j * per < a.heads) raw[j] = load_raw(src(h0 + j * per), at);
+        if (h0 + j * per < a.heads)
+          raw[j] = {ld16(src(h0 + j * per) + at.x), ld16(src(h0 + j * per) + at.y)};
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
         if (h0 + j * per >= a.heads) break;
         Unit r;
         unpack(raw[j], r, a.f16);
         turn(r, cs, a.interleaved);
-        store16(dst(h0 + j * per), at, r, a.f16);
+        uint16_t* const to = dst(h0 + j * per);
+        st16(to + at.x, pack8(r.x, a.f16));
+        st16(to + at.y, pack8(r.x + 8, a.f16));
       }
     }
   }
@@ -122,7 +141,7 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const __grid_constant
   const int before = a.start / 8, skip = a.rot / 8, step = 32 / rest, odd = 32 % rest;
   int h = lane / rest, x = lane % rest;
   while (h < a.heads) {
-    uint4 v[kAtOnce];
+    uint4 v[kCopies];
     int hh = h, xx = x;
     auto next = [&]() {
       hh += step;
@@ -133,15 +152,15 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const __grid_constant
       }
     };
 #pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) {
+    for (int j = 0; j < kCopies; ++j) {
       const int e = (xx < before ? xx : xx + skip) * 8;
-      if (hh < a.heads) v[j] = *reinterpret_cast<const uint4*>(src(hh) + e);
+      if (hh < a.heads) v[j] = ld16(src(hh) + e);
       next();
     }
 #pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) {
+    for (int j = 0; j < kCopies; ++j) {
       const int e = (x < before ? x : x + skip) * 8;
-      if (h < a.heads) *reinterpret_cast<uint4*>(dst(h) + e) = v[j];
+      if (h < a.heads) st16(dst(h) + e, v[j]);
       h += step;
       x += odd;
       if (x >= rest) {

@@ -86,6 +86,17 @@ __device__ __forceinline__ void store16(uint16_t* dst, int2 at, const Unit& r, i
   *reinterpret_cast<uint4*>(dst + at.y) = hi;
 }
 
+// 16 bytes that are read, or written, once: first to leave the caches.
+__device__ __forceinline__ uint4 ld16(const void* p) {
+  return __ldcs(reinterpret_cast<const uint4*>(p));
+}
+__device__ __forceinline__ void st16(void* p, uint4 v) { __stcs(reinterpret_cast<uint4*>(p), v); }
+
+__device__ __forceinline__ uint4 pack8(const float* x, int f16) {
+  return make_uint4(pack2(x[0], x[1], f16), pack2(x[2], x[3], f16), pack2(x[4], x[5], f16),
+                    pack2(x[6], x[7], f16));
+}
+
 // Where a packed token stands: its row of the tables.
 struct Places {
   int num_tokens, seq_len, num_segments, rope_len;
