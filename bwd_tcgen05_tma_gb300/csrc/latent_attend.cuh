@@ -930,85 +930,110 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the pieces of split blocks of rows.  A warp takes 128 coordinates of a row,
-// four a lane, and works alone: it finds the row's statistics itself, a piece a
-// lane, while its first values are on their way.  The grid fills the SMs; its
-// blocks read all descriptors at once.
+// four a lane, and works alone: it finds the row's statistics itself while the
+// first values are on their way, of many pieces a piece a lane.  The grid fills the
+// SMs; its blocks read all descriptors at once.
 constexpr int kJoinThreads = 512;
+constexpr int kJoinMost = (kLatentMaxCtas + 31) / 32;  // pieces a lane
+constexpr int kAhead = 4;                              // pieces whose values are in flight
+
+__device__ __forceinline__ void join_add(float4& acc, const float4& v, float w) {
+  acc = make_float4(fmaf(v.x, w, acc.x), fmaf(v.y, w, acc.y), fmaf(v.z, w, acc.z),
+                    fmaf(v.w, w, acc.w));
+}
 template <bool F16, int DC, int N>
 __global__ void __launch_bounds__(kJoinThreads, 2)
     latent_join_kernel(const __grid_constant__ Args a, int blocks) {
   constexpr float kShift = F16 ? 7.f : 0.f;
   constexpr int kParts = DC / 128, kUnits = N * kParts;
-  constexpr int kMost = (kLatentMaxCtas + 31) / 32;  // pieces a lane
-  constexpr int kAhead = 4;
-  __shared__ int s_first[kLatentMaxCtas], s_warp[kJoinThreads / 32];
+  constexpr int64_t kPiece = N * DC / 4;  // 16-byte units of a piece's O
+  __shared__ int s_first[kLatentMaxCtas];
+  __shared__ unsigned s_has[kJoinMost];
   __shared__ int4 s_desc[kLatentMaxCtas];
   const int tid = threadIdx.x, lane = tid & 31;
   grid_dep_wait();
   // the blocks that hold a first piece, in order
-  int4 desc = make_int4(0, 0, 0, 0);
-  if (tid < blocks) s_desc[tid] = desc = a.split_desc[tid];
-  const unsigned has = __ballot_sync(0xffffffffu, desc.x != 0);
-  if (lane == 0) s_warp[tid >> 5] = __popc(has);
-  __syncthreads();
-  int count = 0, before = 0;
-#pragma unroll
-  for (int i = 0; i < (kLatentMaxCtas + 31) / 32; ++i) {
-    before += i < (tid >> 5) ? s_warp[i] : 0;
-    count += s_warp[i];
+  if (tid < 32 * kJoinMost) {
+    int4 desc = make_int4(0, 0, 0, 0);
+    if (tid < blocks) s_desc[tid] = desc = a.split_desc[tid];
+    const unsigned has = __ballot_sync(0xffffffffu, desc.x != 0);
+    if (lane == 0) s_has[tid >> 5] = has;
   }
-  if (desc.x) s_first[before + __popc(has & ((1u << lane) - 1))] = tid;
+  __syncthreads();
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < kJoinMost; ++i) {
+    const unsigned has = s_has[i];
+    if (tid < 32 && (has >> lane & 1))
+      s_first[count + __popc(has & ((1u << lane) - 1))] = 32 * i + lane;
+    count += __popc(has);
+  }
   __syncthreads();
   const int units = count * kUnits;
   for (int unit = (tid >> 5) * gridDim.x + blockIdx.x; unit < units;
        unit += gridDim.x * (kJoinThreads / 32)) {
     const int first = s_first[unit / kUnits];
-    const int row = unit % kUnits / kParts, col = unit % kParts * 32 + lane;  // (16-byte columns)
     const int4 d = s_desc[first];
     const int pieces = d.x;
-    const Seq q = load_seq(a, d.y);
+    const int row = unit % kUnits / kParts, col = unit % kParts * 32 + lane;  // (16-byte columns)
     auto slot_of = [&](int p) -> int64_t { return 2 * (first + p) + (p == 0 ? 1 : 0); };
+    const float* const ml = reinterpret_cast<const float*>(a.part_ml) + row;
     const float4* const part = reinterpret_cast<const float4*>(a.part) + row * (DC / 4) + col;
     float4 v[kAhead];
     auto fetch = [&](int p0) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j)
-        if (p0 + j < pieces) v[j] = part[slot_of(p0 + j) * (N * DC / 4)];
+        if (p0 + j < pieces) v[j] = part[slot_of(p0 + j) * kPiece];
     };
     fetch(0);
-    // the row's maximum and sum over the pieces, and each piece's weight
-    const float* const ml = reinterpret_cast<const float*>(a.part_ml) + row;
-    float wt[kMost], m = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-      const int p = lane + 32 * i;
-      wt[i] = p < pieces ? ml[slot_of(p) * 2 * N] : -INFINITY;
-      m = fmaxf(m, wt[i]);
-    }
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
-    const float mu = m == -INFINITY ? 0.f : m;
-#pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-      const int p = lane + 32 * i;
-      wt[i] = ex2_approx(wt[i] - mu);
-      if (p < pieces) sum = fmaf(ml[slot_of(p) * 2 * N + N], wt[i], sum);
-    }
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
-    // O
+    const Seq q = load_seq(a, d.y);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float m = -INFINITY, sum = 0.f;
+    if (pieces <= kAhead) {
+      float mx[kAhead], l[kAhead];
 #pragma unroll
-    for (int i = 0; i < kMost; ++i) {
+      for (int j = 0; j < kAhead; ++j) {
+        mx[j] = j < pieces ? ml[slot_of(j) * (2 * N)] : -INFINITY;
+        l[j] = j < pieces ? ml[slot_of(j) * (2 * N) + N] : 0.f;
+        m = fmaxf(m, mx[j]);
+      }
+      const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (j >= pieces) break;
+        const float w = ex2_approx(mx[j] - mu);
+        sum = fmaf(l[j], w, sum);
+        join_add(acc, v[j], w);
+      }
+    } else {
+      float wt[kJoinMost], l[kJoinMost];
+#pragma unroll
+      for (int i = 0; i < kJoinMost; ++i) {
+        const int p = lane + 32 * i;
+        wt[i] = p < pieces ? ml[slot_of(p) * (2 * N)] : -INFINITY;
+        l[i] = p < pieces ? ml[slot_of(p) * (2 * N) + N] : 0.f;
+        m = fmaxf(m, wt[i]);
+      }
+#pragma unroll
+      for (int i = 16; i > 0; i >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+      const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int i = 0; i < kJoinMost; ++i) {
+        wt[i] = ex2_approx(wt[i] - mu);
+        sum = fmaf(l[i], wt[i], sum);
+      }
+#pragma unroll
+      for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+#pragma unroll
+      for (int i = 0; i < kJoinMost; ++i) {
 #pragma unroll 1
-      for (int p0 = 32 * i; p0 < min(pieces, 32 * (i + 1)); p0 += kAhead) {
-        if (p0 > 0) fetch(p0);
+        for (int p0 = 32 * i; p0 < min(pieces, 32 * (i + 1)); p0 += kAhead) {
+          if (p0 > 0) fetch(p0);
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          const float w = __shfl_sync(0xffffffffu, wt[i], (p0 + j) & 31);
-          if (p0 + j < pieces)
-            acc = make_float4(fmaf(v[j].x, w, acc.x), fmaf(v[j].y, w, acc.y),
-                              fmaf(v[j].z, w, acc.z), fmaf(v[j].w, w, acc.w));
+          for (int j = 0; j < kAhead; ++j) {
+            const float w = __shfl_sync(0xffffffffu, wt[i], (p0 + j) & 31);
+            if (p0 + j < pieces) join_add(acc, v[j], w);
+          }
         }
       }
     }
