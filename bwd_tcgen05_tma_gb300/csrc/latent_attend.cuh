@@ -58,19 +58,27 @@ struct Piece {
   int2 any, all;     // keys some row, and every row, of the block keeps
 };
 
-// Units in equal shares, block i from floor(i total / ctas) on: one division of
-// 64 bits a call (they take as long as a read from memory here).
+// a / b for a < 2^20: the approximate quotient (two units in the last of 24 bits)
+// is off by one at most.
+__device__ __forceinline__ uint32_t div_small(uint32_t a, uint32_t b) {
+  const uint32_t q = __float2uint_rz(__fdividef(__uint2float_rz(a), __uint2float_rz(b)));
+  const int32_t r = static_cast<int32_t>(a - q * b);
+  return r < 0 ? q - 1 : r >= static_cast<int32_t>(b) ? q + 1 : q;
+}
+// Units in equal shares, block i from floor(i total / ctas) on.  (The divisions of
+// 64 bits, and of 32, take a tenth of the time to a block's first copy, so the
+// usual sizes go without.)
 struct Shares {
   int64_t each;
   int rest, ctas;
-  __device__ __forceinline__ int64_t begin(int i) const { return i * each + i * rest / ctas; }
+  __device__ __forceinline__ int64_t begin(int i) const {
+    return i * each + div_small(i * rest, ctas);
+  }
 };
 __device__ __forceinline__ Shares shares_of(int64_t total, int ctas) {
   Shares s;
   s.ctas = max(ctas, 1);
-  s.each = total >> 31 ? total / s.ctas
-                       : static_cast<int64_t>(static_cast<uint32_t>(total) /
-                                              static_cast<uint32_t>(s.ctas));
+  s.each = total >> 20 ? total / s.ctas : div_small(static_cast<uint32_t>(total), s.ctas);
   s.rest = static_cast<int>(total - s.each * s.ctas);
   return s;
 }
@@ -245,11 +253,22 @@ __device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* 
   } else {
     for (int i = 0; i < kThreads / 32; ++i) mine += scratch[lane * (kThreads / 32) + i];
   }
+  // sums up to each lane
   int64_t sum = mine;
+  if (__any_sync(0xffffffffu, mine >> 25 != 0)) {
+#pragma unroll 1
+    for (int i = 1; i < 32; i <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, sum, i);
+      if (lane >= i) sum += y;
+    }
+  } else {
+    int x32 = static_cast<int>(mine);
 #pragma unroll
-  for (int i = 1; i < 32; i <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, sum, i);
-    if (lane >= i) sum += y;
+    for (int i = 1; i < 32; i <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x32, i);
+      if (lane >= i) x32 += y;
+    }
+    sum = x32;
   }
   const int64_t total = __shfl_sync(0xffffffffu, sum, 31);
   const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
@@ -275,11 +294,13 @@ __device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* 
     const int nrb = blocks_of<N>(a, v);
     for (rb = 0; rb < nrb; rb += 32) {
       const int n = rb + lane < nrb ? kStart<N> + tiles_of<N>(a, v, rb + lane) : 0;
-      int64_t upto = n;
+      int upto = n;  // (32 row blocks of at most 2^24 tiles)
+      if (nrb > 1) {
 #pragma unroll
-      for (int i = 1; i < 32; i <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, upto, i);
-        if (lane >= i) upto += y;
+        for (int i = 1; i < 32; i <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, i);
+          if (lane >= i) upto += y;
+        }
       }
       const unsigned in = __ballot_sync(0xffffffffu, upto > off);
       if (in) {
@@ -288,7 +309,7 @@ __device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* 
         rb += f;
         break;
       }
-      off -= __shfl_sync(0xffffffffu, upto, 31);
+      off -= __shfl_sync(0xffffffffu, upto, nrb > 1 ? 31 : 0);
     }
     if (rb < nrb) break;
   }
