@@ -537,11 +537,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait(&x->drain[1], 0, 200000000ull);
   } else if (warp == 1) {
     // -------------------------------------------------------------- TMA producer
-    // Lane i looks after box i of a tile: a page, or 64 tokens of one.  The table
-    // is read a tile ahead.
+    // A tile's copies, by blocks of 128 coordinates and then the rotated part.  Where
+    // a page holds a whole tile, lane 0 makes them alone (a copy every 100 clocks or
+    // so; with the warp's votes and syncs around each it was 460, and the copies set
+    // the pace of chunks over long prefixes).  Otherwise a lane looks after one page's
+    // part of 64 coordinates.  The table is read a tile ahead.
     const int rows_log = min(a.page_shift, 6), boxes = kKeys >> rows_log;
     const int page_mask = (1 << a.page_shift) - 1;
-    uint32_t k = 0;
+    const int box = lane % boxes, chunk = lane / boxes;
+    const uint32_t lat0 = smem_u32(sm + L::kLatOff), rope0 = smem_u32(sm + L::kRopeOff);
+    uint32_t k = 0, slot = 0, phase = 0, rslot = 0, rphase = 0;  // tiles; places in the rings
     bool ok = true;
     for (uint32_t pi = 0;; ++pi) {
       const Piece* const p = take(pi, &ok);
@@ -549,64 +554,83 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = p->n, key0 = p->key, end = p->any.y;
       const int32_t* const table = a.table + p->seq * a.table_stride;
       release(pi);
-      // box of this lane's copies: chunks of 64 coordinates take turns over lanes
-      const int box = lane % boxes, chunk = lane / boxes;
       auto key_of = [&](int j) -> int { return key0 + j * kKeys + (box << rows_log); };
       auto load_entry = [&](int j) -> int {
         if (j >= n || key_of(j) >= end) return INT_MIN;
         const int col = key_of(j) >> a.page_shift;
         return col < a.max_pages ? table[col] : -1;
       };
-      int ahead = load_entry(0);
-      for (int j = 0; j < n && ok; ++j, ++k) {
-        int id = ahead;
-        ahead = load_entry(j + 1);
-        if (id < 0 || id >= a.num_pages) {
-          if (id != INT_MIN) flag_bounds(a);
-          id = -1;
+      auto checked = [&](int id) -> int {
+        if (id >= 0 && id < a.num_pages) return id;
+        if (id != INT_MIN) flag_bounds(a);
+        return -1;
+      };
+      if (boxes == 1) {
+        if (lane == 0) {
+          int ahead = load_entry(0);
+          for (int j = 0; j < n && ok; ++j, ++k) {
+            const int id = checked(ahead), first = key_of(j) & page_mask;
+            ahead = load_entry(j + 1);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              if (!(ok = mbar_wait(&x->lat_empty[slot], phase ^ 1))) break;
+              // the arrival (release) publishes the mask; the copy follows it
+              if (b == 0) x->ok_mask[k & 7] = id >= 0 ? 0xf : 0;
+              mbar_arrive_expect_tx(&x->lat_full[slot], id >= 0 ? L::kSlot : 0);
+              if (id >= 0)
+                tma_load_4d(lat0 + slot * L::kSlot, &maps.lat, &x->lat_full[slot], 0, first, 2 * b,
+                            id);
+              if (++slot == NS) slot = 0, phase ^= 1;
+            }
+            if (!ok || !(ok = mbar_wait(&x->rope_empty[rslot], rphase ^ 1))) break;
+            mbar_arrive_expect_tx(&x->rope_full[rslot], id >= 0 ? L::kRope : 0);
+            if (id >= 0)
+              tma_load_4d(rope0 + rslot * L::kRope, &maps.rope, &x->rope_full[rslot], 0, first,
+                          2 * NB, id);
+            if (++rslot == NR) rslot = 0, rphase ^= 1;
+          }
         }
-        const unsigned okm = __ballot_sync(0xffffffffu, id >= 0);
-        const uint32_t count = __popc(okm & ((1u << boxes) - 1));
-        const int slot = key_of(j) & page_mask;
-        const uint32_t rows = count << rows_log;
-        const uint32_t at = static_cast<uint32_t>(box << rows_log) * 128;
+        ok = __all_sync(0xffffffffu, ok);
+      } else {
+        int ahead = load_entry(0);
+        for (int j = 0; j < n && ok; ++j, ++k) {
+          const int id = checked(ahead);
+          ahead = load_entry(j + 1);
+          const unsigned okm = __ballot_sync(0xffffffffu, id >= 0);
+          const uint32_t rows = __popc(okm & ((1u << boxes) - 1)) << rows_log;
+          const int g = (16 * (lane & 3)) >> rows_log;  // 16-key groups whose page exists
+          const unsigned groups = __ballot_sync(0xffffffffu, okm >> g & 1) & 0xfu;
+          const uint32_t at = static_cast<uint32_t>(box << rows_log) * 128;
+          const int first = key_of(j) & page_mask;
 #pragma unroll 1
-        for (int b = 0; b < NB; ++b) {
-          const uint32_t e = k * NB + b, s = e % NS;
-          if (e >= NS && !(ok = mbar_wait_warp(&x->lat_empty[s], (e / NS - 1) & 1))) break;
-          if (b == 0) {
-            const int g = (16 * (lane & 3)) >> rows_log;
-            const unsigned m = __ballot_sync(0xffffffffu, okm >> g & 1) & 0xfu;
-            if (lane == 0) x->ok_mask[k & 7] = m;
+          for (int b = 0; b < NB; ++b) {
+            if (!(ok = mbar_wait_warp(&x->lat_empty[slot], phase ^ 1))) break;
+            if (lane == 0) {
+              if (b == 0) x->ok_mask[k & 7] = groups;
+              mbar_arrive_expect_tx(&x->lat_full[slot], rows * 256);
+            }
+            __syncwarp();
+            if (chunk < 2 && id >= 0)
+              tma_load_4d(lat0 + slot * L::kSlot + chunk * (kKeys * 128) + at, &maps.lat,
+                          &x->lat_full[slot], 0, first, 2 * b + chunk, id);
+            __syncwarp();
+            if (++slot == NS) slot = 0, phase ^= 1;
           }
-          // the arrival (release) publishes the mask; the copies follow it
+          if (!ok || !(ok = mbar_wait_warp(&x->rope_empty[rslot], rphase ^ 1))) break;
+          if (lane == 0) mbar_arrive_expect_tx(&x->rope_full[rslot], rows * 128);
           __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(&x->lat_full[s], rows * 256);
+          if (chunk == 0 && id >= 0)
+            tma_load_4d(rope0 + rslot * L::kRope + at, &maps.rope, &x->rope_full[rslot], 0, first,
+                        2 * NB, id);
           __syncwarp();
-          const uint32_t dst = smem_u32(sm + L::kLatOff) + s * L::kSlot + at;
-          if (boxes == 1) {
-            if (lane == 0 && id >= 0)
-              tma_load_4d(dst, &maps.lat, &x->lat_full[s], 0, slot, 2 * b, id);
-          } else if (chunk < 2 && id >= 0) {
-            tma_load_4d(dst + chunk * (kKeys * 128), &maps.lat, &x->lat_full[s], 0, slot,
-                        2 * b + chunk, id);
-          }
-          __syncwarp();
+          if (++rslot == NR) rslot = 0, rphase ^= 1;
         }
-        if (!ok) break;
-        const uint32_t s = k % NR;
-        if (k >= NR && !(ok = mbar_wait_warp(&x->rope_empty[s], (k / NR - 1) & 1))) break;
-        if (lane == 0) mbar_arrive_expect_tx(&x->rope_full[s], rows * 128);
-        __syncwarp();
-        if (chunk == 0 && id >= 0)
-          tma_load_4d(smem_u32(sm + L::kRopeOff) + s * L::kRope + at, &maps.rope,
-                      &x->rope_full[s], 0, slot, 2 * NB, id);
-        __syncwarp();
       }
       if (!ok) break;
     }
     if (!ok && lane == 0) timeout();
     // copies in flight land before the block may leave
+    k = __shfl_sync(0xffffffffu, k, 0);
     for (uint32_t e = k * NB > NS ? k * NB - NS : 0; e < k * NB; ++e)
       mbar_wait(&x->lat_full[e % NS], (e / NS) & 1, 100000000ull);
     for (uint32_t e = k > NR ? k - NR : 0; e < k; ++e)
