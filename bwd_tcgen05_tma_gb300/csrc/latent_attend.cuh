@@ -154,11 +154,11 @@ __device__ __forceinline__ int2 keys_all(const Args& a, const SeqView& v, int r0
 }
 // A block of rows costs its tiles and about as much as this many more: queries to
 // load, a pipeline to fill, O to write (131 KB of a partial state of 64 rows).  Shares
-// are cut by that sum.  (1, 2, 3, 5, 8: three chunks over long prefixes, 64 rows,
-// 276, 268, 260, 248, 250 us; 64 ragged contexts, 16 rows, 55.9, 55.1, 56.1, 56.1,
-// 56.6.)
+// are cut by that sum.  (6, 8, 10, 12, 15: three chunks over long prefixes, 64 rows,
+// 243, 233, 237, 234, 236 us; 1, 2, 3, 4: 64 ragged contexts, 16 rows, 56.9, 55.6,
+// 56.4, 56.9.)
 template <int N>
-constexpr int kStart = N == 64 ? 6 : 2;
+constexpr int kStart = N == 64 ? 8 : 2;
 template <int N>
 __device__ __forceinline__ int tiles_of(const Args& a, const SeqView& v, int rb) {
   const int2 k = keys_any(a, v, rb * N, (rb + 1) * N);
@@ -241,17 +241,19 @@ __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
 // This block's share, found by the scheduler warp.  With few sequences the warp
 // reads them all; otherwise the block's threads have left their ranges' units in
 // `scratch`.  (The warp alone needs no barrier: the other roles start meanwhile.)
-constexpr int kFewSeqs = 256;
+constexpr int kFewSeqs = 32;
 template <int N, class Aux>
 __device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* scratch, Walk& w) {
   const int lane = threadIdx.x & 31;
+  constexpr int kRanges = kThreads / 32;  // of a lane: thread kRanges * lane + i's at 32 i + lane
   const bool few = a.num_seqs <= kFewSeqs;
   const int ranges = few ? 32 : kThreads, per = (a.num_seqs + ranges - 1) / ranges;
   int64_t mine = 0;
   if (few) {
     mine = units_of<N>(a, lane * per, per);
   } else {
-    for (int i = 0; i < kThreads / 32; ++i) mine += scratch[lane * (kThreads / 32) + i];
+#pragma unroll
+    for (int i = 0; i < kRanges; ++i) mine += scratch[32 * i + lane];
   }
   // sums up to each lane
   int64_t sum = mine;
@@ -283,9 +285,21 @@ __device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* 
   int64_t off = begin - __shfl_sync(0xffffffffu, sum - mine, o);
   int s = o * per;
   if (!few) {
-    int r = o * (kThreads / 32);
-    while (off >= scratch[r]) off -= scratch[r++];
-    s = r * per;
+    int r = 0;
+    if (off >> 24 == 0) {  // all of the lane's ranges at once
+      int upto = lane < kRanges ? static_cast<int>(min(scratch[32 * lane + o], int64_t{1} << 24)) : 0;
+      const int n = upto;
+#pragma unroll
+      for (int i = 1; i < kRanges; i <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, i);
+        if (lane >= i) upto += y;
+      }
+      r = __ffs(__ballot_sync(0xffffffffu, upto > off)) - 1;
+      off -= __shfl_sync(0xffffffffu, upto - n, r);
+    } else {
+      while (off >= scratch[32 * r + o]) off -= scratch[32 * r++ + o];
+    }
+    s = (o * kRanges + r) * per;
   }
   SeqView v;
   int rb = 0;
@@ -400,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t* const scratch = reinterpret_cast<int64_t*>(sm);  // where queries will lie
   if (a.num_seqs > kFewSeqs) {
     const int per = (a.num_seqs + kThreads - 1) / kThreads;
-    scratch[tid] = units_of<N>(a, tid * per, per);
+    scratch[tid % (kThreads / 32) * 32 + tid / (kThreads / 32)] = units_of<N>(a, tid * per, per);
     __syncthreads();
   }
   grid_dep_launch();
@@ -602,27 +616,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           const unsigned groups = __ballot_sync(0xffffffffu, okm >> g & 1) & 0xfu;
           const uint32_t at = static_cast<uint32_t>(box << rows_log) * 128;
           const int first = key_of(j) & page_mask;
+          // (a lane's copy may be under way before lane 0 has told the barrier of
+          // its bytes: the barrier's phase ends with lane 0's arrival at the earliest)
 #pragma unroll 1
-          for (int b = 0; b < NB; ++b) {
-            if (!(ok = mbar_wait_warp(&x->lat_empty[slot], phase ^ 1))) break;
+          for (int b = 0; b < NB && ok; ++b) {
+            ok = mbar_wait(&x->lat_empty[slot], phase ^ 1);
+            if (!ok) break;
             if (lane == 0) {
               if (b == 0) x->ok_mask[k & 7] = groups;
               mbar_arrive_expect_tx(&x->lat_full[slot], rows * 256);
             }
-            __syncwarp();
             if (chunk < 2 && id >= 0)
               tma_load_4d(lat0 + slot * L::kSlot + chunk * (kKeys * 128) + at, &maps.lat,
                           &x->lat_full[slot], 0, first, 2 * b + chunk, id);
-            __syncwarp();
             if (++slot == NS) slot = 0, phase ^= 1;
           }
-          if (!ok || !(ok = mbar_wait_warp(&x->rope_empty[rslot], rphase ^ 1))) break;
+          ok = ok && mbar_wait(&x->rope_empty[rslot], rphase ^ 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&x->rope_full[rslot], rows * 128);
-          __syncwarp();
           if (chunk == 0 && id >= 0)
             tma_load_4d(rope0 + rslot * L::kRope + at, &maps.rope, &x->rope_full[rslot], 0, first,
                         2 * NB, id);
-          __syncwarp();
           if (++rslot == NR) rslot = 0, rphase ^= 1;
         }
       }
@@ -822,18 +837,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                            : "memory");
         }
         if (!whole) {
-          // rows no one keeps become zeros; of the others what is not finite
-          const int r = st >> 2;
-          const bool in = (okm >> (r >> 4) & 1) && key + r >= p->any.x && key + r < p->any.y;
-#pragma unroll 1
+          // keys no row keeps become zeros, and what is not finite of those that
+          // some rows keep and some do not
+#pragma unroll
           for (int b = 0; b < NB; ++b) {
             const uint32_t e = k * NB + b;
             failed |= !mbar_wait_warp(&x->lat_full[e % NS], (e / NS) & 1);
-            const uint32_t at = smem_u32(sm + L::kLatOff) + (e % NS) * L::kSlot +
-                                (st >> 1 & 1) * (kKeys * 128) + r * 128;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t q = at + ((4 * (st & 1) + i) << 4);
+          }
+          const int2 any = p->any, all = p->all;
+#pragma unroll 1
+          for (int r = st >> 3; r < kKeys; r += 32) {
+            const int kk = key + r;
+            const bool in = (okm >> (r >> 4) & 1) && kk >= any.x && kk < any.y;
+            if (in && kk >= all.x && kk < all.y) continue;
+#pragma unroll 1
+            for (int b = 0; b < 2 * NB; ++b) {
+              const uint32_t q = smem_u32(sm + L::kLatOff) + ((k * NB + (b >> 1)) % NS) * L::kSlot +
+                                 (b & 1) * (kKeys * 128) + r * 128 + ((st & 7) << 4);
               if (!in) {
                 st_shared_v4(q, 0, 0, 0, 0);
                 continue;
@@ -868,34 +888,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (softmax_any(failed)) break;
+      float lt = 0.f, mt = 0.f;
+      bool none = false;
+      int head = 0, tok = 0;
       if (st < N) {
-        float norm;
-        const float lsum = x->col[0][st] + x->col[1][st] + (x->col[2][st] + x->col[3][st]);
-        const float mx = x->top[st];
-        const bool none = mx == -FLT_MAX && lsum == 0.f;
-        if (!complete) {
-          norm = none ? 0.f : 1.f;
-          float* const ml = reinterpret_cast<float*>(a.part_ml + static_cast<int64_t>(slot) * N);
-          ml[st] = none ? -INFINITY : mx;
-          ml[N + st] = none ? 0.f : lsum;
-        } else {
-          const int rr = p->rb * N + st, tok = div_group(a, rr), head = rr - tok * a.group;
-          float lt = lsum, mt = mx, keep = 1.f;
+        lt = x->col[0][st] + x->col[1][st] + (x->col[2][st] + x->col[3][st]);
+        const float mx = mt = x->top[st];
+        none = mx == -FLT_MAX && lt == 0.f;
+        const int rr = p->rb * N + st;
+        tok = div_group(a, rr);
+        head = rr - tok * a.group;
+        float keep = 1.f, norm = 1.f;
+        if (complete) {
           if (a.sink && st < rows) {
             const float s2 = a.sink[head] * kLog2e;
             mt = none ? s2 : fmaxf(mx, s2);
             const float mu = mt == -INFINITY ? 0.f : mt;
             keep = ex2_approx(mx - mu);
-            lt = lsum * keep + ex2_approx(s2 - mu + kShift);
+            lt = lt * keep + ex2_approx(s2 - mu + kShift);
           }
-          norm = none ? 0.f : keep / lt;
-          if (a.lse && st < rows)
-            a.lse[static_cast<int64_t>(head) * a.num_tokens + p->row0 + tok] =
-                none ? (a.sink ? a.sink[head] : -INFINITY) : (mt - kShift) * kLn2 + logf(lt);
+          norm = keep / lt;
         }
-        x->fac[st] = norm;
+        x->fac[st] = none ? 0.f : norm;
       }
       softmax_any(false);
+      // (behind the barrier: the other warps are at O already)
+      if (st < N && !complete) {
+        float* const ml = reinterpret_cast<float*>(a.part_ml + static_cast<int64_t>(slot) * N);
+        ml[st] = none ? -INFINITY : mt;
+        ml[N + st] = none ? 0.f : lt;
+      } else if (st < rows && a.lse) {
+        a.lse[static_cast<int64_t>(head) * a.num_tokens + p->row0 + tok] =
+            none ? (a.sink ? a.sink[head] : -INFINITY) : (mt - kShift) * kLn2 + logf(lt);
+      }
       const bool bad = n > 0 && x->bad == it + 1;
       if (n > 0) {
         failed |= !mbar_wait_warp(&x->o_done, (k - 1) & 1);
