@@ -53,7 +53,7 @@ struct Piece {
   int n, key;   // key tiles (0: no row keeps a key, < 0: the end), first key
   int seq, rb;  // sequence, block of rows
   int first, whole;  // begins with the block's first tile; holds all its tiles
-  int pieces;        // of a split block, in its first piece: how many there are
+  int64_t end;       // in the first piece of a split block: of its units, of all
   int row0, new_rows, pos0, hi;  // of the sequence: first row, tokens, first position, keys
   int2 any, all;     // keys some row, and every row, of the block keeps
 };
@@ -73,6 +73,12 @@ struct Shares {
   int rest, ctas;
   __device__ __forceinline__ int64_t begin(int i) const {
     return i * each + div_small(i * rest, ctas);
+  }
+  // The first block that does not begin before unit `end`.
+  __device__ __forceinline__ int before(int64_t end) const {
+    int i = max(0, static_cast<int>(__fdividef(static_cast<float>(end), static_cast<float>(each + 1))) - 2);
+    while (i < ctas && begin(i) < end) ++i;
+    return i;
   }
 };
 __device__ __forceinline__ Shares shares_of(int64_t total, int ctas) {
@@ -447,13 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           p.rb = w.rb;
           p.first = w.t0 == 0;
           p.whole = w.t0 == 0 && w.t1 == w.nt;
-          p.pieces = 0;
-          if (p.first && !p.whole) {  // blocks that begin before the row block ends
-            const int64_t end = x->begin + w.done + (w.nt + kStart<N> - w.u0);
-            int c = blockIdx.x + 1;
-            while (c < x->shares.ctas && x->shares.begin(c) < end) ++c;
-            p.pieces = c - static_cast<int>(blockIdx.x);
-          }
+          p.end = x->begin + w.done + (w.nt + kStart<N> - w.u0);
           p.row0 = w.v.q.row0;
           p.new_rows = w.v.q.n;
           p.pos0 = w.v.q.len - w.v.q.n;
@@ -984,7 +984,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&x->o_empty);
       }
       if (!complete && p->first && st == 0)
-        a.split_desc[blockIdx.x] = make_int4(p->pieces, p->seq, p->rb, 0);
+        a.split_desc[blockIdx.x] =
+            make_int4(x->shares.before(p->end) - static_cast<int>(blockIdx.x), p->seq, p->rb, 0);
       if (softmax_any(failed)) break;  // (row bounds, `fac` and the piece have been read)
       release(pi);
       if (n > 0) ++it;
