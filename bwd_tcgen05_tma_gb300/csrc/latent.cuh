@@ -10,6 +10,7 @@ namespace paged {
 struct LatentArgs {
   Args a;
   int d_c;
+  int pair;  // attention: blocks work in pairs on row blocks of twice the rows (0 or 1)
   const uint16_t* c_new;
   const uint16_t* k_rope;
   const uint16_t* q_rope;

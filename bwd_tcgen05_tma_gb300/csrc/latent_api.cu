@@ -2,6 +2,7 @@
 // layout and launches.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -144,6 +145,22 @@ struct Plan {
 int rows_of(const attn_latent_params_t* p) {
   return latent_rows(static_cast<int64_t>(p->max_q_len) * p->H);
 }
+// Blocks in pairs: two row blocks of a sequence go through its tiles side by side, so
+// that they come from HBM once.  By the rows of the mean sequence (the largest may be
+// alone): always for two row blocks (128 heads: 4 contexts of 100-131 k keys 184 -> 150
+// us, 256 of up to 256 keys 60 -> 52); for more where the caches, at their longest,
+// exceed the L2 cache (three chunks over up to 16 k keys: 232 us without, 239 with;
+// shares are coarser); not for few and odd, where the last pair has one at work.
+bool pairs(const attn_latent_params_t* p, int sms) {
+  const int64_t rows = std::min(static_cast<int64_t>(p->max_q_len) * p->H,
+                                (static_cast<int64_t>(p->num_tokens) * p->H + p->num_seqs - 1) /
+                                    p->num_seqs);
+  const int64_t blocks = (rows + 63) / 64;
+  if (sms < 2 || blocks < 2 || (blocks % 2 && blocks < 7)) return false;
+  constexpr double kL2 = 100e6;
+  return blocks == 2 || static_cast<double>(p->num_seqs) * p->max_pages * p->page_size *
+                                (p->d_c + p->d_r) * 2 > kL2;
+}
 Plan make_plan(const attn_latent_params_t* p) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t rows = size_t{2} * kLatentMaxCtas * rows_of(p);
@@ -243,6 +260,7 @@ attn_status_t attn_latent_fwd(const attn_latent_params_t* p, void* o, float* lse
   if (sms <= 0) return ATTN_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int rows = rows_of(p);
+  l.pair = rows == 64 && pairs(p, sms);
   const cudaError_t e =
       l.a.f16 ? launch_latent_f16(l, rows, sms, st) : launch_latent_bf16(l, rows, sms, st);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;

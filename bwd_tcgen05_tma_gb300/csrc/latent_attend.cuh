@@ -18,7 +18,9 @@
 //
 // Work split.  As in the kernels of the paged cache: all tiles in order (sequence,
 // row block, tile) cut into equal shares, one a block, one block an SM; pieces of
-// a row block meet in a second kernel in a fixed order.
+// a row block meet in a second kernel in a fixed order.  Where a token (or a few)
+// has more rows than a block takes, two neighbouring blocks go through the same
+// tiles, each for its 64 rows: the second finds them in the L2 cache.
 //
 // Roles: an MMA issuer for each product, TMA producer, scheduler (a warp each), eight
 // softmax warps (four read a tile's 64 lanes, for one half of the columns), four
@@ -43,6 +45,12 @@ using namespace sm103;
 constexpr int kKeys = 64;      // keys a tile
 constexpr int kThreads = 512;  // warps: S, TMA, scheduler, P c, 8 softmax, 4 queries
 constexpr float kLazy = 8.f;
+// Blocks in pairs bring tiles to the L2 cache this many ahead of their copies, which
+// then take 740 clocks instead of 2000 or more: two tiles in shared memory do not
+// cover that.  (4 contexts of 100-131 k keys, 128 heads: 150 us with 2 or 3, 157 with
+// 5, 164 without.  Blocks that work alone are paced by HBM, where it only disturbs:
+// 64 heads 108 us without, 111 with 2, 148 with 5.)
+constexpr int kPrefetch = 2;
 
 struct LatentMaps {
   CUtensorMap lat, rope;
@@ -141,9 +149,9 @@ __device__ __forceinline__ SeqView view_of(const Args& a, int s) {
   v.hi = min(v.q.len, a.max_pages << a.page_shift);
   return v;
 }
-template <int N>
-__device__ __forceinline__ int blocks_of(const Args& a, const SeqView& v) {
-  return (v.q.n * a.group + N - 1) / N;
+// Row blocks of `rows` rows (a power of two).
+__device__ __forceinline__ int blocks_of(const Args& a, const SeqView& v, int rows) {
+  return (v.q.n * a.group + rows - 1) >> (31 - __clz(rows));
 }
 // Keys [x, y) that some (any) or every row of rows [r0, r1) keeps.
 __device__ __forceinline__ int2 keys_any(const Args& a, const SeqView& v, int r0, int r1) {
@@ -165,15 +173,14 @@ __device__ __forceinline__ int2 keys_all(const Args& a, const SeqView& v, int r0
 // 56.4, 56.9.)
 template <int N>
 constexpr int kStart = N == 64 ? 8 : 2;
-template <int N>
-__device__ __forceinline__ int tiles_of(const Args& a, const SeqView& v, int rb) {
-  const int2 k = keys_any(a, v, rb * N, (rb + 1) * N);
+__device__ __forceinline__ int tiles_of(const Args& a, const SeqView& v, int rows, int rb) {
+  const int2 k = keys_any(a, v, rb * rows, (rb + 1) * rows);
   return max(1, (k.y - (k.x & ~(kKeys - 1)) + kKeys - 1) / kKeys);
 }
 // Units of a warp's sequences: `per` a lane, from `first` on.  The row blocks of a
 // sequence that has many (a prompt's chunk) are summed by all lanes together.
 template <int N>
-__device__ __forceinline__ int64_t units_of(const Args& a, int first, int per) {
+__device__ __forceinline__ int64_t units_of(const Args& a, int rows, int first, int per) {
   const int lane = threadIdx.x & 31;
   int64_t mine = 0;
   for (int i = 0; i < per; ++i) {
@@ -182,11 +189,11 @@ __device__ __forceinline__ int64_t units_of(const Args& a, int first, int per) {
     if (first + i < a.num_seqs) {
       v = view_of(a, first + i);
       if (outside(a, v.q)) flag_bounds(a);
-      nrb = blocks_of<N>(a, v);
+      nrb = blocks_of(a, v, rows);
     }
     const bool many = nrb > 2;
     if (!many)
-      for (int rb = 0; rb < nrb; ++rb) mine += kStart<N> + tiles_of<N>(a, v, rb);
+      for (int rb = 0; rb < nrb; ++rb) mine += kStart<N> + tiles_of(a, v, rows, rb);
     unsigned todo = __ballot_sync(0xffffffffu, many);
     while (todo) {
       const int o = __ffs(todo) - 1;
@@ -197,7 +204,7 @@ __device__ __forceinline__ int64_t units_of(const Args& a, int first, int per) {
       u.hi = __shfl_sync(0xffffffffu, v.hi, o);
       const int n = __shfl_sync(0xffffffffu, nrb, o);
       int64_t sum = 0;
-      for (int rb = lane; rb < n; rb += 32) sum += kStart<N> + tiles_of<N>(a, u, rb);
+      for (int rb = lane; rb < n; rb += 32) sum += kStart<N> + tiles_of(a, u, rows, rb);
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (lane == o) mine += sum;
@@ -211,21 +218,19 @@ __device__ __forceinline__ int64_t units_of(const Args& a, int first, int per) {
 struct Walk {
   int done, share;  // units behind the current piece's first, and in all
   int seq, rb, u0;
+  int rows;  // of a block of rows
   SeqView v;
   // the current piece: tiles [t0, t1) of nt
   int u1, t0, t1, nt;
-  int2 any;    // keys some row of the block of rows keeps
-  int n, key;  // key tiles (0: no row keeps a key), first key of the first
+  int2 any;  // keys some row of the block of rows keeps
 };
 template <int N>
 __device__ __forceinline__ bool walk_piece(const Args& a, Walk& w) {
-  w.nt = tiles_of<N>(a, w.v, w.rb);
+  w.nt = tiles_of(a, w.v, w.rows, w.rb);
   w.u1 = min(w.nt + kStart<N>, w.u0 + (w.share - w.done));
   w.t0 = max(0, w.u0 - kStart<N>);
   w.t1 = max(0, w.u1 - kStart<N>);
-  w.any = keys_any(a, w.v, w.rb * N, (w.rb + 1) * N);
-  w.key = (w.any.x & ~(kKeys - 1)) + w.t0 * kKeys;
-  w.n = w.any.y > w.any.x ? w.t1 - w.t0 : 0;
+  w.any = keys_any(a, w.v, w.rb * w.rows, (w.rb + 1) * w.rows);
   return w.t1 > w.t0;
 }
 // The next piece with tiles.
@@ -235,7 +240,7 @@ __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
     w.done += w.u1 - w.u0;
     if (w.done >= w.share) return false;
     w.u0 = 0;
-    if (++w.rb >= blocks_of<N>(a, w.v)) {
+    if (++w.rb >= blocks_of(a, w.v, w.rows)) {
       w.rb = 0;
       do w.v = view_of(a, ++w.seq);
       while (w.v.q.n == 0);
@@ -249,14 +254,15 @@ __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
 // `scratch`.  (The warp alone needs no barrier: the other roles start meanwhile.)
 constexpr int kFewSeqs = 32;
 template <int N, class Aux>
-__device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* scratch, Walk& w) {
+__device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* scratch, int block,
+                                          int blocks, int rows, Walk& w) {
   const int lane = threadIdx.x & 31;
   constexpr int kRanges = kThreads / 32;  // of a lane: thread kRanges * lane + i's at 32 i + lane
   const bool few = a.num_seqs <= kFewSeqs;
   const int ranges = few ? 32 : kThreads, per = (a.num_seqs + ranges - 1) / ranges;
   int64_t mine = 0;
   if (few) {
-    mine = units_of<N>(a, lane * per, per);
+    mine = units_of<N>(a, rows, lane * per, per);
   } else {
 #pragma unroll
     for (int i = 0; i < kRanges; ++i) mine += scratch[32 * i + lane];
@@ -279,12 +285,13 @@ __device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* 
     sum = x32;
   }
   const int64_t total = __shfl_sync(0xffffffffu, sum, 31);
-  const int ctas = static_cast<int>(min(static_cast<int64_t>(gridDim.x), total));
+  const int ctas = static_cast<int>(min(static_cast<int64_t>(blocks), total));
   w.done = w.share = 0;
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  w.rows = rows;
+  if (block >= ctas) return;
   const Shares sh = shares_of(total, ctas);
-  const int64_t begin = sh.begin(blockIdx.x);
-  w.share = static_cast<int>(sh.begin(blockIdx.x + 1) - begin);
+  const int64_t begin = sh.begin(block);
+  w.share = static_cast<int>(sh.begin(block + 1) - begin);
   // the lane, the range and the sequence that hold the first unit
   const unsigned at = __ballot_sync(0xffffffffu, sum > begin);
   const int o = __ffs(at) - 1;
@@ -311,9 +318,9 @@ __device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* 
   int rb = 0;
   for (;; ++s) {  // row blocks of 32 at a time, all lanes
     v = view_of(a, s);
-    const int nrb = blocks_of<N>(a, v);
+    const int nrb = blocks_of(a, v, rows);
     for (rb = 0; rb < nrb; rb += 32) {
-      const int n = rb + lane < nrb ? kStart<N> + tiles_of<N>(a, v, rb + lane) : 0;
+      const int n = rb + lane < nrb ? kStart<N> + tiles_of(a, v, rows, rb + lane) : 0;
       int upto = n;  // (32 row blocks of at most 2^24 tiles)
       if (nrb > 1) {
 #pragma unroll
@@ -346,6 +353,13 @@ __device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* 
   if (!walk_piece<N>(a, w) && !walk_next<N>(a, w)) w.share = 0;
 }
 
+// Brings a box into the L2 cache.
+__device__ __forceinline__ void prefetch_4d(const void* map, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map),
+               "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
 // A barrier of the softmax warps that also tells whether any thread's p holds.
 __device__ __forceinline__ bool softmax_any(bool p) {
   uint32_t r;
@@ -358,7 +372,9 @@ __device__ __forceinline__ bool softmax_any(bool p) {
   return r != 0;
 }
 
-template <bool F16, int DC, int N>
+// PAIR: two neighbouring blocks walk the same pieces of row blocks of twice the rows,
+// each for one half of them.
+template <bool F16, int DC, int N, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_kernel(const __grid_constant__ LatentArgs l, const __grid_constant__ LatentMaps maps) {
   using L = LatentCfg<DC, N>;
@@ -417,10 +433,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   grid_dep_wait();
+  constexpr int pair = PAIR ? 1 : 0;
   int64_t* const scratch = reinterpret_cast<int64_t*>(sm);  // where queries will lie
   if (a.num_seqs > kFewSeqs) {
     const int per = (a.num_seqs + kThreads - 1) / kThreads;
-    scratch[tid % (kThreads / 32) * 32 + tid / (kThreads / 32)] = units_of<N>(a, tid * per, per);
+    scratch[tid % (kThreads / 32) * 32 + tid / (kThreads / 32)] = units_of<N>(a, N << pair, tid * per, per);
     __syncthreads();
   }
   grid_dep_launch();
@@ -440,30 +457,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------- scheduler
     if (lane == 0) a.split_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     Walk w;
-    walk_init<N>(a, x, scratch, w);
+    walk_init<N>(a, x, scratch, blockIdx.x >> pair, gridDim.x >> pair, N << pair, w);
+    const int half = blockIdx.x & ((1 << pair) - 1);
     bool ok = true, live = w.share > 0;
-    for (uint32_t i = 0; ok; ++i) {
-      if (i >= 4 && !(ok = mbar_wait_warp(&x->piece_empty[i & 3], ((i >> 2) - 1) & 1))) break;
-      if (lane == 0) {
-        Piece& p = x->piece[i & 3];
-        if (live) {
-          p.n = w.n;
-          p.key = w.key;
-          p.seq = w.seq;
-          p.rb = w.rb;
-          p.first = w.t0 == 0;
-          p.whole = w.t0 == 0 && w.t1 == w.nt;
-          p.end = x->begin + w.done + (w.nt + kStart<N> - w.u0);
-          p.row0 = w.v.q.row0;
-          p.new_rows = w.v.q.n;
-          p.pos0 = w.v.q.len - w.v.q.n;
-          p.hi = w.v.hi;
-          p.any = w.any;
-          p.all = keys_all(a, w.v, w.rb * N, (w.rb + 1) * N);
-        } else {
-          p.n = -1;
+    for (uint32_t i = 0; ok;) {
+      const int rb = (w.rb << pair) + half;
+      if (!live || rb * N < w.v.q.n * a.group) {  // (the last block may have one half)
+        if (i >= 4 && !(ok = mbar_wait_warp(&x->piece_empty[i & 3], ((i >> 2) - 1) & 1))) break;
+        if (lane == 0) {
+          Piece& p = x->piece[i & 3];
+          if (live) {
+            // of the walk's tiles those that some row of the half keeps
+            const int2 any = keys_any(a, w.v, rb * N, (rb + 1) * N);
+            const int base = w.any.x & ~(kKeys - 1);
+            const int lo = max(base + w.t0 * kKeys, any.x & ~(kKeys - 1));
+            const int hi = min(base + w.t1 * kKeys, any.y);
+            p.n = any.y > any.x && hi > lo ? (hi - lo + kKeys - 1) / kKeys : 0;
+            p.key = lo;
+            p.seq = w.seq;
+            p.rb = rb;
+            p.first = w.t0 == 0;
+            p.whole = w.t0 == 0 && w.t1 == w.nt;
+            p.end = x->begin + w.done + (w.nt + kStart<N> - w.u0);
+            p.row0 = w.v.q.row0;
+            p.new_rows = w.v.q.n;
+            p.pos0 = w.v.q.len - w.v.q.n;
+            p.hi = w.v.hi;
+            p.any = any;
+            p.all = keys_all(a, w.v, rb * N, (rb + 1) * N);
+          } else {
+            p.n = -1;
+          }
+          mbar_arrive(&x->piece_full[i & 3]);
         }
-        mbar_arrive(&x->piece_full[i & 3]);
+        ++i;
       }
       if (__any_sync(0xffffffffu, !live || *abort != 0)) break;
       live = walk_next<N>(a, w);
@@ -581,10 +608,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (boxes == 1) {
         if (lane == 0) {
-          int ahead = load_entry(0);
+          int ids[kPrefetch + 1];  // of tiles j, j + 1, ...
+#pragma unroll
+          for (int i = 0; i <= kPrefetch; ++i) ids[i] = load_entry(i);
           for (int j = 0; j < n && ok; ++j, ++k) {
-            const int id = checked(ahead), first = key_of(j) & page_mask;
-            ahead = load_entry(j + 1);
+            const int id = checked(ids[0]), first = key_of(j) & page_mask, far = ids[kPrefetch];
+#pragma unroll
+            for (int i = 0; i < kPrefetch; ++i) ids[i] = ids[i + 1];
+            ids[kPrefetch] = load_entry(j + kPrefetch + 1);
+            if (pair && far >= 0 && far < a.num_pages) {
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+                prefetch_4d(&maps.lat, 0, key_of(j + kPrefetch) & page_mask, 2 * b, far);
+              prefetch_4d(&maps.rope, 0, key_of(j + kPrefetch) & page_mask, 2 * NB, far);
+            }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
               if (!(ok = mbar_wait(&x->lat_empty[slot], phase ^ 1))) break;
@@ -985,7 +1022,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!complete && p->first && st == 0)
         a.split_desc[blockIdx.x] =
-            make_int4(x->shares.before(p->end) - static_cast<int>(blockIdx.x), p->seq, p->rb, 0);
+            make_int4(x->shares.before(p->end) - static_cast<int>(blockIdx.x >> pair), p->seq, p->rb,
+                      0);
       if (softmax_any(failed)) break;  // (row bounds, `fac` and the piece have been read)
       release(pi);
       if (n > 0) ++it;
@@ -1014,7 +1052,7 @@ __device__ __forceinline__ void join_add(float4& acc, const float4& v, float w) 
 }
 template <bool F16, int DC, int N>
 __global__ void __launch_bounds__(kJoinThreads, 2)
-    latent_join_kernel(const __grid_constant__ Args a, int blocks) {
+    latent_join_kernel(const __grid_constant__ Args a, int blocks, int step) {
   constexpr float kShift = F16 ? 7.f : 0.f;
   constexpr int kParts = DC / 128, kUnits = N * kParts;
   constexpr int64_t kPiece = N * DC / 4;  // 16-byte units of a piece's O
@@ -1047,7 +1085,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
     const int4 d = s_desc[first];
     const int pieces = d.x;
     const int row = unit % kUnits / kParts, col = unit % kParts * 32 + lane;  // (16-byte columns)
-    auto slot_of = [&](int p) -> int64_t { return 2 * (first + p) + (p == 0 ? 1 : 0); };
+    auto slot_of = [&](int p) -> int64_t { return 2 * first + p * step + (p == 0 ? 1 : 0); };
     const float* const ml = reinterpret_cast<const float*>(a.part_ml) + row;
     const float4* const part = reinterpret_cast<const float4*>(a.part) + row * (DC / 4) + col;
     float4 v[kAhead];
@@ -1130,10 +1168,10 @@ __global__ void __launch_bounds__(kJoinThreads, 2)
   }
 }
 
-template <bool F16, int DC, int N>
+template <bool F16, int DC, int N, bool PAIR>
 cudaError_t latent_one(const LatentArgs& l, int sms, cudaStream_t st) {
   using L = LatentCfg<DC, N>;
-  auto kern = latent_kernel<F16, DC, N>;
+  auto kern = latent_kernel<F16, DC, N, PAIR>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e != cudaSuccess) return e;
   LatentMaps maps;
@@ -1145,18 +1183,20 @@ cudaError_t latent_one(const LatentArgs& l, int sms, cudaStream_t st) {
   e = launch_early(kern, dim3(ctas), dim3(kThreads), L::kSmem, st, l, maps);
   if (e != cudaSuccess) return e;
   return launch_early(latent_join_kernel<F16, DC, N>, dim3(2 * ctas), dim3(kJoinThreads), 0, st, l.a,
-                      static_cast<int>(ctas));
+                      static_cast<int>(ctas), PAIR ? 4 : 2);
 }
 
+template <bool F16, int DC>
+cudaError_t latent_rows(const LatentArgs& l, int rows, int sms, cudaStream_t st) {
+  return rows == 16   ? latent_one<F16, DC, 16, false>(l, sms, st)
+         : rows == 32 ? latent_one<F16, DC, 32, false>(l, sms, st)
+         : l.pair     ? latent_one<F16, DC, 64, true>(l, sms, st)
+                      : latent_one<F16, DC, 64, false>(l, sms, st);
+}
 template <bool F16>
 cudaError_t launch_latent(const LatentArgs& l, int rows, int sms, cudaStream_t st) {
-  if (l.d_c == 512)
-    return rows == 16   ? latent_one<F16, 512, 16>(l, sms, st)
-           : rows == 32 ? latent_one<F16, 512, 32>(l, sms, st)
-                        : latent_one<F16, 512, 64>(l, sms, st);
-  return rows == 16   ? latent_one<F16, 256, 16>(l, sms, st)
-         : rows == 32 ? latent_one<F16, 256, 32>(l, sms, st)
-                      : latent_one<F16, 256, 64>(l, sms, st);
+  return l.d_c == 512 ? latent_rows<F16, 512>(l, rows, sms, st)
+                      : latent_rows<F16, 256>(l, rows, sms, st);
 }
 
 }  // namespace

@@ -135,6 +135,9 @@ ATTEND = {
     "decode_33": dict(new=[1, 1], ctx=[190, 191], H=33, page=128),
     "decode_64": dict(new=[1, 1], ctx=[1000, 3], H=64, one=True),
     "decode_100": dict(new=[1, 1], ctx=[100, 600], H=100, page=256),
+    "decode_128": dict(new=[1] * 6, ctx=[0, 63, 64, 500, 1300, 127], H=128, one=True),
+    "decode_128_fp16": dict(new=[1, 1], ctx=[900, 10], H=128, d_c=256, dtype="fp16", page=16),
+    "pairs_ragged": dict(new=[2, 1, 0, 5, 1], ctx=[700, 64, 9, 200, 1], H=50),
     "decode_256": dict(new=[1], ctx=[300], H=256, d_c=256, one=True),
     "one_token_total": dict(new=[1], ctx=[0], one=True),
     "verify": dict(new=[4, 1, 3, 2], ctx=[63, 0, 129, 62]),
@@ -176,15 +179,27 @@ def test_attend(name):
 
 @pytest.mark.parametrize("kw", [dict(mask="NONE"), dict(window_left=0), dict(window_left=20),
                                 dict(mask="NONE", window_left=70), dict(window_left=1 << 30)])
-@pytest.mark.parametrize("name", ["decode", "verify", "chunk", "d256_chunk"])
+@pytest.mark.parametrize("name", ["decode", "verify", "chunk", "d256_chunk", "decode_128"])
 def test_attend_masks(name, kw):
     attend_and_check(Latent(seed=22, **ATTEND[name]), **kw)
 
 
-@pytest.mark.parametrize("name", ["decode_7", "verify", "chunk", "decode_100"])
+@pytest.mark.parametrize("name", ["decode_7", "verify", "chunk", "decode_100", "decode_128"])
 def test_attend_sink(name):
     c = Latent(seed=23, **ATTEND[name])
     attend_and_check(c, sink=np.random.default_rng(1).uniform(-3, 9, c.H).astype(np.float32))
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(window_left=100), dict(mask="NONE")])
+@pytest.mark.parametrize("name", ["chunk", "chunks", "decode_256", "d256_chunk", "pairs_ragged"])
+def test_attend_in_a_long_table(name, kw):
+    """A table that could hold more than the L2 cache: blocks work in pairs on more
+    than two row blocks of a sequence too, of which the last may be alone."""
+    c = Latent(seed=42, **ATTEND[name])
+    wide = torch.full((len(c.new), 4000), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    wide[:, :c.table.shape[1]] = c.t["table"]
+    c.t["table"] = wide
+    attend_and_check(c, **kw)
 
 
 @pytest.mark.parametrize("hint", [1, 2, 3, 4, 5, 5000])
@@ -283,7 +298,7 @@ def test_lengths_behind_the_table_are_reported():
     assert torch.equal(bits(lse[:, 1:]), bits(ref[1][:, 1:]))
 
 
-@pytest.mark.parametrize("H,new", [(16, 1), (16, 2), (16, 4), (3, 40)])
+@pytest.mark.parametrize("H,new", [(16, 1), (16, 2), (16, 4), (3, 40), (128, 1)])
 def test_attend_reports_bad_pages(H, new):
     """A page that is none counts as masked; the rest of its sequence, and the
     other sequences, are right."""
@@ -308,6 +323,29 @@ def test_attend_reports_bad_pages(H, new):
 
         lens = [c.lens[0] - 48, c.lens[1]]
         check_attend(c, o, lse, L.attend(c.queries(), rows_of, c.d_c, lens, c.cu, SCALE))
+
+
+def test_offsets_that_start_behind_row_0():
+    """The calls of a batch without its first sequence leave that one's rows and
+    pages alone."""
+    c = Latent([3, 9, 1], [40, 200, 7], seed=44)
+    t = c.t
+    kw = dict(page_table=t["table"][1:], seq_lens=t["lens"][1:], cu_seqlens_q=t["cu"][1:])
+    before = t["cache"].clone()
+    A.attn_latent_append(c.params(**kw))
+    o, lse = c.attend(c.params(**kw))
+    assert c.status() == 0
+    assert torch.isnan(o[:3]).all() and torch.isnan(lse[:, :3]).all()
+    assert torch.isnan(t["q_rot"][:3]).all() and torch.isfinite(t["q_rot"][3:]).all()
+    page = int(c.table[0, 0])
+    assert torch.equal(bits(t["cache"])[page], bits(before)[page])
+    ref = c.oracle_attend()
+    rows = slice(3, 13)
+    u = UNIT["bf16"]
+    delta = (576 + 16) * 2.0 ** -24 * ref[3][rows]
+    tol = u * np.abs(ref[0][rows]) + (u + 2.0 ** -17 + 2 * delta[..., None]) * (
+        ref[2][rows] * (1 + u)) + 1e-7
+    assert (np.abs(o.double().cpu().numpy()[rows] - ref[0][rows]) <= tol).all()
 
 
 def test_offsets_out_of_range_are_reported():
@@ -337,7 +375,7 @@ def test_attention_reports_positions_below_zero():
 # ------------------------------------------------- values that are not finite
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-@pytest.mark.parametrize("H,new", [(16, 1), (16, 2), (16, 4), (3, 40), (64, 1)])
+@pytest.mark.parametrize("H,new", [(16, 1), (16, 2), (16, 4), (3, 40), (64, 1), (128, 1), (50, 4)])
 def test_masked_values_have_no_influence(H, new, dtype):
     """NaN and infinities in slots behind a sequence's end, in front of every
     row's window, and in tokens that only later rows see."""
@@ -368,7 +406,7 @@ def test_masked_values_have_no_influence(H, new, dtype):
 
 
 @pytest.mark.parametrize("sink", [False, True])
-@pytest.mark.parametrize("name", ["decode", "verify", "chunk", "decode_64"])
+@pytest.mark.parametrize("name", ["decode", "verify", "chunk", "decode_64", "decode_128"])
 def test_nan_in_queries(name, sink):
     c = Latent(seed=36, **ATTEND[name])
     A.attn_latent_append(c.params())
@@ -452,9 +490,10 @@ def test_offsets_beyond_32_bits():
     check_append(c)
 
 
-def test_long_context_on_sampled_heads():
+@pytest.mark.parametrize("H", [16, 100])
+def test_long_context(H):
     """100000 keys of one sequence, cut over all blocks, against the oracle."""
-    c = Latent([1], [99999], seed=40, H=16, one=True)
+    c = Latent([1], [99999], seed=40, H=H, one=True)
     attend_and_check(c)
 
 

@@ -24,6 +24,7 @@ def bits(t):
 
 BATCHES = {
     "decode": dict(new=[1] * 4, ctx=[30, 400, 1000, 2500], one=True),
+    "decode_128": dict(new=[1] * 3, ctx=[400, 1000, 2500], one=True, H=128),
     "verify": dict(new=[4, 1, 3], ctx=[900, 30, 2000], H=8),
     "chunk": dict(new=[70, 1, 0, 33], ctx=[1900, 300, 40, 700], d_c=256, dtype="fp16"),
 }
