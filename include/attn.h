@@ -536,8 +536,9 @@ attn_status_t attn_paged_fwd(const attn_paged_params_t* p, void* o, float* lse, 
  *            (linearly; frequencies that turn often in the trained context are
  *            kept, those that hardly turn are divided by factor).
  * Frequencies are computed in 64 bits and angles in fixed point, as turns modulo
- * 1 with 64 bits, so that far positions lose nothing: each value is off by at
- * most 2^-22 * |magnitude|.
+ * 1 with 64 bits, so that far positions lose nothing but the frequencies' own
+ * rounding: each value is off by at most 2^-22 * |magnitude| below position 2^27,
+ * 2^-20 * |magnitude| anywhere.
  *
  * attn_rope:
  *   the rot_dim coordinates from rot_start on of every head of q and k are
@@ -704,8 +705,9 @@ typedef struct {
   int32_t mask;           /* ATTN_MASK_NONE or ATTN_MASK_CAUSAL */
   int32_t num_seqs;
   int32_t num_tokens; /* rows of the new tokens' tensors, padding included */
-  int32_t max_q_len;  /* largest n_s (a hint that chooses the kernel; any value
-                         >= 1 gives right results) */
+  int32_t max_q_len;  /* largest n_s (a hint that, with num_tokens, chooses the
+                         kernel for the whole call; any value >= 1 gives right
+                         results) */
   int32_t H;          /* query heads, 1 to 256 */
   int32_t d_c;        /* 256 or 512 */
   int32_t d_r;        /* 64 */
@@ -747,8 +749,9 @@ typedef struct {
   const float* sink;   /* fp32 [H] or NULL */
 } attn_latent_params_t;
 
-/* Workspace bytes attn_latent_fwd needs (0 on invalid parameters).  Depends on no
- * device data; ask it again when a field changes.  256-byte aligned. */
+/* Workspace bytes attn_latent_fwd needs (0 on invalid parameters): 10, 20 or 40 MB
+ * (d_c = 512; 256: half) for max_q_len * H of at most 16, at most 32, or more.
+ * Depends on no device data; ask it again when a field changes.  256-byte aligned. */
 size_t attn_latent_workspace_size(const attn_latent_params_t* p);
 
 /* Writes the new tokens' rows into the cache and turns the queries' parts. */
