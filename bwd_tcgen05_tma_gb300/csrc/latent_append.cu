@@ -1,7 +1,8 @@
 // Appending new tokens to the paged latent cache.
 //
 // One warp a job: a token's cache row (its latent vector copied, its rotated
-// part behind it), or the rotated parts of sixteen of its query heads.  A row is
+// part behind it) and the rotated parts of its first sixteen query heads, or of the
+// next sixteen.  A row is
 // 16-byte units side by side, so a warp's accesses are whole lines, and all of a
 // job's loads are on their way before the token's place is known.  Bound by HBM
 // for prompts (17349 tokens, 16 heads, 98 MB: 17.9 us, 5.5 TB/s); for single tokens by
@@ -54,21 +55,20 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int u = lane % kUnits, first = lane / kUnits;
 
   // the job's loads
-  uint4 c[kC], r[kHeadsJob / kPer];
-  const int h0 = (part - 1) * kHeadsJob + first;
+  uint4 c[kC], pe, r[kHeadsJob / kPer];
+  const int h0 = part * kHeadsJob + first, heads = l.q_rope ? a.Hq : 0;
   if (part == 0) {
     const uint4* src = reinterpret_cast<const uint4*>(l.c_new + t * l.c_new_stride);
 #pragma unroll
     for (int i = 0; i < kC; ++i) c[i] = src[lane + 32 * i];
-    r[0] = *reinterpret_cast<const uint4*>(l.k_rope + t * l.k_rope_stride + 8 * u);
-  } else {
+    pe = *reinterpret_cast<const uint4*>(l.k_rope + t * l.k_rope_stride + 8 * u);
+  }
 #pragma unroll
-    for (int j = 0; j < kHeadsJob / kPer; ++j) {
-      const int h = h0 + j * kPer;
-      r[j] = h < a.Hq ? *reinterpret_cast<const uint4*>(l.q_rope + t * l.q_rope_tok +
-                                                        h * l.q_rope_head + 8 * u)
-                      : make_uint4(0, 0, 0, 0);
-    }
+  for (int j = 0; j < kHeadsJob / kPer; ++j) {
+    const int h = h0 + j * kPer;
+    r[j] = h < heads ? *reinterpret_cast<const uint4*>(l.q_rope + t * l.q_rope_tok +
+                                                       h * l.q_rope_head + 8 * u)
+                     : make_uint4(0, 0, 0, 0);
   }
 
   // the token's sequence: the last one that starts at or before it
@@ -106,19 +106,19 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
   if (part == 0) {
     const int page = page_of(a, s, pos);
-    if (page < 0) return;
-    char* dst = a.kc + page * a.k_page + (pos & ((1 << a.page_shift) - 1)) * a.k_tok;
-    const uint4 o = turn_unit(r[0], u, cs, sn, a.interleaved, a.f16);
+    if (page >= 0) {
+      char* dst = a.kc + page * a.k_page + (pos & ((1 << a.page_shift) - 1)) * a.k_tok;
+      const uint4 o = turn_unit(pe, u, cs, sn, a.interleaved, a.f16);
 #pragma unroll
-    for (int i = 0; i < kC; ++i) reinterpret_cast<uint4*>(dst)[lane + 32 * i] = c[i];
-    if (first == 0) reinterpret_cast<uint4*>(dst)[32 * kC + u] = o;
-    return;
+      for (int i = 0; i < kC; ++i) reinterpret_cast<uint4*>(dst)[lane + 32 * i] = c[i];
+      if (first == 0) reinterpret_cast<uint4*>(dst)[32 * kC + u] = o;
+    }
   }
 #pragma unroll
   for (int j = 0; j < kHeadsJob / kPer; ++j) {
     const uint4 o = turn_unit(r[j], u, cs, sn, a.interleaved, a.f16);
     const int h = h0 + j * kPer;
-    if (h < a.Hq)
+    if (h < heads)
       *reinterpret_cast<uint4*>(l.q_rot + t * l.q_rot_tok + h * l.q_rot_head + 8 * u) = o;
   }
 }
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 }  // namespace
 
 cudaError_t launch_latent_append(const LatentArgs& l, cudaStream_t st) {
-  const int per = 1 + (l.q_rope ? (l.a.Hq + kHeadsJob - 1) / kHeadsJob : 0);
+  const int per = l.q_rope ? (l.a.Hq + kHeadsJob - 1) / kHeadsJob : 1;
   const int64_t blocks = (static_cast<int64_t>(l.a.num_tokens) * per + kWarps - 1) / kWarps;
   if (blocks >= 1ll << 31) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks)), block(kWarps * 32);
