@@ -216,9 +216,9 @@ __device__ __forceinline__ int64_t units_of(const Args& a, int rows, int first, 
       const int n = __shfl_sync(0xffffffffu, nrb, o);
       int64_t sum = 0;
       for (int rb = lane; rb < n; rb += 32) sum += kStart<N> + tiles_of(a, u, rows, rb);
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      if (lane == o) mine += sum;
+      const int lo = __reduce_add_sync(0xffffffffu, static_cast<int>(sum & 0xffffff));
+      const int hi = __reduce_add_sync(0xffffffffu, static_cast<int>(sum >> 24));
+      if (lane == o) mine += lo + (static_cast<int64_t>(hi) << 24);
     }
   }
   return mine;
@@ -260,23 +260,35 @@ __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
   return true;
 }
 
-// This block's share, found by the scheduler warp.  With few sequences the warp
-// reads them all; otherwise the block's threads have left their ranges' units in
-// `scratch`.  (The warp alone needs no barrier: the other roles start meanwhile.)
-constexpr int kFewSeqs = 32;
+// Where the sequences' units are summed.  Few sequences of few row blocks: by the
+// scheduler warp, `per` a lane, without a barrier, so that the other roles start
+// meanwhile.  Otherwise by all warps: 2 `ranges` lanes of each take `per` sequences
+// and leave their units in shared memory (range r at 32 (r % ranges) + r / ranges),
+// and a lane of the scheduler warp then stands for `ranges` of them.
+struct Split {
+  bool alone;
+  int ranges, per;
+};
+__device__ __forceinline__ Split split_of(const Args& a, int rows) {
+  Split s;
+  s.alone = a.num_seqs <= 32 &&
+            static_cast<int64_t>(a.num_tokens) * a.group <= 2ll * rows * a.num_seqs;
+  s.ranges = s.alone ? 1 : min(kThreads / 32, (a.num_seqs + 31) / 32);
+  s.per = (a.num_seqs + 32 * s.ranges - 1) / (32 * s.ranges);
+  return s;
+}
+
+// This block's share, found by the scheduler warp.
 template <int N, class Aux>
-__device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* scratch, int block,
-                                          int blocks, int rows, Walk& w) {
+__device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* scratch,
+                                          const Split& sp, int block, int blocks, int rows,
+                                          Walk& w) {
   const int lane = threadIdx.x & 31;
-  constexpr int kRanges = kThreads / 32;  // of a lane: thread kRanges * lane + i's at 32 i + lane
-  const bool few = a.num_seqs <= kFewSeqs;
-  const int ranges = few ? 32 : kThreads, per = (a.num_seqs + ranges - 1) / ranges;
   int64_t mine = 0;
-  if (few) {
-    mine = units_of<N>(a, rows, lane * per, per);
+  if (sp.alone) {
+    mine = units_of<N>(a, rows, lane * sp.per, sp.per);
   } else {
-#pragma unroll
-    for (int i = 0; i < kRanges; ++i) mine += scratch[32 * i + lane];
+    for (int i = 0; i < sp.ranges; ++i) mine += scratch[32 * i + lane];
   }
   // sums up to each lane
   int64_t sum = mine;
@@ -307,14 +319,14 @@ __device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* 
   const unsigned at = __ballot_sync(0xffffffffu, sum > begin);
   const int o = __ffs(at) - 1;
   int64_t off = begin - __shfl_sync(0xffffffffu, sum - mine, o);
-  int s = o * per;
-  if (!few) {
-    int r = 0;
+  int r = 0;
+  if (!sp.alone) {
     if (off >> 24 == 0) {  // all of the lane's ranges at once
-      int upto = lane < kRanges ? static_cast<int>(min(scratch[32 * lane + o], int64_t{1} << 24)) : 0;
+      int upto =
+          lane < sp.ranges ? static_cast<int>(min(scratch[32 * lane + o], int64_t{1} << 24)) : 0;
       const int n = upto;
 #pragma unroll
-      for (int i = 1; i < kRanges; i <<= 1) {
+      for (int i = 1; i < kThreads / 32; i <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, upto, i);
         if (lane >= i) upto += y;
       }
@@ -323,8 +335,8 @@ __device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* 
     } else {
       while (off >= scratch[32 * r + o]) off -= scratch[32 * r++ + o];
     }
-    s = (o * kRanges + r) * per;
   }
+  int s = (o * sp.ranges + r) * sp.per;
   SeqView v;
   int rb = 0;
   for (;; ++s) {  // row blocks of 32 at a time, all lanes
@@ -446,9 +458,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_wait();
   constexpr int pair = PAIR ? 1 : 0;
   int64_t* const scratch = reinterpret_cast<int64_t*>(sm);  // where queries will lie
-  if (a.num_seqs > kFewSeqs) {
-    const int per = (a.num_seqs + kThreads - 1) / kThreads;
-    scratch[tid % (kThreads / 32) * 32 + tid / (kThreads / 32)] = units_of<N>(a, N << pair, tid * per, per);
+  const Split split = split_of(a, N << pair);
+  if (!split.alone) {
+    const int r = warp * 2 * split.ranges + lane;
+    const int64_t mine = units_of<N>(a, N << pair,
+                                     lane < 2 * split.ranges ? r * split.per : a.num_seqs, split.per);
+    if (lane < 2 * split.ranges) scratch[32 * (r % split.ranges) + r / split.ranges] = mine;
     __syncthreads();
   }
   grid_dep_launch();
@@ -468,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------- scheduler
     if (lane == 0) a.split_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     Walk w;
-    walk_init<N>(a, x, scratch, blockIdx.x >> pair, gridDim.x >> pair, N << pair, w);
+    walk_init<N>(a, x, scratch, split, blockIdx.x >> pair, gridDim.x >> pair, N << pair, w);
     const int half = blockIdx.x & ((1 << pair) - 1);
     bool ok = true, live = w.share > 0;
     for (uint32_t i = 0; ok;) {
