@@ -36,8 +36,9 @@ attn_status_t validate(const attn_latent_params_t* p) {
   if ((p->d_c != 256 && p->d_c != 512) || p->d_r != kLatentRope) return ATTN_ERR_UNSUPPORTED;
   if (p->page_size < 16 || p->page_size > 256 || (p->page_size & (p->page_size - 1)))
     return ATTN_ERR_UNSUPPORTED;
-  // positions and packed rows are 32-bit, with room for a window or a tile beyond
-  if (static_cast<int64_t>(p->max_pages) * p->page_size > (1ll << 30) ||
+  // positions, packed rows and sequences are 32-bit, with room for a window, a tile or
+  // the sequences of a lane beyond
+  if (p->num_seqs > (1 << 30) || static_cast<int64_t>(p->max_pages) * p->page_size > (1ll << 30) ||
       static_cast<int64_t>(p->num_tokens) * p->H > (1ll << 30))
     return ATTN_ERR_UNSUPPORTED;
   if (!p->cu_seqlens_q && p->num_tokens != p->num_seqs) return ATTN_ERR_SHAPE_MISMATCH;

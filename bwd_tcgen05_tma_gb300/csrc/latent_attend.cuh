@@ -227,7 +227,7 @@ __device__ __forceinline__ int64_t units_of(const Args& a, int rows, int first, 
 // Walks the block's pieces (the scheduler warp does).  Units [0, kStart<N>) of a block
 // of rows are its start, the others its tiles.
 struct Walk {
-  int done, share;  // units behind the current piece's first, and in all
+  int64_t done, share;  // units behind the current piece's first, and in all
   int seq, rb, u0;
   int rows;  // of a block of rows
   SeqView v;
@@ -238,13 +238,14 @@ struct Walk {
 template <int N>
 __device__ __forceinline__ bool walk_piece(const Args& a, Walk& w) {
   w.nt = tiles_of(a, w.v, w.rows, w.rb);
-  w.u1 = min(w.nt + kStart<N>, w.u0 + (w.share - w.done));
+  w.u1 = static_cast<int>(min(static_cast<int64_t>(w.nt + kStart<N>), w.u0 + (w.share - w.done)));
   w.t0 = max(0, w.u0 - kStart<N>);
   w.t1 = max(0, w.u1 - kStart<N>);
   w.any = keys_any(a, w.v, w.rb * w.rows, (w.rb + 1) * w.rows);
   return w.t1 > w.t0;
 }
-// The next piece with tiles.
+// The next piece with tiles.  (There is one while the share lasts, unless the offsets
+// or lengths are changed under the call: then the walk ends with the sequences.)
 template <int N>
 __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
   do {
@@ -253,8 +254,10 @@ __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
     w.u0 = 0;
     if (++w.rb >= blocks_of(a, w.v, w.rows)) {
       w.rb = 0;
-      do w.v = view_of(a, ++w.seq);
-      while (w.v.q.n == 0);
+      do {
+        if (++w.seq >= a.num_seqs) return false;
+        w.v = view_of(a, w.seq);
+      } while (w.v.q.n == 0);
     }
   } while (!walk_piece<N>(a, w));
   return true;
@@ -314,7 +317,7 @@ __device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* 
   if (block >= ctas) return;
   const Shares sh = shares_of(total, ctas);
   const int64_t begin = sh.begin(block);
-  w.share = static_cast<int>(sh.begin(block + 1) - begin);
+  w.share = sh.begin(block + 1) - begin;
   // the lane, the range and the sequence that hold the first unit
   const unsigned at = __ballot_sync(0xffffffffu, sum > begin);
   const int o = __ffs(at) - 1;
@@ -340,6 +343,10 @@ __device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* 
   SeqView v;
   int rb = 0;
   for (;; ++s) {  // row blocks of 32 at a time, all lanes
+    if (s >= a.num_seqs) {
+      w.share = 0;
+      return;
+    }
     v = view_of(a, s);
     const int nrb = blocks_of(a, v, rows);
     for (rb = 0; rb < nrb; rb += 32) {

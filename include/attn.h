@@ -703,7 +703,7 @@ typedef struct {
   int32_t struct_version; /* = ATTN_LATENT_PARAMS_VERSION */
   int32_t dtype;          /* of the cache and of every 16-bit tensor: BF16 or FP16 */
   int32_t mask;           /* ATTN_MASK_NONE or ATTN_MASK_CAUSAL */
-  int32_t num_seqs;
+  int32_t num_seqs;   /* at most 2^30 */
   int32_t num_tokens; /* rows of the new tokens' tensors, padding included */
   int32_t max_q_len;  /* largest n_s (a hint that, with num_tokens, chooses the
                          kernel for the whole call; any value >= 1 gives right

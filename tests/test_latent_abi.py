@@ -230,6 +230,16 @@ def test_nothing_to_do(lib):
         assert fwd(lib, p, o=0, ws=0, ws_bytes=0) == OK
 
 
+def test_sequences_beyond_32_bits_of_work(lib):
+    """Offsets allow more sequences than tokens: their number is bounded by itself."""
+    for n in ((1 << 30) + 1, (1 << 31) - 1):
+        p = params(num_seqs=n, cu_seqlens_q=FAKE)
+        assert size(lib, p) == 0
+        assert call(lib, "attn_latent_append", p) == UNSUPPORTED
+        assert fwd(lib, p) == UNSUPPORTED
+    assert size(lib, params(num_seqs=1 << 30, cu_seqlens_q=FAKE)) > 0
+
+
 def test_workspace_grows_with_the_rows_expected(lib):
     sizes = [size(lib, params(max_q_len=n)) for n in (1, 2, 3, 100)]
     assert sizes == sorted(sizes) and sizes[0] < sizes[1] < sizes[2] == sizes[3]
