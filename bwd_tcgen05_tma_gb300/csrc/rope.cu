@@ -252,8 +252,12 @@ attn_status_t attn_rope_table(const attn_rope_table_params_t* p, void* stream) {
     base *= std::pow(p->factor, p->rot_dim / (p->rot_dim - 2.0));
     if (!std::isfinite(base)) return ATTN_ERR_INVALID_ARG;
   }
+  // powers by eights: two factors, three roundings of 2^-53 a frequency
+  double low[8], high = 1;
+  for (int i = 0; i < 8; ++i) low[i] = std::pow(base, -2.0 * i / p->rot_dim);
   for (int i = 0; i < a.half; ++i) {
-    double f = std::pow(base, -2.0 * i / p->rot_dim);
+    if (i % 8 == 0) high = std::pow(base, -2.0 * i / p->rot_dim);
+    double f = high * low[i % 8];
     if (p->scaling == ATTN_ROPE_LINEAR) f /= p->factor;
     if (p->scaling == ATTN_ROPE_TURNS) {
       const double turns = p->trained_len * f / pi2;
