@@ -30,8 +30,8 @@
 //    (4 contexts of 100-131 k keys, 64 heads: 106 us, 5.0 TB/s);
 //  - chunks of prompts, whose tiles come from the L2 cache: shared memory.  A tile of
 //    64 rows moves 328 KB through it (147 for S, 98 for O, 82 written), 2560 clocks at
-//    128 bytes each, and takes 2500-2700; its MMAs alone take 1960 (232 us for three
-//    chunks over up to 16 k keys, 880 TFLOP/s, tensor pipe 58 % busy).
+//    128 bytes each, and takes 2500-2700; its MMAs alone take 1960 (230 us for three
+//    chunks over up to 16 k keys, 885 TFLOP/s, tensor pipe 58 % busy).
 //
 // Roles: an MMA issuer for each product, TMA producer, scheduler (a warp each), eight
 // softmax warps (four read a tile's 64 lanes, for one half of the columns), four

@@ -9,16 +9,18 @@ namespace paged {
 namespace {
 
 // ---------------------------------------------------------------- tables
-// Angles in turns, modulo 1, as 64-bit fixed-point fractions: position times
-// frequency is one integer product whose overflow is the modulo, exact whatever
-// the position (an error of half a unit of a frequency, 2^-65 turns, grows to
-// 2^-35 at position 2^30).  The nearest quarter is taken off before the rest
-// becomes a float, whose relative rounding is then that of an angle below pi/4.
-// (In fp64 the same products and reductions would run at a sixty-fourth of the
-// fp32 rate here.)  Bound by its stores (131072 positions of 32 pairs, 33.5 MB: 8.7
-// us; with sincospif in place of the series below 9.8); small tables by the launch.
-constexpr int kTableThreads = 256;
-constexpr int kTableRows = 4;  // positions a thread takes
+// Angles in turns, modulo 1, as fixed-point fractions: position times frequency is
+// an integer product whose overflow is the modulo, exact whatever the position (an
+// error of half a unit of a frequency, 2^-65 turns, grows to 2^-35 at position 2^30).
+// Of the product's 64 bits the upper 32 are kept, 2^-32 turns or 1.5e-9 radians, an
+// eightieth of what the angle's roundings to float make of it.  The nearest quarter is
+// taken off first, so that those are relative to an angle below pi/4.  (In fp64 the same
+// products and reductions would run at a sixty-fourth of the fp32 rate here.)  Bound by
+// its stores and a launch's 2 us (131072 positions of 32 pairs, 33.5 MB: 6.1 us; with
+// all 64 bits turned to float 8.7, and with sincospif in place of the series 9.8; 4
+// positions a thread 6.3, blocks of 256 threads 6.4); small tables by the launch (8192 positions of 64 pairs in a graph 2.3 us).
+constexpr int kTableThreads = 128;
+constexpr int kTableRows = 8;  // positions a thread takes
 
 struct TableArgs {
   int rope_len, half;
@@ -60,11 +62,12 @@ __global__ void __launch_bounds__(kTableThreads) table_kernel(const __grid_const
     float c[4], s[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint64_t turn = f[k] * static_cast<uint64_t>(j);
-      const uint32_t q = static_cast<uint32_t>((turn + (1ull << 61)) >> 62);
-      const int64_t rest = static_cast<int64_t>(turn - (static_cast<uint64_t>(q) << 62));
+      const uint32_t turn = static_cast<uint32_t>(f[k] >> 32) * j +
+                            __umulhi(static_cast<uint32_t>(f[k]), static_cast<uint32_t>(j));
+      const uint32_t q = (turn + (1u << 29)) >> 30;
+      const int32_t rest = static_cast<int32_t>(turn - (q << 30));
       float cc, ss;
-      sincos_eighth(__ll2float_rn(rest) * (6.2831853f * 0x1p-64f), cc, ss);
+      sincos_eighth(__int2float_rn(rest) * (6.2831853f * 0x1p-32f), cc, ss);
       const float x = (q & 1) ? ss : cc, y = (q & 1) ? cc : ss;
       // quarters: (c, s), (-s, c), (-c, -s), (s, -c)
       c[k] = (((q + 1) & 2) ? -x : x) * a.magnitude;

@@ -536,8 +536,8 @@ attn_status_t attn_paged_fwd(const attn_paged_params_t* p, void* o, float* lse, 
  *            (linearly; frequencies that turn often in the trained context are
  *            kept, those that hardly turn are divided by factor).
  * Frequencies are computed in 64 bits and angles in fixed point, as turns modulo
- * 1 with 64 bits, so that far positions lose nothing but the frequencies' own
- * rounding: each value is off by at most 2^-22 * |magnitude| below position 2^27,
+ * 1 with 64 bits of which 32 are kept, so that far positions lose nothing but the
+ * frequencies' own rounding: each value is off by at most 2^-22 * |magnitude| below position 2^27,
  * 2^-20 * |magnitude| anywhere.
  *
  * attn_rope:
