@@ -135,7 +135,7 @@ struct LatentCfg {
   static constexpr int kP = kKeys * 128;     // P^T [64 keys][64 rows], N of them used
   static constexpr int kQ = N * (DC + kLatentRope) * 2;
   static constexpr int kRSlots = DC == 512 ? 2 : 4;
-  static constexpr int kAuxRoom = 3072;
+  static constexpr int kAuxRoom = 3 * 1024;
   static constexpr int kFit = (227 * 1024 - kQ - kP - kRSlots * kRope - kAuxRoom) / kSlot;
   static constexpr int kSlots = kFit > 4 * kNB ? 4 * kNB : kFit;
   static_assert(kSlots >= 2 * kNB, "two tiles");
