@@ -7,7 +7,7 @@
 // job's loads are on their way before the token's place is known.  Bound by HBM
 // for prompts (17349 tokens, 16 heads, 98 MB: 17.8 us, 5.5 TB/s); for single tokens by
 // the launch and the chain of reads lengths -> table -> store (64 tokens: 2.2 us in a
-// graph, 4.2 as the host launches them).
+// graph, 3.8 as the host launches them).
 #include "latent.cuh"
 
 namespace attn {

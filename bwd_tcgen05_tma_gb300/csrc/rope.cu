@@ -18,7 +18,8 @@ namespace {
 // products and reductions would run at a sixty-fourth of the fp32 rate here.)  Bound by
 // its stores and a launch's 2 us (131072 positions of 32 pairs, 33.5 MB: 6.1 us; with
 // all 64 bits turned to float 8.7, and with sincospif in place of the series 9.8; 4
-// positions a thread 6.3, blocks of 256 threads 6.4); small tables by the launch (8192 positions of 64 pairs in a graph 2.3 us).
+// positions a thread 6.3, blocks of 256 threads 6.4); small tables by the
+// launch (8192 positions of 64 pairs: 2.3 us in a graph, 4.4 as the host launches them).
 constexpr int kTableThreads = 128;
 constexpr int kTableRows = 8;  // positions a thread takes
 
