@@ -139,3 +139,37 @@ def test_overlapping_calls_and_repeats(name):
     for o, w in zip(outs, want):
         for x, lse in o:
             assert torch.equal(bits(x), w[0]) and torch.equal(bits(lse), w[1])
+
+
+@pytest.mark.parametrize("names", [("decode", "decode_128"), ("verify", "chunk"),
+                                   ("decode_128", "verify")])
+def test_graphs_that_share_a_workspace(names):
+    """Two captured steps of other sizes on one workspace, replayed in turn on one
+    stream without a pause, with an eager call of the first between them."""
+    steps = [Step(91 + i, n) for i, n in enumerate(names)]
+    ws = max((st.ws for st in steps), key=lambda w: w.numel())
+    want = []
+    for st in steps:
+        st.restore(0)
+        st.run()
+        torch.cuda.synchronize()
+        want.append(st.results())
+        st.ws = ws
+    stream, graphs = torch.cuda.Stream(), []
+    for st in steps:
+        st.restore(0)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            st.run()
+        graphs.append(g)
+    with torch.cuda.stream(stream):
+        for _ in range(4):
+            graphs[0].replay()
+            graphs[1].replay()
+            steps[0].run()
+            graphs[1].replay()
+    torch.cuda.synchronize()
+    for st, w in zip(steps, want):
+        assert all(torch.equal(x, y) for x, y in zip(st.results(), w))
+        assert st.c.status() == 0
