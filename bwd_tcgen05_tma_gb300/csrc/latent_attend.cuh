@@ -40,7 +40,8 @@
 // Values that are not finite in a tile that some rows mask in part are taken out of
 // the product (their zero weight would make NaN of them); a row that keeps such a
 // key gets NaN in that coordinate in the epilogue, which is what its score makes of
-// it (0 * inf where the score is -inf, NaN throughout otherwise).
+// it (0 * inf where the score is -inf, NaN throughout otherwise); O = 0 where no
+// score of the row is above -inf.
 #pragma once
 #include <cfloat>
 #include <climits>
@@ -979,7 +980,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           norm = keep / lt;
         }
-        x->fac[st] = none ? 0.f : norm;
+        // (below 0: no score of the row is above -inf, O = 0; a piece does not know of
+        // the others, and hands on what its keys of weight 0 made of O)
+        x->fac[st] = complete && none ? -1.f : norm;
       }
       softmax_any(false);
       // (behind the barrier: the other warps are at O already)
@@ -1015,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            v[i + e] = n > 0 && f[e] != 0.f ? __uint_as_float(o[i + e]) * f[e] : 0.f;
+            v[i + e] = n > 0 && !(f[e] < 0.f) ? __uint_as_float(o[i + e]) * f[e] : 0.f;
         }
         if (bad) {
           for (int kk = max(key0, p->any.x); kk < min(key0 + n * kKeys, p->any.y); ++kk) {
@@ -1029,7 +1032,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (fabsf(e) < INFINITY) continue;
 #pragma unroll
             for (int i = 0; i < kCols; ++i)
-              if (kk >= x->row_lo[cc + i] && kk < x->row_hi[cc + i]) v[i] = NAN;
+              if (kk >= x->row_lo[cc + i] && kk < x->row_hi[cc + i] && !(x->fac[cc + i] < 0.f))
+                v[i] = NAN;
           }
         }
         if (complete) {

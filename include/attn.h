@@ -690,7 +690,9 @@ attn_status_t attn_latent_expand_bwd(const attn_latent_expand_params_t* p, void*
  *   S_ihj = scale (q_lat_ih . c_j + q_rot_ih . k_r_j),  P = softmax_j(S) over the
  *   keys that the mask keeps,  O_ih = sum_j P_ihj c_j,  LSE_ih = ln sum_j exp(S_ihj)
  *   with masks, window, sink logits, rows without a key, scores and values that
- *   are not finite as in attn_paged_fwd.  P is rounded to dtype for the product
+ *   are not finite as in attn_paged_fwd (a kept key whose score is -inf because
+ *   its c holds an infinity makes NaN, 0 * inf, of that coordinate of O, unless
+ *   no score of the row is above -inf).  P is rounded to dtype for the product
  *   with c, not for the normaliser; sums and softmax statistics are fp32,
  *   exponentials the hardware's approximation.  Results do not depend on the
  *   order in which blocks run.
