@@ -113,7 +113,7 @@ __device__ __forceinline__ int place_of(const Places& w, int t) {
     int lo = 0, hi = w.num_segments;  // cu[lo] <= t < cu[hi], where it is anywhere
     if (hi == 0 || t < w.cu[0] || t >= w.cu[hi]) return -1;
     while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
+      const int mid = lo + (hi - lo) / 2;  // (hi + lo may pass 32 bits)
       if (w.cu[mid] <= t) lo = mid;
       else hi = mid;
     }
