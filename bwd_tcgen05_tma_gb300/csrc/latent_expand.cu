@@ -66,7 +66,11 @@ __global__ void __launch_bounds__(kWarps * 32) expand_kernel(const __grid_consta
   sm103::grid_dep_wait();
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (t >= a.w.num_tokens) return;
+  if (t >= a.w.num_tokens) {
+    const int block = blockIdx.x - (a.w.num_tokens + kWarps - 1) / kWarps;
+    if (block >= 0) check_offsets(a.w, block);
+    return;
+  }
   const int row = place_of(a.w, t);
   if (row < 0) return;
   uint16_t *kv = a.kv + t * a.kv_stride, *k = a.k + t * a.k_stride, *v = a.v + t * a.v_stride;
@@ -191,7 +195,7 @@ attn_status_t run(const attn_latent_expand_params_t* p, void* stream) {
   a.pe_stride = p->k_rope_stride;
   a.k_stride = p->k_stride;
   a.v_stride = p->v_stride;
-  const dim3 grid((p->num_tokens + kWarps - 1) / kWarps), block(kWarps * 32);
+  const dim3 grid(token_blocks(p, kWarps)), block(kWarps * 32);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = p->d_r == 32   ? launch_early(expand_kernel<4, kBack>, grid, block, 0, st, a)
                         : p->d_r == 64 ? launch_early(expand_kernel<8, kBack>, grid, block, 0, st, a)

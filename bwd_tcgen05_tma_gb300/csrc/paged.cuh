@@ -75,6 +75,24 @@ __device__ __forceinline__ int div_group(const Args& a, int n) {
   return a.group == 1 ? n : static_cast<int>((t + ((u - t) >> 1)) >> (a.group_shift - 1));
 }
 
+// Is packed token t behind the last of n > 0 segments?  Their end is taken for it only
+// where the last segment's offsets are in order.
+__device__ __forceinline__ bool behind_last(const int32_t* cu, int n, int t) {
+  const int end = cu[n];
+  return t >= end && end >= 0 && end >= cu[n - 1];
+}
+// The segment that holds packed token t, if one does: cu[s] <= t < cu[s + 1], but for
+// the first, which may begin behind t, and the last, which may end before it.
+__device__ __forceinline__ int segment_of(const int32_t* cu, int n, int t) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = lo + (hi - lo) / 2;  // (hi + lo may pass 32 bits)
+    if (cu[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
 // Rows and length of sequence s.  Offsets outside [0, num_tokens] or
 // decreasing, and negative lengths, are reported and read as empty.
 __device__ __forceinline__ Seq load_seq(const Args& a, int s) {

@@ -108,7 +108,11 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const __grid_constant
   sm103::grid_dep_wait();
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (t >= a.w.num_tokens) return;
+  if (t >= a.w.num_tokens) {
+    const int block = blockIdx.x - (a.w.num_tokens + kWarps - 1) / kWarps;
+    if (block >= 0) check_offsets(a.w, block);
+    return;
+  }
   const int row = place_of(a.w, t);
   if (row < 0) return;
   const uint16_t *q = a.q + t * a.q_stride, *k = a.k + t * a.k_stride;
@@ -305,7 +309,7 @@ attn_status_t attn_rope(const attn_rope_params_t* p, void* stream) {
   a.k_stride = p->k_stride;
   a.q_out_stride = p->q_out_stride;
   a.k_out_stride = p->k_out_stride;
-  const unsigned blocks = (p->num_tokens + kWarps - 1) / kWarps;
+  const unsigned blocks = token_blocks(p, kWarps);
   return launch_early(rope_kernel, dim3(blocks), dim3(kWarps * 32), 0,
                       static_cast<cudaStream_t>(stream), a) == cudaSuccess
              ? ATTN_OK

@@ -104,24 +104,30 @@ struct Places {
   const int32_t* cu;
   int32_t* status;
 };
+// Blocks behind those of the tokens look all offsets over, so that a bad one is
+// reported wherever it stands.
+constexpr int kOffsetsThread = 4;
+__device__ __forceinline__ void check_offsets(const Places& w, int block) {
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < kOffsetsThread; ++k) {
+    const int64_t i = (int64_t{block} * kOffsetsThread + k) * blockDim.x + threadIdx.x;
+    if (i > w.num_segments) break;
+    const int x = w.cu[i];
+    bad |= x < 0 || x > w.num_tokens || (i < w.num_segments && w.cu[i + 1] < x);
+  }
+  if (bad && w.status) *w.status = ATTN_ERR_DEVICE_BOUNDS;
+}
 // -1: padding, or (reported) offsets or a position that may not be used.
 __device__ __forceinline__ int place_of(const Places& w, int t) {
   int pos;
   if (w.positions) {
     pos = w.positions[t];
   } else if (w.cu) {
-    int lo = 0, hi = w.num_segments;  // cu[lo] <= t < cu[hi], where it is anywhere
-    if (hi == 0 || t < w.cu[0] || t >= w.cu[hi]) return -1;
-    while (hi - lo > 1) {
-      const int mid = lo + (hi - lo) / 2;  // (hi + lo may pass 32 bits)
-      if (w.cu[mid] <= t) lo = mid;
-      else hi = mid;
-    }
-    const int a = w.cu[lo], b = w.cu[lo + 1];
-    if (a < 0 || b > w.num_tokens || t < a || t >= b) {
-      if (w.status) *w.status = ATTN_ERR_DEVICE_BOUNDS;
-      return -1;
-    }
+    if (w.num_segments == 0 || behind_last(w.cu, w.num_segments, t)) return -1;
+    const int s = segment_of(w.cu, w.num_segments, t);
+    const int a = w.cu[s], b = w.cu[s + 1];
+    if (a < 0 || b > w.num_tokens || t < a || t >= b) return -1;  // (check_offsets reports it)
     pos = t - a;
   } else {
     pos = t % w.seq_len;
@@ -150,6 +156,13 @@ attn_status_t check_places(const P* p) {
   if (p->num_tokens > 0 && p->rope_len > 0 && (!p->rope_cos || !p->rope_sin))
     return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
+}
+// Blocks of `warps` warps, a token each, and those that check the offsets.
+template <class P>
+unsigned token_blocks(const P* p, int warps) {
+  const int64_t each = int64_t{32} * warps * kOffsetsThread;
+  return static_cast<unsigned>((p->num_tokens + warps - 1) / warps +
+                               (p->cu_seqlens ? (p->num_segments + each) / each : 0));
 }
 template <class P>
 Places places(const P* p) {

@@ -559,10 +559,12 @@ attn_status_t attn_paged_fwd(const attn_paged_params_t* p, void* o, float* lse, 
  * inputs and outputs must not overlap.  q may be NULL with Hq = 0, k with Hkv = 0.
  *
  * Streams and errors as above; neither call allocates or synchronises, both can
- * be captured.  Checks on the device: a position outside [0, rope_len), and
- * offsets outside [0, num_tokens] or decreasing, are never used: rows concerned
- * are not written, and ATTN_ERR_DEVICE_BOUNDS is stored in *status, if given;
- * the library never clears it. */
+ * be captured.  Checks on the device: a position outside [0, rope_len), and a
+ * segment whose offsets lie outside [0, num_tokens] or decrease, are never used:
+ * rows concerned are not written, and ATTN_ERR_DEVICE_BOUNDS is stored in
+ * *status, if given, wherever such offsets stand; the library never clears it.
+ * (Among such offsets rows of other segments may be left out too, and a row that
+ * several segments claim is turned for one of them.) */
 typedef enum {
   ATTN_ROPE_NONE = 0,
   ATTN_ROPE_LINEAR = 1,
