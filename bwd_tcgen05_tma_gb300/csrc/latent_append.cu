@@ -49,9 +49,13 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int lane = threadIdx.x & 31;
   const int64_t job = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int64_t tok = job / jobs_token;
-  if (tok >= a.num_tokens) return;
+  if (tok >= a.num_tokens) {
+    const int64_t jobs = static_cast<int64_t>(a.num_tokens) * jobs_token;
+    check_seqs(a, static_cast<int>(blockIdx.x - (jobs + kWarps - 1) / kWarps));
+    return;
+  }
   const int t = static_cast<int>(tok), part = static_cast<int>(job - tok * jobs_token);
-  if (a.cu && t >= a.cu[a.num_seqs]) return;  // padding: its row is not even read
+  if (a.cu && behind_last(a.cu, a.num_seqs, t)) return;  // padding: its row is not even read
   const int u = lane % kUnits, first = lane / kUnits;
 
   // the job's loads
@@ -71,17 +75,7 @@ __global__ void __launch_bounds__(kWarps * 32)
                      : make_uint4(0, 0, 0, 0);
   }
 
-  // the token's sequence: the last one that starts at or before it
-  int s = t;
-  if (a.cu) {
-    int lo = 0, hi = a.num_seqs;  // cu[lo] <= t < cu[hi], where it is anywhere
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (a.cu[mid] <= t) lo = mid;
-      else hi = mid;
-    }
-    s = lo;
-  }
+  const int s = a.cu ? segment_of(a.cu, a.num_seqs, t) : t;
   const Seq q = load_seq(a, s);
   if (t < q.row0 || t >= q.row0 + q.n || q.len <= 0) return;  // padding
   const int pos = q.len - q.n + t - q.row0;
@@ -127,7 +121,8 @@ __global__ void __launch_bounds__(kWarps * 32)
 
 cudaError_t launch_latent_append(const LatentArgs& l, cudaStream_t st) {
   const int per = l.q_rope ? (l.a.Hq + kHeadsJob - 1) / kHeadsJob : 1;
-  const int64_t blocks = (static_cast<int64_t>(l.a.num_tokens) * per + kWarps - 1) / kWarps;
+  const int64_t blocks = (static_cast<int64_t>(l.a.num_tokens) * per + kWarps - 1) / kWarps +
+                         check_blocks(l.a, kWarps * 32);
   if (blocks >= 1ll << 31) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks)), block(kWarps * 32);
   return l.d_c == 512 ? launch_early(latent_append_kernel<2>, grid, block, 0, st, l, per)

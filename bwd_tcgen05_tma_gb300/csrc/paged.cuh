@@ -118,6 +118,23 @@ __device__ __forceinline__ Seq load_seq(const Args& a, int s) {
   return q;
 }
 
+// A token's place is looked up from the token, so that a call may meet few of its
+// sequences: where there are offsets, blocks behind the others (of `threads` threads)
+// go through all of them, and report what is bad wherever it stands.
+constexpr int kSeqsThread = 4;
+inline int64_t check_blocks(const Args& a, int threads) {
+  const int64_t each = int64_t{kSeqsThread} * threads;
+  return a.cu ? (a.num_seqs + each - 1) / each : 0;
+}
+__device__ __forceinline__ void check_seqs(const Args& a, int block) {
+  if (!a.cu || block < 0) return;
+#pragma unroll
+  for (int k = 0; k < kSeqsThread; ++k) {
+    const int64_t s = (int64_t{block} * kSeqsThread + k) * blockDim.x + threadIdx.x;
+    if (s < a.num_seqs) load_seq(a, static_cast<int>(s));
+  }
+}
+
 // Has a sequence positions outside the table's row, or new rows below position
 // 0?  (One of length 0 has padding for rows.)
 __device__ __forceinline__ bool outside(const Args& a, const Seq& q) {

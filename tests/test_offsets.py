@@ -7,10 +7,10 @@ import pytest
 import torch
 
 from bwd_tcgen05_tma_gb300 import attn as A
-from latent_util import turn_tolerance
+from latent_util import Latent, turn_tolerance
 from oracle import latent_ref as L
 from test_latent_expand import Case
-from test_rope import angles, draw, tables
+from test_rope import angles, bits, draw, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -111,6 +111,92 @@ def test_expand(name, back):
         return np.array_equal(got["v"][row], v) and (np.abs(got["k"][row] - k) <= tol).all()
 
     check_rows(name, lambda r: any((x[r] != 77).any() for x in got.values()), right)
+
+
+# ---------------------------------------------------------------- appends
+
+CACHES = {
+    "latent": (Latent, A.attn_latent_append, ["cache"]),
+}
+
+
+def appended(kind, new, ctx, change):
+    """A batch appended whole, and again with its offsets or lengths changed."""
+    make, call, caches = CACHES[kind]
+    good, bad = (make(new, ctx, seed=92, page=16) for _ in range(2))
+    call(good.params())
+    assert good.status() == 0
+    before = {n: bad.t[n].clone() for n in caches}
+    change(bad.t)
+    call(bad.params())
+    return good, bad, before, caches
+
+
+def same_pages(x, y, pages):
+    return all(torch.equal(bits(x[p]), bits(y[p])) for p in pages)
+
+
+@pytest.mark.parametrize("kind", list(CACHES))
+@pytest.mark.parametrize("last", [-5, 1])
+def test_append_with_a_bad_last_offset(kind, last):
+    """The sequences before the last are appended; the last is left out and
+    reported."""
+    def change(t):
+        t["cu"][2] = last
+
+    good, bad, before, caches = appended(kind, [2, 3], [3, 4], change)
+    assert bad.status() == BOUNDS
+    for n in caches:
+        own = [int(good.table[0, 0])]
+        assert same_pages(bad.t[n], good.t[n], own)
+        assert same_pages(bad.t[n], before[n], [i for i in range(len(before[n])) if i not in own])
+    assert torch.equal(bits(bad.t["q_rot"][:2]), bits(good.t["q_rot"][:2]))
+    assert torch.isnan(bad.t["q_rot"][2:]).all()
+
+
+@pytest.mark.parametrize("kind", list(CACHES))
+@pytest.mark.parametrize("what", ["offset", "length"])
+def test_append_reports_what_no_token_meets(kind, what):
+    """Among empty sequences, hundreds of them away from the tokens: an offset or a
+    length that is negative.  The tokens are appended all the same."""
+    new = [1, 1] + [0] * 900 + [1] + [0] * 300
+
+    def change(t):
+        if what == "length":
+            t["lens"][1100] = -4
+        else:
+            t["cu"][700] = -1
+
+    good, bad, before, caches = appended(kind, new, [3] * len(new), change)
+    assert bad.status() == BOUNDS
+    for n in caches:
+        assert same_pages(bad.t[n], good.t[n], range(len(before[n])))
+    assert torch.equal(bits(bad.t["q_rot"]), bits(good.t["q_rot"]))
+
+
+@pytest.mark.parametrize("kind", list(CACHES))
+def test_append_with_an_inner_decrease(kind):
+    """Offsets 0, 8, 4, 10: reported; nothing is written but to the pages of the two
+    sequences whose own offsets are in order."""
+    def change(t):
+        t["cu"][1], t["cu"][2] = 8, 4
+
+    good, bad, before, caches = appended(kind, [4, 4, 2], [8, 8, 8], change)
+    assert bad.status() == BOUNDS
+    left = int(good.table[1, 0])
+    for n in caches:
+        assert same_pages(bad.t[n], before[n], [left])
+    assert torch.isfinite(bad.t["q_rot"]).all()
+
+
+@pytest.mark.parametrize("kind", list(CACHES))
+def test_append_with_padding_reports_nothing(kind):
+    """Sound offsets that end before the last row: no report, and padding stays."""
+    make, call, _ = CACHES[kind]
+    c = make([3, 0, 2], [5, 7, 1], seed=93, pad=70)
+    call(c.params())
+    assert c.status() == 0
+    assert torch.isfinite(c.t["q_rot"][:5]).all() and torch.isnan(c.t["q_rot"][5:]).all()
 
 
 def test_more_segments_than_half_of_32_bits():
