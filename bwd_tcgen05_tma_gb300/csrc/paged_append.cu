@@ -141,7 +141,7 @@ __device__ __forceinline__ void turn_queries(const Args& a, int block) {
   const int u = threadIdx.x % units, i = threadIdx.x / units;
   const int t = (block / groups) * tokens + i, h0 = (block % groups) * kHeads;
   if (i >= tokens || t >= a.num_tokens) return;
-  if (a.cu && t >= a.cu[a.num_seqs]) return;  // padding: its row is not even read
+  if (a.cu && behind_last(a.cu, a.num_seqs, t)) return;  // padding: its row is not even read
   const int2 at = unit_at(u, a.rot, a.interleaved);
   const int heads = min(kHeads, a.Hq - h0);
   const uint16_t* src = a.q + t * a.q_stride + h0 * a.d_qk;
@@ -150,17 +150,7 @@ __device__ __forceinline__ void turn_queries(const Args& a, int block) {
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (j < heads) raw[j] = load_raw(src + j * a.d_qk, at);
-  // the token's sequence: the last one that starts at or before it
-  int s = t;
-  if (a.cu) {
-    int lo = 0, hi = a.num_seqs;  // cu[lo] <= t < cu[hi], where it is anywhere
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (a.cu[mid] <= t) lo = mid;
-      else hi = mid;
-    }
-    s = lo;
-  }
+  const int s = a.cu ? segment_of(a.cu, a.num_seqs, t) : t;
   const Seq q = load_seq(a, s);
   if (t < q.row0 || t >= q.row0 + q.n || q.len <= 0) return;  // padding
   const bool turns = u < a.rot / 16;
@@ -195,11 +185,16 @@ __device__ __forceinline__ void turn_queries(const Args& a, int block) {
 }
 
 // Blocks [0, runs * groups) write keys and values, of `per_block` heads (one
-// with an E4M3 cache), the others turn queries.
+// with an E4M3 cache), the others turn queries; those from `checks` on look over
+// the sequences.
 template <int kKind, int uk, int uv>
 __global__ void __launch_bounds__(kThreads, 3)
-    append_kernel(const __grid_constant__ Args a, int runs, int per_block) {
+    append_kernel(const __grid_constant__ Args a, int runs, int per_block, int checks) {
   sm103::grid_dep_wait();
+  if (static_cast<int>(blockIdx.x) >= checks) {
+    check_seqs(a, blockIdx.x - checks);
+    return;
+  }
   const int groups = (a.Hkv + per_block - 1) / per_block;
   if (static_cast<int>(blockIdx.x) >= runs * groups) {
     turn_queries<uk>(a, blockIdx.x - runs * groups);
@@ -370,18 +365,20 @@ __global__ void __launch_bounds__(kThreads, 3)
 }
 
 template <int kKind, int uk>
-cudaError_t launch_width(const Args& a, dim3 grid, int runs, int per_block, cudaStream_t st) {
+cudaError_t launch_width(const Args& a, dim3 grid, int runs, int per_block, int checks,
+                         cudaStream_t st) {
   return a.d_v == 64
              ? launch_early(append_kernel<kKind, uk, 4>, grid, dim3(kThreads), 0, st, a, runs,
-                            per_block)
+                            per_block, checks)
              : launch_early(append_kernel<kKind, uk, 8>, grid, dim3(kThreads), 0, st, a, runs,
-                            per_block);
+                            per_block, checks);
 }
 template <int kKind>
-cudaError_t launch_dims(const Args& a, dim3 grid, int runs, int per_block, cudaStream_t st) {
-  return a.d_qk == 64    ? launch_width<kKind, 4>(a, grid, runs, per_block, st)
-         : a.d_qk == 128 ? launch_width<kKind, 8>(a, grid, runs, per_block, st)
-                         : launch_width<kKind, 12>(a, grid, runs, per_block, st);
+cudaError_t launch_dims(const Args& a, dim3 grid, int runs, int per_block, int checks,
+                        cudaStream_t st) {
+  return a.d_qk == 64    ? launch_width<kKind, 4>(a, grid, runs, per_block, checks, st)
+         : a.d_qk == 128 ? launch_width<kKind, 8>(a, grid, runs, per_block, checks, st)
+                         : launch_width<kKind, 12>(a, grid, runs, per_block, checks, st);
 }
 
 }  // namespace
@@ -405,12 +402,14 @@ cudaError_t launch_append(const Args& a, int kind, cudaStream_t st) {
     blocks += (static_cast<int64_t>(a.num_tokens) + tokens - 1) / tokens *
               ((a.Hq + kHeads - 1) / kHeads);
   }
+  const int64_t checks = blocks;
+  blocks += check_blocks(a, kThreads);
   if (blocks >= 1ll << 31) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks));
-  const int n = static_cast<int>(runs);
-  return kind == kCacheE4m3  ? launch_dims<kCacheE4m3>(a, grid, n, per_block, st)
-         : kind == kCacheF16 ? launch_dims<kCacheF16>(a, grid, n, per_block, st)
-                             : launch_dims<kCacheBf16>(a, grid, n, per_block, st);
+  const int n = static_cast<int>(runs), c = static_cast<int>(checks);
+  return kind == kCacheE4m3  ? launch_dims<kCacheE4m3>(a, grid, n, per_block, c, st)
+         : kind == kCacheF16 ? launch_dims<kCacheF16>(a, grid, n, per_block, c, st)
+                             : launch_dims<kCacheBf16>(a, grid, n, per_block, c, st);
 }
 
 }  // namespace paged

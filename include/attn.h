@@ -436,9 +436,9 @@ attn_status_t attn_fwd_noalloc(const attn_params_t* p, void* o, float* lse, void
  * the table's row or below 0, a rotation position outside [0, rope_len),
  * a negative length, and offsets outside [0, num_tokens] or decreasing are
  * never used.  The keys and values concerned are not written (append; a query
- * is left out only for its offsets, length or rotation position) or count as
- * masked (attention), and ATTN_ERR_DEVICE_BOUNDS is stored in *status, if
- * given; the library never clears it.  A wait of the attention kernels that
+ * is left out only for its offsets, or bad ones around them, length or rotation
+ * position) or count as masked (attention), and ATTN_ERR_DEVICE_BOUNDS is stored
+ * in *status, if given; the library never clears it.  A wait of the attention kernels that
  * runs past its limit (2 s) stores ATTN_ERR_DEVICE_TIMEOUT there and the
  * kernel ends. */
 #define ATTN_PAGED_PARAMS_VERSION 1

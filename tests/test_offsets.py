@@ -9,6 +9,7 @@ import torch
 from bwd_tcgen05_tma_gb300 import attn as A
 from latent_util import Latent, turn_tolerance
 from oracle import latent_ref as L
+from paged_util import Paged
 from test_latent_expand import Case
 from test_rope import angles, bits, draw, tables
 
@@ -117,13 +118,15 @@ def test_expand(name, back):
 
 CACHES = {
     "latent": (Latent, A.attn_latent_append, ["cache"]),
+    "paged": (Paged, A.attn_paged_append, ["k_cache", "v_cache"]),
 }
 
 
 def appended(kind, new, ctx, change):
     """A batch appended whole, and again with its offsets or lengths changed."""
     make, call, caches = CACHES[kind]
-    good, bad = (make(new, ctx, seed=92, page=16) for _ in range(2))
+    kw = dict(page=16) if kind == "latent" else dict(cache="bf16")
+    good, bad = (make(new, ctx, seed=92, **kw) for _ in range(2))
     call(good.params())
     assert good.status() == 0
     before = {n: bad.t[n].clone() for n in caches}
