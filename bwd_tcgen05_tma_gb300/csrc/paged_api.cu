@@ -46,8 +46,9 @@ attn_status_t validate(const attn_paged_params_t* p) {
   if (p->d_v != 64 && p->d_v != 128) return ATTN_ERR_UNSUPPORTED;
   if (p->page_size < 16 || p->page_size > 256 || (p->page_size & (p->page_size - 1)))
     return ATTN_ERR_UNSUPPORTED;
-  // positions and packed rows are 32-bit, with room for a window or a tile beyond
-  if (static_cast<int64_t>(p->max_pages) * p->page_size > (1ll << 30) ||
+  // positions, packed rows and sequences are 32-bit, with room for a window, a tile or
+  // a block's sequences beyond
+  if (p->num_seqs > (1 << 30) || static_cast<int64_t>(p->max_pages) * p->page_size > (1ll << 30) ||
       static_cast<int64_t>(p->num_tokens) * (p->Hq / p->Hkv) > (1ll << 30))
     return ATTN_ERR_UNSUPPORTED;
   if (!p->cu_seqlens_q && p->num_tokens != p->num_seqs) return ATTN_ERR_SHAPE_MISMATCH;

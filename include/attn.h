@@ -447,7 +447,7 @@ typedef struct {
   int32_t dtype;          /* of q, k_new, v_new, q_rot and o: BF16 or FP16 */
   int32_t cache_dtype;    /* the same, or ATTN_DTYPE_FP8_E4M3 */
   int32_t mask;           /* ATTN_MASK_NONE or ATTN_MASK_CAUSAL */
-  int32_t num_seqs;
+  int32_t num_seqs;   /* at most 2^30 */
   int32_t num_tokens; /* rows of q / k_new / v_new / q_rot / o, padding included */
   int32_t max_q_len;  /* largest n_s (a hint that chooses the kernel for the
                          whole call; any value >= 1 gives right results).  A
