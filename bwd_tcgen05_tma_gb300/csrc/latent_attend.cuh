@@ -1021,7 +1021,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             v[i + e] = n > 0 && !(f[e] < 0.f) ? __uint_as_float(o[i + e]) * f[e] : 0.f;
         }
         if (bad) {
+          // (keys that every row keeps have stayed in the product: only those before and
+          // behind them, no more than the block has tokens, are looked at)
           for (int kk = max(key0, p->any.x); kk < min(key0 + n * kKeys, p->any.y); ++kk) {
+            if (kk >= p->all.x && kk < p->all.y) {
+              kk = p->all.y - 1;
+              continue;
+            }
             const int page = page_of(a, p->seq, kk);
             if (page < 0) continue;
             const float e =

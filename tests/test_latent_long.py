@@ -1,13 +1,15 @@
 """The absorbed attention where the work is cut otherwise than usual: scores of
--inf in pieces of their own."""
+-inf in pieces of their own, and values that are not finite behind long contexts."""
 import numpy as np
 import pytest
 import torch
 
 from bwd_tcgen05_tma_gb300 import attn as A
-from latent_util import Latent
+from latent_util import SCALE, Latent
 
 pytestmark = pytest.mark.gpu
+
+I32 = dict(dtype=torch.int32, device="cuda")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -66,3 +68,59 @@ def test_rows_whose_scores_are_all_minus_infinity(new, ctx, H, sink):
     want = s[:, None].expand(-1, new) if sink else torch.full_like(lse, -np.inf)
     assert torch.equal(lse, want)
     assert c.status() == 0
+
+
+# ------------------------------------------------- long contexts
+
+class Aliased:
+    """Contexts of any length over few pages: the table of every sequence lists the
+    same pages over and over, its last page apart (its own)."""
+
+    def __init__(self, seqs, new, ctx, *, seed, H=16, d_c=512, page=256, pages=8):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+
+        def randn(*shape):
+            return torch.randn(*shape, generator=g, device="cuda").bfloat16()
+
+        assert ctx % page == 0
+        own = -(-new // page)
+        cols = ctx // page + own
+        self.cache = randn(pages + seqs * own, page, d_c + 64)
+        self.table = (torch.arange(cols, **I32) % pages).repeat(seqs, 1)
+        self.table[:, cols - own:] = pages + torch.arange(seqs * own, **I32).view(seqs, own)
+        self.T, self.H, self.new = seqs * new, H, new
+        q_lat, q_rot = randn(self.T, H, d_c), randn(self.T, H, 64)
+        self.status = torch.zeros(1, **I32)
+        self.p = A.make_latent_params(
+            dtype="bf16", cache=self.cache, d_c=d_c, page_table=self.table,
+            seq_lens=torch.full((seqs,), ctx + new, **I32), q_lat=q_lat, q_rot=q_rot,
+            cu_seqlens_q=torch.arange(0, self.T + 1, new, **I32), max_q_len=new, scale=SCALE,
+            status=self.status)
+        self.ws = torch.empty(A.attn_latent_workspace_size(self.p), dtype=torch.uint8,
+                              device="cuda")
+        self.d_c = d_c
+
+    def attend(self):
+        o = torch.full((self.T, self.H, self.d_c), float("nan"), dtype=torch.bfloat16,
+                       device="cuda")
+        lse = torch.full((self.H, self.T), float("nan"), device="cuda")
+        A.attn_latent_fwd(self.p, o, lse, self.ws)
+        torch.cuda.synchronize()
+        return o, lse
+
+
+def test_nan_behind_a_long_context():
+    """A chunk of 700 tokens behind 4 M keys.  The 303rd, the third of the four in its
+    block of rows, is NaN: the rows that keep it are NaN, those before it have the
+    bits that they have without it, and their block's epilogue does not go through
+    all its keys for it (which took seconds, past the limit of the waits)."""
+    c = Aliased(1, 700, 1 << 22, seed=97)
+    ref, ref_lse = c.attend()
+    assert c.status.item() == 0
+    c.cache[c.table[0, -2], 302 - 256, 3] = float("nan")
+    o, lse = c.attend()
+    assert c.status.item() == 0
+    assert torch.isnan(o[302:]).all() and torch.isnan(lse[:, 302:]).all()
+    assert torch.equal(bits(o[:302]), bits(ref[:302]))
+    assert torch.equal(bits(lse[:, :302]), bits(ref_lse[:, :302]))
