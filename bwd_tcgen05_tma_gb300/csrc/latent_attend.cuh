@@ -245,6 +245,25 @@ __device__ __forceinline__ bool walk_piece(const Args& a, Walk& w) {
   w.any = keys_any(a, w.v, w.rb * w.rows, (w.rb + 1) * w.rows);
   return w.t1 > w.t0;
 }
+// The first sequence from s on that has rows (or one behind the last): all lanes, a run
+// of empty ones kSkip a lane at a time.
+constexpr int kSkip = 4;
+__device__ __forceinline__ int next_rows(const Args& a, int s) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (; s < a.num_seqs; s += 32 * kSkip) {
+    unsigned has[kSkip];
+#pragma unroll
+    for (int i = 0; i < kSkip; ++i) {
+      const int x = s + 32 * i + lane;
+      has[i] = __ballot_sync(0xffffffffu, x < a.num_seqs && load_seq(a, min(x, a.num_seqs - 1)).n > 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kSkip; ++i)
+      if (has[i]) return s + 32 * i + __ffs(has[i]) - 1;
+  }
+  return a.num_seqs;
+}
 // The next piece with tiles.  (There is one while the share lasts, unless the offsets
 // or lengths are changed under the call: then the walk ends with the sequences.)
 template <int N>
@@ -255,10 +274,13 @@ __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
     w.u0 = 0;
     if (++w.rb >= blocks_of(a, w.v, w.rows)) {
       w.rb = 0;
-      do {
-        if (++w.seq >= a.num_seqs) return false;
+      if (++w.seq < a.num_seqs) w.v = view_of(a, w.seq);
+      if (w.seq >= a.num_seqs || w.v.q.n == 0) {
+        w.seq = next_rows(a, w.seq + 1);
+        if (w.seq >= a.num_seqs) return false;
         w.v = view_of(a, w.seq);
-      } while (w.v.q.n == 0);
+        if (w.v.q.n == 0) return false;
+      }
     }
   } while (!walk_piece<N>(a, w));
   return true;
@@ -341,6 +363,27 @@ __device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* 
     }
   }
   int s = (o * sp.ranges + r) * sp.per;
+  if (sp.per > 1) {  // the range's sequence: 32 at a time, a lane each
+    const int last = min(a.num_seqs, s + sp.per);
+#pragma unroll 1
+    for (; s < last; s += 32) {
+      const int64_t n = units_of<N>(a, rows, s + lane < last ? s + lane : a.num_seqs, 1);
+      int64_t upto = n;
+#pragma unroll 1
+      for (int i = 1; i < 32; i <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, upto, i);
+        if (lane >= i) upto += y;
+      }
+      const unsigned in = __ballot_sync(0xffffffffu, upto > off);
+      if (in) {
+        const int f = __ffs(in) - 1;
+        off -= __shfl_sync(0xffffffffu, upto - n, f);
+        s += f;
+        break;
+      }
+      off -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
   SeqView v;
   int rb = 0;
   for (;; ++s) {  // row blocks of 32 at a time, all lanes

@@ -1,11 +1,13 @@
 """The absorbed attention where the work is cut otherwise than usual: scores of
--inf in pieces of their own, and values that are not finite behind long contexts."""
+-inf in pieces of their own, values that are not finite behind long contexts, and
+many sequences with long runs of empty ones."""
 import numpy as np
 import pytest
 import torch
 
 from bwd_tcgen05_tma_gb300 import attn as A
 from latent_util import SCALE, Latent
+from paged_util import check_attend
 
 pytestmark = pytest.mark.gpu
 
@@ -124,3 +126,44 @@ def test_nan_behind_a_long_context():
     assert torch.isnan(o[302:]).all() and torch.isnan(lse[:, 302:]).all()
     assert torch.equal(bits(o[:302]), bits(ref[:302]))
     assert torch.equal(bits(lse[:, :302]), bits(ref_lse[:, :302]))
+
+
+# ------------------------------------------------- many sequences
+
+@pytest.mark.parametrize("H", [2, 40])
+@pytest.mark.parametrize("kind", ["spread", "runs"])
+def test_thousands_of_sequences(kind, H):
+    """Several sequences for every thread that sums their work, empty ones among them
+    one by one or in long runs, and a prompt of many row blocks."""
+    n = 5000
+    if kind == "spread":
+        new = [1 if i % 7 == 3 else 2 if i % 41 == 0 else 0 for i in range(n)]
+    else:
+        new = [1 if i // 600 % 2 else 0 for i in range(n)]
+    new[2345] = 150
+    ctx = [(i * 7) % 90 if new[i] else 0 for i in range(n)]
+    c = Latent(new, ctx, seed=99, H=H, d_c=256, page=16)
+    o, lse = c.append_and_attend()
+    assert c.status() == 0
+    check_attend(c, o, lse, c.oracle_attend())
+
+
+def test_a_long_run_of_empty_sequences():
+    """Two prompts with 2^25 empty sequences between them: the block that goes from
+    one to the other finds it without a look at each (which took it past the limit
+    of the waits)."""
+    gap = 1 << 25
+    c = Latent([400, 250], [0, 30], seed=100, H=16, d_c=256, page=256)
+    ref = c.append_and_attend()
+    check_attend(c, *ref, c.oracle_attend())
+    cols = c.table.shape[1]
+    table = torch.full((gap + 2, cols), 2 ** 31 - 1, **I32)
+    lens = torch.full((gap + 2,), 5, **I32)
+    cu = torch.full((gap + 3,), 400, **I32)
+    cu[0], cu[-1] = 0, 650
+    for at, s in ((0, 0), (-1, 1)):
+        table[at] = c.t["table"][s]
+        lens[at] = c.lens[s]
+    o, lse = c.attend(c.params(page_table=table, seq_lens=lens, cu_seqlens_q=cu))
+    assert c.status() == 0
+    check_attend(c, o, lse, c.oracle_attend())
