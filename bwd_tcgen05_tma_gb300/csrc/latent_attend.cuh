@@ -246,9 +246,10 @@ __device__ __forceinline__ bool walk_piece(const Args& a, Walk& w) {
   return w.t1 > w.t0;
 }
 // The first sequence from s on that has rows (or one behind the last): all lanes, a run
-// of empty ones kSkip a lane at a time.
+// of empty ones kSkip a lane at a time.  (Not inlined, as range_at below: what few calls
+// reach would delay the start of all, by the instructions to be fetched.)
 constexpr int kSkip = 4;
-__device__ __forceinline__ int next_rows(const Args& a, int s) {
+__device__ __noinline__ int next_rows(const Args& a, int s) {
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
   for (; s < a.num_seqs; s += 32 * kSkip) {
@@ -274,12 +275,10 @@ __device__ __forceinline__ bool walk_next(const Args& a, Walk& w) {
     w.u0 = 0;
     if (++w.rb >= blocks_of(a, w.v, w.rows)) {
       w.rb = 0;
-      if (++w.seq < a.num_seqs) w.v = view_of(a, w.seq);
-      if (w.seq >= a.num_seqs || w.v.q.n == 0) {
-        w.seq = next_rows(a, w.seq + 1);
+      for (++w.seq;; w.seq = next_rows(a, w.seq + 1)) {
         if (w.seq >= a.num_seqs) return false;
         w.v = view_of(a, w.seq);
-        if (w.v.q.n == 0) return false;
+        if (w.v.q.n > 0) break;
       }
     }
   } while (!walk_piece<N>(a, w));
@@ -302,6 +301,34 @@ __device__ __forceinline__ Split split_of(const Args& a, int rows) {
   s.ranges = s.alone ? 1 : min(kThreads / 32, (a.num_seqs + 31) / 32);
   s.per = (a.num_seqs + 32 * s.ranges - 1) / (32 * s.ranges);
   return s;
+}
+
+// The sequence of [s, last) that holds unit `off` of theirs, and the unit's number in it:
+// 32 at a time, a lane each.
+struct At {
+  int64_t off;
+  int seq;
+};
+template <int N>
+__device__ __noinline__ At range_at(const Args& a, int rows, int s, int last, int64_t off) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (; s < last; s += 32) {
+    const int64_t n = units_of<N>(a, rows, s + lane < last ? s + lane : a.num_seqs, 1);
+    int64_t upto = n;
+#pragma unroll 1
+    for (int i = 1; i < 32; i <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, upto, i);
+      if (lane >= i) upto += y;
+    }
+    const unsigned in = __ballot_sync(0xffffffffu, upto > off);
+    if (in) {
+      const int f = __ffs(in) - 1;
+      return {off - __shfl_sync(0xffffffffu, upto - n, f), s + f};
+    }
+    off -= __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return {off, last};
 }
 
 // This block's share, found by the scheduler warp.
@@ -363,26 +390,10 @@ __device__ __forceinline__ void walk_init(const Args& a, Aux* x, const int64_t* 
     }
   }
   int s = (o * sp.ranges + r) * sp.per;
-  if (sp.per > 1) {  // the range's sequence: 32 at a time, a lane each
-    const int last = min(a.num_seqs, s + sp.per);
-#pragma unroll 1
-    for (; s < last; s += 32) {
-      const int64_t n = units_of<N>(a, rows, s + lane < last ? s + lane : a.num_seqs, 1);
-      int64_t upto = n;
-#pragma unroll 1
-      for (int i = 1; i < 32; i <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, upto, i);
-        if (lane >= i) upto += y;
-      }
-      const unsigned in = __ballot_sync(0xffffffffu, upto > off);
-      if (in) {
-        const int f = __ffs(in) - 1;
-        off -= __shfl_sync(0xffffffffu, upto - n, f);
-        s += f;
-        break;
-      }
-      off -= __shfl_sync(0xffffffffu, upto, 31);
-    }
+  if (sp.per > 1) {
+    const At at = range_at<N>(a, rows, s, min(a.num_seqs, s + sp.per), off);
+    s = at.seq;
+    off = at.off;
   }
   SeqView v;
   int rb = 0;
@@ -540,7 +551,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t i = 0; ok;) {
       const int rb = (w.rb << pair) + half;
       if (!live || rb * N < w.v.q.n * a.group) {  // (the last block may have one half)
-        if (i >= 4 && !(ok = mbar_wait_warp(&x->piece_empty[i & 3], ((i >> 2) - 1) & 1))) break;
+        if (i >= 4 &&
+            !(ok = mbar_wait_warp(&x->piece_empty[i & 3], ((i >> 2) - 1) & 1)))
+          break;
         if (lane == 0) {
           Piece& p = x->piece[i & 3];
           if (live) {
@@ -1026,6 +1039,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (below 0: no score of the row is above -inf, O = 0; a piece does not know of
         // the others, and hands on what its keys of weight 0 made of O)
         x->fac[st] = complete && none ? -1.f : norm;
+        if (complete && none) x->row_hi[st] = 0;
       }
       softmax_any(false);
       // (behind the barrier: the other warps are at O already)
@@ -1081,8 +1095,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (fabsf(e) < INFINITY) continue;
 #pragma unroll
             for (int i = 0; i < kCols; ++i)
-              if (kk >= x->row_lo[cc + i] && kk < x->row_hi[cc + i] && !(x->fac[cc + i] < 0.f))
-                v[i] = NAN;
+              if (kk >= x->row_lo[cc + i] && kk < x->row_hi[cc + i]) v[i] = NAN;
           }
         }
         if (complete) {
