@@ -11,6 +11,7 @@ struct LatentArgs {
   Args a;
   int d_c;
   int pair;  // attention: blocks work in pairs on row blocks of twice the rows (0 or 1)
+  uint64_t wait_ns;  // attention: limit of the waits that may last for whole pieces
   const uint16_t* c_new;
   const uint16_t* k_rope;
   const uint16_t* q_rope;

@@ -262,6 +262,10 @@ attn_status_t attn_latent_fwd(const attn_latent_params_t* p, void* o, float* lse
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int rows = rows_of(p);
   l.pair = rows == 64 && pairs(p, sms);
+  // Queries are copied, and pieces handed out, up to four pieces ahead of the softmax: a
+  // piece has at most the keys of a table's row, of which 64 take 1 to 2 us (4 us are
+  // allowed them), and its search passes empty sequences in some 10 ns each (64).
+  l.wait_ns = sm103::kWaitNs + 64ull * p->num_seqs + 250ull * p->max_pages * p->page_size;
   const cudaError_t e =
       l.a.f16 ? launch_latent_f16(l, rows, sms, st) : launch_latent_bf16(l, rows, sms, st);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;

@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // The i-th piece (in shared memory), and this warp's release of it.
   auto take = [&](uint32_t i, bool* ok) -> const Piece* {
-    *ok = mbar_wait_warp(&x->piece_full[i & 3], (i >> 2) & 1);
+    *ok = mbar_wait_warp(&x->piece_full[i & 3], (i >> 2) & 1, l.wait_ns);
     return &x->piece[i & 3];
   };
   auto release = [&](uint32_t i) {
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rb = (w.rb << pair) + half;
       if (!live || rb * N < w.v.q.n * a.group) {  // (the last block may have one half)
         if (i >= 4 &&
-            !(ok = mbar_wait_warp(&x->piece_empty[i & 3], ((i >> 2) - 1) & 1)))
+            !(ok = mbar_wait_warp(&x->piece_empty[i & 3], ((i >> 2) - 1) & 1, l.wait_ns)))
           break;
         if (lane == 0) {
           Piece& p = x->piece[i & 3];
@@ -788,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = p->n, r0 = p->rb * N, row0 = p->row0, new_rows = p->new_rows;
       release(pi);
       if (n == 0) continue;
-      if (it > 0 && !(ok = mbar_wait_warp(&x->q_empty, (it - 1) & 1))) break;
+      if (it > 0 && !(ok = mbar_wait_warp(&x->q_empty, (it - 1) & 1, l.wait_ns))) break;
       // a lane finds a row's addresses (offsets in 16-byte units, < 0: no such row)
       constexpr int kRowsWarp = N / 4;
       int64_t lat_at = -1, rot_at = 0;

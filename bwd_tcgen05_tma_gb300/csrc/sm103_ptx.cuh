@@ -69,11 +69,14 @@ SM103_DEV bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Limit of a wait where none is given.
+constexpr uint64_t kWaitNs = 2000000000;
+
 // Bounded wait for the phase with the given parity to complete.  Returns false
 // once `limit_ns` of wall time has passed without completion (the caller then
 // records a timeout status and unwinds).  The limit is far above any
 // legitimate wait of these kernels.
-SM103_DEV bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns = 2000000000ull) {
+SM103_DEV bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kWaitNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
@@ -552,8 +555,8 @@ SM103_DEV void st_shared_v4(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, 
 
 // Warp-uniform bounded wait: every lane waits, and the warp agrees on failure
 // so that later .sync.aligned instructions stay convergent.
-SM103_DEV bool mbar_wait_warp(uint64_t* bar, uint32_t parity) {
-  const bool ok = mbar_wait(bar, parity);
+SM103_DEV bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kWaitNs) {
+  const bool ok = mbar_wait(bar, parity, limit_ns);
   return __all_sync(0xffffffffu, ok);
 }
 

@@ -700,9 +700,11 @@ attn_status_t attn_latent_expand_bwd(const attn_latent_expand_params_t* p, void*
  *   order in which blocks run.
  *
  * Streams, workspaces, errors, device checks and the status word are those of
- * the paged calls.  (Among bad offsets the append may leave out tokens of other
- * sequences too, and writes a token that several claim for one of them.)  An E4M3
- * cache is not offered (cache and queries share dtype). */
+ * the paged calls.  (The limit of waits that last for whole contexts grows with
+ * the call: 2 s, 64 ns a sequence and 250 ns a key of a table's row.  Among bad
+ * offsets the append may leave out tokens of other sequences too, and writes a
+ * token that several claim for one of them.)  An E4M3 cache is not offered (cache
+ * and queries share dtype). */
 #define ATTN_LATENT_PARAMS_VERSION 1
 typedef struct {
   int32_t struct_version; /* = ATTN_LATENT_PARAMS_VERSION */

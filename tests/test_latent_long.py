@@ -1,6 +1,6 @@
 """The absorbed attention where the work is cut otherwise than usual: scores of
--inf in pieces of their own, values that are not finite behind long contexts, and
-many sequences with long runs of empty ones."""
+-inf in pieces of their own, values that are not finite behind long contexts, many
+sequences with long runs of empty ones, and pieces that take seconds."""
 import numpy as np
 import pytest
 import torch
@@ -126,6 +126,15 @@ def test_nan_behind_a_long_context():
     assert torch.isnan(o[302:]).all() and torch.isnan(lse[:, 302:]).all()
     assert torch.equal(bits(o[:302]), bits(ref[:302]))
     assert torch.equal(bits(lse[:, :302]), bits(ref_lse[:, :302]))
+
+
+def test_pieces_that_take_longer_than_a_wait():
+    """160 contexts of 140 M keys: a block works on one of them for some 3 s, which
+    is no failure."""
+    c = Aliased(160, 1, 550000 * 256, seed=98, H=64, pages=64)
+    o, lse = c.attend()
+    assert c.status.item() == 0
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
 
 
 # ------------------------------------------------- many sequences
