@@ -579,8 +579,6 @@ def make_rope_table_params(*, cos, sin, base=10000.0, scaling="NONE", factor=1.0
 
 def _fill_places(p, given, tokens, seq_len):
     """Positions, tables and status of a block that turns packed tokens."""
-    import torch
-
     pos, cu = given["positions"], given["cu_seqlens"]
     if pos is not None and cu is not None:
         raise ValueError("positions and cu_seqlens: one of the two")

@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float fac = a.scale * kLog2e;
     uint32_t k = 0, it = 0;
     // A wait that ran out here is told to the other softmax warps at their next
-    // vote, so that all four leave together and none stays at their barrier.
+    // vote, so that all eight leave together and none stays at their barrier.
     bool failed = false;
     for (uint32_t pi = 0;; ++pi) {
       bool ok;
