@@ -558,7 +558,8 @@ def make_rope_table_params(*, cos, sin, base=10000.0, scaling="NONE", factor=1.0
     """Fill an ``attn_rope_table_params_t`` (see attn.h).  cos, sin: fp32
     [rope_len, rot_dim / 2], which ``attn_rope_table`` fills; scaling: "NONE",
     "LINEAR", "BASE" or "TURNS", with its factor (and, for "TURNS", the trained
-    length and the turns between which frequencies go from stretched to kept)."""
+    length and the turns between which frequencies go from stretched to kept, linearly
+    in the turns and not in the pair's index)."""
     import torch
 
     given = dict(rope_cos=cos, rope_sin=sin)

@@ -149,7 +149,7 @@ int rows_of(const attn_latent_params_t* p) {
 // Blocks in pairs: two row blocks of a sequence go through its tiles side by side, so
 // that they come from HBM once.  By the rows of the mean sequence (the largest may be
 // alone): always for two row blocks (128 heads: 4 contexts of 100-131 k keys 184 -> 150
-// us, 256 of up to 256 keys 60 -> 52); for more where the caches, at their longest,
+// us, 256 of up to 256 keys 60 -> 53); for more where the caches, at their longest,
 // exceed the L2 cache (three chunks over up to 16 k keys: 232 us without, 239 with;
 // shares are coarser); not for few and odd, where the last pair has one at work.
 bool pairs(const attn_latent_params_t* p, int sms) {

@@ -5,9 +5,9 @@
 // next sixteen.  A row is
 // 16-byte units side by side, so a warp's accesses are whole lines, and all of a
 // job's loads are on their way before the token's place is known.  Bound by HBM
-// for prompts (17349 tokens, 16 heads, 98 MB: 17.8 us, 5.5 TB/s); for single tokens by
-// the launch and the chain of reads lengths -> table -> store (64 tokens: 2.2 us in a
-// graph, 3.8 as the host launches them).
+// for prompts (17349 tokens, 16 heads, 98 MB: 18.0 us, 5.4 TB/s); for single tokens by
+// the launch and the chain of reads lengths -> table -> store (64 tokens: 2.4 us in a
+// graph, 3.9 as the host launches them).
 #include "latent.cuh"
 
 namespace attn {

@@ -23,15 +23,16 @@
 // tiles, each for its 64 rows: the second finds them in the L2 cache.
 //
 // What bounds it.  One row read is 1152 bytes (d_c 512) for 2176 FLOP a (token, head):
-//  - 16 rows: HBM (64 ragged contexts, 16 heads, 262 MB: 55.5 us, of which 39 at 6.7
+//  - 16 rows: HBM (64 ragged contexts, 16 heads, 262 MB: 56 us, of which 39 at 6.7
 //    TB/s; the rest are a block's start, 3 us, its state, 1.6, and the join);
 //  - 64 rows: two tiles in shared memory, so that a tile's copies wait for the
 //    products of the one before the last: 3570 clocks a tile where HBM allows 3390
-//    (4 contexts of 100-131 k keys, 64 heads: 106 us, 5.0 TB/s);
+//    (4 contexts of 100-131 k keys, 64 heads: 107 us, 4.9 TB/s);
 //  - chunks of prompts, whose tiles come from the L2 cache: shared memory.  A tile of
 //    64 rows moves 328 KB through it (147 for S, 98 for O, 82 written), 2560 clocks at
-//    128 bytes each, and takes 2500-2700; its MMAs alone take 1960 (230 us for three
-//    chunks over up to 16 k keys, 885 TFLOP/s, tensor pipe 58 % busy).
+//    128 bytes each, and takes 2500-2700; its MMAs alone take 1960 (231 us for three
+//    chunks over up to 16 k keys, 882 TFLOP/s, tensor pipe 58 % busy).  Pairs of blocks
+//    are bound by it too (128 heads, 4 contexts: 148 us, one read of 527 MB, 54 % busy).
 //
 // Roles: an MMA issuer for each product, TMA producer, scheduler (a warp each), eight
 // softmax warps (four read a tile's 64 lanes, for one half of the columns), four

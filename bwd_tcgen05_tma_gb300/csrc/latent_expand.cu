@@ -7,7 +7,7 @@
 // (forward), or is summed over the heads in registers, lanes meeting in a fixed
 // order, and turned back once (gradient).  Bound by HBM: nothing is read or
 // written twice (8192 tokens of 16 heads, 128 + 64 and 128 wide, 153 MB: 25.3 us
-// forward, 25.9 back, 6.0 TB/s).
+// forward, 25.8 back, 6.0 TB/s).
 #include "rotate.cuh"
 
 namespace attn {

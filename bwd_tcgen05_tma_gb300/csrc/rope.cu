@@ -19,7 +19,7 @@ namespace {
 // its stores and a launch's 2 us (131072 positions of 32 pairs, 33.5 MB: 6.1 us; with
 // all 64 bits turned to float 8.7, and with sincospif in place of the series 9.8; 4
 // positions a thread 6.3, blocks of 256 threads 6.4); small tables by the
-// launch (8192 positions of 64 pairs: 2.3 us in a graph, 4.4 as the host launches them).
+// launch (8192 positions of 64 pairs: 2.3 us in a graph, 4.5 as the host launches them).
 constexpr int kTableThreads = 128;
 constexpr int kTableRows = 8;  // positions a thread takes
 
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kTableThreads) table_kernel(const __grid_const
 // One warp a token: its lanes take the units of several heads side by side, so
 // that a warp's accesses are whole lines, and each lane keeps its unit's cosines
 // and sines for all heads.  Bound by HBM, two bytes an element each way: 2 x 8192
-// tokens of 32 + 8 heads, d 128, 52.0 us, 6.5 TB/s; 8192 tokens of 16 + 16 heads, d
+// tokens of 32 + 8 heads, d 128, 52.1 us, 6.5 TB/s; 8192 tokens of 16 + 16 heads, d
 // 192 of which 64 turn, 32.2 us, 6.3 TB/s.  (Blocks of 4 warps instead of 8, so that
 // they leave one by one, 58 -> 54 and 42 -> 36; accesses that leave the caches first
 // 52 and 34.5; eight copies in flight 32.2.)

@@ -534,7 +534,11 @@ attn_status_t attn_paged_fwd(const attn_paged_params_t* p, void* o, float* lse, 
  *   TURNS:   f_p = g_p (w + (1 - w) / factor) with w going from 0 to 1 as the
  *            turns trained_len * g_p / (2 pi) go from turns_low to turns_high
  *            (linearly; frequencies that turn often in the trained context are
- *            kept, those that hardly turn are divided by factor).
+ *            kept, those that hardly turn are divided by factor).  The ramp is
+ *            over the turns.  Models whose tables were made with a ramp over the
+ *            pair's index, between the indices at which the two bounds fall, have
+ *            other frequencies in between: make their tables elsewhere (all calls
+ *            take any table).
  * Frequencies are computed in 64 bits and angles in fixed point, as turns modulo
  * 1 with 64 bits of which 32 are kept, so that far positions lose nothing but the
  * frequencies' own rounding: each value is off by at most 2^-22 * |magnitude| below position 2^27,
