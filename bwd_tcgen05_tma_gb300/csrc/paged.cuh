@@ -120,13 +120,14 @@ __device__ __forceinline__ Seq load_seq(const Args& a, int s) {
 
 // A token's place is looked up from the token, so that a call may meet few of its
 // sequences: where there are offsets, blocks behind the others (of `threads` threads)
-// go through all of them, and report what is bad wherever it stands.
+// go through all of them, and report what is bad wherever it stands.  (Out of line: the
+// append of 64 tokens to a cache of heads takes 7.0 us, inlined 7.2.)
 constexpr int kSeqsThread = 4;
 inline int64_t check_blocks(const Args& a, int threads) {
   const int64_t each = int64_t{kSeqsThread} * threads;
   return a.cu ? (a.num_seqs + each - 1) / each : 0;
 }
-__device__ __forceinline__ void check_seqs(const Args& a, int block) {
+inline __device__ __noinline__ void check_seqs(const Args& a, int block) {
   if (!a.cu || block < 0) return;
 #pragma unroll
   for (int k = 0; k < kSeqsThread; ++k) {
